@@ -248,7 +248,7 @@ def _plain_glr_bwd(s):
     r, i, a, f = _gates(s)
     hp = torch.cat([s["h0"].unsqueeze(0), s["h"][:-1].float()])
     # delta_t = dh_t + a_{t+1} delta_{t+1}, the scan in reverse time
-    d = s["dh"].float()
+    d = s["dh"].float().clone()
     d[-1] += s["dh_last"]
     an = torch.zeros_like(a)
     an[:-1] = a[1:]

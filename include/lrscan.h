@@ -64,7 +64,8 @@
  *  - CUDA graphs: the carry packets are tagged with an epoch that the kernels
  *    take on the device from the workspace's ticket word (every launch takes
  *    a fresh one), so a call of lr_scan_fwd, lr_scan_bwd, sru_fwd, sru_bwd,
- *    lstm_cell_fwd, lstm_cell_bwd or deer_diag_bwd captured into a graph
+ *    lstm_cell_fwd, lstm_cell_bwd, glr_fwd, glr_bwd, glr_step or deer_diag_bwd
+ *    captured into a graph
  *    gives the right result on every replay, with whatever the captured
  *    buffers hold then.  Make one uncaptured call of the same shape first
  *    (it sizes the workspace and sets up the kernels; capture fails if the
@@ -103,7 +104,8 @@ typedef enum {
     LR_ERR_TIMEOUT = 4,       /* device: a carry wait ran out; outputs are NaN */
     LR_ERR_NONFINITE = 5,     /* DEER: a residual was NaN or Inf */
     LR_ERR_NOT_CONVERGED = 6, /* DEER: kmax iterations without residual < eps */
-    LR_ERR_TOO_LARGE = 7      /* sizes beyond the supported range */
+    LR_ERR_TOO_LARGE = 7,     /* sizes beyond the supported range */
+    LR_ERR_INDEX = 8          /* device: an index in a caller's tensor was out of range */
 } lr_status;
 
 /*
@@ -311,6 +313,60 @@ int lstm_cell_bwd(const void* zf, const void* zi, const void* zc, const void* zo
                   int64_t B, int64_t T, int64_t D, int dtype, void* stream);
 
 /*
+ * Gated linear recurrence, forward: the scan of row a1 with a decay set by the
+ * input and the input scaled so that the state keeps its size ([P1]
+ * parallel-scan paragraph for the scan; the pages name no such cell).  One launch:
+ *   r = sigmoid(zr + br),  i = sigmoid(zi + bi),
+ *   a = exp(-lam r),  f = sqrt(1 - a^2),
+ *   h_t = a_t h_{t-1} + f_t i_t x_t   (h_{-1} = h0).
+ * On a reset step a = 0 and f = 1: a new document starts there.
+ *   x, zr, zi    : [T,B,D] in   input, decay and input gate pre-activations
+ *   lam, br, bi  : [D] fp32 in  decay rate (>= 0; a negative one gives NaN where
+ *                               a > 1) and biases
+ *   h0           : [B,D] fp32 in   NULL means zeros
+ *   reset        : [T,B] bytes in  nonzero: reset; NULL means none
+ *   h            : [T,B,D] out
+ *   h_last       : [B,D] fp32 out  the state after the last step, not rounded to
+ *                                  the storage type (NULL: not wanted); T = 0: h0
+ * The states are fp32 whatever the storage type.
+ */
+int glr_fwd(const void* x, const void* zr, const void* zi, const float* lam, const float* br,
+            const float* bi, const float* h0, const uint8_t* reset, void* h, float* h_last,
+            int64_t B, int64_t T, int64_t D, int dtype, void* stream);
+
+/*
+ * Gated linear recurrence, backward, given the forward h (as stored) and the
+ * upstream dh = dL/dh_t:
+ *   d_t = dh_t + a_{t+1} d_{t+1}  (the last step: + dh_last),
+ *   dx = d f i,  dzi = d f x i (1-i),  dh0 = a_0 d_0,
+ *   K = a h_{t-1} - i x a^2 / f (0 on a reset step and where 1 - a^2 = 0),
+ *   dzr = -lam d K r (1-r),  dlam = -sum d K r,  dbr = sum dzr,  dbi = sum dzi
+ * (sums over t and batch in a fixed order).
+ *   h, dh       : [T,B,D] in;  dh_last : [B,D] fp32 in, the gradient that reaches
+ *                 the state after the last step (NULL = zeros)
+ *   dx, dzr, dzi : [T,B,D] out;  dlam, dbr, dbi : [D] fp32 out (overwritten);
+ *   dh0         : [B,D] fp32 out (NULL = skip)
+ */
+int glr_bwd(const void* x, const void* zr, const void* zi, const float* lam, const float* br,
+            const float* bi, const float* h0, const uint8_t* reset, const void* h, const void* dh,
+            const float* dh_last, void* dx, void* dzr, void* dzi, float* dlam, float* dbr,
+            float* dbi, float* dh0, int64_t B, int64_t T, int64_t D, int dtype, void* stream);
+
+/*
+ * Gated linear recurrence, one step of B sequences (decoding): the states sit
+ * in a pool of slots and are updated in place.
+ *   x, zr, zi : [B,D] in;  reset : [B] bytes in (NULL = none);  h : [B,D] out
+ *   state     : [n_slots,D] fp32 in and out
+ *   slots     : [B] int32 in, the slot of each row; a negative one is padding (its
+ *               h row is zeros), NULL means slot b for row b (n_slots >= B).  No
+ *               slot may appear twice.  A slot >= n_slots is treated as padding
+ *               and recorded as LR_ERR_INDEX in the device error word.
+ */
+int glr_step(const void* x, const void* zr, const void* zi, const float* lam, const float* br,
+             const float* bi, const uint8_t* reset, const int32_t* slots, float* state, void* h,
+             int64_t B, int64_t n_slots, int64_t D, int dtype, void* stream);
+
+/*
  * Forward scan that allocates nothing (no counterpart in the pages: this is a
  * deployment variant of lr_scan_fwd, same arguments and results).
  * For callers that may not allocate device memory: code running under an
@@ -345,8 +401,8 @@ int lr_scan_fwd_noalloc(const void* a, const void* b, const void* h0, void* h,
 
 /*
  * Reads and clears the device error word of the current device (synchronises
- * the device).  Returns LR_OK or the first recorded device error
- * (LR_ERR_TIMEOUT).  After an error it also resets the tile ticket, which a
+ * the device).  Returns LR_OK or the gravest recorded device error
+ * (LR_ERR_TIMEOUT, then LR_ERR_INDEX).  After an error it also resets the tile ticket, which a
  * launch that gave up leaves mid-count: call it after LR_ERR_TIMEOUT before
  * any further call on that device.
  */
@@ -371,7 +427,9 @@ typedef enum {
     LR_OP_DEER_BWD = 5,
     LR_OP_LSTM_FWD = 6,
     LR_OP_LSTM_BWD = 7,
-    LR_OP_DEER_ODE = 8
+    LR_OP_DEER_ODE = 8,
+    LR_OP_GLR_FWD = 16, /* 9 to 15 are not operations */
+    LR_OP_GLR_BWD = 17
 } lr_op;
 typedef enum {
     LR_PROTO_CHAIN = 0,   /* a tile waits for the state after the chunk before it,

@@ -23,7 +23,7 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "lrscan.h")
 
 LR_F32, LR_BF16 = 0, 1
 (LR_OK, LR_ERR_INVALID_ARG, LR_ERR_ALIGN, LR_ERR_CUDA, LR_ERR_TIMEOUT, LR_ERR_NONFINITE,
- LR_ERR_NOT_CONVERGED, LR_ERR_TOO_LARGE) = range(8)
+ LR_ERR_NOT_CONVERGED, LR_ERR_TOO_LARGE, LR_ERR_INDEX) = range(9)
 
 _lib = None
 
@@ -64,6 +64,9 @@ def load():
     lib.deer_ode_solve.argtypes = [P, P, P, P, P, I64, I64, I64, ctypes.c_float, I, P, P, P, P,
                                    I, P]
     lib.deer_diag_bwd.argtypes = [P] * 7 + [I64, I64, I64, I, P]
+    lib.glr_fwd.argtypes = [P] * 10 + [I64, I64, I64, I, P]
+    lib.glr_bwd.argtypes = [P] * 18 + [I64, I64, I64, I, P]
+    lib.glr_step.argtypes = [P] * 10 + [I64, I64, I64, I, P]
     lib.lr_last_error.argtypes = []
     lib.lr_status_str.argtypes = [I]
     lib.lr_status_str.restype = ctypes.c_char_p
@@ -358,6 +361,109 @@ def deer_diag_bwd(w, y, dy, h0=None, du=None, dw=None, dh0=None, want_dh0=True, 
     return du, dw, dh0
 
 
+def _state32(name, t, B, D, ref):
+    if t is None:
+        return None
+    if tuple(t.shape) != (B, D) or t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 [{B}, {D}] CUDA tensor")
+    if t.device != ref.device:
+        raise ValueError(f"{name} is on {t.device}, the sequence tensors on {ref.device}")
+    return t
+
+
+def _flags(name, t, shape, ref):
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype not in (torch.uint8, torch.bool) or not t.is_cuda \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous uint8 or bool {list(shape)} CUDA tensor")
+    if t.device != ref.device:
+        raise ValueError(f"{name} is on {t.device}, the sequence tensors on {ref.device}")
+    return t
+
+
+def glr_fwd(x, zr, zi, lam, br, bi, h0=None, reset=None, h=None, h_last=None, want_last=True,
+            stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t with
+    a = exp(-lam sigmoid(zr + br)), i = sigmoid(zi + bi) (x, zr, zi [T, B, D];
+    lam, br, bi [D] fp32; h0 [B, D] fp32; reset [T, B] uint8 or bool, nonzero
+    where a new document starts). Returns (h, h_last), h_last the fp32 state
+    after the last step (None with want_last=False)."""
+    _seq("x", x)
+    _seq("zr", zr, x)
+    _seq("zi", zi, x)
+    T, B, D = x.shape
+    for n, t in (("lam", lam), ("br", br), ("bi", bi)):
+        _param(n, t, D, x)
+    _state32("h0", h0, B, D, x)
+    _flags("reset", reset, (T, B), x)
+    h = torch.empty_like(x) if h is None else _seq("h", h, x)
+    if h_last is None and want_last:
+        h_last = torch.empty((B, D), dtype=torch.float32, device=x.device)
+    _state32("h_last", h_last, B, D, x)
+    _check(load().glr_fwd(_p(x), _p(zr), _p(zi), _p(lam), _p(br), _p(bi), _p(h0), _p(reset), _p(h),
+                          _p(h_last), B, T, D, _code(x), _stream(stream, x)))
+    return h, h_last
+
+
+def glr_bwd(x, zr, zi, lam, br, bi, h, dh, h0=None, reset=None, dh_last=None, out=None,
+            want_dh0=True, stream=None):
+    """Backward of glr_fwd for the upstream dh [T, B, D] and dh_last [B, D] fp32
+    (the gradient of h_last). Returns dict dx, dzr, dzi, dlam, dbr, dbi, dh0."""
+    _seq("x", x)
+    for n, t in (("zr", zr), ("zi", zi), ("h", h), ("dh", dh)):
+        _seq(n, t, x)
+    T, B, D = x.shape
+    for n, t in (("lam", lam), ("br", br), ("bi", bi)):
+        _param(n, t, D, x)
+    _state32("h0", h0, B, D, x)
+    _state32("dh_last", dh_last, B, D, x)
+    _flags("reset", reset, (T, B), x)
+    o = dict(out or {})
+    for k in ("dx", "dzr", "dzi"):
+        o[k] = torch.empty_like(x) if o.get(k) is None else _seq(k, o[k], x)
+    for k in ("dlam", "dbr", "dbi"):
+        o[k] = torch.empty(D, dtype=torch.float32, device=x.device) if o.get(k) is None else _param(k, o[k], D, x)
+    if o.get("dh0") is None and want_dh0:
+        o["dh0"] = torch.empty((B, D), dtype=torch.float32, device=x.device)
+    _state32("dh0", o.get("dh0"), B, D, x)
+    _check(load().glr_bwd(_p(x), _p(zr), _p(zi), _p(lam), _p(br), _p(bi), _p(h0), _p(reset), _p(h),
+                          _p(dh), _p(dh_last), _p(o["dx"]), _p(o["dzr"]), _p(o["dzi"]), _p(o["dlam"]),
+                          _p(o["dbr"]), _p(o["dbi"]), _p(o.get("dh0")), B, T, D, _code(x),
+                          _stream(stream, x)))
+    return o
+
+
+def glr_step(x, zr, zi, lam, br, bi, state, slots=None, reset=None, h=None, stream=None):
+    """One step of the gated linear recurrence for B sequences (x, zr, zi
+    [B, D]), whose fp32 states sit in the pool state [n_slots, D] and are
+    updated in place. slots [B] int32: the slot of each row, negative for a
+    padding row (None: slot b for row b); no slot twice. A slot past the pool
+    counts as padding and sets LR_ERR_INDEX (last_error). Returns h [B, D]."""
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"x must be a contiguous [B, D] CUDA tensor, got shape {tuple(x.shape)}")
+    B, D = x.shape
+    for n, t in (("zr", zr), ("zi", zi)) + ((("h", h),) if h is not None else ()):
+        if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous and match shape/dtype/device of x")
+    for n, t in (("lam", lam), ("br", br), ("bi", bi)):
+        _param(n, t, D, x)
+    if state.dim() != 2:
+        raise ValueError(f"state must be [n_slots, D], got shape {tuple(state.shape)}")
+    _state32("state", state, state.shape[0], D, x)
+    if slots is not None:
+        if slots.dtype != torch.int32 or tuple(slots.shape) != (B,) or slots.device != x.device \
+                or not slots.is_contiguous():
+            raise ValueError("slots must be a contiguous int32 [B] CUDA tensor on the device of x")
+    elif state.shape[0] < B:
+        raise ValueError(f"state has {state.shape[0]} slots for {B} rows")
+    _flags("reset", reset, (B,), x)
+    h = torch.empty_like(x) if h is None else h
+    _check(load().glr_step(_p(x), _p(zr), _p(zi), _p(lam), _p(br), _p(bi), _p(reset), _p(slots),
+                           _p(state), _p(h), B, state.shape[0], D, _code(x), _stream(stream, x)))
+    return h
+
+
 def last_error() -> int:
     """Reads and clears the device error word (synchronises the device)."""
     return int(load().lr_last_error())
@@ -370,6 +476,7 @@ def workspace_bytes() -> int:
 # lr_op and lr_protocol of the header
 OPS = ("scan_fwd", "scan_bwd", "sru_fwd", "sru_bwd", "deer", "deer_bwd", "lstm_fwd", "lstm_bwd",
        "deer_ode")
+GLR_OPS = {"glr_fwd": 16, "glr_bwd": 17}
 PROTOCOLS = ("chain", "walk", "look", "cluster")
 
 
@@ -382,7 +489,8 @@ def plan_info(op: str, dtype: str, vec: bool, T: int, C: int) -> dict:
     rows, nch = ctypes.c_int64(-1), ctypes.c_int64(-1)
     if dtype not in ("f32", "bf16"):
         raise ValueError(f"dtype must be 'f32' or 'bf16', got {dtype!r}")
-    st = lib.lr_plan_info(OPS.index(op), LR_F32 if dtype == "f32" else LR_BF16, 1 if vec else 0, int(T), int(C),
+    code = GLR_OPS[op] if op in GLR_OPS else OPS.index(op)
+    st = lib.lr_plan_info(code, LR_F32 if dtype == "f32" else LR_BF16, 1 if vec else 0, int(T), int(C),
                           ctypes.byref(proto), ctypes.byref(tma), ctypes.byref(rows),
                           ctypes.byref(nch))
     if st != LR_OK:

@@ -89,4 +89,39 @@ __device__ __forceinline__ float act_expm1(float x) {
     return ex2_ftz(kLog2e * x) - 1.f;
 }
 
+// Square root and reciprocal square root, hardware approximations (relative
+// error about 2^-23 and 2^-22), subnormals flushed to zero.
+__device__ __forceinline__ float sqrt_ftz(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rsqrt_ftz(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The decay of the gated linear recurrence, a = e^l for l <= 0, and
+// q = 1 - a^2 without the cancellation where a is near 1 (long memories): with
+// m = e^l - 1 by its Taylor series near 0, a = 1 + m and q = -m (2 + m).
+// The series stops at l^7/7!: the first omitted term is under 4e-9 |l| at
+// |l| = 1/4.  Below, the hardware exponential: q > 0.39 there.
+__device__ __forceinline__ void act_decay(float l, float& a, float& q) {
+    if (l > -0.25f) {
+        float p = fmaf(l, 1.f / 7.f, 1.f);
+        p = fmaf(l * (1.f / 6.f), p, 1.f);
+        p = fmaf(l * 0.2f, p, 1.f);
+        p = fmaf(l * 0.25f, p, 1.f);
+        p = fmaf(l * (1.f / 3.f), p, 1.f);
+        p = fmaf(l * 0.5f, p, 1.f);
+        const float m = l * p;
+        a = 1.f + m;
+        q = -m * (2.f + m);
+    } else {
+        a = ex2_ftz(kLog2e * l);
+        q = fmaf(-a, a, 1.f);
+    }
+}
+
 }  // namespace lrs

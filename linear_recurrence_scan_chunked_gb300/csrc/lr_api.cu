@@ -477,6 +477,97 @@ int lstm_cell_bwd(const void* zf, const void* zi, const void* zc, const void* zo
     return lv.done();
 }
 
+int glr_fwd(const void* x, const void* zr, const void* zi, const float* lam, const float* br,
+            const float* bi, const float* h0, const uint8_t* reset, void* h, float* h_last, int64_t B,
+            int64_t T, int64_t D, int dtype, void* stream) {
+    TRY(check_sizes(B, T, D, dtype));
+    cudaStream_t s = (cudaStream_t)stream;
+    if (B * T * D == 0) {  // no step: the state passes through
+        if (h_last && B * D > 0) {
+            if (!aligned(h_last, 4) || !aligned(h0, 4)) return LR_ERR_ALIGN;
+            if (h0) CK(cudaMemcpyAsync(h_last, h0, (size_t)(B * D) * 4, cudaMemcpyDeviceToDevice, s));
+            else CK(cudaMemsetAsync(h_last, 0, (size_t)(B * D) * 4, s));
+        }
+        return LR_OK;
+    }
+    bool vec, vecp;
+    TRY(check_ptrs({x, zr, zi, h}, {}, {lam, br, bi}, dtype, D, &vec));
+    TRY(check_ptrs({}, {h0, h_last}, {}, LR_F32, D, &vecp));
+    vec = vec && vecp;
+    GUARD;
+    DevWS* ws;
+    TRY(get_ws(&ws));
+    Geom g;
+    Carry cr;
+    TRY(enter(*ws, s));
+    Leave lv(*ws, s);
+    TRY(plan(*ws, OP_GLR_FWD, dtype, vec, T, B * D, D, &g, &cr, s));
+    CK(launch_glr_fwd(dtype, vec, GlrIn{x, zr, zi, lam, br, bi, reset}, h0, h, h_last, g, cr, s));
+    return lv.done();
+}
+
+int glr_bwd(const void* x, const void* zr, const void* zi, const float* lam, const float* br,
+            const float* bi, const float* h0, const uint8_t* reset, const void* h, const void* dh,
+            const float* dh_last, void* dx, void* dzr, void* dzi, float* dlam, float* dbr, float* dbi,
+            float* dh0, int64_t B, int64_t T, int64_t D, int dtype, void* stream) {
+    TRY(check_sizes(B, T, D, dtype));
+    cudaStream_t s = (cudaStream_t)stream;
+    if (B * T * D == 0) {
+        if (D > 0) {
+            for (float* dp : {dlam, dbr, dbi}) {
+                if (!dp) return LR_ERR_INVALID_ARG;
+                if (!aligned(dp, 4)) return LR_ERR_ALIGN;
+                CK(cudaMemsetAsync(dp, 0, (size_t)D * 4, s));
+            }
+        }
+        if (dh0 && B * D > 0) {  // no step: the gradient passes through
+            if (!aligned(dh0, 4) || !aligned(dh_last, 4)) return LR_ERR_ALIGN;
+            if (dh_last) CK(cudaMemcpyAsync(dh0, dh_last, (size_t)(B * D) * 4, cudaMemcpyDeviceToDevice, s));
+            else CK(cudaMemsetAsync(dh0, 0, (size_t)(B * D) * 4, s));
+        }
+        return LR_OK;
+    }
+    bool vec, vecp;
+    TRY(check_ptrs({x, zr, zi, h, dh, dx, dzr, dzi}, {}, {lam, br, bi, dlam, dbr, dbi}, dtype, D, &vec));
+    TRY(check_ptrs({}, {h0, dh_last, dh0}, {}, LR_F32, D, &vecp));
+    vec = vec && vecp;
+    GUARD;
+    DevWS* ws;
+    TRY(get_ws(&ws));
+    Geom g;
+    Carry cr;
+    TRY(enter(*ws, s));
+    Leave lv(*ws, s);
+    TRY(plan(*ws, OP_GLR_BWD, dtype, vec, T, B * D, D, &g, &cr, s));
+    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(3 * g.n_chunks * g.C + 3 * g.C), false,
+             true));
+    CK(launch_glr_bwd(dtype, vec, GlrIn{x, zr, zi, lam, br, bi, reset}, h0, h, dh, dh_last, dx, dzr,
+                      dzi, dh0, ws->partials, g, cr, s));
+    CK(launch_bias_reduce(ws->partials, g.n_chunks, 3, B, D, BiasOut{{dlam, dbr, dbi, nullptr}}, s));
+    return lv.done();
+}
+
+int glr_step(const void* x, const void* zr, const void* zi, const float* lam, const float* br,
+             const float* bi, const uint8_t* reset, const int32_t* slots, float* state, void* h,
+             int64_t B, int64_t n_slots, int64_t D, int dtype, void* stream) {
+    TRY(check_sizes(B, 1, D, dtype));
+    TRY(check_sizes(n_slots, 1, D, dtype));
+    if (!slots && n_slots < B) return LR_ERR_INVALID_ARG;
+    if (B * D == 0) return LR_OK;
+    bool vec, vecs;
+    TRY(check_ptrs({x, zr, zi, h}, {}, {lam, br, bi}, dtype, D, &vec));
+    TRY(check_ptrs({}, {state}, {}, LR_F32, D, &vecs));
+    if (!state && n_slots > 0) return LR_ERR_INVALID_ARG;
+    if (!aligned(slots, 4)) return LR_ERR_ALIGN;
+    GUARD;
+    DevWS* ws;
+    TRY(get_ws(&ws));
+    // no workspace but the error word: nothing to order against other streams
+    CK(launch_glr_step(dtype, vec && vecs, GlrIn{x, zr, zi, lam, br, bi, reset}, slots, state, h, B,
+                       n_slots, D, ws->words + kWordErr, (cudaStream_t)stream));
+    return LR_OK;
+}
+
 static int grow_host(DevWS& ws, size_t need) {
     if (need <= ws.seq_host_cap) return LR_OK;
     const size_t n = need + need / 4;
@@ -880,6 +971,7 @@ int lr_last_error(void) {
         CK(cudaMemcpy(ws->words, &tw, sizeof tw, cudaMemcpyHostToDevice));
     }
     if (bits & ERRBIT_TIMEOUT) return LR_ERR_TIMEOUT;
+    if (bits & ERRBIT_INDEX) return LR_ERR_INDEX;
     return LR_OK;
 }
 
@@ -893,6 +985,7 @@ const char* lr_status_str(int st) {
         case LR_ERR_NONFINITE: return "non-finite residual";
         case LR_ERR_NOT_CONVERGED: return "not converged within kmax iterations";
         case LR_ERR_TOO_LARGE: return "problem size beyond the supported range";
+        case LR_ERR_INDEX: return "an index in a tensor was out of range on the device";
         default: return "unknown status";
     }
 }
@@ -911,7 +1004,8 @@ static_assert((int)LR_OP_SCAN_FWD == (int)OP_SCAN_FWD && (int)LR_OP_SCAN_BWD == 
                   (int)LR_OP_SRU_FWD == (int)OP_SRU_FWD && (int)LR_OP_SRU_BWD == (int)OP_SRU_BWD &&
                   (int)LR_OP_DEER == (int)OP_DEER && (int)LR_OP_DEER_BWD == (int)OP_DEER_BWD &&
                   (int)LR_OP_LSTM_FWD == (int)OP_LSTM_FWD && (int)LR_OP_LSTM_BWD == (int)OP_LSTM_BWD &&
-                  (int)LR_OP_DEER_ODE == (int)OP_DEER_ODE && (int)OP_DEER_ODE + 1 == (int)OP_COUNT,
+                  (int)LR_OP_DEER_ODE == (int)OP_DEER_ODE && (int)OP_DEER_ODE + 1 == (int)OP_GLR_FWD &&
+                  (int)OP_GLR_FWD + 1 == (int)OP_GLR_BWD && (int)OP_GLR_BWD + 1 == (int)OP_COUNT,
               "lr_op follows the library's operation order");
 static_assert(LR_PROTO_CHAIN == CARRY_CHAIN && LR_PROTO_WALK == CARRY_WALK &&
                   LR_PROTO_LOOK == CARRY_LOOK && LR_PROTO_CLUSTER == CARRY_CLUSTER,
@@ -919,7 +1013,9 @@ static_assert(LR_PROTO_CHAIN == CARRY_CHAIN && LR_PROTO_WALK == CARRY_WALK &&
 
 int lr_plan_info(int op, int dtype, int vec, int64_t T, int64_t C, int* protocol, int* tma,
                  int64_t* tile_rows, int64_t* n_chunks) {
-    if (op < 0 || op >= (int)OP_COUNT || (dtype != LR_F32 && dtype != LR_BF16) || T < 1 || C < 1)
+    if (op == LR_OP_GLR_FWD || op == LR_OP_GLR_BWD) op = (int)OP_GLR_FWD + (op - LR_OP_GLR_FWD);
+    else if (op > LR_OP_DEER_ODE) return LR_ERR_INVALID_ARG;
+    if (op < 0 || (dtype != LR_F32 && dtype != LR_BF16) || T < 1 || C < 1)
         return LR_ERR_INVALID_ARG;
     const bool v = vec != 0;
     // the same plan the entry points make (plan(), onepass_begin)

@@ -58,6 +58,7 @@
 namespace lrs {
 
 constexpr uint32_t ERRBIT_TIMEOUT = 1u;
+constexpr uint32_t ERRBIT_INDEX = 2u;  // an index in a caller's tensor is out of range
 constexpr int CARRY_CHAIN = 0;
 constexpr int CARRY_WALK = 1;
 constexpr int CARRY_LOOK = 2;

@@ -68,6 +68,8 @@ enum Op {
     OP_LSTM_FWD,
     OP_LSTM_BWD,
     OP_DEER_ODE,
+    OP_GLR_FWD,
+    OP_GLR_BWD,
     OP_COUNT
 };
 
@@ -94,10 +96,14 @@ constexpr KCfg kcfg(Op op, int dtype, int mode) {
     // both storage types).  The LSTM cell stages as many arrays per direction
     // as the SRU cell and takes its rows; DEER's ODE form takes the tanh
     // form's rows at eight warps per CTA (its heavier producer measured slower
-    // with four).
+    // with four).  The gated linear recurrence takes the SRU cell's rows, and
+    // the TMA-staged kernels' rows for its walker protocol too, so that long,
+    // narrow problems run the segmented walker kernel.
     return mode == TILE_CLUSTER ? KCfg{8, 16, 0}  // 16 rows of 32 channels per warp, 128 per CTA
            : op == OP_DEER_ODE   ? KCfg{8, mode == CARRY_CHAIN ? 2 : 4, mode == TILE_TMA ? 3 : 0}
            : op == OP_DEER && dtype == 1 ? kcfg(OP_DEER, 0, mode)
+           : op == OP_GLR_FWD || op == OP_GLR_BWD
+               ? KCfg{8, op == OP_GLR_FWD && dtype == 1 ? 4 : 2, mode != TILE_TMA ? 0 : op == OP_GLR_FWD ? 3 : 2}
            : op == OP_LSTM_FWD ? kcfg(OP_SRU_FWD, dtype, mode)
            : op == OP_LSTM_BWD ? kcfg(OP_SRU_BWD, dtype, mode)
            : op == OP_DEER_BWD ? KCfg{8, mode == CARRY_CHAIN ? 2 : 4, mode == TILE_TMA ? 3 : 0}
@@ -371,6 +377,32 @@ cudaError_t launch_deer_ode_iter(int dtype, bool vec, const float* w, const void
                                  uint32_t* resid, const uint32_t* prev_resid, float eps,
                                  unsigned long long* clamps, const NextAgg& nx, const Geom& g,
                                  const Carry& cr, cudaStream_t s);
+
+// Gated linear recurrence: the input and the two gate pre-activations, [T, C]
+// each, the per-feature decay rate and biases, [D] each, the reset flags [T, B]
+// (nullptr: none), and the states in fp32.
+struct GlrIn {
+    const void* x;
+    const void* zr;
+    const void* zi;
+    const float* lam;
+    const float* br;
+    const float* bi;
+    const uint8_t* reset;
+};
+cudaError_t launch_glr_fwd(int dtype, bool vec, const GlrIn& in, const float* h0, void* h,
+                           float* h_last, const Geom& g, const Carry& cr, cudaStream_t s);
+// partials: [3][n_chunks][C] fp32 scratch (rate, decay bias, input bias),
+// followed by 3*C floats for launch_bias_reduce
+cudaError_t launch_glr_bwd(int dtype, bool vec, const GlrIn& in, const float* h0, const void* h,
+                           const void* dh, const float* dh_last, void* dx, void* dzr, void* dzi,
+                           float* dh0, float* partials, const Geom& g, const Carry& cr,
+                           cudaStream_t s);
+// One step of `rows` sequences: h and the states of their slots (slots ==
+// nullptr: slot b is row b; a negative slot is padding).  in.reset: [rows].
+cudaError_t launch_glr_step(int dtype, bool vec, const GlrIn& in, const int32_t* slots, float* state,
+                            void* h, int64_t rows, int64_t n_slots, int64_t D, uint32_t* err,
+                            cudaStream_t s);
 
 // DEER backward: partials is [n_chunks][C] fp32 scratch (dw per tile),
 // followed by C floats that launch_bias_reduce uses for its per-channel sums

@@ -64,7 +64,9 @@
  *  - CUDA graphs: the carry packets are tagged with an epoch that the kernels
  *    take on the device from the workspace's ticket word (every launch takes
  *    a fresh one), so a call of lr_scan_fwd, lr_scan_bwd, sru_fwd, sru_bwd,
- *    lstm_cell_fwd, lstm_cell_bwd, glr_fwd, glr_bwd, glr_step or deer_diag_bwd
+ *    lstm_cell_fwd, lstm_cell_bwd, glr_fwd, glr_bwd, glr_step,
+ *    layer_norm_fwd, layer_norm_bwd, lce_fwd, lce_bwd, adamw_step, adamw8_step
+ *    or deer_diag_bwd
  *    captured into a graph
  *    gives the right result on every replay, with whatever the captured
  *    buffers hold then.  Make one uncaptured call of the same shape first
@@ -365,6 +367,106 @@ int glr_bwd(const void* x, const void* zr, const void* zi, const float* lam, con
 int glr_step(const void* x, const void* zr, const void* zi, const float* lam, const float* br,
              const float* bi, const uint8_t* reset, const int32_t* slots, float* state, void* h,
              int64_t B, int64_t n_slots, int64_t D, int dtype, void* stream);
+
+/*
+ * Layer norm over the last axis of [N, D], with the residual add of a
+ * pre-norm block fused (the pages name no norm; it is what a model puts around
+ * its recurrent layers).  Per row:
+ *   s = x + res (rounded to the storage type),  mean = sum s / D,
+ *   var = sum (s - mean)^2 / D,  rstd = 1 / sqrt(var + eps),
+ *   y = (s - mean) rstd w + b.
+ *   x          : [N,D] in;   res : [N,D] in, NULL means none (s = x)
+ *   w, b       : [D] fp32 in (b NULL means zeros);   eps >= 0
+ *   y          : [N,D] out;  sum : [N,D] out, s (given exactly when res is)
+ *   mean, rstd : [N] fp32 out (kept for layer_norm_bwd)
+ * 1 <= D <= 16384 (LR_ERR_TOO_LARGE beyond); N = 0 is a no-op.
+ */
+int layer_norm_fwd(const void* x, const void* res, const float* w, const float* b, void* y,
+                   void* sum, float* mean, float* rstd, int64_t N, int64_t D, float eps, int dtype,
+                   void* stream);
+
+/*
+ * Layer norm backward for the upstream dy, with x the tensor the norm was
+ * taken of (sum, when a residual was added):
+ *   xh = (x - mean) rstd,  t = dy w,
+ *   dx = rstd (t - mean(t) - xh mean(t xh)) + dres,
+ *   dw = sum over rows of dy xh,  db = sum over rows of dy (fixed order).
+ *   dres   : [N,D] in, the gradient that reaches s along the residual stream
+ *            (NULL = none); dx is then the gradient of both x and res
+ *   dx     : [N,D] out;  dw, db : [D] fp32 out (overwritten)
+ */
+int layer_norm_bwd(const void* x, const float* w, const float* mean, const float* rstd,
+                   const void* dy, const void* dres, void* dx, float* dw, float* db, int64_t N,
+                   int64_t D, int dtype, void* stream);
+
+/*
+ * Softmax cross entropy of the logits x W^T over a large vocabulary, without
+ * keeping the logits (the loss of a language model on the layer's output; the
+ * pages name none):
+ *   l[n][v] = sum_d x[n][d] w[v][d],  lse[n] = log sum_v exp l[n][v],
+ *   loss[n] = lse[n] - l[n][target[n]]   (0 where target[n] = ignore).
+ *   x         : [N,D] in;  w : [V,D] in (one storage type);
+ *   target    : [N] int64 in, 0 .. V-1 or `ignore`; another value counts as
+ *               ignored and is recorded as LR_ERR_INDEX in the device error word
+ *   loss, lse : [N] fp32 out (lse is kept for lce_bwd)
+ * V >= 1, 1 <= D <= 65536; N = 0 is a no-op.  Sums and statistics are fp32.
+ */
+int lce_fwd(const void* x, const void* w, const int64_t* target, int64_t ignore, float* loss,
+            float* lse, int64_t N, int64_t V, int64_t D, int dtype, void* stream);
+
+/*
+ * Its gradient for the upstream dloss[n] = dL/dloss[n]:
+ *   g[n][v] = (exp(l[n][v] - lse[n]) - [v = target[n]]) dloss[n]  (0 on ignored
+ *   rows),   dx = g w,   dw = g^T x.
+ * The logits are computed again, one piece of the vocabulary at a time.
+ *   lse   : [N] fp32 in (lce_fwd's);  dloss : [N] fp32 in
+ *   dx    : [N,D] out;  dw : [V,D] out (overwritten; N = 0: zeros)
+ * Results are bitwise reproducible (no atomics on values).
+ */
+int lce_bwd(const void* x, const void* w, const int64_t* target, int64_t ignore, const float* lse,
+            const float* dloss, void* dx, void* dw, int64_t N, int64_t V, int64_t D, int dtype,
+            void* stream);
+
+/*
+ * One AdamW step over n_tensors tensors (the optimizer a recurrent model is
+ * trained with; the pages leave it to the caller).  Per element:
+ *   g' = grad_scale g,  m = beta1 m + (1-beta1) g',  v = beta2 v + (1-beta2) g'^2,
+ *   p = (1 - lr weight_decay) p - lr m^ / (sqrt(v^) + eps),
+ *   m^ = m / (1 - beta1^step),  v^ = v / (1 - beta2^step).
+ *   n          : host int64[n_tensors], the elements of each tensor (0 allowed)
+ *   p, g, m, v : host arrays of device pointers: weights fp32 (updated),
+ *                gradients of type gdtype, moments fp32 (updated)
+ *   copies     : host array of device pointers to bf16 copies of the weights
+ *                (written), or NULL
+ *   step       : 1 for the first call;  0 <= beta1, beta2 < 1;  eps >= 0
+ *   grad_scale : device fp32 scalar (gradient clipping's factor), NULL = 1
+ * The pointer arrays are read before the call returns; no tensor may overlap
+ * another.  Up to 400 tensors take one launch.
+ */
+int adamw_step(int64_t n_tensors, const int64_t* n, float* const* p, const void* const* g,
+               float* const* m, float* const* v, void* const* copies, int64_t step, double lr,
+               double beta1, double beta2, double eps, double weight_decay, const float* grad_scale,
+               int gdtype, void* stream);
+
+/*
+ * The same with the moments in 8 bits: every 256 consecutive elements of a
+ * tensor share a scale (their largest magnitude), ms[i] and vs[i] holding
+ * ceil(n[i] / 256) of them, and the codes stand for
+ *   m = scale sign(q) (q / 127)^2  (int8),   v = scale (q / 255)^4  (uint8).
+ * Zero codes and scales are zero moments.  The new codes are rounded up or down
+ * at random, right in the mean, by a hash of (element, tensor index, seed): give
+ * another seed at every step.  A positive v keeps a positive code.
+ */
+int adamw8_step(int64_t n_tensors, const int64_t* n, float* const* p, const void* const* g,
+                int8_t* const* m, uint8_t* const* v, float* const* ms, float* const* vs,
+                void* const* copies, int64_t step, double lr, double beta1, double beta2, double eps,
+                double weight_decay, const float* grad_scale, uint32_t seed, int gdtype, void* stream);
+
+/* The fp32 values that 8-bit moments stand for (m, v: host arrays of device
+ * pointers, written), e.g. for a checkpoint in a portable form. */
+int adamw8_values(int64_t n_tensors, const int64_t* n, const int8_t* const* mq,
+                  const uint8_t* const* vq, const float* const* ms, const float* const* vs,
+                  float* const* m, float* const* v, void* stream);
 
 /*
  * Forward scan that allocates nothing (no counterpart in the pages: this is a

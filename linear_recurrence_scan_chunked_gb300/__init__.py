@@ -67,6 +67,14 @@ def load():
     lib.glr_fwd.argtypes = [P] * 10 + [I64, I64, I64, I, P]
     lib.glr_bwd.argtypes = [P] * 18 + [I64, I64, I64, I, P]
     lib.glr_step.argtypes = [P] * 10 + [I64, I64, I64, I, P]
+    lib.layer_norm_fwd.argtypes = [P] * 8 + [I64, I64, ctypes.c_float, I, P]
+    lib.layer_norm_bwd.argtypes = [P] * 9 + [I64, I64, I, P]
+    lib.lce_fwd.argtypes = [P, P, P, I64, P, P, I64, I64, I64, I, P]
+    lib.lce_bwd.argtypes = [P, P, P, I64, P, P, P, P, I64, I64, I64, I, P]
+    F64 = ctypes.c_double
+    lib.adamw_step.argtypes = [I64] + [P] * 6 + [I64] + [F64] * 5 + [P, I, P]
+    lib.adamw8_step.argtypes = [I64] + [P] * 8 + [I64] + [F64] * 5 + [P, ctypes.c_uint32, I, P]
+    lib.adamw8_values.argtypes = [I64] + [P] * 8
     lib.lr_last_error.argtypes = []
     lib.lr_status_str.argtypes = [I]
     lib.lr_status_str.restype = ctypes.c_char_p
@@ -462,6 +470,198 @@ def glr_step(x, zr, zi, lam, br, bi, state, slots=None, reset=None, h=None, stre
     _check(load().glr_step(_p(x), _p(zr), _p(zi), _p(lam), _p(br), _p(bi), _p(reset), _p(slots),
                            _p(state), _p(h), B, state.shape[0], D, _code(x), _stream(stream, x)))
     return h
+
+
+def _rows(name, t, like=None):
+    if t.dim() < 1 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [..., D] CUDA tensor")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must match shape/dtype/device of x")
+    return t
+
+
+def _row_stat(name, t, x):
+    if t.dtype != torch.float32 or t.shape != x.shape[:-1] or t.device != x.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 {list(x.shape[:-1])} CUDA tensor on the device of x")
+    return t
+
+
+def layer_norm_fwd(x, w, b=None, res=None, eps=1e-5, y=None, s=None, stream=None):
+    """Layer norm over the last axis (x [..., D]; w, b [D] fp32), of x or, with
+    res, of s = x + res. Returns (y, mean, rstd), with res (y, mean, rstd, s);
+    mean and rstd are fp32 [...]."""
+    _rows("x", x)
+    D = x.shape[-1]
+    _param("w", w, D, x)
+    if b is not None:
+        _param("b", b, D, x)
+    if res is not None:
+        _rows("res", res, x)
+        s = torch.empty_like(x) if s is None else _rows("s", s, x)
+    elif s is not None:
+        raise ValueError("s is an output of the residual add: give res with it")
+    y = torch.empty_like(x) if y is None else _rows("y", y, x)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    _check(load().layer_norm_fwd(_p(x), _p(res), _p(w), _p(b), _p(y), _p(s), _p(mean), _p(rstd),
+                                 mean.numel(), D, eps, _code(x), _stream(stream, x)))
+    return (y, mean, rstd) if res is None else (y, mean, rstd, s)
+
+
+def layer_norm_bwd(x, w, mean, rstd, dy, dres=None, out=None, stream=None):
+    """Layer norm backward (x: what the norm was taken of; dres: the gradient
+    that reaches it along the residual stream). Returns dict dx, dw, db."""
+    _rows("x", x)
+    _rows("dy", dy, x)
+    D = x.shape[-1]
+    _param("w", w, D, x)
+    _row_stat("mean", mean, x)
+    _row_stat("rstd", rstd, x)
+    if dres is not None:
+        _rows("dres", dres, x)
+    o = dict(out or {})
+    o["dx"] = torch.empty_like(x) if o.get("dx") is None else _rows("dx", o["dx"], x)
+    for k in ("dw", "db"):
+        o[k] = torch.empty(D, dtype=torch.float32, device=x.device) if o.get(k) is None else _param(k, o[k], D, x)
+    _check(load().layer_norm_bwd(_p(x), _p(w), _p(mean), _p(rstd), _p(dy), _p(dres), _p(o["dx"]),
+                                 _p(o["dw"]), _p(o["db"]), mean.numel(), D, _code(x),
+                                 _stream(stream, x)))
+    return o
+
+
+def _lce_args(x, w, target):
+    _rows("x", x)
+    if w.dim() != 2 or w.shape[1] != x.shape[-1] or w.dtype != x.dtype or w.device != x.device or not w.is_contiguous():
+        raise ValueError("w must be a contiguous [V, D] CUDA tensor of the dtype and device of x")
+    if target.dtype != torch.int64 or target.shape != x.shape[:-1] or target.device != x.device \
+            or not target.is_contiguous():
+        raise ValueError(f"target must be a contiguous int64 {list(x.shape[:-1])} CUDA tensor on the device of x")
+    return target.numel(), w.shape[0], w.shape[1]
+
+
+def lce_fwd(x, w, target, ignore=-100, loss=None, lse=None, stream=None):
+    """Softmax cross entropy of the logits x w^T (x [..., D], w [V, D]) against
+    target [...] int64, without keeping the logits. Returns (loss, lse), fp32
+    [...]; loss is 0 where target == ignore. A target outside 0 .. V-1 counts
+    as ignored and sets LR_ERR_INDEX (last_error)."""
+    N, V, D = _lce_args(x, w, target)
+    loss = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if loss is None else _row_stat("loss", loss, x)
+    lse = torch.empty_like(loss) if lse is None else _row_stat("lse", lse, x)
+    _check(load().lce_fwd(_p(x), _p(w), _p(target), ignore, _p(loss), _p(lse), N, V, D, _code(x),
+                          _stream(stream, x)))
+    return loss, lse
+
+
+def lce_bwd(x, w, target, lse, dloss, ignore=-100, dx=None, dw=None, stream=None):
+    """Gradient of lce_fwd for the upstream dloss [...] fp32 (lse: lce_fwd's).
+    Returns (dx, dw)."""
+    N, V, D = _lce_args(x, w, target)
+    _row_stat("lse", lse, x)
+    _row_stat("dloss", dloss, x)
+    dx = torch.empty_like(x) if dx is None else _rows("dx", dx, x)
+    dw = torch.empty_like(w) if dw is None else _rows("dw", dw, w)
+    _check(load().lce_bwd(_p(x), _p(w), _p(target), ignore, _p(lse), _p(dloss), _p(dx), _p(dw), N, V, D,
+                          _code(x), _stream(stream, x)))
+    return dx, dw
+
+
+def _tensor_list(name, ts, dtype, numels, ref):
+    """The addresses of a list of contiguous CUDA tensors of one dtype on the
+    device of `ref`, with the given numbers of elements, as a ctypes array."""
+    if len(ts) != len(numels):
+        raise ValueError(f"{name} has {len(ts)} tensors, params {len(numels)}")
+    dev = ref.get_device()
+    for t, n in zip(ts, numels):
+        if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda or t.get_device() != dev:
+            raise ValueError(f"{name} must hold contiguous {dtype} CUDA tensors on {ref.device}, as many elements "
+                             f"each as it takes ({n}), got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+
+
+def _adamw_args(params, grads, copies, grad_scale):
+    ref = params[0]
+    if not ref.is_cuda:
+        raise ValueError("params must be CUDA tensors")
+    numels = [t.numel() for t in params]
+    gd = grads[0].dtype if len(grads) else torch.float32
+    if gd not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"gradients must be float32 or bfloat16, got {gd}")
+    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
+                                   or grad_scale.device != ref.device):
+        raise ValueError("grad_scale must be one fp32 value on the device of the params")
+    return (ref, numels, (ctypes.c_int64 * len(numels))(*numels),
+            _tensor_list("params", params, torch.float32, numels, ref),
+            _tensor_list("grads", grads, gd, numels, ref),
+            None if copies is None else _tensor_list("copies", copies, torch.bfloat16, numels, ref),
+            LR_F32 if gd == torch.float32 else LR_BF16)
+
+
+def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
+               grad_scale=None, copies=None, stream=None):
+    """One AdamW step over lists of tensors, in place: params fp32, grads fp32 or
+    bf16, moments m and v fp32; copies: bf16 copies of the new weights; step
+    counts from 1; grad_scale: one fp32 value on the device."""
+    if len(params) == 0:
+        return
+    ref, numels, n, p, g, c, gd = _adamw_args(params, grads, copies, grad_scale)
+    _check(load().adamw_step(len(numels), n, p, g, _tensor_list("m", m, torch.float32, numels, ref),
+                             _tensor_list("v", v, torch.float32, numels, ref), c, step, lr, beta1, beta2,
+                             eps, weight_decay, _p(grad_scale), gd, _stream(stream, ref)))
+
+
+ADAMW8_BLOCK = 256
+
+
+def _scale_numels(numels):
+    return [(k + ADAMW8_BLOCK - 1) // ADAMW8_BLOCK for k in numels]
+
+
+def adamw8_state(params):
+    """Zero 8-bit moments for adamw8_step: lists m (int8), v (uint8), and their
+    scales ms, vs (fp32, one per 256 elements)."""
+    e = lambda t, n, dt: torch.zeros(n, dtype=dt, device=t.device)
+    nb = _scale_numels([t.numel() for t in params])
+    return ([e(t, t.numel(), torch.int8) for t in params], [e(t, t.numel(), torch.uint8) for t in params],
+            [e(t, k, torch.float32) for t, k in zip(params, nb)],
+            [e(t, k, torch.float32) for t, k in zip(params, nb)])
+
+
+def adamw8_step(params, grads, m, v, ms, vs, step, lr, seed, beta1=0.9, beta2=0.999, eps=1e-8,
+                weight_decay=0.01, grad_scale=None, copies=None, stream=None):
+    """adamw_step with the moments in 8 bits (adamw8_state). seed: another one
+    at every step (the rounding's random bits)."""
+    if len(params) == 0:
+        return
+    ref, numels, n, p, g, c, gd = _adamw_args(params, grads, copies, grad_scale)
+    nb = _scale_numels(numels)
+    _check(load().adamw8_step(len(numels), n, p, g, _tensor_list("m", m, torch.int8, numels, ref),
+                              _tensor_list("v", v, torch.uint8, numels, ref),
+                              _tensor_list("ms", ms, torch.float32, nb, ref),
+                              _tensor_list("vs", vs, torch.float32, nb, ref), c, step, lr, beta1, beta2,
+                              eps, weight_decay, _p(grad_scale), int(seed) & 0xFFFFFFFF, gd,
+                              _stream(stream, ref)))
+
+
+def adamw8_values(mq, vq, ms, vs, m=None, v=None, stream=None):
+    """The fp32 values that 8-bit moments stand for. Returns (m, v), lists of
+    1-d tensors unless given."""
+    if len(mq) == 0:
+        return [], []
+    ref = mq[0]
+    if not ref.is_cuda:
+        raise ValueError("the codes must be CUDA tensors")
+    numels = [t.numel() for t in mq]
+    nb = _scale_numels(numels)
+    m = [torch.empty(k, dtype=torch.float32, device=ref.device) for k in numels] if m is None else m
+    v = [torch.empty(k, dtype=torch.float32, device=ref.device) for k in numels] if v is None else v
+    _check(load().adamw8_values(len(numels), (ctypes.c_int64 * len(numels))(*numels),
+                                _tensor_list("mq", mq, torch.int8, numels, ref),
+                                _tensor_list("vq", vq, torch.uint8, numels, ref),
+                                _tensor_list("ms", ms, torch.float32, nb, ref),
+                                _tensor_list("vs", vs, torch.float32, nb, ref),
+                                _tensor_list("m", m, torch.float32, numels, ref),
+                                _tensor_list("v", v, torch.float32, numels, ref), _stream(stream, ref)))
+    return m, v
 
 
 def last_error() -> int:

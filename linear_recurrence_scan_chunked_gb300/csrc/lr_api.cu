@@ -1,10 +1,12 @@
 // lr_api.cu -- the C ABI declared in include/lrscan.h: argument checks, the
 // per-device workspace, launch geometry, and the DEER host loop.
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <stdio.h>
 #include <string.h>
 
+#include <exception>
 #include <mutex>
 #include <vector>
 
@@ -119,6 +121,7 @@ struct DevWS {
     uint32_t* words = nullptr;   // ticket word, error bits, DEER residual slots (kWord*)
     float* partials = nullptr;   size_t partials_cap = 0; // floats
     void* ybuf = nullptr;        size_t ybuf_cap = 0;     // bytes
+    char* lce = nullptr;         size_t lce_cap = 0;      // cross entropy scratch, bytes
     uint32_t* host_word = nullptr;                        // pinned [kMaxIters], residual reads
     void* test_buf = nullptr;                             // timeout-test problem
     uint32_t* seq = nullptr;     size_t seq_cap = 0;      // DEER per-sequence state (words)
@@ -565,6 +568,215 @@ int glr_step(const void* x, const void* zr, const void* zi, const float* lam, co
     // no workspace but the error word: nothing to order against other streams
     CK(launch_glr_step(dtype, vec && vecs, GlrIn{x, zr, zi, lam, br, bi, reset}, slots, state, h, B,
                        n_slots, D, ws->words + kWordErr, (cudaStream_t)stream));
+    return LR_OK;
+}
+
+// Pointers of a layer norm call: *vec when all allow 16-byte accesses.
+static int ln_ptrs(std::initializer_list<const void*> req, std::initializer_list<const void*> opt,
+                   std::initializer_list<const void*> f32, std::initializer_list<const void*> f32_opt,
+                   int dtype, int64_t D, bool* vec) {
+    bool a, b;
+    int st = check_ptrs(req, opt, f32, dtype, D, &a);
+    if (st) return st;
+    st = check_ptrs({}, f32_opt, {}, LR_F32, D, &b);
+    if (st) return st;
+    *vec = a && b && D % (16 / (int64_t)esize(dtype)) == 0;
+    return LR_OK;
+}
+
+int layer_norm_fwd(const void* x, const void* res, const float* w, const float* b, void* y, void* sum,
+                   float* mean, float* rstd, int64_t N, int64_t D, float eps, int dtype, void* stream) {
+    TRY(check_sizes(N, 1, D, dtype));
+    if (!(eps >= 0.f)) return LR_ERR_INVALID_ARG;
+    if (N * D == 0) return N > 0 ? LR_ERR_INVALID_ARG : LR_OK;  // rows of no element have no mean
+    if (D > kLnMaxD) return LR_ERR_TOO_LARGE;
+    if ((res == nullptr) != (sum == nullptr)) return LR_ERR_INVALID_ARG;
+    bool vec;
+    TRY(ln_ptrs({x, y}, {res, sum}, {w}, {b}, dtype, D, &vec));
+    if (!mean || !rstd) return LR_ERR_INVALID_ARG;
+    if (!aligned(mean, 4) || !aligned(rstd, 4)) return LR_ERR_ALIGN;
+    CK(launch_ln_fwd(dtype, vec, x, res, w, b, y, sum, mean, rstd, N, D, eps, (cudaStream_t)stream));
+    return LR_OK;
+}
+
+int layer_norm_bwd(const void* x, const float* w, const float* mean, const float* rstd, const void* dy,
+                   const void* dres, void* dx, float* dw, float* db, int64_t N, int64_t D, int dtype,
+                   void* stream) {
+    TRY(check_sizes(N, 1, D, dtype));
+    cudaStream_t s = (cudaStream_t)stream;
+    if (N * D == 0) {
+        if (N > 0) return LR_ERR_INVALID_ARG;
+        if (D > 0) {  // no row: sums of nothing
+            for (float* p : {dw, db}) {
+                if (!p) return LR_ERR_INVALID_ARG;
+                if (!aligned(p, 4)) return LR_ERR_ALIGN;
+                CK(cudaMemsetAsync(p, 0, (size_t)D * 4, s));
+            }
+        }
+        return LR_OK;
+    }
+    if (D > kLnMaxD) return LR_ERR_TOO_LARGE;
+    bool vec;
+    TRY(ln_ptrs({x, dy, dx}, {dres}, {w}, {}, dtype, D, &vec));
+    for (const float* p : {mean, rstd, (const float*)dw, (const float*)db}) {
+        if (!p) return LR_ERR_INVALID_ARG;
+        if (!aligned(p, 4)) return LR_ERR_ALIGN;
+    }
+    GUARD;
+    DevWS* ws;
+    TRY(get_ws(&ws));
+    TRY(enter(*ws, s));
+    Leave lv(*ws, s);
+    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)2 * kLnMaxPartials * D, false, true));
+    CK(launch_ln_bwd(dtype, vec, x, w, mean, rstd, dy, dres, dx, dw, db, ws->partials, N, D, s));
+    return lv.done();
+}
+
+static int lce_check(const void* x, const void* w, const int64_t* target, int64_t N, int64_t V, int64_t D, int dtype) {
+    TRY(check_sizes(N, V, D, dtype));
+    if (N == 0) return LR_OK;
+    if (V < 1 || D < 1) return LR_ERR_INVALID_ARG;
+    if (N >= (int64_t)1 << 31 || V >= (int64_t)1 << 31 || D > 65536) return LR_ERR_TOO_LARGE;
+    if (!x || !w || !target) return LR_ERR_INVALID_ARG;
+    if (!aligned(x, esize(dtype)) || !aligned(w, esize(dtype)) || !aligned(target, 8)) return LR_ERR_ALIGN;
+    return LR_OK;
+}
+
+int lce_fwd(const void* x, const void* w, const int64_t* target, int64_t ignore, float* loss, float* lse, int64_t N,
+            int64_t V, int64_t D, int dtype, void* stream) {
+    TRY(lce_check(x, w, target, N, V, D, dtype));
+    if (N == 0) return LR_OK;
+    if (!loss || !lse) return LR_ERR_INVALID_ARG;
+    if (!aligned(loss, 4) || !aligned(lse, 4)) return LR_ERR_ALIGN;
+    GUARD;
+    cudaStream_t s = (cudaStream_t)stream;
+    DevWS* ws;
+    TRY(get_ws(&ws));
+    TRY(enter(*ws, s));
+    Leave lv(*ws, s);
+    const LcePlan pl = lce_plan(dtype, N, V, D);
+    TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.fwd_bytes, false, true));
+    CK(launch_lce_fwd(dtype, x, w, target, ignore, loss, lse, N, V, D, pl, ws->lce, ws->words + kWordErr, s));
+    return lv.done();
+}
+
+int lce_bwd(const void* x, const void* w, const int64_t* target, int64_t ignore, const float* lse, const float* dloss,
+            void* dx, void* dw, int64_t N, int64_t V, int64_t D, int dtype, void* stream) {
+    TRY(lce_check(x, w, target, N, V, D, dtype));
+    cudaStream_t s = (cudaStream_t)stream;
+    if (N == 0) {  // no row: the weights' gradient is a sum of nothing
+        if (V * D > 0) {
+            if (!dw) return LR_ERR_INVALID_ARG;
+            if (!aligned(dw, esize(dtype))) return LR_ERR_ALIGN;
+            CK(cudaMemsetAsync(dw, 0, (size_t)(V * D) * esize(dtype), s));
+        }
+        return LR_OK;
+    }
+    if (!lse || !dloss || !dx || !dw) return LR_ERR_INVALID_ARG;
+    if (!aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dx, esize(dtype)) || !aligned(dw, esize(dtype)))
+        return LR_ERR_ALIGN;
+    GUARD;
+    DevWS* ws;
+    TRY(get_ws(&ws));
+    TRY(enter(*ws, s));
+    Leave lv(*ws, s);
+    const LcePlan pl = lce_plan(dtype, N, V, D);
+    TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.bwd_bytes, false, true));
+    CK(launch_lce_bwd(dtype, x, w, target, ignore, lse, dloss, dx, dw, N, V, D, pl, ws->lce, ws->words + kWordErr, s));
+    return lv.done();
+}
+
+static int adamw_hyper(int64_t step, double lr, double beta1, double beta2, double eps,
+                       double weight_decay, AdamHyper* h) {
+    if (step < 1 || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0))
+        return LR_ERR_INVALID_ARG;
+    h->b1 = (float)beta1;
+    h->c1 = (float)(1.0 - beta1);
+    h->b2 = (float)beta2;
+    h->c2 = (float)(1.0 - beta2);
+    h->b1_lo = (float)(beta1 - (double)h->b1);
+    h->c1_lo = (float)((1.0 - beta1) - (double)h->c1);
+    h->b2_lo = (float)(beta2 - (double)h->b2);
+    h->eps = (float)eps;
+    h->decay = (float)(1.0 - lr * weight_decay);
+    const double a = lr / (1.0 - pow(beta1, (double)step));
+    h->step = (float)a;
+    h->step_lo = (float)(a - (double)h->step);
+    h->rk2 = (float)(1.0 / sqrt(1.0 - pow(beta2, (double)step)));
+    return LR_OK;
+}
+
+// Collects the tensors of a call and checks their pointers.
+static int adamw_tensors(std::vector<AdamTensor>& out, int64_t n_tensors, const int64_t* n, float* const* p,
+                         const void* const* g, void* const* m, void* const* v, float* const* ms,
+                         float* const* vs, void* const* copies, int gdtype, bool eight) {
+    if (gdtype != LR_F32 && gdtype != LR_BF16) return LR_ERR_INVALID_ARG;
+    if (n_tensors < 0) return LR_ERR_INVALID_ARG;
+    if (n_tensors == 0) return LR_OK;
+    if (n_tensors > INT32_MAX) return LR_ERR_TOO_LARGE;
+    if (!n || !p || !g || !m || !v || (eight && (!ms || !vs))) return LR_ERR_INVALID_ARG;
+    try {
+        out.resize((size_t)n_tensors);
+    } catch (const std::exception&) {
+        return LR_ERR_TOO_LARGE;
+    }
+    const size_t ges = esize(gdtype);
+    for (int64_t i = 0; i < n_tensors; ++i) {
+        AdamTensor& t = out[(size_t)i];
+        if (n[i] < 0) return LR_ERR_INVALID_ARG;
+        if (n[i] >= (int64_t)1 << 42) return LR_ERR_TOO_LARGE;
+        t = AdamTensor{p[i], g[i], m[i], v[i], eight ? ms[i] : nullptr, eight ? vs[i] : nullptr,
+                       copies ? copies[i] : nullptr, n[i], 0};
+        if (n[i] == 0) continue;
+        if (!t.p || !t.g || !t.m || !t.v || (eight && (!t.ms || !t.vs)) || (copies && !t.copy))
+            return LR_ERR_INVALID_ARG;
+        if (!aligned(t.p, 4) || !aligned(t.g, ges) || !aligned(t.copy, 2) || !aligned(t.ms, 4) || !aligned(t.vs, 4))
+            return LR_ERR_ALIGN;
+        if (!eight && (!aligned(t.m, 4) || !aligned(t.v, 4))) return LR_ERR_ALIGN;
+        const size_t sa = eight ? 8 : 16;
+        t.vec = aligned(t.p, 16) && aligned(t.g, eight ? 16 : 4 * ges) && aligned(t.m, sa) && aligned(t.v, sa) &&
+                aligned(t.copy, eight ? 16 : 8);
+    }
+    return LR_OK;
+}
+
+int adamw_step(int64_t n_tensors, const int64_t* n, float* const* p, const void* const* g,
+               float* const* m, float* const* v, void* const* copies, int64_t step, double lr,
+               double beta1, double beta2, double eps, double weight_decay, const float* grad_scale,
+               int gdtype, void* stream) {
+    AdamHyper h;
+    TRY(adamw_hyper(step, lr, beta1, beta2, eps, weight_decay, &h));
+    if (!aligned(grad_scale, 4)) return LR_ERR_ALIGN;
+    std::vector<AdamTensor> t;
+    TRY(adamw_tensors(t, n_tensors, n, p, g, (void* const*)m, (void* const*)v, nullptr, nullptr, copies,
+                      gdtype, false));
+    CK(launch_adamw(ADAM_32BIT, gdtype, t.data(), n_tensors, h, grad_scale, 0, (cudaStream_t)stream));
+    return LR_OK;
+}
+
+int adamw8_step(int64_t n_tensors, const int64_t* n, float* const* p, const void* const* g,
+                int8_t* const* m, uint8_t* const* v, float* const* ms, float* const* vs,
+                void* const* copies, int64_t step, double lr, double beta1, double beta2, double eps,
+                double weight_decay, const float* grad_scale, uint32_t seed, int gdtype, void* stream) {
+    AdamHyper h;
+    TRY(adamw_hyper(step, lr, beta1, beta2, eps, weight_decay, &h));
+    if (!aligned(grad_scale, 4)) return LR_ERR_ALIGN;
+    std::vector<AdamTensor> t;
+    TRY(adamw_tensors(t, n_tensors, n, p, g, (void* const*)m, (void* const*)v, ms, vs, copies, gdtype, true));
+    CK(launch_adamw(ADAM_8BIT, gdtype, t.data(), n_tensors, h, grad_scale, seed, (cudaStream_t)stream));
+    return LR_OK;
+}
+
+int adamw8_values(int64_t n_tensors, const int64_t* n, const int8_t* const* mq, const uint8_t* const* vq,
+                  const float* const* ms, const float* const* vs, float* const* m, float* const* v,
+                  void* stream) {
+    std::vector<AdamTensor> t;
+    // p: where m goes (also in g's place, which is not read), copy: where v goes
+    TRY(adamw_tensors(t, n_tensors, n, m, (const void* const*)m, (void* const*)mq, (void* const*)vq,
+                      (float* const*)ms, (float* const*)vs, (void* const*)v, LR_F32, true));
+    for (AdamTensor& x : t)
+        if (x.n > 0 && !aligned(x.copy, 4)) return LR_ERR_ALIGN;
+    CK(launch_adamw(ADAM_VALUES, LR_F32, t.data(), n_tensors, AdamHyper{}, nullptr, 0, (cudaStream_t)stream));
     return LR_OK;
 }
 

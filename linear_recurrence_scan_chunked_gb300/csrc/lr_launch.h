@@ -404,6 +404,62 @@ cudaError_t launch_glr_step(int dtype, bool vec, const GlrIn& in, const int32_t*
                             void* h, int64_t rows, int64_t n_slots, int64_t D, uint32_t* err,
                             cudaStream_t s);
 
+// Layer norm over the last axis of [N, D] (sum: x + res, with res only).
+// D <= kLnMaxD.  vec: every pointer 16-byte aligned and D a multiple of the
+// 16-byte vector (4 fp32, 8 bf16).
+constexpr int64_t kLnMaxD = 16384;
+constexpr int kLnMaxPartials = 2048;  // CTAs of the backward kernel, one row of partials each
+cudaError_t launch_ln_fwd(int dtype, bool vec, const void* x, const void* res, const float* w,
+                          const float* b, void* y, void* sum, float* mean, float* rstd, int64_t N,
+                          int64_t D, float eps, cudaStream_t s);
+// partials: [2][kLnMaxPartials][D] fp32 scratch (the CTAs launched use its head)
+cudaError_t launch_ln_bwd(int dtype, bool vec, const void* x, const float* w, const float* mean,
+                          const float* rstd, const void* dy, const void* dres, void* dx, float* dw,
+                          float* db, float* partials, int64_t N, int64_t D, cudaStream_t s);
+
+// AdamW over many tensors.  vec: every pointer of the tensor allows the vector
+// path (16-byte fp32 / 8-byte bf16 and code accesses).
+struct AdamTensor {
+    float* p;
+    const void* g;
+    void* m;     // fp32, or int8 codes
+    void* v;     // fp32, or uint8 codes
+    float* ms;   // 8 bits: one scale per 256 elements
+    float* vs;
+    void* copy;  // bf16 copy of p, or nullptr
+    int64_t n : 63;
+    uint64_t vec : 1;
+};
+struct AdamHyper {
+    float b1, c1;  // beta1, 1 - beta1
+    float b2, c2;
+    float b1_lo, c1_lo, b2_lo;  // what their rounding to fp32 left
+    float eps;
+    float decay;   // 1 - lr * weight_decay
+    float step, step_lo;  // lr / (1 - beta1^t)
+    float rk2;     // 1 / sqrt(1 - beta2^t)
+};
+constexpr int kAdamTensors = 400;  // per launch: their pointers are kernel arguments (< 32 KB)
+enum AdamKind { ADAM_32BIT, ADAM_8BIT, ADAM_VALUES };
+cudaError_t launch_adamw(AdamKind kind, int gdtype, const AdamTensor* t, int64_t n_tensors,
+                         const AdamHyper& h, const float* gscale, uint32_t seed, cudaStream_t s);
+
+// Softmax cross entropy of x W^T ([N, D] by [V, D]), in pieces.
+struct LcePlan {
+    int64_t tiles;     // forward: vocabulary tiles (a pair of statistics each, per row)
+    int64_t rows;      // forward: rows per round
+    int64_t piece;     // backward: vocabulary rows per piece
+    size_t fwd_bytes;  // scratch of either direction
+    size_t bwd_bytes;
+};
+LcePlan lce_plan(int dtype, int64_t N, int64_t V, int64_t D);
+cudaError_t launch_lce_fwd(int dtype, const void* x, const void* w, const int64_t* target, int64_t ignore, float* loss,
+                           float* lse, int64_t N, int64_t V, int64_t D, const LcePlan& pl, void* scratch, uint32_t* err,
+                           cudaStream_t s);
+cudaError_t launch_lce_bwd(int dtype, const void* x, const void* w, const int64_t* target, int64_t ignore,
+                           const float* lse, const float* dloss, void* dx, void* dw, int64_t N, int64_t V, int64_t D,
+                           const LcePlan& pl, void* scratch, uint32_t* err, cudaStream_t s);
+
 // DEER backward: partials is [n_chunks][C] fp32 scratch (dw per tile),
 // followed by C floats that launch_bias_reduce uses for its per-channel sums
 cudaError_t launch_deer_bwd(int dtype, bool vec, const float* w, const void* y, const void* h0,

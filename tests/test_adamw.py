@@ -1,0 +1,255 @@
+"""AdamW over many tensors, moments in fp32 and in 8 bits, against fp64 and (the
+codes) against the same separately rounded fp32 operations in numpy.
+
+Tolerances: fp32 moments a few roundings of 2^-24; a weight 2^-23 |p| for its own
+rounding and 1e-6 of the distance that the step moves it (the roundings of m, v,
+the root, the quotient and the products, 2^-24 each), taken as at least 10 lr.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import linear_recurrence_scan_chunked_gb300 as lrs
+
+H = dict(lr=1e-2, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1)
+SIZES = [1, 7, 255, 256, 257, 4096, 4097, 0, 10000, 33, 70001]
+
+
+def make(sizes, gdtype, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    rn = lambda n, s=1.0: s * torch.randn(n, generator=g)
+    return dict(p=[rn(n, 0.02) for n in sizes], g=[rn(n, 1e-2).to(gdtype) for n in sizes],
+                m=[rn(n, 1e-2) for n in sizes], v=[rn(n, 1e-2).square() for n in sizes])
+
+
+def ref_step(p, g, m, v, step, scale=1.0):
+    g = g.double() * scale
+    m = H["beta1"] * m.double() + (1 - H["beta1"]) * g
+    v = H["beta2"] * v.double() + (1 - H["beta2"]) * g * g
+    mh, vh = m / (1 - H["beta1"] ** step), v / (1 - H["beta2"] ** step)
+    return p.double() * (1 - H["lr"] * H["weight_decay"]) - H["lr"] * mh / (vh.sqrt() + H["eps"]), m, v
+
+
+def check_p(got, ref, before):
+    e = (got.double().cpu() - ref).abs()
+    moved = (ref - before.double()).abs().clamp(min=10 * H["lr"])
+    assert bool((e <= 2.0 ** -23 * ref.abs() + 1e-6 * moved).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gdtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scaled", [False, True])
+def test_step_32(cuda, gdtype, scaled):
+    c = make(SIZES, gdtype)
+    d = {k: [t.cuda() for t in v] for k, v in c.items()}
+    copies = [torch.zeros(n, dtype=torch.bfloat16, device="cuda") for n in SIZES]
+    s = torch.tensor([0.625], device="cuda") if scaled else None
+    cuda.adamw_step(d["p"], d["g"], d["m"], d["v"], step=3, grad_scale=s, copies=copies, **H)
+    for i in range(len(SIZES)):
+        rp, rm, rv = ref_step(c["p"][i], c["g"][i], c["m"][i], c["v"][i], 3, 0.625 if scaled else 1.0)
+        check_p(d["p"][i], rp, c["p"][i])
+        assert torch.allclose(d["m"][i].double().cpu(), rm, rtol=0, atol=2.0 ** -22 * 0.1)
+        assert torch.allclose(d["v"][i].double().cpu(), rv, rtol=2.0 ** -21, atol=0)
+        assert torch.equal(copies[i], d["p"][i].bfloat16())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("eight", [False, True])
+def test_unaligned_tensors_and_more_than_one_launch(cuda, eight):
+    """950 tensors, views at odd offsets of one buffer: three launches, the
+    scalar path, the hash of the tensor's index in the call."""
+    sizes = [1 + (i * 37) % 600 for i in range(950)]
+    offs = np.concatenate([[0], np.cumsum(np.array(sizes) + 1)])
+    c = make(sizes, torch.float32, seed=2)
+
+    def view(ts, dt=torch.float32):
+        buf = torch.zeros(int(offs[-1]) + 1, dtype=dt, device="cuda")
+        vs = [buf[int(o) + 1:int(o) + 1 + n] for o, n in zip(offs, sizes)]
+        for a, b in zip(vs, ts):
+            a.copy_(b)
+        return buf, vs
+
+    pb, p = view(c["p"])
+    _, g = view(c["g"])
+    if eight:
+        _, m = view([torch.zeros(n) for n in sizes], torch.int8)
+        _, v = view([torch.zeros(n) for n in sizes], torch.uint8)
+        _, _, ms, vs = cuda.adamw8_state(p)
+        cuda.adamw8_step(p, g, m, v, ms, vs, step=1, seed=9, **H)
+        for i in (0, 399, 400, 800, 949):
+            rm, rv, _, _ = np_moments(c["g"][i].numpy(), np.zeros(sizes[i], np.float32), np.zeros(sizes[i], np.float32))
+            qm, sm = np_encode_m(rm, np_noise(sizes[i], 9, i)[0])
+            qv, sv = np_encode_v(rv, np_noise(sizes[i], 9, i)[1])
+            assert np.array_equal(m[i].cpu().numpy(), qm) and np.array_equal(ms[i].cpu().numpy(), sm)
+            assert np.array_equal(v[i].cpu().numpy(), qv) and np.array_equal(vs[i].cpu().numpy(), sv)
+    else:
+        _, m = view(c["m"])
+        _, v = view(c["v"])
+        cuda.adamw_step(p, g, m, v, step=1, **H)
+    for i in range(0, 950, 13):
+        z = torch.zeros(sizes[i])
+        check_p(p[i], ref_step(c["p"][i], c["g"][i], z if eight else c["m"][i], z if eight else c["v"][i], 1)[0],
+                c["p"][i])
+    gaps = torch.ones(pb.numel(), dtype=torch.bool)
+    for o, n in zip(offs, sizes):
+        gaps[int(o) + 1:int(o) + 1 + n] = False
+    assert not pb.cpu()[gaps].any()  # nothing written between the tensors
+
+
+# ---- the 8-bit codes in numpy: every operation rounded to fp32 by itself
+
+F = np.float32
+
+
+def np_noise(n, seed, tensor):
+    M = (1 << 32) - 1
+    out = []
+    for i in range(n):
+        h = (i + tensor * 0x9E3779B1 + seed * 0xBB67AE85) & M
+        h = ((h ^ (h >> 16)) * 0x6A09E667) & M
+        h = ((h ^ (h >> 15)) * 0x3C6EF373) & M
+        out.append(h ^ (h >> 16))
+    h = np.array(out, dtype=np.int64).reshape(-1)
+    return (h >> 16).astype(F) / F(65536), (h & 0xFFFF).astype(F) / F(65536)
+
+
+def np_moments(g, m, v):
+    c1, c2 = F(1 - H["beta1"]), F(1 - H["beta2"])
+    g = g.astype(F)
+    return F(H["beta1"]) * m + c1 * g, F(H["beta2"]) * v + c2 * (g * g), None, None
+
+
+def np_scale(x):
+    nb = -(-len(x) // 256)
+    pad = np.zeros(nb * 256, F)
+    pad[:len(x)] = np.abs(x)
+    s = pad.reshape(nb, 256).max(1)
+    inv = np.where(s > 0, F(1) / np.where(s > 0, s, F(1)), F(0)).astype(F)
+    return s, (pad.reshape(nb, 256) * inv[:, None]).reshape(-1)[:len(x)]
+
+
+def np_encode_m(m, u):
+    s, r = np_scale(m)
+    q = np.minimum(np.floor(np.sqrt(r) * F(127) + u), 127)
+    return np.where(m < 0, -q, q).astype(np.int8), s
+
+
+def np_encode_v(v, u):
+    s, r = np_scale(v)
+    q = np.minimum(np.floor(np.sqrt(np.sqrt(r)) * F(255) + u), 255)
+    return np.where((v > 0) & (q < 1), 1, q).astype(np.uint8), s
+
+
+def np_decode(qm, sm, qv, sv):
+    n = len(qm)
+    t = qm.astype(F) * F(1 / 127.0)
+    m = (t * np.abs(t)) * np.repeat(sm, 256)[:n]
+    t = qv.astype(F) * F(1 / 255.0)
+    t = t * t
+    return m, (t * t) * np.repeat(sv, 256)[:n]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gdtype", [torch.float32, torch.bfloat16])
+def test_step_8_bits(cuda, gdtype):
+    """Three steps: codes, scales and values equal to the numpy operations bit for bit, weights to fp64."""
+    sizes = [1, 5, 256, 257, 1000, 0, 4100]
+    c = make(sizes, gdtype, seed=5)
+    d = {k: [t.cuda() for t in v] for k, v in c.items()}
+    m, v, ms, vs = cuda.adamw8_state(d["p"])
+    copies = [torch.zeros(n, dtype=torch.bfloat16, device="cuda") for n in sizes]
+    have = [np_decode(np.zeros(n, np.int8), np.zeros(-(-n // 256), F), np.zeros(n, np.uint8),
+                      np.zeros(-(-n // 256), F)) for n in sizes]
+    for step in (1, 2, 3):
+        g = [(t.float() * (1 + step)).to(gdtype) for t in c["g"]]
+        before = [t.clone() for t in d["p"]]
+        cuda.adamw8_step(d["p"], [t.cuda() for t in g], m, v, ms, vs, step=step, seed=100 + step, copies=copies, **H)
+        mv, vv = cuda.adamw8_values(m, v, ms, vs)
+        for i, n in enumerate(sizes):
+            rp, _, _ = ref_step(before[i].cpu(), g[i], torch.from_numpy(have[i][0]), torch.from_numpy(have[i][1]), step)
+            check_p(d["p"][i], rp, before[i].cpu())
+            nm, nv, _, _ = np_moments(g[i].float().numpy(), *have[i])
+            um, uv = np_noise(n, 100 + step, i)
+            qm, sm = np_encode_m(nm, um)
+            qv, sv = np_encode_v(nv, uv)
+            assert np.array_equal(m[i].cpu().numpy(), qm) and np.array_equal(v[i].cpu().numpy(), qv)
+            assert np.array_equal(ms[i].cpu().numpy(), sm) and np.array_equal(vs[i].cpu().numpy(), sv)
+            have[i] = np_decode(qm, sm, qv, sv)
+            assert np.array_equal(mv[i].cpu().numpy(), have[i][0]) and np.array_equal(vv[i].cpu().numpy(), have[i][1])
+            assert torch.equal(copies[i], d["p"][i].bfloat16())
+
+
+def test_codes_are_right_in_the_mean():
+    """The rounding of the rooted values is unbiased and never off by a code step (CPU)."""
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal(256).astype(F)
+    acc = np.zeros(256)
+    rounds = 400
+    for seed in range(rounds):
+        q, s = np_encode_m(x, np_noise(256, seed, 3)[0])
+        root = np.sqrt(np.abs(x) / s[0]) * 127
+        assert np.all(np.abs(np.abs(q.astype(float)) - root) < 1 + 1e-4)
+        acc += np.abs(q) - root
+    # each rounding's variance is at most 1/4: the mean of 400 within 5 sigma, and 16 bits of noise
+    assert np.abs(acc / rounds).max() <= 5 * 0.5 / rounds ** 0.5 + 2.0 ** -16
+
+
+@pytest.mark.gpu
+def test_zero_gradients_and_nonfinite(cuda):
+    p = [torch.ones(300, device="cuda")]
+    m, v, ms, vs = cuda.adamw8_state(p)
+    g = [torch.zeros(300, device="cuda")]
+    cuda.adamw8_step(p, g, m, v, ms, vs, step=1, seed=1, **H)
+    assert torch.allclose(p[0], torch.full_like(p[0], 1 - H["lr"] * H["weight_decay"]))
+    assert not m[0].any() and not v[0].any() and not ms[0].any()
+    # an infinite gradient stays in its own tensor (fp32 moments: in its own element)
+    g32 = [torch.zeros(300, device="cuda"), torch.zeros(300, device="cuda")]
+    g32[0][5] = float("inf")
+    q = [torch.ones(300, device="cuda") for _ in range(2)]
+    z = lambda: [torch.zeros(300, device="cuda") for _ in range(2)]
+    cuda.adamw_step(q, g32, z(), z(), step=1, **H)
+    assert not torch.isfinite(q[0][5]) and int(torch.isfinite(q[0]).sum()) == 299 and torch.isfinite(q[1]).all()
+
+
+def test_refusals():
+    t = [torch.zeros(4)]
+    with pytest.raises(ValueError):
+        lrs.adamw_step(t, t, t, t, step=1, lr=1e-3)
+    lib = lrs.load()
+    P = None
+    n = (ctypes.c_int64 * 1)(4)
+    ptr = (ctypes.c_void_p * 1)(4096)
+    odd = (ctypes.c_void_p * 1)(4097)
+    nul = (ctypes.c_void_p * 1)(None)
+    f = lambda count, nn, p, step=1, b1=0.9, gd=0, eps=1e-8: lib.adamw_step(
+        count, nn, p, p, p, p, P, step, 1e-3, b1, 0.95, eps, 0.1, P, gd, P)
+    assert f(-1, n, ptr) == lrs.LR_ERR_INVALID_ARG
+    assert f(0, P, P) == lrs.LR_OK
+    assert f(1, P, P) == lrs.LR_ERR_INVALID_ARG
+    assert f(1, n, nul) == lrs.LR_ERR_INVALID_ARG
+    assert f(1, n, odd) == lrs.LR_ERR_ALIGN
+    assert f(1, n, ptr, step=0) == lrs.LR_ERR_INVALID_ARG
+    assert f(1, n, ptr, b1=1.0) == lrs.LR_ERR_INVALID_ARG
+    assert f(1, n, ptr, eps=float("nan")) == lrs.LR_ERR_INVALID_ARG
+    assert f(1, n, ptr, gd=2) == lrs.LR_ERR_INVALID_ARG
+    assert f(1, (ctypes.c_int64 * 1)(-3), ptr) == lrs.LR_ERR_INVALID_ARG
+    assert f(1, (ctypes.c_int64 * 1)(0), nul) == lrs.LR_OK  # an empty tensor needs no memory
+    assert lib.adamw8_step(1, n, ptr, ptr, ptr, ptr, P, P, P, 1, 1e-3, 0.9, 0.95, 1e-8, 0.1, P, 1, 0,
+                           P) == lrs.LR_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+def test_refusals_on_device_tensors(cuda):
+    t = [torch.zeros(8, device="cuda")]
+    h = [torch.zeros(8, device="cuda", dtype=torch.float16)]
+    for call in (lambda: cuda.adamw_step(t, t, t, [t[0][:4]], step=1, lr=1e-3),
+                 lambda: cuda.adamw_step(t, t, t, t + t, step=1, lr=1e-3),
+                 lambda: cuda.adamw_step(t, t, [t[0].double()], t, step=1, lr=1e-3),
+                 lambda: cuda.adamw_step(t, t, t, t, step=1, lr=1e-3, copies=t),
+                 lambda: cuda.adamw_step(t, t, t, t, step=1, lr=1e-3, grad_scale=torch.ones(2, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        cuda.adamw_step(t, h, t, t, step=1, lr=1e-3)

@@ -1,0 +1,300 @@
+"""Cross entropy over a large vocabulary against fp64, its gradients against
+differences, masks that leave rows or everything out, and the refusals.
+
+Tolerances: loss and lse, max|got - ref| / max(1, max|ref|) <= 1e-5 for both
+storage types (bf16 products are exact in fp32 and the sums are fp32: D = 4096
+terms of |x||w| about 2 / sqrt(D) each, 4096 * 6e-8 worst case times a logit's
+term 0.03 = 7e-6).  Gradients ||got - ref|| / ||ref||: fp32 1e-5; bf16 4e-3 (the
+result's rounding, 2^-9 / sqrt(3) = 1.1e-3, the same once more for g, and room
+for values just above a power of two), and what no fp32 logit can give: a logit
+l is off by about 2^-24 max|l| a few times over, which makes exp(l - lse) off by
+as much of itself, and where p is near 1 that is much of p - 1: 2^-21 max|l| of
+||p dloss|| ||w|| (||x|| for dw) on top.
+"""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import linear_recurrence_scan_chunked_gb300 as lrs
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+GTOL = {"f32": 1e-5, "bf16": 4e-3}
+
+
+def make(N, V, D, dtype, seed=0, pad=0.1):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(N, D, generator=g).to(DT[dtype])
+    w = (2 / math.sqrt(D) * torch.randn(V, D, generator=g)).to(DT[dtype])
+    t = torch.randint(0, V, (N,), generator=g)
+    t[torch.rand(N, generator=g) < pad] = -100
+    return x, w, t, torch.randn(N, generator=g) / N
+
+
+def ref(x, w, t, dloss, ignore=-100, lse_in=None):
+    """lse_in: the backward pass's input, as it is given (fp32: 2^-24 of its
+    size, which the exponentials of a row all share)."""
+    x, w = x.double(), w.double()
+    l = x @ w.T
+    lse = torch.logsumexp(l, 1)
+    live = (t != ignore) & (t >= 0) & (t < w.shape[0])
+    at = torch.where(live, t, 0)
+    loss = torch.where(live, lse - l[torch.arange(len(t)), at], 0.0)
+    g = torch.softmax(l, 1) if lse_in is None else torch.exp(l - lse_in.double().cpu()[:, None])
+    g[torch.arange(len(t)), at] -= 1
+    g *= torch.where(live, dloss.double(), 0.0)[:, None]
+    return loss, lse, g @ w, g.T @ x
+
+
+def slack(x, w, t, dloss, rdx, rdw):
+    """2^-21 max|l| ||p dloss|| ||w|| relative to ||dx||, and for dw."""
+    x, w = x.double(), w.double()
+    l = x @ w.T
+    p = torch.softmax(l, 1) * torch.where(t != -100, dloss.double(), 0.0)[:, None]
+    e = 2.0 ** -21 * float(l.abs().max())
+    return (e * float((p.abs() @ w.abs()).norm()) / max(float(rdx.norm()), 1e-300),
+            e * float((p.abs().T @ x.abs()).norm()) / max(float(rdw.norm()), 1e-300))
+
+
+def dist(got, want):
+    got, want = got.double().cpu(), want.double()
+    assert got.shape == want.shape and torch.isfinite(got).all()
+    n = float(want.norm())
+    return float((got - want).norm()) / n if n else float(got.norm())
+
+
+def mx(got, want):
+    got, want = got.double().cpu(), want.double()
+    assert got.shape == want.shape and torch.isfinite(got).all()
+    return float((got - want).abs().max() / max(1.0, float(want.abs().max())))
+
+
+# one of everything, exact tiles, one past and one short of them, odd widths (no 16-byte rows)
+SHAPES = [(1, 1, 1), (1, 2, 8), (2, 3, 5), (1, 1000, 64), (5, 257, 64), (128, 256, 64), (129, 255, 72), (64, 128, 128),
+          (200, 1000, 250), (300, 513, 33), (256, 512, 256), (257, 777, 264), (130, 5000, 1000), (1, 20000, 136),
+          (1000, 130, 64), (513, 129, 1024), (40, 300, 4096), (31, 9000, 1023)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,V,D", SHAPES)
+def test_loss_and_gradients(cuda, N, V, D, dtype):
+    x, w, t, dl = make(N, V, D, dtype, seed=N + V + D)
+    rl, rz, rdx, rdw = ref(x, w, t, dl)
+    xd, wd, td, dd = (v.cuda() for v in (x, w, t, dl))
+    loss, lse = cuda.lce_fwd(xd, wd, td)
+    assert mx(loss, rl) <= 1e-5 and mx(lse, rz) <= 1e-5
+    _, _, rdx, rdw = ref(x, w, t, dl, lse_in=lse)
+    dx, dw = cuda.lce_bwd(xd, wd, td, lse, dd)
+    assert dx.dtype == dw.dtype == DT[dtype]
+    if V > 1:  # one word: the gradient is 0 but for roundings
+        sx, sw = slack(x, w, t, dl, rdx, rdw)
+        assert dist(dx, rdx) <= GTOL[dtype] + sx and dist(dw, rdw) <= GTOL[dtype] + sw
+    else:
+        assert float(dx.abs().max()) <= 1e-6 and float(dw.abs().max()) <= 1e-6
+    # the same bits again, into buffers that hold something else
+    loss2, lse2 = cuda.lce_fwd(xd, wd, td, loss=torch.full_like(loss, 9.0), lse=torch.full_like(lse, 9.0))
+    assert torch.equal(loss, loss2) and torch.equal(lse, lse2)
+    dx2, dw2 = cuda.lce_bwd(xd, wd, td, lse, dd, dx=torch.full_like(dx, 9.0), dw=torch.full_like(dw, 9.0))
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_more_than_one_piece(cuda, dtype):
+    """A vocabulary of several pieces, ragged at the end, and a last tile of one word."""
+    N, V, D = 70, 40001, 96
+    x, w, t, dl = make(N, V, D, dtype, seed=3)
+    t[0], t[1], t[2] = 0, V - 1, V - 2
+    rl, rz, rdx, rdw = ref(x, w, t, dl)
+    xd, wd, td, dd = (v.cuda() for v in (x, w, t, dl))
+    loss, lse = cuda.lce_fwd(xd, wd, td)
+    dx, dw = cuda.lce_bwd(xd, wd, td, lse, dd)
+    assert mx(loss, rl) <= 1e-5 and mx(lse, rz) <= 1e-5
+    assert dist(dx, rdx) <= GTOL[dtype] and dist(dw, rdw) <= GTOL[dtype]
+
+
+@pytest.mark.gpu
+def test_many_rows(cuda):
+    N, V, D = 20000, 300, 64
+    x, w, t, dl = make(N, V, D, "bf16", seed=4)
+    rl, rz, rdx, rdw = ref(x, w, t, dl)
+    xd, wd, td, dd = (v.cuda() for v in (x, w, t, dl))
+    loss, lse = cuda.lce_fwd(xd, wd, td)
+    dx, dw = cuda.lce_bwd(xd, wd, td, lse, dd)
+    assert mx(loss, rl) <= 1e-5 and mx(lse, rz) <= 1e-5
+    assert dist(dx, rdx) <= GTOL["bf16"] and dist(dw, rdw) <= GTOL["bf16"]
+
+
+@pytest.mark.gpu
+def test_uniform_upstream_is_not_biased(cuda):
+    """dloss = 1/N, which bf16 cannot hold: the rounding of g must not shift dw as a whole."""
+    N, V, D = 1021, 500, 64
+    x, w, t, _ = make(N, V, D, "bf16", seed=5, pad=0.0)
+    x = x.abs()  # rows that add up
+    dl = torch.full((N,), 1.0 / N)
+    _, _, rdx, rdw = ref(x, w, t, dl)
+    xd, wd, td, dd = (v.cuda() for v in (x, w, t, dl))
+    _, lse = cuda.lce_fwd(xd, wd, td)
+    dx, dw = cuda.lce_bwd(xd, wd, td, lse, dd)
+    assert dist(dx, rdx) <= GTOL["bf16"] and dist(dw, rdw) <= GTOL["bf16"]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_all_rows_ignored_and_other_ignore(cuda, dtype):
+    x, w, t, dl = make(9, 100, 64, dtype, seed=6)
+    xd, wd, dd = x.cuda(), w.cuda(), dl.cuda()
+    off = torch.full((9,), -100).cuda()
+    loss, lse = cuda.lce_fwd(xd, wd, off)
+    assert not loss.any() and mx(lse, ref(x, w, t, dl)[1]) <= 1e-5
+    dd[3] = float("inf")  # masked: must not reach the result
+    dd[4] = float("nan")
+    dx, dw = cuda.lce_bwd(xd, wd, off, lse, dd)
+    assert not dx.any() and not dw.any()
+    # a word of the vocabulary as the ignored one
+    t[:] = 7
+    t[2] = 8
+    rl, _, rdx, rdw = ref(x, w, t, dl, ignore=7)
+    dd = dl.cuda()
+    loss, lse = cuda.lce_fwd(xd, wd, t.cuda(), ignore=7)
+    dx, dw = cuda.lce_bwd(xd, wd, t.cuda(), lse, dd, ignore=7)
+    assert mx(loss, rl) <= 1e-5 and dist(dx, rdx) <= GTOL[dtype] and dist(dw, rdw) <= GTOL[dtype]
+
+
+@pytest.mark.gpu
+def test_large_logits(cuda):
+    """Logits of +-1e4 (sums of exponentials relative to the maximum), and a vocabulary word at -inf's edge."""
+    N, V, D = 20, 700, 64
+    x, w, t, dl = make(N, V, D, "f32", seed=7, pad=0.0)
+    x = x * 3e3
+    rl, rz, rdx, rdw = ref(x, w, t, dl)
+    xd, wd, td, dd = (v.cuda() for v in (x, w, t, dl))
+    loss, lse = cuda.lce_fwd(xd, wd, td)
+    assert mx(loss, rl) <= 1e-5 and mx(lse, rz) <= 1e-5
+    # a logit near 1e4 is good to 1e4 * 1e-6: g to a few 1e-2 where the softmax is not saturated
+    dx, dw = cuda.lce_bwd(xd, wd, td, lse, dd)
+    assert dist(dx, rdx) <= 5e-2 and dist(dw, rdw) <= 5e-2
+
+
+@pytest.mark.gpu
+def test_nan_stays_in_its_rows(cuda):
+    N, V, D = 140, 300, 64
+    x, w, t, dl = make(N, V, D, "bf16", seed=8, pad=0.0)
+    x[5, 3] = float("nan")
+    loss, lse = cuda.lce_fwd(x.cuda(), w.cuda(), t.cuda())
+    bad = torch.isnan(loss).cpu()
+    assert bad[5] and int(bad.sum()) == 1
+    dx, _ = cuda.lce_bwd(x.cuda(), w.cuda(), t.cuda(), lse, dl.cuda())
+    bad = torch.isnan(dx).any(1).cpu()
+    assert bad[5] and int(bad.sum()) == 1
+
+
+@pytest.mark.gpu
+def test_targets_out_of_range_are_recorded(cuda):
+    x, w, t, dl = make(6, 50, 64, "f32", seed=9, pad=0.0)
+    t[1], t[4] = 50, -7
+    rl, rz, rdx, rdw = ref(x, w, t, dl)
+    xd, wd, td = x.cuda(), w.cuda(), t.cuda()
+    loss, lse = cuda.lce_fwd(xd, wd, td)
+    assert cuda.last_error() == cuda.LR_ERR_INDEX and cuda.last_error() == cuda.LR_OK
+    assert mx(loss, rl) <= 1e-5 and not loss[1] and not loss[4]
+    dx, dw = cuda.lce_bwd(xd, wd, td, lse, dl.cuda())
+    assert dist(dx, rdx) <= 1e-5 and dist(dw, rdw) <= 1e-5
+    cuda.last_error()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_unaligned_views_batched_shapes_streams_and_empty(cuda, dtype):
+    N, V, D = 12, 90, 64
+    x, w, t, dl = make(N, V, D, dtype, seed=10)
+    rl, _, rdx, rdw = ref(x, w, t, dl)
+    bx = torch.zeros(N * D + 1, dtype=DT[dtype], device="cuda")
+    bw = torch.zeros(V * D + 3, dtype=DT[dtype], device="cuda")
+    xv, wv = bx[1:].view(3, 4, D), bw[3:].view(V, D)
+    xv.copy_(x.view(3, 4, D))
+    wv.copy_(w)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    td, dd = t.view(3, 4).cuda(), dl.view(3, 4).cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        loss, lse = cuda.lce_fwd(xv, wv, td)
+        dx, dw = cuda.lce_bwd(xv, wv, td, lse, dd)
+    s.synchronize()
+    assert loss.shape == (3, 4) and mx(loss.view(-1), rl) <= 1e-5
+    assert dx.shape == (3, 4, D) and dist(dx.view(N, D), rdx) <= GTOL[dtype] and dist(dw, rdw) <= GTOL[dtype]
+    e = torch.empty(0, D, dtype=DT[dtype], device="cuda")
+    te = torch.empty(0, dtype=torch.int64, device="cuda")
+    loss, lse = cuda.lce_fwd(e, wv, te)
+    dx, dw = cuda.lce_bwd(e, wv, te, lse, loss)
+    assert loss.shape == (0,) and dx.shape == (0, D) and not dw.any()
+
+
+@pytest.mark.gpu
+def test_captured_into_a_graph(cuda):
+    x, w, t, dl = (v.cuda() for v in make(50, 400, 128, "bf16", seed=11))
+    loss, lse = cuda.lce_fwd(x, w, t)
+    dx, dw = cuda.lce_bwd(x, w, t, lse, dl)
+    want = [v.clone() for v in (loss, dx, dw)]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cuda.lce_fwd(x, w, t, loss=loss, lse=lse)
+        cuda.lce_bwd(x, w, t, lse, dl, dx=dx, dw=dw)
+    for v in (loss, dx, dw):
+        v.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip((loss, dx, dw), want):
+        assert torch.equal(a, b)
+
+
+def test_reference_gradients_against_differences():
+    x, w, t, dl = make(3, 6, 4, "f32", seed=12, pad=0.0)
+    x, w, t[1] = x.double(), w.double(), -100
+    _, _, rdx, rdw = ref(x, w, t, dl)
+    loss = lambda a, b: float((ref(a, b, t, dl)[0] * dl.double()).sum())
+    for which, r in ((0, rdx), (1, rdw)):
+        for at in np.ndindex(*r.shape):
+            args = [[x.clone(), w.clone()] for _ in range(2)]
+            args[0][which][at] += 1e-5
+            args[1][which][at] -= 1e-5
+            assert abs((loss(*args[0]) - loss(*args[1])) / 2e-5 - float(r[at])) <= 1e-8
+
+
+def test_refusals():
+    x, w, t = torch.zeros(3, 4), torch.zeros(5, 4), torch.zeros(3, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        lrs.lce_fwd(x, w, t)
+    with pytest.raises(ValueError):
+        lrs.lce_bwd(x, w, t, x[:, 0], x[:, 0])
+    lib = lrs.load()
+    P = None
+    f = lambda n, v, d, p=P, dt=0: lib.lce_fwd(p, p, p, -100, p, p, n, v, d, dt, P)
+    b = lambda n, v, d, p=P, dt=0: lib.lce_bwd(p, p, p, -100, p, p, p, p, n, v, d, dt, P)
+    for call in (f, b):
+        assert call(3, 5, 4) == lrs.LR_ERR_INVALID_ARG
+        assert call(3, 5, 4, dt=3) == lrs.LR_ERR_INVALID_ARG
+        assert call(-1, 5, 4) == lrs.LR_ERR_INVALID_ARG
+        assert call(3, 0, 4) == lrs.LR_ERR_INVALID_ARG
+        assert call(3, 5, 0) == lrs.LR_ERR_INVALID_ARG
+        assert call(3, 5, 65537) == lrs.LR_ERR_TOO_LARGE
+        assert call(1 << 31, 5, 4) == lrs.LR_ERR_TOO_LARGE
+        assert call(3, 5, 4, ctypes.c_void_p(4097)) == lrs.LR_ERR_ALIGN
+    assert f(0, 5, 4) == lrs.LR_OK
+    assert b(0, 5, 4) == lrs.LR_ERR_INVALID_ARG  # dw is written even for no row
+
+
+@pytest.mark.gpu
+def test_refusals_on_device_tensors(cuda):
+    x, w, t, dl = (v.cuda() for v in make(6, 50, 64, "f32"))
+    for call in (lambda: cuda.lce_fwd(x, w.bfloat16(), t), lambda: cuda.lce_fwd(x, w[:, :32], t),
+                 lambda: cuda.lce_fwd(x, w, t.int()), lambda: cuda.lce_fwd(x, w, t[:3]),
+                 lambda: cuda.lce_fwd(x.t(), w, t), lambda: cuda.lce_bwd(x, w, t, dl.double(), dl),
+                 lambda: cuda.lce_bwd(x, w, t, dl, dl, dx=x.bfloat16())):
+        with pytest.raises(ValueError):
+            call()

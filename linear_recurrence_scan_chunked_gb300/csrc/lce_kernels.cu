@@ -6,89 +6,155 @@
 //   g[n][v] = (exp(l[n][v] - lse[n]) - [v = target[n]]) dloss[n],
 //   dx = g W,   dW = g^T x.
 //
-// Forward: a tile of logits lives in registers; each leaves, per row, its
-// maximum and its sum of exponentials relative to that maximum, and a second
-// kernel joins the tiles' pairs.  Backward: for a piece of the vocabulary the
-// logits are computed again and g is written, then the piece's dW and its share
-// of dx (summed over the pieces in fp32).
+// Forward: the epilogue of the product x W^T reduces each 256-column tile of
+// logits to a pair per row, a power-of-two bound 2^M of its exponentials and
+// their sum relative to it, and a second kernel joins the tiles' pairs.  Backward:
+// for a piece of the vocabulary the product runs again, its epilogue writes g
+// (scratch, bounded by kPieceBytes), and two more products give the piece's dW and
+// its share of dx.  That is 8 N V D operations where a form that kept the logits
+// needs 6, but no N x V array of them.
+//
+// Types.  g is held in bf16 for bf16 data: relative error 2^-9 an element,
+// independent from element to element, as much as the rounding of the results.
+// It is scaled by 1 / max|dloss| (put back in fp32 at the end), so that with a
+// uniform dloss the -1 of the targets is exact and no common rounding error adds
+// up in dW.  fp32 data runs as three bf16 planes (lce_mma.cuh), g included.  All
+// sums and statistics are fp32.
+//
+// No floating-point atomics: sums over parts of the k loop are stored as parts and
+// added in order.
+#include <algorithm>
+
+#include "lce_mma.cuh"
+#include "lr_act.cuh"
 #include "lr_launch.h"
 
 namespace lrs {
 
 namespace {
 
-constexpr int kT = 64, kK = 16;  // tile edge, depth of a step
+using mm::kTile;
+using mm::Shape;
+using mm::Tile;
 
-__device__ __forceinline__ float ldf(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float ldf(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+constexpr int64_t kPieceBytes = (int64_t)2 << 30;  // g of one piece, all planes
+constexpr float kLn2 = 0.6931471805599453f;
 
-// C[m][n] = sum_k A[m*am + k*ak] B[n*bn + k*bk] over one 64 x 64 tile, 4 x 4 a
-// thread (rows ty + 16 i, columns tx + 16 j), handed to the epilogue.
-template <typename TA, typename TB, class Epi>
-__device__ __forceinline__ void tile_mm(const TA* A, int64_t am, int64_t ak, const TB* B, int64_t bn, int64_t bk,
-                                        int64_t M, int64_t N, int64_t K, int64_t m0, int64_t n0, Epi epi) {
-    __shared__ float sa[kK][kT + 1], sb[kK][kT + 1];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < K; k0 += kK) {
-        for (int i = threadIdx.x; i < kT * kK; i += 256) {
-            // neighbouring threads along the contiguous axis
-            const int ma = ak == 1 ? i / kK : i % kT, ka = ak == 1 ? i % kK : i / kT;
-            const int nb = bk == 1 ? i / kK : i % kT, kb = bk == 1 ? i % kK : i / kT;
-            sa[ka][ma] = m0 + ma < M && k0 + ka < K ? ldf(A + (m0 + ma) * am + (k0 + ka) * ak) : 0.f;
-            sb[kb][nb] = n0 + nb < N && k0 + kb < K ? ldf(B + (n0 + nb) * bn + (k0 + kb) * bk) : 0.f;
+// 32 bytes of a row (sm_100+: one sector in one store).
+__device__ __forceinline__ void st_32b(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+// 32 consecutive elements of a row, the first n of them inside it; wide: p is
+// 32-byte aligned.
+__device__ __forceinline__ void st_row32(__nv_bfloat16* p, const float (&v)[32], int64_t n, bool wide) {
+    if (wide && n >= 32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = bf_pack(v[16 * h + 2 * i], v[16 * h + 2 * i + 1]);
+            st_32b(p + 16 * h, w);
         }
-        __syncthreads();
+    } else {
 #pragma unroll
-        for (int k = 0; k < kK; ++k) {
-            float a[4], b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { a[i] = sa[k][ty + 16 * i]; b[i] = sb[k][tx + 16 * i]; }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-        }
-        __syncthreads();
+        for (int i = 0; i < 32; ++i)
+            if (i < n) p[i] = __float2bfloat16_rn(v[i]);
     }
-    epi(acc, m0 + ty, n0 + tx);
 }
-
-template <typename S>
-__global__ void __launch_bounds__(256)
-    k_lce_stats(const S* x, const S* w, const int64_t* target, float2* part, float* tl, int64_t N, int64_t V, int64_t D) {
-    const int64_t m0 = (int64_t)blockIdx.y * kT, n0 = (int64_t)blockIdx.x * kT;
-    tile_mm(x, D, 1, w, D, 1, N, V, D, m0, n0, [&](float (&acc)[4][4], int64_t m, int64_t n) {
+__device__ __forceinline__ void st_row32(float* p, const float (&v)[32], int64_t n, bool wide) {
+    if (wide && n >= 32) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t row = m + 16 * i;
-            const int64_t t = row < N ? target[row] : -1;
-            float top = -INFINITY, sum = 0.f;
+        for (int h = 0; h < 4; ++h) {
+            uint32_t w[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n + 16 * j < V) {
-                    top = fmaxf(top, acc[i][j]);
-                    if (n + 16 * j == t) tl[row] = acc[i][j];
-                }
-            for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n + 16 * j < V) sum += expf(acc[i][j] - top);
-            for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-            if (row < N && (threadIdx.x & 15) == 0) part[(int64_t)blockIdx.x * N + row] = make_float2(top, sum);
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+            st_32b(p + 8 * h, w);
         }
-    });
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < n) p[i] = v[i];
+    }
 }
 
-__global__ void __launch_bounds__(256)
-    k_lce_join(const float2* part, int64_t tiles, const float* tl, const int64_t* target, int64_t ignore, float* loss,
-               float* lse, int64_t N, int64_t V, uint32_t* err) {
-    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (n >= N) return;
-    float top = -INFINITY, sum = 0.f;
-    for (int64_t k = 0; k < tiles; ++k) top = fmaxf(top, part[k * N + n].x);
-    for (int64_t k = 0; k < tiles; ++k) sum += part[k * N + n].y * expf(part[k * N + n].x - top);
-    const float z = top + logf(sum);
+// v[j] of a runtime j, by selection (the array stays in registers).
+__device__ __forceinline__ float pick32(const float (&v)[32], int j) {
+    float r = v[0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) r = i == j ? v[i] : r;
+    return r;
+}
+
+// Forward: the pair of a tile and a row.  With M = ceil(max l log2 e), the sum
+// of 2^(l log2 e - M): M is an integer, so its subtraction inside the
+// multiply-add rounds nothing but the result, and no common error enters the sum.
+struct StatsEpi {
+    float2* part;           // [tiles][rows]
+    float* tl;              // the targets' logits
+    const int64_t* target;
+    int64_t rows, V;
+    template <class Cols>
+    __device__ void tile(const Tile& t, int row, Cols cols) const {
+        const int64_t n = (int64_t)t.m * kTile + row;
+        const int64_t v0 = (int64_t)t.n * kTile;
+        const int width = (int)(V - v0 < kTile ? V - v0 : kTile);
+        const int64_t tg = n < rows ? __ldg(target + n) - v0 : -1;
+        const int at = tg >= 0 && tg < width ? (int)tg : -1;
+        float M = -INFINITY, s = 0.f;
+        for (int c = 0; c * 32 < width; ++c) {
+            float v[32];
+            cols(c, v);
+            if (width < c * 32 + 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = c * 32 + i < width ? v[i] : -INFINITY;
+            }
+            if (__any_sync(0xffffffffu, at >> 5 == c)) {
+                const float x = pick32(v, at & 31);
+                if (at >> 5 == c) tl[n] = x;
+            }
+            float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+            for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+            const float m = ceilf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e);
+            if (m > M) {
+                s *= ex2_ftz(M - m);  // the first time 2^-inf = 0
+                M = m;
+            }
+            float e[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) e[i & 3] += ex2_ftz(fmaf(v[i], kLog2e, -M));
+            s += (e[0] + e[1]) + (e[2] + e[3]);
+        }
+        if (n < rows) part[(int64_t)t.n * rows + n] = make_float2(M, s);
+    }
+};
+
+// Joins the tiles' pairs of 32 rows (x): lane y folds tiles y, y + 32, ..., then
+// the lanes' pairs fold in order.
+__global__ void __launch_bounds__(1024)
+    k_lce_join(const float2* __restrict__ part, int64_t tiles, const float* __restrict__ tl,
+               const int64_t* __restrict__ target, int64_t ignore, float* __restrict__ loss, float* __restrict__ lse,
+               int64_t rows, int64_t V, uint32_t* err) {
+    __shared__ float2 sm[32][33];
+    const int64_t n = (int64_t)blockIdx.x * 32 + threadIdx.x;
+    float M = -INFINITY, s = 0.f;
+    auto fold = [&](const float2 p) {
+        // a tile's M is -inf or NaN only where its logits are: its sum is NaN then
+        const float m = fmaxf(M, p.x);
+        s = s * (M == m ? 1.f : ex2_ftz(M - m)) + p.y * (p.x == m ? 1.f : ex2_ftz(p.x - m));
+        M = m;
+    };
+    if (n < rows)
+        for (int64_t k = threadIdx.y; k < tiles; k += 32) fold(__ldg(part + k * rows + n));
+    sm[threadIdx.y][threadIdx.x] = make_float2(M, s);
+    __syncthreads();
+    if (threadIdx.y != 0 || n >= rows) return;
+    M = -INFINITY;
+    s = 0.f;
+    for (int k = 0; k < 32 && k < tiles; ++k) fold(sm[k][threadIdx.x]);
+    const float z = fmaf(M, kLn2, logf(s));
     lse[n] = z;
     const int64_t t = target[n];
     const bool in = t >= 0 && t < V;
@@ -96,127 +162,429 @@ __global__ void __launch_bounds__(256)
     loss[n] = t == ignore || !in ? 0.f : z - tl[n];
 }
 
-template <typename S>
+// max |dloss| over the rows that count (finite ones), as float bits: the maximum
+// of non-negative floats is the maximum of their bits, in any order.
 __global__ void __launch_bounds__(256)
-    k_lce_grad(const S* x, const S* w, const int64_t* target, int64_t ignore, const float* lse, const float* dloss,
-               float* g, int64_t N, int64_t v0, int64_t vc, int64_t V, int64_t D) {
-    const int64_t m0 = (int64_t)blockIdx.y * kT, n0 = (int64_t)blockIdx.x * kT;
-    tile_mm(x, D, 1, w + v0 * D, D, 1, N, vc, D, m0, n0, [&](float (&acc)[4][4], int64_t m, int64_t n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t row = m + 16 * i;
-            if (row >= N) continue;
-            const int64_t t = target[row];
-            const float s = t == ignore || t < 0 || t >= V ? 0.f : dloss[row];
-            const float z = lse[row];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n + 16 * j < vc)
-                    // the target's p - 1 without cancellation where p is near 1
-                    g[row * vc + n + 16 * j] =
-                        s == 0.f ? 0.f : (v0 + n + 16 * j == t ? expm1f(acc[i][j] - z) : expf(acc[i][j] - z)) * s;
+    k_lce_scale(const float* __restrict__ dloss, const int64_t* __restrict__ target, int64_t ignore, int64_t N, int64_t V,
+                uint32_t* __restrict__ top) {
+    uint32_t m = 0;
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < N; n += (int64_t)gridDim.x * 256) {
+        const int64_t t = target[n];
+        const float a = fabsf(dloss[n]);
+        if (t != ignore && t >= 0 && t < V && a < INFINITY) m = max(m, __float_as_uint(a));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0 && m) atomicMax(top, m);
+}
+__device__ __forceinline__ float scale_of(const uint32_t* top) {
+    const float s = __uint_as_float(__ldg(top));
+    return s > 0.f ? s : 1.f;
+}
+
+// Backward: g / max|dloss| of a tile, in P bf16 planes.
+template <int P>
+struct GradEpi {
+    __nv_bfloat16* g;  // [P][rows][pitch]
+    int64_t pitch;     // a multiple of 16
+    int64_t plane;     // elements of a plane
+    const float* lse;
+    const float* dloss;
+    const int64_t* target;
+    const uint32_t* top;
+    int64_t ignore, rows, v0, vc, V;
+    template <class Cols>
+    __device__ void tile(const Tile& t, int row, Cols cols) const {
+        const int64_t n = (int64_t)t.m * kTile + row;
+        const int64_t c0 = (int64_t)t.n * kTile;
+        const int width = (int)(vc - c0 < kTile ? vc - c0 : kTile);
+        float f = 0.f, ds = 0.f, hi = INFINITY, z = 0.f;  // a row that does not count: 2^-inf = 0
+        int at = -1;
+        if (n < rows) {
+            const int64_t tg = __ldg(target + n);
+            if (tg != ignore && tg >= 0 && tg < V) {
+                ds = __fdiv_rn(__ldg(dloss + n), scale_of(top));
+                z = __ldg(lse + n);
+                // lse log2 e = hi + lo: 2^-lo goes into the row's factor, so that
+                // hi's rounding is no common error of the row
+                hi = z * kLog2e;
+                f = ds * ex2_ftz(fmaf(-z, kLog2e, hi));
+                const int64_t r = tg - v0 - c0;
+                if (r >= 0 && r < width) at = (int)r;
+            }
         }
-    });
-}
+        __nv_bfloat16* out = g + n * pitch + c0;
+        for (int c = 0; c * 32 < width; ++c) {
+            float v[32];
+            cols(c, v);
+            const bool mine = at >> 5 == c;
+            float gt = 0.f;
+            // the target's p - 1 without cancellation where p is near 1
+            if (__any_sync(0xffffffffu, mine)) gt = expm1f(pick32(v, at & 31) - z) * ds;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = ex2_ftz(fmaf(v[i], kLog2e, -hi)) * f;
+            if (__any_sync(0xffffffffu, mine)) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = mine && i == (at & 31) ? gt : v[i];
+            }
+            if (n < rows) {
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    st_row32(out + p * plane + c * 32, v, width - c * 32, true);
+                    if (p + 1 < P) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] -= bf_lo(bf_bits(v[i]));
+                    }
+                }
+            }
+        }
+    }
+};
 
-// dx: out[n][d] (+)= sum over the piece; the last piece rounds to the storage type
+// A product's tile: rounded to the result (scaled by max|dloss|), or one part of
+// the k loop, fp32.
+template <typename S>
+struct OutEpi {
+    S* out;         // nullptr: parts
+    float* part;    // [splits][rows x cols]
+    int64_t pitch;  // elements of a part
+    const uint32_t* top;
+    int64_t rows, cols_n;
+    bool wide;      // rows of the destination are 32-byte aligned
+    template <class Cols>
+    __device__ void tile(const Tile& t, int row, Cols cols) const {
+        const int64_t m = (int64_t)t.m * kTile + row;
+        const int64_t c0 = (int64_t)t.n * kTile;
+        const int64_t width = cols_n - c0 < kTile ? cols_n - c0 : kTile;
+        const float a = out ? scale_of(top) : 1.f;
+        for (int c = 0; c * 32 < width; ++c) {
+            float v[32];
+            cols(c, v);
+            if (m >= rows) continue;
+            if (out) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= a;
+                st_row32(out + m * cols_n + c0 + c * 32, v, width - c * 32, wide);
+            } else {
+                st_row32(part + t.split * pitch + m * cols_n + c0 + c * 32, v, width - c * 32, wide);
+            }
+        }
+    }
+};
+
+// out = max|dloss| * the sum of the parts, in order.
 template <typename S>
 __global__ void __launch_bounds__(256)
-    k_lce_dx(const float* g, const S* w, float* acc32, S* dx, int64_t N, int64_t v0, int64_t vc, int64_t D, bool first,
-             bool last) {
-    tile_mm(g, vc, 1, w + v0 * D, 1, D, N, D, vc, (int64_t)blockIdx.y * kT, (int64_t)blockIdx.x * kT,
-            [&](float (&acc)[4][4], int64_t m, int64_t n) {
+    k_lce_sum(const float* __restrict__ part, int64_t parts, int64_t pitch, int64_t n, const uint32_t* __restrict__ top,
+              S* __restrict__ out, bool vec) {
+    const float a = scale_of(top);
+    const int64_t step = (int64_t)gridDim.x * 256;
+    if (vec) {
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n / 4; i += step) {
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int64_t k = 0; k < parts; ++k) {
+                Pack<float, 4> p;
+                p.load(part + k * pitch + 4 * i);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int j = 0; j < 4; ++j) s[j] += p.get(j);
+            }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int64_t row = m + 16 * i, col = n + 16 * j;
-                        if (row >= N || col >= D) continue;
-                        const float s = acc[i][j] + (first ? 0.f : acc32[row * D + col]);
-                        if (last) {
-                            const float o[1] = {s};
-                            store_vec<S, 1>(dx + row * D + col, o);
-                        } else {
-                            acc32[row * D + col] = s;
-                        }
-                    }
-            });
+            for (int j = 0; j < 4; ++j) s[j] *= a;
+            store_vec<S, 4>(out + 4 * i, s);
+        }
+    }
+    for (int64_t i = (vec ? n / 4 * 4 : 0) + (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+        float s[1] = {0.f};
+        for (int64_t k = 0; k < parts; ++k) s[0] += __ldg(part + k * pitch + i);
+        s[0] *= a;
+        store_vec<S, 1>(out + i, s);
+    }
 }
 
-template <typename S>
+// [rows][D] into P bf16 planes of pitch ld (a multiple of 8): fp32 data split into
+// three, bf16 data whose rows TMA cannot read (odd widths, unaligned views) copied.
+template <typename S, int P>
 __global__ void __launch_bounds__(256)
-    k_lce_dw(const float* g, const S* x, S* dw, int64_t N, int64_t v0, int64_t vc, int64_t D) {
-    tile_mm(g, 1, vc, x, 1, D, vc, D, N, (int64_t)blockIdx.y * kT, (int64_t)blockIdx.x * kT,
-            [&](float (&acc)[4][4], int64_t m, int64_t n) {
+    k_lce_pack(const S* __restrict__ src, __nv_bfloat16* __restrict__ dst, int64_t rows, int64_t D, int64_t ld) {
+    const int64_t plane = rows * ld, n = rows * ld;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / ld, d = i - r * ld;
+        float v = 0.f;
+        if (d < D) {
+            Pack<S, 1> p;
+            p.load(src + r * D + d);
+            v = p.get(0);
+        }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int64_t row = m + 16 * i, col = n + 16 * j;
-                        const float o[1] = {acc[i][j]};
-                        if (row < vc && col < D) store_vec<S, 1>(dw + (v0 + row) * D + col, o);
-                    }
-            });
+        for (int k = 0; k < P; ++k) {
+            const __nv_bfloat16 b = __float2bfloat16_rn(v);
+            dst[k * plane + i] = b;
+            v -= __bfloat162float(b);
+        }
+    }
 }
+
+// ------------------------------------------------------------------- host
+
+// An operand as the products take it: bf16 planes [planes][rows][ld].
+struct Operand {
+    const __nv_bfloat16* p;
+    int64_t rows, cols, ld, plane;
+    int planes;
+};
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// mn: the product takes it MN-major (boxes of 64 x 64), else K-major (64 x 128).
+bool operand_map(CUtensorMap* m, const Operand& o, bool mn) {
+    return tma_encode_planes(m, o.p, o.cols, o.rows, o.planes, o.ld, o.plane, mm::kBlockK, mn ? mm::kBlockK : mm::kHalf);
+}
+
+// Pairs of CTAs resident at once.
+template <class Epi>
+cudaError_t mm_pairs(int* pairs) {
+    static int known[64] = {0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int& n = known[dev & 63];
+    if (n <= 0) {
+        cudaError_t e = cudaFuncSetAttribute(mm::k_mm<Epi>, cudaFuncAttributeMaxDynamicSharedMemorySize, mm::kSmem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t lc{};
+        lc.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
+        lc.blockDim = dim3(mm::kThreads);
+        lc.dynamicSmemBytes = mm::kSmem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 2;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        lc.attrs = at;
+        lc.numAttrs = 1;
+        int c = 0;
+        if (cudaOccupancyMaxActiveClusters(&c, mm::k_mm<Epi>, &lc) != cudaSuccess || c < 1) c = 1;
+        n = c < sm_count() / 2 ? c : sm_count() / 2;
+    }
+    *pairs = n;
+    return cudaSuccess;
+}
+
+template <class Epi>
+cudaError_t mm_run(const Operand& a, const Operand& b, Shape sh, const Epi& epi, uint32_t* err, cudaStream_t s) {
+    CUtensorMap ma, mb;
+    if (!operand_map(&ma, a, sh.a_mn) || !operand_map(&mb, b, sh.b_mn)) return cudaErrorInvalidValue;
+    int pairs = 1;
+    const cudaError_t e = mm_pairs<Epi>(&pairs);
+    if (e != cudaSuccess) return e;
+    const uint64_t tiles = (uint64_t)sh.tm * sh.tn * sh.splits;
+    if (tiles > 0x7fffffffull) return cudaErrorInvalidValue;
+    const unsigned grid = 2 * (unsigned)std::min<uint64_t>(tiles, (uint64_t)pairs);
+    mm::k_mm<Epi><<<grid, mm::kThreads, mm::kSmem, s>>>(ma, mb, sh, epi, err);
+    return cudaGetLastError();
+}
+
+Shape mm_shape(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, bool n_fast, int64_t splits) {
+    Shape s{};
+    s.tm = (uint32_t)((M + kTile - 1) / kTile);
+    s.tn = (uint32_t)((N + kTile - 1) / kTile);
+    s.kb = (uint32_t)((K + mm::kBlockK - 1) / mm::kBlockK);
+    s.kb_split = (uint32_t)((s.kb + splits - 1) / splits);
+    s.splits = (s.kb + s.kb_split - 1) / s.kb_split;
+    s.pairs = planes == 1 ? 1 : 6;
+    s.n_fast = n_fast;
+    s.a_mn = a_mn;
+    s.b_mn = b_mn;
+    return s;
+}
+
+// Parts of the k loop of a product M x N x K: the number that gives the shortest
+// time in a simple model, rounds of tiles over the pairs at a pair's rate (a
+// k-block of 64 takes about 512 cycles) plus the parts' way to memory and back
+// (about 3.5 KB a cycle over the GPU).  With few tiles the parts fill the GPU;
+// with many they even out its last round.
+int64_t mm_splits(int64_t M, int64_t N, int64_t K, int planes) {
+    const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
+    const int64_t kb = (K + mm::kBlockK - 1) / mm::kBlockK, pairs = sm_count() / 2;
+    int64_t best = 1;
+    double best_t = 0;
+    for (int64_t s = 1; s <= 64 && s <= kb; ++s) {
+        const int64_t per = (kb + s - 1) / s, real = (kb + per - 1) / per;
+        if (real != s) continue;
+        const double rounds = (double)((tiles * s + pairs - 1) / pairs);
+        double t = rounds * (double)per * (planes == 1 ? 1 : 6) * 512 + rounds * 1500;
+        if (s > 1) t += (double)(s * M * N) * 8 / 3500 + 4000;
+        if (best_t == 0 || t < 0.98 * best_t) {
+            best = s;
+            best_t = t;
+        }
+    }
+    return best;
+}
+
+struct Layout {  // offsets into the scratch
+    size_t x, w, top, part, tl, g, px, pw, bytes;
+};
+
+bool packed(int dtype, const void* p, int64_t D) { return dtype == 0 || D % 8 != 0 || ((uintptr_t)p & 15) != 0; }
+
+size_t take(size_t& at, size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return o;
+}
+
+Layout layout(int dtype, const void* x, const void* w, int64_t N, int64_t V, int64_t D, const LcePlan& p, bool bwd) {
+    Layout l{};
+    const size_t planes = dtype == 0 ? 3 : 1;
+    const int64_t ld = round_up(D, 8);
+    size_t at = 0;
+    l.top = take(at, 4);
+    if (packed(dtype, x, D)) l.x = take(at, planes * N * ld * 2);
+    if (packed(dtype, w, D)) l.w = take(at, planes * V * ld * 2);
+    if (bwd) {
+        l.g = take(at, planes * N * round_up(p.piece, 16) * 2);
+        if (p.dx_parts > 1) l.px = take(at, (size_t)p.dx_parts * round_up(N * D, 8) * 4);
+        if (p.dw_splits > 1) l.pw = take(at, (size_t)p.dw_splits * round_up(p.piece * D, 8) * 4);
+    } else {
+        l.part = take(at, (size_t)(p.tiles * p.rows) * 8);
+        l.tl = take(at, (size_t)p.rows * 4);
+    }
+    l.bytes = at;
+    return l;
+}
+
+// The operand of a caller's matrix, packed into the scratch where it has to be.
+template <typename S>
+cudaError_t operand(const void* src, int64_t rows, int64_t D, void* scratch, Operand* o, cudaStream_t s) {
+    constexpr int P = sizeof(S) == 4 ? 3 : 1;
+    *o = Operand{(const __nv_bfloat16*)src, rows, D, D, rows * D, P};
+    if (!packed(sizeof(S) == 4 ? 0 : 1, src, D)) return cudaSuccess;
+    const int64_t ld = round_up(D, 8);
+    const int64_t blocks = std::min<int64_t>((rows * ld + 255) / 256, (int64_t)sm_count() * 16);
+    k_lce_pack<S, P><<<(unsigned)blocks, 256, 0, s>>>((const S*)src, (__nv_bfloat16*)scratch, rows, D, ld);
+    *o = Operand{(const __nv_bfloat16*)scratch, rows, D, ld, rows * ld, P};
+    return cudaGetLastError();
+}
+
+#define LCE_TRY(x)                            \
+    do {                                      \
+        const cudaError_t e_ = (x);           \
+        if (e_ != cudaSuccess) return e_;     \
+    } while (0)
 
 template <typename S>
 cudaError_t lce_fwd_t(const void* x, const void* w, const int64_t* target, int64_t ignore, float* loss, float* lse,
-                      int64_t N, int64_t V, int64_t D, const LcePlan& pl, void* scratch, uint32_t* err, cudaStream_t s) {
-    float2* part = (float2*)scratch;
-    float* tl = (float*)(part + pl.tiles * pl.rows);
+                      int64_t N, int64_t V, int64_t D, const LcePlan& pl, char* sc, uint32_t* err, cudaStream_t s) {
+    const Layout l = layout(sizeof(S) == 4 ? 0 : 1, x, w, N, V, D, pl, false);
+    Operand ox, ow;
+    LCE_TRY(operand<S>(x, N, D, sc + l.x, &ox, s));
+    LCE_TRY(operand<S>(w, V, D, sc + l.w, &ow, s));
+    float2* part = (float2*)(sc + l.part);
+    float* tl = (float*)(sc + l.tl);
     for (int64_t r = 0; r < N; r += pl.rows) {
-        const int64_t n = N - r < pl.rows ? N - r : pl.rows;
-        k_lce_stats<S><<<dim3((unsigned)pl.tiles, (unsigned)((n + kT - 1) / kT)), 256, 0, s>>>(
-            (const S*)x + r * D, (const S*)w, target + r, part, tl, n, V, D);
-        k_lce_join<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(part, pl.tiles, tl, target + r, ignore, loss + r, lse + r,
-                                                               n, V, err);
+        const int64_t n = std::min(pl.rows, N - r);
+        Operand a = ox;
+        a.p += r * a.ld;
+        a.rows = n;
+        LCE_TRY(mm_run(a, ow, mm_shape(n, V, D, ox.planes, false, false, false, 1),
+                       StatsEpi{part, tl, target + r, n, V}, err, s));
+        k_lce_join<<<(unsigned)((n + 31) / 32), dim3(32, 32), 0, s>>>(part, pl.tiles, tl, target + r, ignore, loss + r,
+                                                                     lse + r, n, V, err);
+        LCE_TRY(cudaGetLastError());
     }
+    return cudaSuccess;
+}
+
+template <typename S>
+cudaError_t sum_parts(const float* part, int64_t parts, int64_t pitch, int64_t n, const uint32_t* top, S* out,
+                      cudaStream_t s) {
+    const bool vec = ((uintptr_t)out & (4 * sizeof(S) - 1)) == 0;
+    const int64_t blocks = std::min<int64_t>((n / (vec ? 4 : 1) + 255) / 256 + 1, (int64_t)sm_count() * 8);
+    k_lce_sum<S><<<(unsigned)blocks, 256, 0, s>>>(part, parts, pitch, n, top, out, vec);
     return cudaGetLastError();
 }
 
 template <typename S>
 cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64_t ignore, const float* lse,
-                      const float* dloss, void* dx, void* dw, int64_t N, int64_t V, int64_t D, const LcePlan& pl,
-                      void* scratch, cudaStream_t s) {
-    float* g = (float*)scratch;
-    float* acc = g + N * pl.piece;
+                      const float* dloss, void* dx, void* dw, int64_t N, int64_t V, int64_t D, const LcePlan& pl, char* sc,
+                      uint32_t* err, cudaStream_t s) {
+    constexpr int P = sizeof(S) == 4 ? 3 : 1;
+    const Layout l = layout(sizeof(S) == 4 ? 0 : 1, x, w, N, V, D, pl, true);
+    uint32_t* top = (uint32_t*)(sc + l.top);
+    LCE_TRY(cudaMemsetAsync(top, 0, 4, s));
+    k_lce_scale<<<(unsigned)std::min<int64_t>((N + 255) / 256, sm_count()), 256, 0, s>>>(dloss, target, ignore, N, V, top);
+    LCE_TRY(cudaGetLastError());
+    Operand ox, ow;
+    LCE_TRY(operand<S>(x, N, D, sc + l.x, &ox, s));
+    LCE_TRY(operand<S>(w, V, D, sc + l.w, &ow, s));
+    __nv_bfloat16* g = (__nv_bfloat16*)(sc + l.g);
+    float* px = (float*)(sc + l.px);
+    float* pw = (float*)(sc + l.pw);
+    const int64_t xpitch = round_up(N * D, 8), wpitch = round_up(pl.piece * D, 8);
+    const bool wide_s = D * (int64_t)sizeof(S) % 32 == 0, wide_f = D % 8 == 0;
+    int64_t part = 0;
     for (int64_t v0 = 0; v0 < V; v0 += pl.piece) {
-        const int64_t vc = V - v0 < pl.piece ? V - v0 : pl.piece;
-        const unsigned tn = (unsigned)((N + kT - 1) / kT), tv = (unsigned)((vc + kT - 1) / kT),
-                       td = (unsigned)((D + kT - 1) / kT);
-        k_lce_grad<S><<<dim3(tv, tn), 256, 0, s>>>((const S*)x, (const S*)w, target, ignore, lse, dloss, g, N, v0, vc, V, D);
-        k_lce_dx<S><<<dim3(td, tn), 256, 0, s>>>(g, (const S*)w, acc, (S*)dx, N, v0, vc, D, v0 == 0, v0 + vc == V);
-        k_lce_dw<S><<<dim3(td, tv), 256, 0, s>>>(g, (const S*)x, (S*)dw, N, v0, vc, D);
+        const int64_t vc = std::min(pl.piece, V - v0), pitch = round_up(vc, 16);
+        Operand wp = ow;
+        wp.p += v0 * ow.ld;
+        wp.rows = vc;
+        const Operand og{g, N, vc, pitch, N * pitch, P};
+        LCE_TRY(mm_run(ox, wp, mm_shape(N, vc, D, P, false, false, false, 1),
+                       GradEpi<P>{g, pitch, N * pitch, lse, dloss, target, top, ignore, N, v0, vc, V}, err, s));
+        // dx: rows of x by features, over the words of the piece
+        const Shape sx = mm_shape(N, D, vc, P, false, true, true, pl.dx_splits);
+        const bool dx_direct = pl.dx_parts == 1;
+        LCE_TRY(mm_run(og, wp, sx,
+                       OutEpi<S>{dx_direct ? (S*)dx : nullptr, px + part * xpitch, xpitch, top, N, D,
+                                 dx_direct ? wide_s && ((uintptr_t)dx & 31) == 0 : wide_f},
+                       err, s));
+        part += sx.splits;
+        // dw: words of the piece by features, over the rows of x
+        const Shape sw = mm_shape(vc, D, N, P, true, true, true, pl.dw_splits);
+        const bool dw_direct = pl.dw_splits == 1;
+        S* dwp = (S*)dw + v0 * D;
+        LCE_TRY(mm_run(og, ox, sw,
+                       OutEpi<S>{dw_direct ? dwp : nullptr, pw, wpitch, top, vc, D,
+                                 dw_direct ? wide_s && ((uintptr_t)dwp & 31) == 0 : wide_f},
+                       err, s));
+        if (!dw_direct) LCE_TRY(sum_parts<S>(pw, sw.splits, wpitch, vc * D, top, dwp, s));
     }
-    return cudaGetLastError();
+    if (pl.dx_parts > 1) LCE_TRY(sum_parts<S>(px, part, xpitch, N * D, top, (S*)dx, s));
+    return cudaSuccess;
 }
 
 }  // namespace
 
-LcePlan lce_plan(int dtype, int64_t N, int64_t V, int64_t D) {
-    (void)dtype;
-    LcePlan p;
-    p.tiles = (V + kT - 1) / kT;
-    p.rows = N < 16384 ? N : 16384;
-    p.piece = V < 8192 ? V : 8192;
-    p.fwd_bytes = (size_t)(p.tiles * p.rows) * 8 + (size_t)p.rows * 4;
-    p.bwd_bytes = (size_t)(N * p.piece) * 4 + (size_t)(N * D) * 4;
+LcePlan lce_plan(int dtype, const void* x, const void* w, int64_t N, int64_t V, int64_t D, bool bwd) {
+    LcePlan p{};
+    const int planes = dtype == 0 ? 3 : 1;
+    if (!bwd) {
+        p.tiles = (V + kTile - 1) / kTile;
+        p.rows = std::min<int64_t>(N, 16384);
+    } else {
+        p.piece = std::max<int64_t>(kPieceBytes / (N * 2 * planes) / kTile, 1) * kTile;
+        if (p.piece >= V) p.piece = V;
+        p.dx_splits = mm_splits(N, D, p.piece, planes);
+        p.dw_splits = mm_splits(p.piece, D, N, planes);
+        p.dx_parts = 0;
+        for (int64_t v0 = 0; v0 < V; v0 += p.piece)
+            p.dx_parts += mm_shape(N, D, std::min(p.piece, V - v0), planes, false, true, true, p.dx_splits).splits;
+    }
+    p.bytes = layout(dtype, x, w, N, V, D, p, bwd).bytes;
     return p;
 }
 
 cudaError_t launch_lce_fwd(int dtype, const void* x, const void* w, const int64_t* target, int64_t ignore, float* loss,
                            float* lse, int64_t N, int64_t V, int64_t D, const LcePlan& pl, void* scratch, uint32_t* err,
                            cudaStream_t s) {
-    return dtype == 0 ? lce_fwd_t<float>(x, w, target, ignore, loss, lse, N, V, D, pl, scratch, err, s)
-                      : lce_fwd_t<__nv_bfloat16>(x, w, target, ignore, loss, lse, N, V, D, pl, scratch, err, s);
+    return dtype == 0 ? lce_fwd_t<float>(x, w, target, ignore, loss, lse, N, V, D, pl, (char*)scratch, err, s)
+                      : lce_fwd_t<__nv_bfloat16>(x, w, target, ignore, loss, lse, N, V, D, pl, (char*)scratch, err, s);
 }
 
 cudaError_t launch_lce_bwd(int dtype, const void* x, const void* w, const int64_t* target, int64_t ignore,
                            const float* lse, const float* dloss, void* dx, void* dw, int64_t N, int64_t V, int64_t D,
                            const LcePlan& pl, void* scratch, uint32_t* err, cudaStream_t s) {
-    (void)err;
-    return dtype == 0 ? lce_bwd_t<float>(x, w, target, ignore, lse, dloss, dx, dw, N, V, D, pl, scratch, s)
-                      : lce_bwd_t<__nv_bfloat16>(x, w, target, ignore, lse, dloss, dx, dw, N, V, D, pl, scratch, s);
+    return dtype == 0
+               ? lce_bwd_t<float>(x, w, target, ignore, lse, dloss, dx, dw, N, V, D, pl, (char*)scratch, err, s)
+               : lce_bwd_t<__nv_bfloat16>(x, w, target, ignore, lse, dloss, dx, dw, N, V, D, pl, (char*)scratch, err, s);
 }
 
 }  // namespace lrs

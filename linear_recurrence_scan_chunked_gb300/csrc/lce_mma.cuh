@@ -1,0 +1,308 @@
+// lce_mma.cuh -- the matrix products of the cross entropy on the tensor cores
+// (tcgen05.mma, bf16 operands, fp32 accumulators in TMEM).
+//
+// One kernel, three products: logits x W^T, g W and g^T x.  A pair of CTAs
+// (cta_group::2, a cluster of two on neighbouring SMs) owns a 256 x 256 tile of
+// the result: each holds 128 rows of A, half of B and the accumulators of its
+// 128 rows, so an operand byte in shared memory feeds twice the arithmetic of a
+// single CTA's tile.  Per CTA: a producer thread keeps a ring of kStages k-blocks
+// of 64 in flight by TMA (128-byte swizzle), one thread of the pair's first CTA
+// issues the MMAs, and four warps read finished accumulators back and run the
+// epilogue while the next tile accumulates in the other half of TMEM.
+//
+// Operands are [rows][cols] matrices of bf16 planes: one plane for bf16 data,
+// three for fp32 data split as a = a1 + a2 + a3 (8 bits of mantissa each), whose
+// six leading products a_i b_j, i + j <= 4, give the fp32 product to 2^-24.  An
+// operand is K-major when k runs along its rows' contiguous axis, MN-major when
+// it runs across them; both come out of TMA in the layouts that the matrix
+// descriptors name, so no product needs a transposed copy.
+//
+// Every wait is bounded: one that runs out records LR_ERR_TIMEOUT, and every role
+// then leaves its loop, the pair meets, lets its copies land and frees its TMEM.
+#pragma once
+
+#include "lr_tma.cuh"
+
+namespace lrs {
+namespace mm {
+
+constexpr int kTile = 256;       // rows and columns of a pair's tile
+constexpr int kHalf = 128;       // rows of A and of B that a CTA holds
+constexpr int kBlockK = 64;      // k-block: 128 bytes of bf16, the swizzle's width
+constexpr int kStages = 6;
+constexpr int kOperand = kHalf * kBlockK * 2;  // 16 KB: one operand of a stage
+constexpr int kStageBytes = 2 * kOperand;
+constexpr int kThreads = 192;    // producer warp, MMA warp, 4 epilogue warps
+constexpr int kSmem = kStages * kStageBytes + 1024;  // + alignment to 1024
+
+// What the products share: the tile grid and the k loop.
+struct Shape {
+    uint32_t tm, tn;        // tiles along the result's rows and columns
+    uint32_t splits;        // parts of the k loop, each a tile of its own
+    uint32_t kb;            // k-blocks of the whole loop (of one plane pair)
+    uint32_t kb_split;      // k-blocks of a part
+    uint32_t pairs;         // plane pairs: 1 or 6
+    uint32_t n_fast;        // neighbouring tiles along the columns (else along the rows)
+    uint32_t a_mn, b_mn;    // MN-major operands
+};
+
+// Both CTAs of the pair, all threads.
+__device__ __forceinline__ void pair_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) { return cluster_map(p, rank); }
+
+// 3-D box {x, y, plane} into this CTA's shared memory; the bytes count on the
+// barrier at cluster address `bar` (the pair's first CTA's).
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* m, int32_t x, int32_t y, int32_t z,
+                                              uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* b, uint32_t parity, const uint32_t* err) {
+    if (mbar_try_wait_cluster(b, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait_cluster(b, parity)) return true;
+        if ((n & 255u) == 0) {
+            if (globaltimer_ns() - t0 > kMbarLimitNs) return false;
+            if (ld_relaxed_u32(err) & ERRBIT_TIMEOUT) return false;
+        }
+    }
+}
+
+// ---- tcgen05
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// The barrier at this offset in both CTAs completes when the MMAs issued so far have.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+// 32 columns of this warp's 32 accumulator rows.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+        "%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle.  K-major: rows of 128 bytes,
+// groups of 8 rows 1024 bytes apart.  MN-major: blocks of 64 elements (128 bytes)
+// by 64 k-rows, groups of 8 k-rows 1024 bytes apart, blocks 8192 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn) {
+    const uint64_t lead = mn ? 8192 >> 4 : 1;
+    return (uint64_t)((addr >> 4) & 0x3fff) | lead << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+// bf16 x bf16 -> fp32, 256 x 256.
+__device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 | (uint32_t)(kTile >> 3) << 17 |
+           (uint32_t)(kTile >> 4) << 24;
+}
+
+// The plane pairs of fp32 data, smallest products first.
+__device__ __forceinline__ int pair_a(uint32_t p, uint32_t pairs) { return pairs == 1 ? 0 : (0x001012 >> (4 * p)) & 3; }
+__device__ __forceinline__ int pair_b(uint32_t p, uint32_t pairs) { return pairs == 1 ? 0 : (0x010210 >> (4 * p)) & 3; }
+
+struct Tile {
+    uint32_t m, n, split;
+};
+__device__ __forceinline__ Tile tile_of(const Shape& s, uint32_t t) {
+    Tile r;
+    const uint32_t per = s.tm * s.tn;
+    r.split = t / per;
+    t -= r.split * per;
+    if (s.n_fast) {
+        r.m = t / s.tn;
+        r.n = t - r.m * s.tn;
+    } else {
+        r.n = t / s.tm;
+        r.m = t - r.n * s.tm;
+    }
+    return r;
+}
+
+// Epilogue: struct with  __device__ void tile(const Tile&, int row /* in the
+// tile, 0 .. 255 */, Cols) const, where Cols(c, v) loads columns 32c .. 32c + 31 of
+// the row into v[32]; all lanes of a warp call it together.
+template <class Epi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_mm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Shape sh,
+         const Epi epi, uint32_t* err) {
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2];
+    __shared__ uint32_t tmem_base;
+    unsigned char* ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const uint32_t pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+    const uint32_t n_tiles = sh.tm * sh.tn * sh.splits;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 8);  // 4 epilogue warps of each CTA
+        }
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc(&tmem_base, 512);
+    fence_before();
+    __syncthreads();
+    pair_sync();
+    fence_after();
+    const uint32_t tmem = tmem_base;
+
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {  // producer
+            uint32_t it = 0;
+            for (uint32_t t = pair; t < n_tiles && ok; t += n_pairs) {
+                const Tile tl = tile_of(sh, t);
+                const int32_t m0 = (int32_t)(tl.m * kTile + rank * kHalf), n0 = (int32_t)(tl.n * kTile + rank * kHalf);
+                const uint32_t k0 = tl.split * sh.kb_split;
+                const uint32_t k1 = k0 + sh.kb_split < sh.kb ? k0 + sh.kb_split : sh.kb;
+                for (uint32_t p = 0; p < sh.pairs && ok; ++p) {
+                    const int pa = pair_a(p, sh.pairs), pb = pair_b(p, sh.pairs);
+                    for (uint32_t k = k0; k < k1; ++k, ++it) {
+                        const uint32_t st = it % kStages;
+                        if (it >= kStages && !wait_cluster(&empty[st], (it / kStages - 1) & 1, err)) {
+                            ok = false;
+                            break;
+                        }
+                        if (rank == 0) mbar_arrive_tx(&full[st], 2 * kStageBytes);
+                        const uint32_t bar = cluster_addr(&full[st], 0);
+                        unsigned char* a = ring + st * kStageBytes;
+                        unsigned char* b = a + kOperand;
+                        const int32_t kk = (int32_t)(k * kBlockK);
+                        if (sh.a_mn) {
+                            tma_load_pair(a, &map_a, m0, kk, pa, bar);
+                            tma_load_pair(a + kOperand / 2, &map_a, m0 + 64, kk, pa, bar);
+                        } else {
+                            tma_load_pair(a, &map_a, kk, m0, pa, bar);
+                        }
+                        if (sh.b_mn) {
+                            tma_load_pair(b, &map_b, n0, kk, pb, bar);
+                            tma_load_pair(b + kOperand / 2, &map_b, n0 + 64, kk, pb, bar);
+                        } else {
+                            tma_load_pair(b, &map_b, kk, n0, pb, bar);
+                        }
+                    }
+                }
+            }
+            // the MMAs have read every stage (and every arrival on this CTA's
+            // barriers has landed) before the CTA ends
+            const uint32_t tail = it < kStages ? it : kStages;
+            for (uint32_t i = it - tail; i < it && ok; ++i)
+                ok = wait_cluster(&empty[i % kStages], (i / kStages) & 1, err);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {  // MMA issue
+            const uint32_t idesc = instr_desc(sh.a_mn, sh.b_mn);
+            const uint32_t step_a = sh.a_mn ? 2048 >> 4 : 32 >> 4, step_b = sh.b_mn ? 2048 >> 4 : 32 >> 4;
+            uint32_t it = 0, seq = 0;
+            for (uint32_t t = pair; t < n_tiles && ok; t += n_pairs, ++seq) {
+                const Tile tl = tile_of(sh, t);
+                const uint32_t k0 = tl.split * sh.kb_split;
+                const uint32_t k1 = k0 + sh.kb_split < sh.kb ? k0 + sh.kb_split : sh.kb;
+                const uint32_t buf = seq & 1;
+                if (seq >= 2 && !wait_cluster(&tempty[buf], (seq / 2 - 1) & 1, err)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                const uint32_t d = tmem + buf * kTile;
+                const uint32_t steps = (k1 - k0) * sh.pairs;
+                for (uint32_t k = 0; k < steps; ++k, ++it) {
+                    const uint32_t st = it % kStages;
+                    if (!wait_cluster(&full[st], (it / kStages) & 1, err)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+                    const uint32_t a = smem_u32(ring + st * kStageBytes);
+                    const uint64_t da = smem_desc(a, sh.a_mn), db = smem_desc(a + kOperand, sh.b_mn);
+#pragma unroll
+                    for (uint32_t j = 0; j < kBlockK / 16; ++j)
+                        mma(d, da + j * step_a, db + j * step_b, idesc, k > 0 || j > 0);
+                    commit_pair(&empty[st]);
+                }
+                if (ok) commit_pair(&tfull[buf]);
+            }
+        }
+    } else {  // epilogue
+        const int quarter = warp & 3;
+        const int row = (int)rank * kHalf + quarter * 32 + lane;
+        uint32_t seq = 0;
+        for (uint32_t t = pair; t < n_tiles; t += n_pairs, ++seq) {
+            const uint32_t buf = seq & 1;
+            ok = wait_cluster(&tfull[buf], (seq / 2) & 1, err);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            fence_after();
+            const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile;
+            epi.tile(tile_of(sh, t), row, [&](int c, float (&v)[32]) {
+                __syncwarp();  // the load is one instruction of the whole warp
+                tmem_load32(base + c * 32, v);
+            });
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(cluster_addr(&tempty[buf], 0));
+        }
+    }
+    if (!ok) {
+        atomicOr(err, ERRBIT_TIMEOUT);
+        // let what is in flight land before the shared memory and TMEM go
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(10000);
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    pair_sync();  // the peer's arrivals on this CTA's barriers have landed
+    fence_after();
+    if (warp == 1) tmem_free(tmem, 512);
+}
+
+}  // namespace mm
+}  // namespace lrs

@@ -19,12 +19,11 @@ namespace lrs {
 
 // cuTensorMapEncodeTiled, looked up once through the runtime (no link-time
 // dependency on the driver library).
-bool tma_encode(CUtensorMap* m, const void* ptr, int dtype, int64_t T, int64_t C, int box_c,
-                int box_rows) {
-    typedef CUresult (*encode_fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+typedef CUresult (*encode_fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                              CUtensorMapFloatOOBfill);
+static encode_fn tma_encoder() {
     static encode_fn fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -35,6 +34,12 @@ bool tma_encode(CUtensorMap* m, const void* ptr, int dtype, int64_t T, int64_t C
             q == cudaDriverEntryPointSuccess)
             fn = (encode_fn)f;
     });
+    return fn;
+}
+
+bool tma_encode(CUtensorMap* m, const void* ptr, int dtype, int64_t T, int64_t C, int box_c,
+                int box_rows) {
+    const encode_fn fn = tma_encoder();
     if (!fn) return false;
     const size_t es = dtype == 1 ? 2 : 4;
     const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)T};
@@ -45,6 +50,20 @@ bool tma_encode(CUtensorMap* m, const void* ptr, int dtype, int64_t T, int64_t C
               const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool tma_encode_planes(CUtensorMap* m, const void* ptr, int64_t cols, int64_t rows, int64_t planes,
+                       int64_t ld, int64_t plane, int box_c, int box_rows) {
+    const encode_fn fn = tma_encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+    // one plane: its stride is never used, but has to be a multiple of 16 bytes
+    const cuuint64_t strides[2] = {(cuuint64_t)(ld * 2), (cuuint64_t)((planes == 1 ? ld : plane) * 2)};
+    const cuuint32_t box[3] = {(cuuint32_t)box_c, (cuuint32_t)box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Retire the current epoch of a workspace (the ticket word's high half):
@@ -654,8 +673,8 @@ int lce_fwd(const void* x, const void* w, const int64_t* target, int64_t ignore,
     TRY(get_ws(&ws));
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
-    const LcePlan pl = lce_plan(dtype, N, V, D);
-    TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.fwd_bytes, false, true));
+    const LcePlan pl = lce_plan(dtype, x, w, N, V, D, false);
+    TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.bytes, false, true));
     CK(launch_lce_fwd(dtype, x, w, target, ignore, loss, lse, N, V, D, pl, ws->lce, ws->words + kWordErr, s));
     return lv.done();
 }
@@ -680,8 +699,8 @@ int lce_bwd(const void* x, const void* w, const int64_t* target, int64_t ignore,
     TRY(get_ws(&ws));
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
-    const LcePlan pl = lce_plan(dtype, N, V, D);
-    TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.bwd_bytes, false, true));
+    const LcePlan pl = lce_plan(dtype, x, w, N, V, D, true);
+    TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.bytes, false, true));
     CK(launch_lce_bwd(dtype, x, w, target, ignore, lse, dloss, dx, dw, N, V, D, pl, ws->lce, ws->words + kWordErr, s));
     return lv.done();
 }

@@ -446,13 +446,15 @@ cudaError_t launch_adamw(AdamKind kind, int gdtype, const AdamTensor* t, int64_t
 
 // Softmax cross entropy of x W^T ([N, D] by [V, D]), in pieces.
 struct LcePlan {
-    int64_t tiles;     // forward: vocabulary tiles (a pair of statistics each, per row)
-    int64_t rows;      // forward: rows per round
-    int64_t piece;     // backward: vocabulary rows per piece
-    size_t fwd_bytes;  // scratch of either direction
-    size_t bwd_bytes;
+    int64_t tiles;      // forward: vocabulary tiles (a pair of statistics each, per row)
+    int64_t rows;       // forward: rows per round
+    int64_t piece;      // backward: vocabulary rows per piece
+    int64_t dx_splits;  // backward: parts of the k loops
+    int64_t dw_splits;
+    int64_t dx_parts;   // parts of dx over all pieces
+    size_t bytes;       // scratch
 };
-LcePlan lce_plan(int dtype, int64_t N, int64_t V, int64_t D);
+LcePlan lce_plan(int dtype, const void* x, const void* w, int64_t N, int64_t V, int64_t D, bool bwd);
 cudaError_t launch_lce_fwd(int dtype, const void* x, const void* w, const int64_t* target, int64_t ignore, float* loss,
                            float* lse, int64_t N, int64_t V, int64_t D, const LcePlan& pl, void* scratch, uint32_t* err,
                            cudaStream_t s);

@@ -46,6 +46,12 @@ struct TmaDesc {
 bool tma_encode(CUtensorMap* m, const void* ptr, int dtype, int64_t T, int64_t C, int box_c,
                 int box_rows);
 
+// Host: 3-D tensor map over bf16 planes [planes][rows][ld] (the first `cols` of
+// each row; ld and plane in elements, multiples of 8) with a box of 64 columns --
+// 128 bytes, swizzled -- by box_rows rows of one plane, zero fill outside.
+bool tma_encode_planes(CUtensorMap* m, const void* ptr, int64_t cols, int64_t rows, int64_t planes,
+                       int64_t ld, int64_t plane, int box_c, int box_rows);
+
 template <class Op>
 __host__ __device__ constexpr uint32_t tma_arr_bytes(int k) {
     return (uint32_t)(Op::NW * Op::R + Op::tma_extra(k)) * 32u * Op::VEC *

@@ -6,7 +6,7 @@
 //   g[n][v] = (exp(l[n][v] - lse[n]) - [v = target[n]]) dloss[n],
 //   dx = g W,   dW = g^T x.
 //
-// Forward: the epilogue of the product x W^T reduces each 256-column tile of
+// Forward: the epilogue of the product x W^T reduces each 128 columns of
 // logits to a pair per row, a power-of-two bound 2^M of its exponentials and
 // their sum relative to it, and a second kernel joins the tiles' pairs.  Backward:
 // for a piece of the vocabulary the product runs again, its epilogue writes g
@@ -90,44 +90,57 @@ __device__ __forceinline__ float pick32(const float (&v)[32], int j) {
 // Forward: the pair of a tile and a row.  With M = ceil(max l log2 e), the sum
 // of 2^(l log2 e - M): M is an integer, so its subtraction inside the
 // multiply-add rounds nothing but the result, and no common error enters the sum.
+template <bool CHUNKED>
 struct StatsEpi {
-    float2* part;           // [tiles][rows]
+    static constexpr bool kChunked = CHUNKED;
+    float2* part;           // [half tiles][rows]
     float* tl;              // the targets' logits
     const int64_t* target;
     int64_t rows, V;
-    template <class Cols>
-    __device__ void tile(const Tile& t, int row, Cols cols) const {
-        const int64_t n = (int64_t)t.m * kTile + row;
-        const int64_t v0 = (int64_t)t.n * kTile;
-        const int width = (int)(V - v0 < kTile ? V - v0 : kTile);
-        const int64_t tg = n < rows ? __ldg(target + n) - v0 : -1;
-        const int at = tg >= 0 && tg < width ? (int)tg : -1;
-        float M = -INFINITY, s = 0.f;
-        for (int c = 0; c * 32 < width; ++c) {
-            float v[32];
-            cols(c, v);
-            if (width < c * 32 + 32) {
+    struct Row {
+        int64_t n, slot;
+        int width, at;
+        float M, s;
+    };
+    __device__ int width(const Tile& t, int half) const {
+        const int64_t w = V - (int64_t)t.n * kTile - half * mm::kHalf;
+        return (int)(w < mm::kHalf ? w : mm::kHalf);
+    }
+    __device__ Row begin(const Tile& t, int row, int half) const {
+        Row r;
+        r.n = (int64_t)t.m * kTile + row;
+        r.slot = (int64_t)t.n * 2 + half;
+        r.width = width(t, half);
+        const int64_t tg = r.n < rows ? __ldg(target + r.n) - r.slot * mm::kHalf : -1;
+        r.at = tg >= 0 && tg < r.width ? (int)tg : -1;
+        r.M = -INFINITY;
+        r.s = 0.f;
+        return r;
+    }
+    __device__ void cols(Row& r, int c, float (&v)[32]) const {
+        if (r.width < c * 32 + 32) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = c * 32 + i < width ? v[i] : -INFINITY;
-            }
-            if (__any_sync(0xffffffffu, at >> 5 == c)) {
-                const float x = pick32(v, at & 31);
-                if (at >> 5 == c) tl[n] = x;
-            }
-            float mx[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-            for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
-            const float m = ceilf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e);
-            if (m > M) {
-                s *= ex2_ftz(M - m);  // the first time 2^-inf = 0
-                M = m;
-            }
-            float e[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 32; ++i) e[i & 3] += ex2_ftz(fmaf(v[i], kLog2e, -M));
-            s += (e[0] + e[1]) + (e[2] + e[3]);
+            for (int i = 0; i < 32; ++i) v[i] = c * 32 + i < r.width ? v[i] : -INFINITY;
         }
-        if (n < rows) part[(int64_t)t.n * rows + n] = make_float2(M, s);
+        if (__any_sync(0xffffffffu, r.at >> 5 == c)) {
+            const float x = pick32(v, r.at & 31);
+            if (r.at >> 5 == c) tl[r.n] = x;
+        }
+        float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+        const float m = ceilf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e);
+        if (m > r.M) {
+            r.s *= ex2_ftz(r.M - m);  // the first time 2^-inf = 0
+            r.M = m;
+        }
+        float e[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) e[i & 3] += ex2_ftz(fmaf(v[i], kLog2e, -r.M));
+        r.s += (e[0] + e[1]) + (e[2] + e[3]);
+    }
+    __device__ void end(Row& r) const {
+        if (r.n < rows && r.width > 0) part[r.slot * rows + r.n] = make_float2(r.M, r.s);
     }
 };
 
@@ -184,6 +197,7 @@ __device__ __forceinline__ float scale_of(const uint32_t* top) {
 // Backward: g / max|dloss| of a tile, in P bf16 planes.
 template <int P>
 struct GradEpi {
+    static constexpr bool kChunked = P > 1;
     __nv_bfloat16* g;  // [P][rows][pitch]
     int64_t pitch;     // a multiple of 16
     int64_t plane;     // elements of a plane
@@ -192,83 +206,103 @@ struct GradEpi {
     const int64_t* target;
     const uint32_t* top;
     int64_t ignore, rows, v0, vc, V;
-    template <class Cols>
-    __device__ void tile(const Tile& t, int row, Cols cols) const {
-        const int64_t n = (int64_t)t.m * kTile + row;
-        const int64_t c0 = (int64_t)t.n * kTile;
-        const int width = (int)(vc - c0 < kTile ? vc - c0 : kTile);
-        float f = 0.f, ds = 0.f, hi = INFINITY, z = 0.f;  // a row that does not count: 2^-inf = 0
-        int at = -1;
-        if (n < rows) {
-            const int64_t tg = __ldg(target + n);
+    struct Row {
+        int64_t n;
+        __nv_bfloat16* out;
+        int width, at;
+        float f, ds, hi, z;
+    };
+    __device__ int width(const Tile& t, int half) const {
+        const int64_t w = vc - (int64_t)t.n * kTile - half * mm::kHalf;
+        return (int)(w < mm::kHalf ? w : mm::kHalf);
+    }
+    __device__ Row begin(const Tile& t, int row, int half) const {
+        Row r;
+        r.n = (int64_t)t.m * kTile + row;
+        const int64_t c0 = (int64_t)t.n * kTile + half * mm::kHalf;
+        r.width = width(t, half);
+        r.out = g + r.n * pitch + c0;
+        r.f = r.ds = r.z = 0.f;
+        r.hi = INFINITY;  // a row that does not count: 2^-inf = 0
+        r.at = -1;
+        if (r.n < rows) {
+            const int64_t tg = __ldg(target + r.n);
             if (tg != ignore && tg >= 0 && tg < V) {
-                ds = __fdiv_rn(__ldg(dloss + n), scale_of(top));
-                z = __ldg(lse + n);
+                r.ds = __fdiv_rn(__ldg(dloss + r.n), scale_of(top));
+                r.z = __ldg(lse + r.n);
                 // lse log2 e = hi + lo: 2^-lo goes into the row's factor, so that
                 // hi's rounding is no common error of the row
-                hi = z * kLog2e;
-                f = ds * ex2_ftz(fmaf(-z, kLog2e, hi));
-                const int64_t r = tg - v0 - c0;
-                if (r >= 0 && r < width) at = (int)r;
+                r.hi = r.z * kLog2e;
+                r.f = r.ds * ex2_ftz(fmaf(-r.z, kLog2e, r.hi));
+                const int64_t q = tg - v0 - c0;
+                if (q >= 0 && q < r.width) r.at = (int)q;
             }
         }
-        __nv_bfloat16* out = g + n * pitch + c0;
-        for (int c = 0; c * 32 < width; ++c) {
-            float v[32];
-            cols(c, v);
-            const bool mine = at >> 5 == c;
-            float gt = 0.f;
-            // the target's p - 1 without cancellation where p is near 1
-            if (__any_sync(0xffffffffu, mine)) gt = expm1f(pick32(v, at & 31) - z) * ds;
+        return r;
+    }
+    __device__ void cols(Row& r, int c, float (&v)[32]) const {
+        const bool mine = r.at >> 5 == c, any = __any_sync(0xffffffffu, mine);
+        float gt = 0.f;
+        // the target's p - 1 without cancellation where p is near 1
+        if (any) gt = expm1f(pick32(v, r.at & 31) - r.z) * r.ds;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = ex2_ftz(fmaf(v[i], kLog2e, -hi)) * f;
-            if (__any_sync(0xffffffffu, mine)) {
+        for (int i = 0; i < 32; ++i) v[i] = ex2_ftz(fmaf(v[i], kLog2e, -r.hi)) * r.f;
+        if (any) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = mine && i == (at & 31) ? gt : v[i];
-            }
-            if (n < rows) {
+            for (int i = 0; i < 32; ++i) v[i] = mine && i == (r.at & 31) ? gt : v[i];
+        }
+        if (r.n >= rows) return;
 #pragma unroll
-                for (int p = 0; p < P; ++p) {
-                    st_row32(out + p * plane + c * 32, v, width - c * 32, true);
-                    if (p + 1 < P) {
+        for (int p = 0; p < P; ++p) {
+            st_row32(r.out + p * plane + c * 32, v, r.width - c * 32, true);
+            if (p + 1 < P) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] -= bf_lo(bf_bits(v[i]));
-                    }
-                }
+                for (int i = 0; i < 32; ++i) v[i] -= bf_lo(bf_bits(v[i]));
             }
         }
     }
+    __device__ void end(Row&) const {}
 };
 
 // A product's tile: rounded to the result (scaled by max|dloss|), or one part of
 // the k loop, fp32.
 template <typename S>
 struct OutEpi {
+    static constexpr bool kChunked = sizeof(S) == 4;
     S* out;         // nullptr: parts
     float* part;    // [splits][rows x cols]
     int64_t pitch;  // elements of a part
     const uint32_t* top;
     int64_t rows, cols_n;
     bool wide;      // rows of the destination are 32-byte aligned
-    template <class Cols>
-    __device__ void tile(const Tile& t, int row, Cols cols) const {
-        const int64_t m = (int64_t)t.m * kTile + row;
-        const int64_t c0 = (int64_t)t.n * kTile;
-        const int64_t width = cols_n - c0 < kTile ? cols_n - c0 : kTile;
-        const float a = out ? scale_of(top) : 1.f;
-        for (int c = 0; c * 32 < width; ++c) {
-            float v[32];
-            cols(c, v);
-            if (m >= rows) continue;
-            if (out) {
+    struct Row {
+        int64_t m, at;
+        int width;
+        float a;
+    };
+    __device__ int width(const Tile& t, int half) const {
+        const int64_t w = cols_n - (int64_t)t.n * kTile - half * mm::kHalf;
+        return (int)(w < mm::kHalf ? w : mm::kHalf);
+    }
+    __device__ Row begin(const Tile& t, int row, int half) const {
+        Row r;
+        r.m = (int64_t)t.m * kTile + row;
+        r.width = width(t, half);
+        r.at = (out ? 0 : t.split * pitch) + r.m * cols_n + (int64_t)t.n * kTile + half * mm::kHalf;
+        r.a = out ? scale_of(top) : 1.f;
+        return r;
+    }
+    __device__ void cols(Row& r, int c, float (&v)[32]) const {
+        if (r.m >= rows) return;
+        if (out) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= a;
-                st_row32(out + m * cols_n + c0 + c * 32, v, width - c * 32, wide);
-            } else {
-                st_row32(part + t.split * pitch + m * cols_n + c0 + c * 32, v, width - c * 32, wide);
-            }
+            for (int i = 0; i < 32; ++i) v[i] *= r.a;
+            st_row32(out + r.at + c * 32, v, r.width - c * 32, wide);
+        } else {
+            st_row32(part + r.at + c * 32, v, r.width - c * 32, wide);
         }
     }
+    __device__ void end(Row&) const {}
 };
 
 // out = max|dloss| * the sum of the parts, in order.
@@ -484,8 +518,11 @@ cudaError_t lce_fwd_t(const void* x, const void* w, const int64_t* target, int64
         Operand a = ox;
         a.p += r * a.ld;
         a.rows = n;
-        LCE_TRY(mm_run(a, ow, mm_shape(n, V, D, ox.planes, false, false, false, 1),
-                       StatsEpi{part, tl, target + r, n, V}, err, s));
+        const Shape sh = mm_shape(n, V, D, ox.planes, false, false, false, 1);
+        if (sh.kb * sh.pairs > mm::kChunk)
+            LCE_TRY(mm_run(a, ow, sh, StatsEpi<true>{part, tl, target + r, n, V}, err, s));
+        else
+            LCE_TRY(mm_run(a, ow, sh, StatsEpi<false>{part, tl, target + r, n, V}, err, s));
         k_lce_join<<<(unsigned)((n + 31) / 32), dim3(32, 32), 0, s>>>(part, pl.tiles, tl, target + r, ignore, loss + r,
                                                                      lse + r, n, V, err);
         LCE_TRY(cudaGetLastError());
@@ -557,7 +594,7 @@ LcePlan lce_plan(int dtype, const void* x, const void* w, int64_t N, int64_t V, 
     LcePlan p{};
     const int planes = dtype == 0 ? 3 : 1;
     if (!bwd) {
-        p.tiles = (V + kTile - 1) / kTile;
+        p.tiles = (V + mm::kHalf - 1) / mm::kHalf;
         p.rows = std::min<int64_t>(N, 16384);
     } else {
         p.piece = std::max<int64_t>(kPieceBytes / (N * 2 * planes) / kTile, 1) * kTile;

@@ -7,8 +7,14 @@
 // 128 rows, so an operand byte in shared memory feeds twice the arithmetic of a
 // single CTA's tile.  Per CTA: a producer thread keeps a ring of kStages k-blocks
 // of 64 in flight by TMA (128-byte swizzle), one thread of the pair's first CTA
-// issues the MMAs, and four warps read finished accumulators back and run the
+// issues the MMAs, and eight warps read finished accumulators back and run the
 // epilogue while the next tile accumulates in the other half of TMEM.
+//
+// The tensor cores add into their fp32 accumulators by truncation: a long k loop
+// shrinks its sum by about 5e-9 a step of 16 (measured on the loss: 1.3e-6 over
+// k = 4096).  Where the result is fp32, the loop is cut into chunks of kChunk
+// k-blocks whose accumulators the epilogue warps add up in registers, rounding to
+// nearest; where it is rounded to bf16 (2^-9) one accumulator does.
 //
 // Operands are [rows][cols] matrices of bf16 planes: one plane for bf16 data,
 // three for fp32 data split as a = a1 + a2 + a3 (8 bits of mantissa each), whose
@@ -32,7 +38,8 @@ constexpr int kBlockK = 64;      // k-block: 128 bytes of bf16, the swizzle's wi
 constexpr int kStages = 6;
 constexpr int kOperand = kHalf * kBlockK * 2;  // 16 KB: one operand of a stage
 constexpr int kStageBytes = 2 * kOperand;
-constexpr int kThreads = 192;    // producer warp, MMA warp, 4 epilogue warps
+constexpr int kThreads = 320;    // producer warp, MMA warp, 8 epilogue warps
+constexpr uint32_t kChunk = 16;  // k-blocks of a chunk: k = 1024, a shrinkage of 3e-7
 constexpr int kSmem = kStages * kStageBytes + 1024;  // + alignment to 1024
 
 // What the products share: the tile grid and the k loop.
@@ -157,9 +164,20 @@ __device__ __forceinline__ Tile tile_of(const Shape& s, uint32_t t) {
     return r;
 }
 
-// Epilogue: struct with  __device__ void tile(const Tile&, int row /* in the
-// tile, 0 .. 255 */, Cols) const, where Cols(c, v) loads columns 32c .. 32c + 31 of
-// the row into v[32]; all lanes of a warp call it together.
+// k-blocks of a tile, all plane pairs.
+__device__ __forceinline__ uint32_t tile_steps(const Shape& s, const Tile& t) {
+    const uint32_t k0 = t.split * s.kb_split;
+    const uint32_t k1 = k0 + s.kb_split < s.kb ? k0 + s.kb_split : s.kb;
+    return (k1 - k0) * s.pairs;
+}
+
+// Epilogue: a struct with
+//   kChunked                       sum the k loop in chunks
+//   Row                            what a thread keeps of its row of a tile
+//   begin(tile, row, half) -> Row  row 0 .. 255 of the tile, half 0 / 1 of its columns
+//   width(tile, half)              columns of the half inside the result (may be <= 0)
+//   cols(Row&, c, v[32])           columns 32c .. 32c + 31 of the half (whole warps)
+//   end(Row&)
 template <class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_mm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Shape sh,
@@ -180,7 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 8);  // 4 epilogue warps of each CTA
+            mbar_init(&tempty[i], 16);  // 8 epilogue warps of each CTA
         }
         mbar_init_fence();
     }
@@ -239,55 +257,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t idesc = instr_desc(sh.a_mn, sh.b_mn);
             const uint32_t step_a = sh.a_mn ? 2048 >> 4 : 32 >> 4, step_b = sh.b_mn ? 2048 >> 4 : 32 >> 4;
             uint32_t it = 0, seq = 0;
-            for (uint32_t t = pair; t < n_tiles && ok; t += n_pairs, ++seq) {
-                const Tile tl = tile_of(sh, t);
-                const uint32_t k0 = tl.split * sh.kb_split;
-                const uint32_t k1 = k0 + sh.kb_split < sh.kb ? k0 + sh.kb_split : sh.kb;
-                const uint32_t buf = seq & 1;
-                if (seq >= 2 && !wait_cluster(&tempty[buf], (seq / 2 - 1) & 1, err)) {
-                    ok = false;
-                    break;
-                }
-                fence_after();
-                const uint32_t d = tmem + buf * kTile;
-                const uint32_t steps = (k1 - k0) * sh.pairs;
-                for (uint32_t k = 0; k < steps; ++k, ++it) {
-                    const uint32_t st = it % kStages;
-                    if (!wait_cluster(&full[st], (it / kStages) & 1, err)) {
+            for (uint32_t t = pair; t < n_tiles && ok; t += n_pairs) {
+                const uint32_t steps = tile_steps(sh, tile_of(sh, t));
+                const uint32_t chunk = Epi::kChunked ? kChunk : steps;
+                for (uint32_t c0 = 0; c0 < steps && ok; c0 += chunk, ++seq) {
+                    const uint32_t buf = seq & 1;
+                    if (seq >= 2 && !wait_cluster(&tempty[buf], (seq / 2 - 1) & 1, err)) {
                         ok = false;
                         break;
                     }
                     fence_after();
-                    const uint32_t a = smem_u32(ring + st * kStageBytes);
-                    const uint64_t da = smem_desc(a, sh.a_mn), db = smem_desc(a + kOperand, sh.b_mn);
+                    const uint32_t d = tmem + buf * kTile;
+                    const uint32_t n = steps - c0 < chunk ? steps - c0 : chunk;
+                    for (uint32_t k = 0; k < n; ++k, ++it) {
+                        const uint32_t st = it % kStages;
+                        if (!wait_cluster(&full[st], (it / kStages) & 1, err)) {
+                            ok = false;
+                            break;
+                        }
+                        fence_after();
+                        const uint32_t a = smem_u32(ring + st * kStageBytes);
+                        const uint64_t da = smem_desc(a, sh.a_mn), db = smem_desc(a + kOperand, sh.b_mn);
 #pragma unroll
-                    for (uint32_t j = 0; j < kBlockK / 16; ++j)
-                        mma(d, da + j * step_a, db + j * step_b, idesc, k > 0 || j > 0);
-                    commit_pair(&empty[st]);
+                        for (uint32_t j = 0; j < kBlockK / 16; ++j)
+                            mma(d, da + j * step_a, db + j * step_b, idesc, k > 0 || j > 0);
+                        commit_pair(&empty[st]);
+                    }
+                    if (ok) commit_pair(&tfull[buf]);
                 }
-                if (ok) commit_pair(&tfull[buf]);
             }
         }
-    } else {  // epilogue
-        const int quarter = warp & 3;
+    } else {  // epilogue: a quarter of the rows, a half of the columns a warp
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
         const int row = (int)rank * kHalf + quarter * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
         uint32_t seq = 0;
-        for (uint32_t t = pair; t < n_tiles; t += n_pairs, ++seq) {
-            const uint32_t buf = seq & 1;
-            ok = wait_cluster(&tfull[buf], (seq / 2) & 1, err);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
-            }
+        auto wait = [&](uint32_t buf) {
+            const bool good = __all_sync(0xffffffffu, wait_cluster(&tfull[buf], (seq / 2) & 1, err));
             fence_after();
-            const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile;
-            epi.tile(tile_of(sh, t), row, [&](int c, float (&v)[32]) {
-                __syncwarp();  // the load is one instruction of the whole warp
-                tmem_load32(base + c * 32, v);
-            });
+            return good;
+        };
+        auto done = [&](uint32_t buf) {
             fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(cluster_addr(&tempty[buf], 0));
+        };
+        for (uint32_t t = pair; t < n_tiles && ok; t += n_pairs) {
+            const Tile tl = tile_of(sh, t);
+            const int width = epi.width(tl, half);
+            if constexpr (Epi::kChunked) {
+                const uint32_t chunks = (tile_steps(sh, tl) + kChunk - 1) / kChunk;
+                float acc[kHalf];
+#pragma unroll
+                for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
+                for (uint32_t c = 0; c < chunks && ok; ++c, ++seq) {
+                    const uint32_t buf = seq & 1;
+                    ok = wait(buf);
+                    if (!ok) break;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        float v[32];
+                        __syncwarp();
+                        tmem_load32(lanes + buf * kTile + g * 32, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) acc[32 * g + i] += v[i];
+                    }
+                    done(buf);
+                }
+                if (!ok) break;
+                typename Epi::Row r = epi.begin(tl, row, half);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    if (g * 32 >= width) continue;
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = acc[32 * g + i];
+                    __syncwarp();
+                    epi.cols(r, g, v);
+                }
+                epi.end(r);
+            } else {
+                const uint32_t buf = seq & 1;
+                typename Epi::Row r = epi.begin(tl, row, half);
+                ok = wait(buf);
+                if (!ok) break;
+                for (int g = 0; g < 4 && g * 32 < width; ++g) {
+                    float v[32];
+                    __syncwarp();  // the load is one instruction of the whole warp
+                    tmem_load32(lanes + buf * kTile + g * 32, v);
+                    epi.cols(r, g, v);
+                }
+                epi.end(r);
+                __syncwarp();
+                done(buf);
+                ++seq;
+            }
         }
     }
     if (!ok) {

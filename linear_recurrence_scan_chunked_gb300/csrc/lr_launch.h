@@ -446,7 +446,7 @@ cudaError_t launch_adamw(AdamKind kind, int gdtype, const AdamTensor* t, int64_t
 
 // Softmax cross entropy of x W^T ([N, D] by [V, D]), in pieces.
 struct LcePlan {
-    int64_t tiles;      // forward: vocabulary tiles (a pair of statistics each, per row)
+    int64_t tiles;      // forward: half tiles of the vocabulary (a pair of statistics each, per row)
     int64_t rows;       // forward: rows per round
     int64_t piece;      // backward: vocabulary rows per piece
     int64_t dx_splits;  // backward: parts of the k loops

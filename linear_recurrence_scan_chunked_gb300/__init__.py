@@ -11,7 +11,9 @@ Tensors are CUDA, contiguous, [T, B, D] for sequences, [B, D] for states and
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 import re
 
@@ -369,25 +371,51 @@ def deer_diag_bwd(w, y, dy, h0=None, du=None, dw=None, dh0=None, want_dh0=True, 
     return du, dw, dh0
 
 
-def _state32(name, t, B, D, ref):
-    if t is None:
-        return None
-    if tuple(t.shape) != (B, D) or t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous fp32 [{B}, {D}] CUDA tensor")
-    if t.device != ref.device:
-        raise ValueError(f"{name} is on {t.device}, the sequence tensors on {ref.device}")
-    return t
+# The calls below may be a few microseconds of work on the device: their checks
+# take one look at each tensor (a host tensor's get_device() is -1), and the
+# addresses go to ctypes as plain integers.
+def _like(name, t, shape, dtype, dev):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on cuda:{dev}, got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}"
+                         + ("" if t.is_contiguous() else ", not contiguous"))
+    return t.data_ptr()
 
 
-def _flags(name, t, shape, ref):
-    if t is None:
-        return None
-    if tuple(t.shape) != tuple(shape) or t.dtype not in (torch.uint8, torch.bool) or not t.is_cuda \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous uint8 or bool {list(shape)} CUDA tensor")
-    if t.device != ref.device:
-        raise ValueError(f"{name} is on {t.device}, the sequence tensors on {ref.device}")
-    return t
+def _opt(name, t, shape, dtype, dev):
+    return None if t is None else _like(name, t, shape, dtype, dev)
+
+
+def _first(name, t, dims):
+    """The device index of a call's first tensor."""
+    dev = t.get_device()
+    if dev < 0 or not t.is_contiguous() or (t.dim() < 1 if dims is None else t.dim() != len(dims)):
+        raise ValueError(f"{name} must be a contiguous [{', '.join(dims or ('...', 'D'))}] CUDA tensor, got "
+                         f"{list(t.shape)} on {t.device}")
+    return dev
+
+
+def _reset_flags(t, shape, dev):
+    return None if t is None else _like("reset", t, shape, torch.bool if t.dtype is torch.bool else torch.uint8, dev)
+
+
+def _stream_on(stream, dev):
+    """The stream handle for a call on tensors of device `dev`, as _stream."""
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{dev} but the current CUDA device is "
+                         f"cuda:{torch.cuda.current_device()}: call under torch.cuda.device({dev})")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _glr_inputs(x, zr, zi, lam, br, bi, dev):
+    shape, dt, D = x.shape, x.dtype, x.shape[-1:]
+    f32 = torch.float32
+    return (x.data_ptr(), _like("zr", zr, shape, dt, dev), _like("zi", zi, shape, dt, dev),
+            _like("lam", lam, D, f32, dev), _like("br", br, D, f32, dev), _like("bi", bi, D, f32, dev))
 
 
 def glr_fwd(x, zr, zi, lam, br, bi, h0=None, reset=None, h=None, h_last=None, want_last=True,
@@ -397,20 +425,16 @@ def glr_fwd(x, zr, zi, lam, br, bi, h0=None, reset=None, h=None, h_last=None, wa
     lam, br, bi [D] fp32; h0 [B, D] fp32; reset [T, B] uint8 or bool, nonzero
     where a new document starts). Returns (h, h_last), h_last the fp32 state
     after the last step (None with want_last=False)."""
-    _seq("x", x)
-    _seq("zr", zr, x)
-    _seq("zi", zi, x)
+    dev = _first("x", x, ("T", "B", "D"))
     T, B, D = x.shape
-    for n, t in (("lam", lam), ("br", br), ("bi", bi)):
-        _param(n, t, D, x)
-    _state32("h0", h0, B, D, x)
-    _flags("reset", reset, (T, B), x)
-    h = torch.empty_like(x) if h is None else _seq("h", h, x)
+    f32, st = torch.float32, x.shape[1:]
+    args = _glr_inputs(x, zr, zi, lam, br, bi, dev)
+    args += (_opt("h0", h0, st, f32, dev), _reset_flags(reset, x.shape[:2], dev))
+    h = torch.empty_like(x) if h is None else h
     if h_last is None and want_last:
-        h_last = torch.empty((B, D), dtype=torch.float32, device=x.device)
-    _state32("h_last", h_last, B, D, x)
-    _check(load().glr_fwd(_p(x), _p(zr), _p(zi), _p(lam), _p(br), _p(bi), _p(h0), _p(reset), _p(h),
-                          _p(h_last), B, T, D, _code(x), _stream(stream, x)))
+        h_last = torch.empty(st, dtype=f32, device=x.device)
+    _check(load().glr_fwd(*args, _like("h", h, x.shape, x.dtype, dev), _opt("h_last", h_last, st, f32, dev), B, T, D,
+                          _code(x), _stream_on(stream, dev)))
     return h, h_last
 
 
@@ -418,27 +442,24 @@ def glr_bwd(x, zr, zi, lam, br, bi, h, dh, h0=None, reset=None, dh_last=None, ou
             want_dh0=True, stream=None):
     """Backward of glr_fwd for the upstream dh [T, B, D] and dh_last [B, D] fp32
     (the gradient of h_last). Returns dict dx, dzr, dzi, dlam, dbr, dbi, dh0."""
-    _seq("x", x)
-    for n, t in (("zr", zr), ("zi", zi), ("h", h), ("dh", dh)):
-        _seq(n, t, x)
+    dev = _first("x", x, ("T", "B", "D"))
     T, B, D = x.shape
-    for n, t in (("lam", lam), ("br", br), ("bi", bi)):
-        _param(n, t, D, x)
-    _state32("h0", h0, B, D, x)
-    _state32("dh_last", dh_last, B, D, x)
-    _flags("reset", reset, (T, B), x)
+    f32, st, dt = torch.float32, x.shape[1:], x.dtype
+    args = _glr_inputs(x, zr, zi, lam, br, bi, dev)
+    args += (_opt("h0", h0, st, f32, dev), _reset_flags(reset, x.shape[:2], dev),
+             _like("h", h, x.shape, dt, dev), _like("dh", dh, x.shape, dt, dev),
+             _opt("dh_last", dh_last, st, f32, dev))
     o = dict(out or {})
     for k in ("dx", "dzr", "dzi"):
-        o[k] = torch.empty_like(x) if o.get(k) is None else _seq(k, o[k], x)
+        o[k] = torch.empty_like(x) if o.get(k) is None else o[k]
     for k in ("dlam", "dbr", "dbi"):
-        o[k] = torch.empty(D, dtype=torch.float32, device=x.device) if o.get(k) is None else _param(k, o[k], D, x)
+        o[k] = torch.empty_like(lam) if o.get(k) is None else o[k]
     if o.get("dh0") is None and want_dh0:
-        o["dh0"] = torch.empty((B, D), dtype=torch.float32, device=x.device)
-    _state32("dh0", o.get("dh0"), B, D, x)
-    _check(load().glr_bwd(_p(x), _p(zr), _p(zi), _p(lam), _p(br), _p(bi), _p(h0), _p(reset), _p(h),
-                          _p(dh), _p(dh_last), _p(o["dx"]), _p(o["dzr"]), _p(o["dzi"]), _p(o["dlam"]),
-                          _p(o["dbr"]), _p(o["dbi"]), _p(o.get("dh0")), B, T, D, _code(x),
-                          _stream(stream, x)))
+        o["dh0"] = torch.empty(st, dtype=f32, device=x.device)
+    args += tuple(_like(k, o[k], x.shape, dt, dev) for k in ("dx", "dzr", "dzi"))
+    args += tuple(_like(k, o[k], lam.shape, f32, dev) for k in ("dlam", "dbr", "dbi"))
+    _check(load().glr_bwd(*args, _opt("dh0", o.get("dh0"), st, f32, dev), B, T, D, _code(x),
+                          _stream_on(stream, dev)))
     return o
 
 
@@ -448,95 +469,64 @@ def glr_step(x, zr, zi, lam, br, bi, state, slots=None, reset=None, h=None, stre
     updated in place. slots [B] int32: the slot of each row, negative for a
     padding row (None: slot b for row b); no slot twice. A slot past the pool
     counts as padding and sets LR_ERR_INDEX (last_error). Returns h [B, D]."""
-    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
-        raise ValueError(f"x must be a contiguous [B, D] CUDA tensor, got shape {tuple(x.shape)}")
+    dev = _first("x", x, ("B", "D"))
     B, D = x.shape
-    for n, t in (("zr", zr), ("zi", zi)) + ((("h", h),) if h is not None else ()):
-        if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous and match shape/dtype/device of x")
-    for n, t in (("lam", lam), ("br", br), ("bi", bi)):
-        _param(n, t, D, x)
-    if state.dim() != 2:
-        raise ValueError(f"state must be [n_slots, D], got shape {tuple(state.shape)}")
-    _state32("state", state, state.shape[0], D, x)
-    if slots is not None:
-        if slots.dtype != torch.int32 or tuple(slots.shape) != (B,) or slots.device != x.device \
-                or not slots.is_contiguous():
-            raise ValueError("slots must be a contiguous int32 [B] CUDA tensor on the device of x")
-    elif state.shape[0] < B:
-        raise ValueError(f"state has {state.shape[0]} slots for {B} rows")
-    _flags("reset", reset, (B,), x)
+    args = _glr_inputs(x, zr, zi, lam, br, bi, dev)
+    n_slots = state.shape[0]
+    if slots is None and n_slots < B:
+        raise ValueError(f"state has {n_slots} slots for {B} rows")
     h = torch.empty_like(x) if h is None else h
-    _check(load().glr_step(_p(x), _p(zr), _p(zi), _p(lam), _p(br), _p(bi), _p(reset), _p(slots),
-                           _p(state), _p(h), B, state.shape[0], D, _code(x), _stream(stream, x)))
+    _check(load().glr_step(*args, _reset_flags(reset, x.shape[:1], dev),
+                           _opt("slots", slots, x.shape[:1], torch.int32, dev),
+                           _like("state", state, (n_slots, D), torch.float32, dev),
+                           _like("h", h, x.shape, x.dtype, dev), B, n_slots, D, _code(x), _stream_on(stream, dev)))
     return h
-
-
-def _rows(name, t, like=None):
-    if t.dim() < 1 or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [..., D] CUDA tensor")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must match shape/dtype/device of x")
-    return t
-
-
-def _row_stat(name, t, x):
-    if t.dtype != torch.float32 or t.shape != x.shape[:-1] or t.device != x.device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous fp32 {list(x.shape[:-1])} CUDA tensor on the device of x")
-    return t
 
 
 def layer_norm_fwd(x, w, b=None, res=None, eps=1e-5, y=None, s=None, stream=None):
     """Layer norm over the last axis (x [..., D]; w, b [D] fp32), of x or, with
     res, of s = x + res. Returns (y, mean, rstd), with res (y, mean, rstd, s);
     mean and rstd are fp32 [...]."""
-    _rows("x", x)
-    D = x.shape[-1]
-    _param("w", w, D, x)
-    if b is not None:
-        _param("b", b, D, x)
+    dev = _first("x", x, None)
+    shape, dt, f32 = x.shape, x.dtype, torch.float32
+    row, D = shape[:-1], shape[-1:]
     if res is not None:
-        _rows("res", res, x)
-        s = torch.empty_like(x) if s is None else _rows("s", s, x)
+        s = torch.empty_like(x) if s is None else s
     elif s is not None:
         raise ValueError("s is an output of the residual add: give res with it")
-    y = torch.empty_like(x) if y is None else _rows("y", y, x)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    y = torch.empty_like(x) if y is None else y
+    mean = torch.empty(row, dtype=f32, device=x.device)
     rstd = torch.empty_like(mean)
-    _check(load().layer_norm_fwd(_p(x), _p(res), _p(w), _p(b), _p(y), _p(s), _p(mean), _p(rstd),
-                                 mean.numel(), D, eps, _code(x), _stream(stream, x)))
+    _check(load().layer_norm_fwd(x.data_ptr(), _opt("res", res, shape, dt, dev), _like("w", w, D, f32, dev),
+                                 _opt("b", b, D, f32, dev), _like("y", y, shape, dt, dev),
+                                 _opt("s", s, shape, dt, dev), mean.data_ptr(), rstd.data_ptr(), mean.numel(),
+                                 D[0], eps, _code(x), _stream_on(stream, dev)))
     return (y, mean, rstd) if res is None else (y, mean, rstd, s)
 
 
 def layer_norm_bwd(x, w, mean, rstd, dy, dres=None, out=None, stream=None):
     """Layer norm backward (x: what the norm was taken of; dres: the gradient
     that reaches it along the residual stream). Returns dict dx, dw, db."""
-    _rows("x", x)
-    _rows("dy", dy, x)
-    D = x.shape[-1]
-    _param("w", w, D, x)
-    _row_stat("mean", mean, x)
-    _row_stat("rstd", rstd, x)
-    if dres is not None:
-        _rows("dres", dres, x)
+    dev = _first("x", x, None)
+    shape, dt, f32 = x.shape, x.dtype, torch.float32
+    row, D = shape[:-1], shape[-1:]
     o = dict(out or {})
-    o["dx"] = torch.empty_like(x) if o.get("dx") is None else _rows("dx", o["dx"], x)
+    o["dx"] = torch.empty_like(x) if o.get("dx") is None else o["dx"]
     for k in ("dw", "db"):
-        o[k] = torch.empty(D, dtype=torch.float32, device=x.device) if o.get(k) is None else _param(k, o[k], D, x)
-    _check(load().layer_norm_bwd(_p(x), _p(w), _p(mean), _p(rstd), _p(dy), _p(dres), _p(o["dx"]),
-                                 _p(o["dw"]), _p(o["db"]), mean.numel(), D, _code(x),
-                                 _stream(stream, x)))
+        o[k] = torch.empty_like(w) if o.get(k) is None else o[k]
+    _check(load().layer_norm_bwd(x.data_ptr(), _like("w", w, D, f32, dev), _like("mean", mean, row, f32, dev),
+                                 _like("rstd", rstd, row, f32, dev), _like("dy", dy, shape, dt, dev),
+                                 _opt("dres", dres, shape, dt, dev), _like("dx", o["dx"], shape, dt, dev),
+                                 _like("dw", o["dw"], D, f32, dev), _like("db", o["db"], D, f32, dev),
+                                 mean.numel(), D[0], _code(x), _stream_on(stream, dev)))
     return o
 
 
-def _lce_args(x, w, target):
-    _rows("x", x)
-    if w.dim() != 2 or w.shape[1] != x.shape[-1] or w.dtype != x.dtype or w.device != x.device or not w.is_contiguous():
-        raise ValueError("w must be a contiguous [V, D] CUDA tensor of the dtype and device of x")
-    if target.dtype != torch.int64 or target.shape != x.shape[:-1] or target.device != x.device \
-            or not target.is_contiguous():
-        raise ValueError(f"target must be a contiguous int64 {list(x.shape[:-1])} CUDA tensor on the device of x")
-    return target.numel(), w.shape[0], w.shape[1]
+def _lce_inputs(x, w, target):
+    dev = _first("x", x, None)
+    V = w.shape[0] if w.dim() else 0
+    return dev, V, (x.data_ptr(), _like("w", w, (V, x.shape[-1]), x.dtype, dev),
+                    _like("target", target, x.shape[:-1], torch.int64, dev))
 
 
 def lce_fwd(x, w, target, ignore=-100, loss=None, lse=None, stream=None):
@@ -544,56 +534,67 @@ def lce_fwd(x, w, target, ignore=-100, loss=None, lse=None, stream=None):
     target [...] int64, without keeping the logits. Returns (loss, lse), fp32
     [...]; loss is 0 where target == ignore. A target outside 0 .. V-1 counts
     as ignored and sets LR_ERR_INDEX (last_error)."""
-    N, V, D = _lce_args(x, w, target)
-    loss = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if loss is None else _row_stat("loss", loss, x)
-    lse = torch.empty_like(loss) if lse is None else _row_stat("lse", lse, x)
-    _check(load().lce_fwd(_p(x), _p(w), _p(target), ignore, _p(loss), _p(lse), N, V, D, _code(x),
-                          _stream(stream, x)))
+    dev, V, args = _lce_inputs(x, w, target)
+    row, f32 = x.shape[:-1], torch.float32
+    loss = torch.empty(row, dtype=f32, device=x.device) if loss is None else loss
+    lse = torch.empty_like(loss) if lse is None else lse
+    _check(load().lce_fwd(*args, ignore, _like("loss", loss, row, f32, dev), _like("lse", lse, row, f32, dev),
+                          target.numel(), V, x.shape[-1], _code(x), _stream_on(stream, dev)))
     return loss, lse
 
 
 def lce_bwd(x, w, target, lse, dloss, ignore=-100, dx=None, dw=None, stream=None):
     """Gradient of lce_fwd for the upstream dloss [...] fp32 (lse: lce_fwd's).
     Returns (dx, dw)."""
-    N, V, D = _lce_args(x, w, target)
-    _row_stat("lse", lse, x)
-    _row_stat("dloss", dloss, x)
-    dx = torch.empty_like(x) if dx is None else _rows("dx", dx, x)
-    dw = torch.empty_like(w) if dw is None else _rows("dw", dw, w)
-    _check(load().lce_bwd(_p(x), _p(w), _p(target), ignore, _p(lse), _p(dloss), _p(dx), _p(dw), N, V, D,
-                          _code(x), _stream(stream, x)))
+    dev, V, args = _lce_inputs(x, w, target)
+    row, f32 = x.shape[:-1], torch.float32
+    dx = torch.empty_like(x) if dx is None else dx
+    dw = torch.empty_like(w) if dw is None else dw
+    _check(load().lce_bwd(*args, ignore, _like("lse", lse, row, f32, dev), _like("dloss", dloss, row, f32, dev),
+                          _like("dx", dx, x.shape, x.dtype, dev), _like("dw", dw, w.shape, x.dtype, dev),
+                          target.numel(), V, x.shape[-1], _code(x), _stream_on(stream, dev)))
     return dx, dw
 
 
-def _tensor_list(name, ts, dtype, numels, ref):
-    """The addresses of a list of contiguous CUDA tensors of one dtype on the
-    device of `ref`, with the given numbers of elements, as a ctypes array."""
-    if len(ts) != len(numels):
-        raise ValueError(f"{name} has {len(ts)} tensors, params {len(numels)}")
-    dev = ref.get_device()
-    for t, n in zip(ts, numels):
-        if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda or t.get_device() != dev:
-            raise ValueError(f"{name} must hold contiguous {dtype} CUDA tensors on {ref.device}, as many elements "
-                             f"each as it takes ({n}), got {tuple(t.shape)} {t.dtype} on {t.device}")
-    return (ctypes.c_void_p * len(ts))(*[t.data_ptr() for t in ts])
+_T = torch.Tensor
+_dtype_of = operator.attrgetter("dtype")
 
 
-def _adamw_args(params, grads, copies, grad_scale):
-    ref = params[0]
-    if not ref.is_cuda:
+def _addresses(name, ts, dtype, numels, dev):
+    """The addresses of a list of contiguous CUDA tensors of one dtype on device
+    `dev`, with the given numbers of elements (one C loop per property: a call
+    may hold hundreds of tensors)."""
+    if list(map(_T.numel, ts)) != numels or set(map(_dtype_of, ts)) != {dtype} \
+            or set(map(_T.get_device, ts)) != {dev} or not all(map(_T.is_contiguous, ts)):
+        raise ValueError(f"{name} must hold one contiguous {dtype} tensor on cuda:{dev} per parameter, of as many "
+                         "elements (the scales: one per 256)")
+    return array.array("Q", map(_T.data_ptr, ts))
+
+
+def _adamw_call(fn, params, grads, moments, scales, copies, grad_scale, step, hyper, extra, stream):
+    dev = params[0].get_device()
+    if dev < 0:
         raise ValueError("params must be CUDA tensors")
-    numels = [t.numel() for t in params]
+    numels = list(map(_T.numel, params))
+    nb = [(k + ADAMW8_BLOCK - 1) // ADAMW8_BLOCK for k in numels]
     gd = grads[0].dtype if len(grads) else torch.float32
     if gd not in (torch.float32, torch.bfloat16):
         raise TypeError(f"gradients must be float32 or bfloat16, got {gd}")
-    if grad_scale is not None and (grad_scale.dtype != torch.float32 or grad_scale.numel() != 1
-                                   or grad_scale.device != ref.device):
-        raise ValueError("grad_scale must be one fp32 value on the device of the params")
-    return (ref, numels, (ctypes.c_int64 * len(numels))(*numels),
-            _tensor_list("params", params, torch.float32, numels, ref),
-            _tensor_list("grads", grads, gd, numels, ref),
-            None if copies is None else _tensor_list("copies", copies, torch.bfloat16, numels, ref),
-            LR_F32 if gd == torch.float32 else LR_BF16)
+    keep = [array.array("q", numels), _addresses("params", params, torch.float32, numels, dev),
+            _addresses("grads", grads, gd, numels, dev)]
+    keep += [_addresses(name, ts, dt, numels, dev) for name, ts, dt in moments]
+    keep += [_addresses(name, ts, torch.float32, nb, dev) for name, ts in scales]
+    args = [a.buffer_info()[0] for a in keep]
+    if copies is not None:
+        keep.append(_addresses("copies", copies, torch.bfloat16, numels, dev))
+        args.append(keep[-1].buffer_info()[0])
+    else:
+        args.append(None)
+    gs = None
+    if grad_scale is not None:
+        gs = _like("grad_scale", grad_scale, grad_scale.shape if grad_scale.numel() == 1 else (1,), torch.float32, dev)
+    _check(fn(len(numels), *args, step, *hyper, gs, *extra, LR_F32 if gd == torch.float32 else LR_BF16,
+              _stream_on(stream, dev)))
 
 
 def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
@@ -603,24 +604,19 @@ def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, 
     counts from 1; grad_scale: one fp32 value on the device."""
     if len(params) == 0:
         return
-    ref, numels, n, p, g, c, gd = _adamw_args(params, grads, copies, grad_scale)
-    _check(load().adamw_step(len(numels), n, p, g, _tensor_list("m", m, torch.float32, numels, ref),
-                             _tensor_list("v", v, torch.float32, numels, ref), c, step, lr, beta1, beta2,
-                             eps, weight_decay, _p(grad_scale), gd, _stream(stream, ref)))
+    f32 = torch.float32
+    _adamw_call(load().adamw_step, params, grads, (("m", m, f32), ("v", v, f32)), (), copies, grad_scale, step,
+                (lr, beta1, beta2, eps, weight_decay), (), stream)
 
 
 ADAMW8_BLOCK = 256
-
-
-def _scale_numels(numels):
-    return [(k + ADAMW8_BLOCK - 1) // ADAMW8_BLOCK for k in numels]
 
 
 def adamw8_state(params):
     """Zero 8-bit moments for adamw8_step: lists m (int8), v (uint8), and their
     scales ms, vs (fp32, one per 256 elements)."""
     e = lambda t, n, dt: torch.zeros(n, dtype=dt, device=t.device)
-    nb = _scale_numels([t.numel() for t in params])
+    nb = [(t.numel() + ADAMW8_BLOCK - 1) // ADAMW8_BLOCK for t in params]
     return ([e(t, t.numel(), torch.int8) for t in params], [e(t, t.numel(), torch.uint8) for t in params],
             [e(t, k, torch.float32) for t, k in zip(params, nb)],
             [e(t, k, torch.float32) for t, k in zip(params, nb)])
@@ -632,14 +628,9 @@ def adamw8_step(params, grads, m, v, ms, vs, step, lr, seed, beta1=0.9, beta2=0.
     at every step (the rounding's random bits)."""
     if len(params) == 0:
         return
-    ref, numels, n, p, g, c, gd = _adamw_args(params, grads, copies, grad_scale)
-    nb = _scale_numels(numels)
-    _check(load().adamw8_step(len(numels), n, p, g, _tensor_list("m", m, torch.int8, numels, ref),
-                              _tensor_list("v", v, torch.uint8, numels, ref),
-                              _tensor_list("ms", ms, torch.float32, nb, ref),
-                              _tensor_list("vs", vs, torch.float32, nb, ref), c, step, lr, beta1, beta2,
-                              eps, weight_decay, _p(grad_scale), int(seed) & 0xFFFFFFFF, gd,
-                              _stream(stream, ref)))
+    _adamw_call(load().adamw8_step, params, grads, (("m", m, torch.int8), ("v", v, torch.uint8)),
+                (("ms", ms), ("vs", vs)), copies, grad_scale, step, (lr, beta1, beta2, eps, weight_decay),
+                (int(seed) & 0xFFFFFFFF,), stream)
 
 
 def adamw8_values(mq, vq, ms, vs, m=None, v=None, stream=None):
@@ -647,20 +638,19 @@ def adamw8_values(mq, vq, ms, vs, m=None, v=None, stream=None):
     1-d tensors unless given."""
     if len(mq) == 0:
         return [], []
-    ref = mq[0]
-    if not ref.is_cuda:
+    dev = mq[0].get_device()
+    if dev < 0:
         raise ValueError("the codes must be CUDA tensors")
-    numels = [t.numel() for t in mq]
-    nb = _scale_numels(numels)
-    m = [torch.empty(k, dtype=torch.float32, device=ref.device) for k in numels] if m is None else m
-    v = [torch.empty(k, dtype=torch.float32, device=ref.device) for k in numels] if v is None else v
-    _check(load().adamw8_values(len(numels), (ctypes.c_int64 * len(numels))(*numels),
-                                _tensor_list("mq", mq, torch.int8, numels, ref),
-                                _tensor_list("vq", vq, torch.uint8, numels, ref),
-                                _tensor_list("ms", ms, torch.float32, nb, ref),
-                                _tensor_list("vs", vs, torch.float32, nb, ref),
-                                _tensor_list("m", m, torch.float32, numels, ref),
-                                _tensor_list("v", v, torch.float32, numels, ref), _stream(stream, ref)))
+    f32 = torch.float32
+    numels = list(map(_T.numel, mq))
+    nb = [(k + ADAMW8_BLOCK - 1) // ADAMW8_BLOCK for k in numels]
+    m = [torch.empty(k, dtype=f32, device=mq[0].device) for k in numels] if m is None else m
+    v = [torch.empty(k, dtype=f32, device=mq[0].device) for k in numels] if v is None else v
+    keep = [array.array("q", numels), _addresses("mq", mq, torch.int8, numels, dev),
+            _addresses("vq", vq, torch.uint8, numels, dev), _addresses("ms", ms, f32, nb, dev),
+            _addresses("vs", vs, f32, nb, dev), _addresses("m", m, f32, numels, dev),
+            _addresses("v", v, f32, numels, dev)]
+    _check(load().adamw8_values(len(numels), *[a.buffer_info()[0] for a in keep], _stream_on(stream, dev)))
     return m, v
 
 

@@ -92,9 +92,14 @@ struct GlrFwdOp {
             }
         }
     }
+    // Two elements at a time (neighbouring channels on the vector path,
+    // neighbouring rows on the scalar one), one reciprocal for both gates:
+    // 1/(AB) times B and A.  Gates shut past 2^-60 and decays past e^-2 take the
+    // general forms.
     __device__ static void aggregate(const Params& p, const Geom& g, const TileCoord& tc,
                                      const Regs& rg, Work& w, float (&A)[VEC], float (&B)[VEC],
                                      bool) {
+        static_assert(R * VEC % 2 == 0, "pairs");
         float lam[VEC], br[VEC], bi[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) { lam[v] = br[v] = bi[v] = 0.f; A[v] = 1.f; B[v] = 0.f; }
@@ -103,21 +108,63 @@ struct GlrFwdOp {
             load_param<VEC>(p.br + tc.cd, br);
             load_param<VEC>(p.bi + tc.cd, bi);
         }
+        float l8[VEC], b2r[VEC], b2i[VEC];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool ok = tc.cok && tc.t0 + r < g.T;
-            const bool reset = rg.rs[r] != 0;
+        for (int v = 0; v < VEC; ++v) {
+            l8[v] = -0.125f * lam[v];
+            b2r[v] = -kLog2e * br[v];
+            b2i[v] = -kLog2e * bi[v];
+        }
+        const f32x2 one = f2(1.f), nl = f2(-kLog2e);
+        float emax = 0.f, xmin = 0.f;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                float a, q;
-                act_decay(-lam[v] * act_sigmoid(rg.zr[r].get(v) + br[v]), a, q);
-                const float u = act_sigmoid(rg.zi[r].get(v) + bi[v]) * rg.x[r].get(v);
-                w.fa[r][v] = ok ? (reset ? 0.f : a) : 1.f;
-                w.fb[r][v] = ok ? (reset ? u : sqrt_ftz(q) * u) : 0.f;
-                B[v] = w.fa[r][v] * B[v] + w.fb[r][v];
-                A[v] *= w.fa[r][v];
+        for (int e = 0; e < R * VEC; e += 2) {
+            const int r0 = e / VEC, v0 = e % VEC, r1 = (e + 1) / VEC, v1 = (e + 1) % VEC;
+            float er0, er1, ei0, ei1;
+            f2_get(f2_fma(f2(rg.zr[r0].get(v0), rg.zr[r1].get(v1)), nl, f2(b2r[v0], b2r[v1])), er0, er1);
+            f2_get(f2_fma(f2(rg.zi[r0].get(v0), rg.zi[r1].get(v1)), nl, f2(b2i[v0], b2i[v1])), ei0, ei1);
+            emax = fmaxf(fmaxf(emax, fmaxf(er0, er1)), fmaxf(ei0, ei1));
+            const f32x2 P = f2_add(f2(ex2_ftz(er0), ex2_ftz(er1)), one);
+            const f32x2 Q = f2_add(f2(ex2_ftz(ei0), ex2_ftz(ei1)), one);
+            float t0, t1;
+            f2_get(f2_mul(P, Q), t0, t1);
+            const f32x2 t = f2(rcp_ftz(t0), rcp_ftz(t1));
+            const f32x2 x = f2_mul(f2_mul(t, Q), f2(l8[v0], l8[v1]));
+            const f32x2 u = f2_mul(f2_mul(t, P), f2(rg.x[r0].get(v0), rg.x[r1].get(v1)));
+            float x0, x1, q0, q1;
+            f2_get(x, x0, x1);
+            xmin = fminf(xmin, fminf(x0, x1));
+            f32x2 a, nq;
+            act_decay2(x, a, nq);
+            f2_get(nq, q0, q1);
+            f2_get(a, w.fa[r0][v0], w.fa[r1][v1]);
+            f2_get(f2_mul(u, f2(sqrt_ftz(-q0), sqrt_ftz(-q1))), w.fb[r0][v0], w.fb[r1][v1]);
+        }
+        bool any = emax > kGateMaxExp || xmin < kDecayMinX || !(tc.cok && tc.t0 + R - 1 < g.T);
+#pragma unroll
+        for (int r = 0; r < R; ++r) any = any || rg.rs[r] != 0;
+        if (any) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const bool ok = tc.cok && tc.t0 + r < g.T, reset = rg.rs[r] != 0;
+                if (ok && !reset && !(emax > kGateMaxExp || xmin < kDecayMinX)) continue;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    float a, q;
+                    act_decay(-lam[v] * act_sigmoid(rg.zr[r].get(v) + br[v]), a, q);
+                    const float u = act_sigmoid(rg.zi[r].get(v) + bi[v]) * rg.x[r].get(v);
+                    w.fa[r][v] = ok ? (reset ? 0.f : a) : 1.f;
+                    w.fb[r][v] = ok ? (reset ? u : sqrt_ftz(q) * u) : 0.f;
+                }
             }
         }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                B[v] = __fmaf_rn(w.fa[r][v], B[v], w.fb[r][v]);
+                A[v] *= w.fa[r][v];
+            }
     }
     __device__ static void finish(const Params& p, const Geom& g, const TileCoord& tc,
                                   const Regs&, Work& w, float (&s)[VEC], Smem&, Acc&) {
@@ -228,9 +275,13 @@ struct GlrBwdOp {
             }
         }
     }
+    // As the forward pass, two elements at a time; a square root's pole (a decay
+    // of 1 to the last bit) takes the general form too.  The pass that only wants
+    // the aggregate (side = false) needs no more than the decay.
     __device__ static void aggregate(const Params& p, const Geom& g, const TileCoord& tc,
                                      const Regs& rg, Work& w, float (&A)[VEC], float (&B)[VEC],
-                                     bool) {
+                                     bool side) {
+        static_assert(R * VEC % 2 == 0, "pairs");
         float lam[VEC], br[VEC], bi[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) { lam[v] = br[v] = bi[v] = 0.f; A[v] = 1.f; B[v] = 0.f; }
@@ -239,38 +290,98 @@ struct GlrBwdOp {
             load_param<VEC>(p.br + tc.cd, br);
             load_param<VEC>(p.bi + tc.cd, bi);
         }
+        float l8[VEC], b2r[VEC], b2i[VEC];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int64_t t = tc.t0 - r;
-            const bool ok = tc.cok && t < g.T;
-            const bool reset = rg.rs[r] != 0;
-            float hp[VEC];
+        for (int v = 0; v < VEC; ++v) {
+            l8[v] = -0.125f * lam[v];
+            b2r[v] = -kLog2e * br[v];
+            b2i[v] = -kLog2e * bi[v];
+        }
+        const f32x2 one = f2(1.f), none = f2(-1.f), nl = f2(-kLog2e);
+        float emax = 0.f, xmin = 0.f, qmin = 1.f;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) hp[v] = rg.hp[r].get(v);
-            if (ok && t == 0 && p.h0 != nullptr) load_vec<float, VEC>(p.h0 + tc.c, hp);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float rr = act_sigmoid(rg.zr[r].get(v) + br[v]);
-                const float ii = act_sigmoid(rg.zi[r].get(v) + bi[v]);
-                float a, q;
-                act_decay(-lam[v] * rr, a, q);
-                // f = q / sqrt(q); where the decay is 1 to the last bit (q = 0) the
-                // gradient of the decay is 0: K's pole is cancelled by r (1-r) -> 0
-                const float rf = q > 0.f ? rsqrt_ftz(q) : q;
-                const float f = reset ? 1.f : q * rf;
-                const float xv = rg.x[r].get(v);
-                const float u = ii * xv;
-                const float K = reset || q == 0.f ? 0.f : a * (hp[v] - u * a * rf);
-                w.F[r][v] = ok ? (reset ? 0.f : a) : 1.f;
-                w.CX[r][v] = f * ii;
-                w.CI[r][v] = f * u * (1.f - ii);
-                w.KR[r][v] = -K * rr;
-                w.CR[r][v] = lam[v] * (w.KR[r][v] * (1.f - rr));
-                const float e = ok ? rg.dh[r].get(v) : 0.f;
-                B[v] = w.F[r][v] * (e + B[v]);
-                A[v] *= w.F[r][v];
+        for (int e = 0; e < R * VEC; e += 2) {
+            const int r0 = e / VEC, v0 = e % VEC, r1 = (e + 1) / VEC, v1 = (e + 1) % VEC;
+            float er0, er1;
+            f2_get(f2_fma(f2(rg.zr[r0].get(v0), rg.zr[r1].get(v1)), nl, f2(b2r[v0], b2r[v1])), er0, er1);
+            emax = fmaxf(emax, fmaxf(er0, er1));
+            float t0, t1;
+            f2_get(f2_add(f2(ex2_ftz(er0), ex2_ftz(er1)), one), t0, t1);
+            const f32x2 rr = f2(rcp_ftz(t0), rcp_ftz(t1));
+            const f32x2 x = f2_mul(rr, f2(l8[v0], l8[v1]));
+            float x0, x1;
+            f2_get(x, x0, x1);
+            xmin = fminf(xmin, fminf(x0, x1));
+            f32x2 a, nq;
+            act_decay2(x, a, nq);
+            f2_get(a, w.F[r0][v0], w.F[r1][v1]);
+            if (side) {
+                float ei0, ei1, q0, q1;
+                f2_get(f2_fma(f2(rg.zi[r0].get(v0), rg.zi[r1].get(v1)), nl, f2(b2i[v0], b2i[v1])), ei0, ei1);
+                emax = fmaxf(emax, fmaxf(ei0, ei1));
+                f2_get(f2_add(f2(ex2_ftz(ei0), ex2_ftz(ei1)), one), t0, t1);
+                const f32x2 ii = f2(rcp_ftz(t0), rcp_ftz(t1));
+                f2_get(nq, q0, q1);
+                qmin = fminf(qmin, fminf(-q0, -q1));
+                const f32x2 nrf = f2(-rsqrt_ftz(-q0), -rsqrt_ftz(-q1));  // -1/f
+                const f32x2 f = f2_mul(nq, nrf);
+                const f32x2 u = f2_mul(ii, f2(rg.x[r0].get(v0), rg.x[r1].get(v1)));
+                const f32x2 h = f2(rg.hp[r0].get(v0), rg.hp[r1].get(v1));
+                // K = a (h - u a / f);  -K r, its product with lam (1 - r)
+                const f32x2 K = f2_mul(a, f2_fma(f2_mul(u, a), nrf, h));
+                const f32x2 nr = f2_mul(rr, none);
+                const f32x2 KR = f2_mul(K, nr);
+                const f32x2 CR = f2_mul(f2_mul(KR, f2(lam[v0], lam[v1])), f2_add(nr, one));
+                const f32x2 CI = f2_mul(f2_mul(f, u), f2_fma(ii, none, one));
+                f2_get(f2_mul(f, ii), w.CX[r0][v0], w.CX[r1][v1]);
+                f2_get(CI, w.CI[r0][v0], w.CI[r1][v1]);
+                f2_get(KR, w.KR[r0][v0], w.KR[r1][v1]);
+                f2_get(CR, w.CR[r0][v0], w.CR[r1][v1]);
             }
         }
+        const bool gen = emax > kGateMaxExp || xmin < kDecayMinX || !(qmin > 0.f);
+        bool any = gen || !(tc.cok && tc.t0 < g.T) || (p.h0 != nullptr && tc.t0 - (R - 1) <= 0);
+#pragma unroll
+        for (int r = 0; r < R; ++r) any = any || rg.rs[r] != 0;
+        if (any) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t t = tc.t0 - r;
+                const bool ok = tc.cok && t < g.T, reset = rg.rs[r] != 0;
+                const bool first = ok && t == 0 && p.h0 != nullptr;  // h0 is fp32
+                if (ok && !reset && !gen && !first) continue;
+                float hp[VEC];
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) hp[v] = rg.hp[r].get(v);
+                if (first) load_vec<float, VEC>(p.h0 + tc.c, hp);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float rr = act_sigmoid(rg.zr[r].get(v) + br[v]);
+                    const float ii = act_sigmoid(rg.zi[r].get(v) + bi[v]);
+                    float a, q;
+                    act_decay(-lam[v] * rr, a, q);
+                    // where the decay is 1 to the last bit (q = 0) its gradient is
+                    // 0: K's pole is cancelled by r (1-r) -> 0
+                    const float rf = q > 0.f ? rsqrt_ftz(q) : q;
+                    const float f = reset ? 1.f : q * rf;
+                    const float u = ii * rg.x[r].get(v);
+                    const float K = reset || q == 0.f ? 0.f : a * (hp[v] - u * a * rf);
+                    w.F[r][v] = ok ? (reset ? 0.f : a) : 1.f;
+                    w.CX[r][v] = f * ii;
+                    w.CI[r][v] = f * u * (1.f - ii);
+                    w.KR[r][v] = -K * rr;
+                    w.CR[r][v] = lam[v] * (w.KR[r][v] * (1.f - rr));
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                // rows outside hold dh = 0 and F = 1
+                B[v] = w.F[r][v] * (rg.dh[r].get(v) + B[v]);
+                A[v] *= w.F[r][v];
+            }
     }
     __device__ static void finish(const Params& p, const Geom& g, const TileCoord& tc,
                                   const Regs& rg, Work& w, float (&s)[VEC], Smem& xs, Acc& acc) {
@@ -287,7 +398,7 @@ struct GlrBwdOp {
             float dx[VEC], dzr[VEC], dzi[VEC];
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                const float d = (ok ? rg.dh[r].get(v) : 0.f) + s[v];
+                const float d = rg.dh[r].get(v) + s[v];
                 dx[v] = d * w.CX[r][v];
                 dzr[v] = d * w.CR[r][v];
                 dzi[v] = d * w.CI[r][v];

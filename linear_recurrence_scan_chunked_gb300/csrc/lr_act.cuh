@@ -124,4 +124,53 @@ __device__ __forceinline__ void act_decay(float l, float& a, float& q) {
     }
 }
 
+// ---- two fp32 values in one 64-bit register (sm_100+: one instruction issues
+// both operations, which is what a kernel bound by instruction issue counts).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 f2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ f32x2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void f2_get(f32x2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 f2_fma(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 f2_mul(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// act_decay for a pair, without a branch or the exponential: x = l / 8 in
+// [-1/4, 0], m = e^x - 1 by its series (the first omitted term is under
+// 5e-8 |x|), then three times e^2x - 1 = (e^x - 1)(2 + (e^x - 1)).  nq = -(1 - a^2).
+constexpr float kDecayMinX = -0.25f;  // below: act_decay
+__device__ __forceinline__ void act_decay2(f32x2 x, f32x2& a, f32x2& nq) {
+    const f32x2 one = f2(1.f), two = f2(2.f);
+    f32x2 p = f2_fma(x, f2(1.f / 720.f), f2(1.f / 120.f));
+    p = f2_fma(p, x, f2(1.f / 24.f));
+    p = f2_fma(p, x, f2(1.f / 6.f));
+    p = f2_fma(p, x, f2(0.5f));
+    p = f2_fma(p, x, one);
+    f32x2 m = f2_mul(p, x);
+    m = f2_mul(m, f2_add(m, two));
+    m = f2_mul(m, f2_add(m, two));
+    m = f2_mul(m, f2_add(m, two));
+    a = f2_add(m, one);
+    nq = f2_mul(m, f2_add(m, two));
+}
+// Exponents of two above which a gate's 1 + 2^x is left to act_sigmoid.
+constexpr float kGateMaxExp = 60.f;
+
 }  // namespace lrs

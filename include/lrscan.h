@@ -317,7 +317,8 @@ int lstm_cell_bwd(const void* zf, const void* zi, const void* zc, const void* zo
 /*
  * Gated linear recurrence, forward: the scan of row a1 with a decay set by the
  * input and the input scaled so that the state keeps its size ([P1]
- * parallel-scan paragraph for the scan; the pages name no such cell).  One launch:
+ * parallel-scan paragraph for the scan; the pages name no such cell).  One
+ * launch, two for narrow problems:
  *   r = sigmoid(zr + br),  i = sigmoid(zi + bi),
  *   a = exp(-lam r),  f = sqrt(1 - a^2),
  *   h_t = a_t h_{t-1} + f_t i_t x_t   (h_{-1} = h0).
@@ -330,7 +331,8 @@ int lstm_cell_bwd(const void* zf, const void* zi, const void* zc, const void* zo
  *   h            : [T,B,D] out
  *   h_last       : [B,D] fp32 out  the state after the last step, not rounded to
  *                                  the storage type (NULL: not wanted); T = 0: h0
- * The states are fp32 whatever the storage type.
+ * The states are fp32 whatever the storage type.  B*D <= 2^25 channels
+ * (LR_ERR_TOO_LARGE beyond).
  */
 int glr_fwd(const void* x, const void* zr, const void* zi, const float* lam, const float* br,
             const float* bi, const float* h0, const uint8_t* reset, void* h, float* h_last,
@@ -538,8 +540,10 @@ typedef enum {
                              or a CTA walks its channel strip through time */
     LR_PROTO_WALK = 1,    /* walker warps fold the published chunk aggregates */
     LR_PROTO_LOOK = 2,    /* every tile folds all earlier chunks' published aggregates */
-    LR_PROTO_CLUSTER = 3  /* one thread-block cluster per channel tile, aggregates
+    LR_PROTO_CLUSTER = 3, /* one thread-block cluster per channel tile, aggregates
                              passed through distributed shared memory */
+    LR_PROTO_SPANS = 4    /* gated recurrence: the spans' aggregates in a first
+                             launch, then a CTA walks each span (one span: CHAIN) */
 } lr_protocol;
 
 /*

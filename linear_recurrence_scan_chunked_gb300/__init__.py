@@ -667,7 +667,7 @@ def workspace_bytes() -> int:
 OPS = ("scan_fwd", "scan_bwd", "sru_fwd", "sru_bwd", "deer", "deer_bwd", "lstm_fwd", "lstm_bwd",
        "deer_ode")
 GLR_OPS = {"glr_fwd": 16, "glr_bwd": 17}
-PROTOCOLS = ("chain", "walk", "look", "cluster")
+PROTOCOLS = ("chain", "walk", "look", "cluster", "spans")
 
 
 def plan_info(op: str, dtype: str, vec: bool, T: int, C: int) -> dict:

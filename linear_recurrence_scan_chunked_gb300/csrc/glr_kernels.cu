@@ -16,181 +16,328 @@
 // h_{t-1} as the forward pass stored it (bf16 storage: rounded once, 2^-9), the
 // way the other cells do: keeping fp32 states would double what it reads of h.
 //
-// Bytes bound it: 4 arrays forward, 8 backward, each element crossing HBM once.
+// The split.  An element costs about 45 instructions forward and 75 backward (two
+// gates, a decay, a square root), so at 8 to 32 bytes an element the issue slots
+// are as scarce as the bytes, and the carry must not make an element's gates be
+// computed twice.  The time axis is cut into S spans; a CTA owns one span of one
+// channel strip and walks it through time, tile by tile, its state in shared
+// memory, so CTAs wait for nothing but their own loads.  Wide problems have strips
+// enough: S = 1 and one launch.  Narrow ones first run k_glr_agg, which computes only
+// the spans' aggregates (A, B) -- backward that takes the decay and dh, two of the
+// five inputs -- with every warp folding a run of its own and no barrier but the
+// last; each CTA of k_glr_span then folds the aggregates of the spans before its
+// own.  Every association depends on the shape alone: the same bits every run.
 #include "lr_act.cuh"
 #include "lr_launch.h"
-#include "lr_persist.cuh"
+#include "lr_tma.cuh"
+
+#include <string.h>
+
+#include <type_traits>
 
 namespace lrs {
 
+namespace {
+
+// A problem's tiles: L = NW R rows by 32 VEC channels; S spans of cps chunks.
+struct SpanGeom {
+    Geom g;         // T, C, D, n_chunks, n_ct and c / D
+    uint32_t cps;   // chunks per span
+    uint32_t S;
+    int64_t nb;     // sequences (row pitch of reset)
+};
+
+// A thread's place in a block of rows: VEC channels of R rows, consecutive in scan
+// order (reverse: falling time).  An address is the block's (the same for the
+// whole warp) plus a 32-bit offset that no block changes.
+template <class Op, int BLOCK_ROWS>
+struct Lane {
+    using S = typename Op::S;
+    int64_t c;           // first channel
+    int64_t cd;          // c mod D
+    uint32_t seq;        // c / D
+    uint32_t row0;       // time row of the thread's first row within the block
+    bool cok;
+    uint32_t vo[Op::R];  // byte offset of each row within the block
+    __device__ __forceinline__ Lane(const SpanGeom& sg, uint32_t j, int first_row) {
+        const int lane = threadIdx.x & 31;
+        c = (int64_t)j * (32 * Op::VEC) + lane * Op::VEC;
+        seq = (uint32_t)chan_seq(sg.g, c);
+        cd = c - (int64_t)seq * sg.g.D;
+        cok = c < sg.g.C;
+        row0 = (uint32_t)(Op::REV ? BLOCK_ROWS - 1 - first_row : first_row);
+#pragma unroll
+        for (int r = 0; r < Op::R; ++r) vo[r] = (uint32_t)((row(r) * sg.g.C + c) * (int64_t)sizeof(S));
+    }
+    __device__ __forceinline__ int64_t row(int r) const { return Op::REV ? (int64_t)row0 - r : (int64_t)row0 + r; }
+    // row r of an array whose block starts at `block`
+    template <typename T>
+    __device__ __forceinline__ T* at(T* block, int r) const {
+        using B = typename std::conditional<std::is_const<T>::value, const char, char>::type;
+        return reinterpret_cast<T*>(reinterpret_cast<B*>(block) + vo[r]);
+    }
+};
+// A block of rows: its first time row, that row's element offset, and whether
+// all its rows are inside.
+struct Block {
+    int64_t t, at;
+    bool full;
+};
+// Row r of the block's thread is inside the problem.
+template <class L>
+__device__ __forceinline__ bool inside(const L& ln, const Block& bk, const SpanGeom& sg, int r) {
+    return ln.cok && (bk.full || bk.t + ln.row(r) < sg.g.T);
+}
+// The reset flags of the thread's rows, bit r.  Where the warp's channels are one
+// sequence's (one: the usual case), lane r reads row r's and a vote tells all.
+template <class Op, class L>
+__device__ __forceinline__ uint32_t resets(const GlrIn& in, const L& ln, const Block& bk, const SpanGeom& sg, bool one) {
+    if (in.reset == nullptr) return 0u;
+    const uint8_t* b = in.reset + bk.t * sg.nb;
+    if (one) {
+        const int r = (int)(threadIdx.x & 31);
+        const uint32_t row = Op::REV ? ln.row0 - r : ln.row0 + r;
+        bool hit = false;
+        if (r < Op::R && (bk.full || bk.t + row < sg.g.T)) hit = __ldg(b + row * (uint32_t)sg.nb + ln.seq) != 0;
+        return __ballot_sync(0xffffffffu, hit);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int r = 0; r < Op::R; ++r) {
+        const uint32_t o = (uint32_t)ln.row(r) * (uint32_t)sg.nb + ln.seq;
+        if (inside(ln, bk, sg, r) && __ldg(b + o) != 0) m |= 1u << r;
+    }
+    return m;
+}
+// Whether the warp's channels all belong to its first lane's sequence.
+template <class L>
+__device__ __forceinline__ bool one_sequence(const L& ln) {
+    const uint32_t first = __shfl_sync(0xffffffffu, ln.seq, 0);  // every lane takes part
+    const bool same = ln.cok && ln.seq == first;
+    return __all_sync(0xffffffffu, same) != 0;
+}
+// One row's VEC channels: from global memory (a block whose rows are all inside,
+// h_{t-1}'s too, or any), or from the staged tile.
+template <class Op, class L>
+struct FromInside {
+    const L& ln;
+    int64_t at, C;
+    template <typename S>
+    __device__ __forceinline__ void ld(Pack<S, Op::VEC>& pk, int, const S* base, int r, int back = 0) const {
+        pk.load(ln.at(base + at - back * C, r));
+    }
+};
+template <class Op, class L>
+struct FromGlobal {
+    const L& ln;
+    const Block& bk;
+    const SpanGeom& sg;
+    template <typename S>
+    __device__ __forceinline__ void ld(Pack<S, Op::VEC>& pk, int, const S* base, int r, int back = 0) const {
+        if (inside(ln, bk, sg, r) && bk.t + ln.row(r) >= back) pk.load(ln.at(base + bk.at - back * sg.g.C, r));
+        else pk.ident(0.f);
+    }
+};
+template <bool AGG, class Op, class L>
+__device__ __forceinline__ void load_global(const typename Op::Params& p, const L& ln, const Block& bk, const SpanGeom& sg,
+                                            typename Op::Regs& rg) {
+    if (bk.full && ln.cok && bk.t > 0) Op::template load<AGG>(FromInside<Op, L>{ln, bk.at, sg.g.C}, p, rg);
+    else Op::template load<AGG>(FromGlobal<Op, L>{ln, bk, sg}, p, rg);
+}
+template <class Op>
+struct FromStage {  // rows and channels outside were filled with zeros
+    const unsigned char* mine;  // the thread's first row in array 0
+    template <typename S>
+    __device__ __forceinline__ void ld(Pack<S, Op::VEC>& pk, int k, const S*, int r, int = 0) const {
+        constexpr int pitch = 32 * Op::VEC * (int)sizeof(S);
+        pk.load_shared(reinterpret_cast<const S*>(mine + tma_off<Op>(k) + (Op::REV ? -r : r) * pitch));
+    }
+};
+
+// The per-feature constants of a lane: -lam / 16 and the biases times -log2 e;
+// gen: a rate past the pairs' range (act_decay2), or 0, where the gradient of the
+// decay is 0 by definition.
+template <int VEC>
+struct Feat {
+    float l16[VEC], b2r[VEC], b2i[VEC];
+    bool gen;
+    __device__ __forceinline__ void load(const GlrIn& in, int64_t cd, bool cok) {
+        float lam[VEC], br[VEC], bi[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) { lam[v] = 1.f; br[v] = bi[v] = 0.f; }
+        if (cok) {
+            load_feat(in.lam + cd, lam);
+            load_feat(in.br + cd, br);
+            load_feat(in.bi + cd, bi);
+        }
+        gen = false;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            gen = gen || !(lam[v] > 0.f && lam[v] <= kDecayMaxRate);
+            l16[v] = -0.0625f * lam[v];
+            b2r[v] = -kLog2e * br[v];
+            b2i[v] = -kLog2e * bi[v];
+        }
+    }
+    // the general forms' arguments, exact up to the last bits of the products
+    __device__ __forceinline__ float log_a(int v, float r) const { return 16.f * l16[v] * r; }
+    __device__ __forceinline__ float gate(float z, float b2) const {
+        return rcp_ftz(1.f + ex2_ftz(fmaf(z, -kLog2e, b2)));
+    }
+    __device__ static __forceinline__ void load_feat(const float* p, float (&x)[VEC]) {
+        if constexpr (VEC == 2) {
+            const float2 f = __ldg(reinterpret_cast<const float2*>(p));
+            x[0] = f.x; x[1] = f.y;
+        } else {
+            x[0] = __ldg(p);
+        }
+    }
+};
+
+// A row's VEC values (bf16: one conversion for a pair).
+template <typename S, int VEC>
+__device__ __forceinline__ void store_row(S* p, const float (&x)[VEC]) {
+    if constexpr (sizeof(S) == 2 && VEC == 2) {
+        uint32_t w;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(x[1]), "f"(x[0]));
+        asm volatile("st.global.cs.b32 [%0], %1;" ::"l"(p), "r"(w) : "memory");
+    } else {
+        store_vec<S, VEC>(p, x);
+    }
+}
+
+// ------------------------------------------------------------------ forward
+
 template <typename S>
 struct GlrFwdParams {
-    const S* x;
-    const S* zr;
-    const S* zi;
-    const float* lam;
-    const float* br;
-    const float* bi;
-    const uint8_t* reset;
+    GlrIn in;
     const float* h0;
     S* h;
     float* h_last;
-    int64_t nb;  // sequences (row pitch of reset)
 };
 
-template <typename S_, int VEC_, int NW_, int R_>
+template <typename S_, int VEC_>
 struct GlrFwdOp {
     using S = S_;
-    static constexpr bool STRIP_ONE_BARRIER = LR_STRIP_ONEB != 0;
-    static constexpr int VEC = VEC_, NW = NW_, R = R_, MINB = 2;
+    static constexpr int VEC = VEC_, NW = 4, R = 4, MINB = 7;
     static constexpr bool REV = false;
-    static constexpr int IN_ARRAYS = 3;  // x, zr, zi
-    static constexpr bool SCRATCH_IN_CARRY = false;
+    static constexpr int NSUM = 0;
     using Params = GlrFwdParams<S>;
     struct Regs {
         Pack<S, VEC> x[R], zr[R], zi[R];
-        uint8_t rs[R];
+        uint32_t rs;  // reset rows
     };
     struct Work {
         float fa[R][VEC], fb[R][VEC];  // scan element (a, f i x)
     };
-    struct Smem {
-        int unused;
-    };
-    struct Acc {};
-    __device__ static void acc_init(Acc&) {}
-    __device__ static bool skip(const Params&) { return false; }
-    __host__ __device__ static const float* init_ptr(const Params& p) { return p.h0; }
+    __device__ static const float* init_ptr(const Params& p) { return p.h0; }
 
     static constexpr int TMA_N = 3;  // staged: x, zr, zi
     __host__ __device__ static constexpr int tma_shift(int) { return 0; }
     __host__ __device__ static constexpr int tma_extra(int) { return 0; }
     static void tma_arrays(const Params& p, const void** ptr) {
-        ptr[0] = p.x;
-        ptr[1] = p.zr;
-        ptr[2] = p.zi;
+        ptr[0] = p.in.x;
+        ptr[1] = p.in.zr;
+        ptr[2] = p.in.zi;
     }
 
-    template <class Src>
-    __device__ static void load(const Src& src, const Params& p, const Geom& g,
-                                const TileCoord& tc, Regs& rg) {
-        // a lane's channels belong to one sequence (VEC divides D)
-        const uint8_t* rs = p.reset != nullptr && tc.cok ? p.reset + chan_seq(g, tc.c) : nullptr;
+    template <bool AGG, class Src>
+    __device__ static __forceinline__ void load(const Src& src, const Params& p, Regs& rg) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t t = tc.t0 + r;
-            rg.rs[r] = 0;
-            if (tc.cok && t < g.T) {
-                src.ld(rg.x[r], 0, p.x, t);
-                src.ld(rg.zr[r], 1, p.zr, t);
-                src.ld(rg.zi[r], 2, p.zi, t);
-                if (rs != nullptr) rg.rs[r] = __ldg(rs + t * p.nb);
-            } else {
-                rg.x[r].ident(0.f);
-                rg.zr[r].ident(0.f);
-                rg.zi[r].ident(0.f);
-            }
+            src.ld(rg.x[r], 0, (const S*)p.in.x, r);
+            src.ld(rg.zr[r], 1, (const S*)p.in.zr, r);
+            src.ld(rg.zi[r], 2, (const S*)p.in.zi, r);
         }
     }
-    // Two elements at a time (neighbouring channels on the vector path,
-    // neighbouring rows on the scalar one), one reciprocal for both gates:
-    // 1/(AB) times B and A.  Gates shut past 2^-60 and decays past e^-2 take the
-    // general forms.
-    __device__ static void aggregate(const Params& p, const Geom& g, const TileCoord& tc,
-                                     const Regs& rg, Work& w, float (&A)[VEC], float (&B)[VEC],
-                                     bool) {
+    // Two elements at a time (neighbouring channels, on the scalar path
+    // neighbouring rows), one reciprocal for both gates: 1/(PQ) times Q and P.
+    // Where PQ overflows or a rate is past the pairs' range, the general forms.
+    template <class L>
+    __device__ static __forceinline__ void gates(const Params& p, const SpanGeom& sg, const L& ln, const Block& bk,
+                                                 const Feat<VEC>& ft, const Regs& rg, Work& w,
+                                                 float (&A)[VEC], float (&B)[VEC]) {
         static_assert(R * VEC % 2 == 0, "pairs");
-        float lam[VEC], br[VEC], bi[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) { lam[v] = br[v] = bi[v] = 0.f; A[v] = 1.f; B[v] = 0.f; }
-        if (tc.cok) {
-            load_param<VEC>(p.lam + tc.cd, lam);
-            load_param<VEC>(p.br + tc.cd, br);
-            load_param<VEC>(p.bi + tc.cd, bi);
-        }
-        float l8[VEC], b2r[VEC], b2i[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            l8[v] = -0.125f * lam[v];
-            b2r[v] = -kLog2e * br[v];
-            b2i[v] = -kLog2e * bi[v];
-        }
         const f32x2 one = f2(1.f), nl = f2(-kLog2e);
-        float emax = 0.f, xmin = 0.f;
+        float pmax = 0.f;
 #pragma unroll
         for (int e = 0; e < R * VEC; e += 2) {
             const int r0 = e / VEC, v0 = e % VEC, r1 = (e + 1) / VEC, v1 = (e + 1) % VEC;
-            float er0, er1, ei0, ei1;
-            f2_get(f2_fma(f2(rg.zr[r0].get(v0), rg.zr[r1].get(v1)), nl, f2(b2r[v0], b2r[v1])), er0, er1);
-            f2_get(f2_fma(f2(rg.zi[r0].get(v0), rg.zi[r1].get(v1)), nl, f2(b2i[v0], b2i[v1])), ei0, ei1);
-            emax = fmaxf(fmaxf(emax, fmaxf(er0, er1)), fmaxf(ei0, ei1));
-            const f32x2 P = f2_add(f2(ex2_ftz(er0), ex2_ftz(er1)), one);
-            const f32x2 Q = f2_add(f2(ex2_ftz(ei0), ex2_ftz(ei1)), one);
-            float t0, t1;
+            float a0, a1, b0, b1, t0, t1;
+            f2_get(f2_fma(f2(rg.zr[r0].get(v0), rg.zr[r1].get(v1)), nl, f2(ft.b2r[v0], ft.b2r[v1])), a0, a1);
+            f2_get(f2_fma(f2(rg.zi[r0].get(v0), rg.zi[r1].get(v1)), nl, f2(ft.b2i[v0], ft.b2i[v1])), b0, b1);
+            const f32x2 P = f2_add(f2(ex2_ftz(a0), ex2_ftz(a1)), one);
+            const f32x2 Q = f2_add(f2(ex2_ftz(b0), ex2_ftz(b1)), one);
             f2_get(f2_mul(P, Q), t0, t1);
+            pmax = fmaxf(pmax, fmaxf(t0, t1));
             const f32x2 t = f2(rcp_ftz(t0), rcp_ftz(t1));
-            const f32x2 x = f2_mul(f2_mul(t, Q), f2(l8[v0], l8[v1]));
             const f32x2 u = f2_mul(f2_mul(t, P), f2(rg.x[r0].get(v0), rg.x[r1].get(v1)));
-            float x0, x1, q0, q1;
-            f2_get(x, x0, x1);
-            xmin = fminf(xmin, fminf(x0, x1));
-            f32x2 a, nq;
-            act_decay2(x, a, nq);
-            f2_get(nq, q0, q1);
+            float q0, q1;
+            f32x2 a, q;
+            act_decay2(f2_mul(f2_mul(t, Q), f2(ft.l16[v0], ft.l16[v1])), a, q);
+            f2_get(q, q0, q1);
             f2_get(a, w.fa[r0][v0], w.fa[r1][v1]);
-            f2_get(f2_mul(u, f2(sqrt_ftz(-q0), sqrt_ftz(-q1))), w.fb[r0][v0], w.fb[r1][v1]);
+            f2_get(f2_mul(u, f2_mul(q, f2(rsqrt_ftz(q0), rsqrt_ftz(q1)))), w.fb[r0][v0], w.fb[r1][v1]);
         }
-        bool any = emax > kGateMaxExp || xmin < kDecayMinX || !(tc.cok && tc.t0 + R - 1 < g.T);
-#pragma unroll
-        for (int r = 0; r < R; ++r) any = any || rg.rs[r] != 0;
-        if (any) {
+        const bool gen = ft.gen || pmax > 1e38f;
+        if (gen || rg.rs != 0 || !ln.cok || !bk.full) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const bool ok = tc.cok && tc.t0 + r < g.T, reset = rg.rs[r] != 0;
-                if (ok && !reset && !(emax > kGateMaxExp || xmin < kDecayMinX)) continue;
+                const bool ok = inside(ln, bk, sg, r), reset = (rg.rs >> r & 1u) != 0;
+                if (ok && !reset && !gen) continue;
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     float a, q;
-                    act_decay(-lam[v] * act_sigmoid(rg.zr[r].get(v) + br[v]), a, q);
-                    const float u = act_sigmoid(rg.zi[r].get(v) + bi[v]) * rg.x[r].get(v);
+                    act_decay(ft.log_a(v, ft.gate(rg.zr[r].get(v), ft.b2r[v])), a, q);
+                    const float u = ft.gate(rg.zi[r].get(v), ft.b2i[v]) * rg.x[r].get(v);
                     w.fa[r][v] = ok ? (reset ? 0.f : a) : 1.f;
                     w.fb[r][v] = ok ? (reset ? u : sqrt_ftz(q) * u) : 0.f;
                 }
             }
         }
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int v = 0; v < VEC; ++v) { A[v] = w.fa[0][v]; B[v] = w.fb[0][v]; }
+#pragma unroll
+        for (int r = 1; r < R; ++r)
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 B[v] = __fmaf_rn(w.fa[r][v], B[v], w.fb[r][v]);
                 A[v] *= w.fa[r][v];
             }
     }
-    __device__ static void finish(const Params& p, const Geom& g, const TileCoord& tc,
-                                  const Regs&, Work& w, float (&s)[VEC], Smem&, Acc&) {
+    template <class L>
+    __device__ static __forceinline__ void finish(const Params& p, const SpanGeom& sg, const L& ln, const Block& bk,
+                                                  const Feat<VEC>&, const Regs&, const Work& w,
+                                                  float (&s)[VEC], float (&)[1][VEC]) {
+        S* h = p.h + bk.at;
+        float o[R][VEC];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int64_t t = tc.t0 + r;
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) s[v] = w.fa[r][v] * s[v] + w.fb[r][v];
-            if (tc.cok && t < g.T) {
-                store_vec<S, VEC>(p.h + t * g.C + tc.c, s);
-                if (t == g.T - 1 && p.h_last != nullptr) store_vec<float, VEC>(p.h_last + tc.c, s);
+            for (int v = 0; v < VEC; ++v) o[r][v] = s[v] = __fmaf_rn(w.fa[r][v], s[v], w.fb[r][v]);
+        if (bk.full) {
+            if (ln.cok) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) store_row(ln.at(h, r), o[r]);
             }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (inside(ln, bk, sg, r)) store_row(ln.at(h, r), o[r]);
         }
+        if (bk.t + NW * R >= sg.g.T && p.h_last != nullptr && inside(ln, bk, sg, 0) && bk.t + ln.row(R) >= sg.g.T)
+            store_vec<float, VEC>(p.h_last + ln.c, s);  // rows past the end kept s
     }
-    __device__ static void at_exit(const Params&, Smem&, Acc&) {}
+    template <class L>
+    __device__ static __forceinline__ void last(const Params&, const L&, const float (&)[VEC]) {}
+    __device__ static float* sums(const Params&) { return nullptr; }
 };
+
+// ----------------------------------------------------------------- backward
 
 template <typename S>
 struct GlrBwdParams {
-    const S* x;
-    const S* zr;
-    const S* zi;
-    const float* lam;
-    const float* br;
-    const float* bi;
-    const uint8_t* reset;
+    GlrIn in;
     const float* h0;
     const S* h;
     const S* dh;
@@ -199,270 +346,437 @@ struct GlrBwdParams {
     S* dzr;
     S* dzi;
     float* dh0;
-    float* partials;  // [3][n_chunks][C]: rate, decay bias, input bias
-    int64_t nb;
+    float* partials;  // [3][S][C]: rate, decay bias, input bias
 };
 
-template <typename S_, int VEC_, int NW_, int R_>
+template <typename S_, int VEC_>
 struct GlrBwdOp {
     using S = S_;
-    static constexpr int VEC = VEC_, NW = NW_, R = R_, MINB = 2;
+    static constexpr int VEC = VEC_, NW = 4, R = 4, MINB = 5;
     static constexpr bool REV = true;
-    static constexpr int IN_ARRAYS = 5;  // x, zr, zi, dh, h_{t-1}
+    static constexpr int NSUM = 3;
     using Params = GlrBwdParams<S>;
     struct Regs {
         Pack<S, VEC> x[R], zr[R], zi[R], dh[R], hp[R];
-        uint8_t rs[R];
+        uint32_t rs;  // reset rows
     };
     struct Work {
-        float F[R][VEC];   // a
-        float CX[R][VEC];  // dx / d = f i
-        float CI[R][VEC];  // dzi / d = f x i (1-i)
-        float KR[R][VEC];  // dlam's term / d = -K r
-        float CR[R][VEC];  // dzr / d = -lam K r (1-r)
+        float F[R][VEC];   // a (0 on a reset step, 1 outside)
+        float rr[R][VEC];  // r
+        float q[R][VEC];   // 1 - a^2
+        bool gen;          // some row needs the general forms
     };
-    struct Smem {
-        float ps[3][NW][32][VEC];
-    };
-    // 12 KB of their own: more than the carry's warp aggregates hold, and two
-    // CTAs of 40 KB stages still fit an SM.
-    static constexpr bool SCRATCH_IN_CARRY = false;
-    struct Acc {
-        float s[3][VEC];  // parameter sums over a run of tiles (acc_run)
-    };
-    __device__ static void acc_init(Acc& a) {
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) a.s[k][v] = 0.f;
-    }
-    __device__ static bool skip(const Params&) { return false; }
-    __host__ __device__ static const float* init_ptr(const Params& p) { return p.dh_last; }  // w_T
+    __device__ static const float* init_ptr(const Params& p) { return p.dh_last; }  // w_T
 
     static constexpr int TMA_N = 5;  // staged: x, zr, zi, dh, h (rows t0-1 .. t0+L-2)
     __host__ __device__ static constexpr int tma_shift(int k) { return k == 4 ? -1 : 0; }
     __host__ __device__ static constexpr int tma_extra(int) { return 0; }
     static void tma_arrays(const Params& p, const void** ptr) {
-        ptr[0] = p.x;
-        ptr[1] = p.zr;
-        ptr[2] = p.zi;
+        ptr[0] = p.in.x;
+        ptr[1] = p.in.zr;
+        ptr[2] = p.in.zi;
         ptr[3] = p.dh;
         ptr[4] = p.h;
     }
 
-    template <class Src>
-    __device__ static void load(const Src& src, const Params& p, const Geom& g,
-                                const TileCoord& tc, Regs& rg) {
-        const uint8_t* rs = p.reset != nullptr && tc.cok ? p.reset + chan_seq(g, tc.c) : nullptr;
+    // AGG: what the aggregate needs, zr and dh.
+    template <bool AGG, class Src>
+    __device__ static __forceinline__ void load(const Src& src, const Params& p, Regs& rg) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t t = tc.t0 - r;
-            rg.rs[r] = 0;
-            if (tc.cok && t < g.T) {
-                src.ld(rg.x[r], 0, p.x, t);
-                src.ld(rg.zr[r], 1, p.zr, t);
-                src.ld(rg.zi[r], 2, p.zi, t);
-                src.ld(rg.dh[r], 3, p.dh, t);
-                if (t > 0) src.ld(rg.hp[r], 4, p.h, t - 1);
-                else rg.hp[r].ident(0.f);  // h0 is fp32: aggregate() reads it
-                if (rs != nullptr) rg.rs[r] = __ldg(rs + t * p.nb);
-            } else {
-                rg.x[r].ident(0.f);
-                rg.zr[r].ident(0.f);
-                rg.zi[r].ident(0.f);
-                rg.dh[r].ident(0.f);
-                rg.hp[r].ident(0.f);
+            src.ld(rg.zr[r], 1, (const S*)p.in.zr, r);
+            src.ld(rg.dh[r], 3, p.dh, r);
+            if constexpr (!AGG) {
+                src.ld(rg.x[r], 0, (const S*)p.in.x, r);
+                src.ld(rg.zi[r], 2, (const S*)p.in.zi, r);
+                src.ld(rg.hp[r], 4, p.h, r, 1);  // h_{t-1}; h0 is fp32: finish() reads it
             }
         }
     }
-    // As the forward pass, two elements at a time; a square root's pole (a decay
-    // of 1 to the last bit) takes the general form too.  The pass that only wants
-    // the aggregate (side = false) needs no more than the decay.
-    __device__ static void aggregate(const Params& p, const Geom& g, const TileCoord& tc,
-                                     const Regs& rg, Work& w, float (&A)[VEC], float (&B)[VEC],
-                                     bool side) {
+    // The decay alone, and the scan's element (F, F dh): w = F (dh + w').
+    template <class L>
+    __device__ static __forceinline__ void gates(const Params& p, const SpanGeom& sg, const L& ln, const Block& bk,
+                                                 const Feat<VEC>& ft, const Regs& rg, Work& w,
+                                                 float (&A)[VEC], float (&B)[VEC]) {
         static_assert(R * VEC % 2 == 0, "pairs");
-        float lam[VEC], br[VEC], bi[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) { lam[v] = br[v] = bi[v] = 0.f; A[v] = 1.f; B[v] = 0.f; }
-        if (tc.cok) {
-            load_param<VEC>(p.lam + tc.cd, lam);
-            load_param<VEC>(p.br + tc.cd, br);
-            load_param<VEC>(p.bi + tc.cd, bi);
-        }
-        float l8[VEC], b2r[VEC], b2i[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            l8[v] = -0.125f * lam[v];
-            b2r[v] = -kLog2e * br[v];
-            b2i[v] = -kLog2e * bi[v];
-        }
-        const f32x2 one = f2(1.f), none = f2(-1.f), nl = f2(-kLog2e);
-        float emax = 0.f, xmin = 0.f, qmin = 1.f;
+        const f32x2 one = f2(1.f), nl = f2(-kLog2e);
 #pragma unroll
         for (int e = 0; e < R * VEC; e += 2) {
             const int r0 = e / VEC, v0 = e % VEC, r1 = (e + 1) / VEC, v1 = (e + 1) % VEC;
-            float er0, er1;
-            f2_get(f2_fma(f2(rg.zr[r0].get(v0), rg.zr[r1].get(v1)), nl, f2(b2r[v0], b2r[v1])), er0, er1);
-            emax = fmaxf(emax, fmaxf(er0, er1));
-            float t0, t1;
-            f2_get(f2_add(f2(ex2_ftz(er0), ex2_ftz(er1)), one), t0, t1);
-            const f32x2 rr = f2(rcp_ftz(t0), rcp_ftz(t1));
-            const f32x2 x = f2_mul(rr, f2(l8[v0], l8[v1]));
-            float x0, x1;
-            f2_get(x, x0, x1);
-            xmin = fminf(xmin, fminf(x0, x1));
-            f32x2 a, nq;
-            act_decay2(x, a, nq);
+            float a0, a1, t0, t1;
+            f2_get(f2_fma(f2(rg.zr[r0].get(v0), rg.zr[r1].get(v1)), nl, f2(ft.b2r[v0], ft.b2r[v1])), a0, a1);
+            f2_get(f2_add(f2(ex2_ftz(a0), ex2_ftz(a1)), one), t0, t1);
+            w.rr[r0][v0] = rcp_ftz(t0);
+            w.rr[r1][v1] = rcp_ftz(t1);
+            f32x2 a, q;
+            act_decay2(f2_mul(f2(w.rr[r0][v0], w.rr[r1][v1]), f2(ft.l16[v0], ft.l16[v1])), a, q);
             f2_get(a, w.F[r0][v0], w.F[r1][v1]);
-            if (side) {
-                float ei0, ei1, q0, q1;
-                f2_get(f2_fma(f2(rg.zi[r0].get(v0), rg.zi[r1].get(v1)), nl, f2(b2i[v0], b2i[v1])), ei0, ei1);
-                emax = fmaxf(emax, fmaxf(ei0, ei1));
-                f2_get(f2_add(f2(ex2_ftz(ei0), ex2_ftz(ei1)), one), t0, t1);
-                const f32x2 ii = f2(rcp_ftz(t0), rcp_ftz(t1));
-                f2_get(nq, q0, q1);
-                qmin = fminf(qmin, fminf(-q0, -q1));
-                const f32x2 nrf = f2(-rsqrt_ftz(-q0), -rsqrt_ftz(-q1));  // -1/f
-                const f32x2 f = f2_mul(nq, nrf);
-                const f32x2 u = f2_mul(ii, f2(rg.x[r0].get(v0), rg.x[r1].get(v1)));
-                const f32x2 h = f2(rg.hp[r0].get(v0), rg.hp[r1].get(v1));
-                // K = a (h - u a / f);  -K r, its product with lam (1 - r)
-                const f32x2 K = f2_mul(a, f2_fma(f2_mul(u, a), nrf, h));
-                const f32x2 nr = f2_mul(rr, none);
-                const f32x2 KR = f2_mul(K, nr);
-                const f32x2 CR = f2_mul(f2_mul(KR, f2(lam[v0], lam[v1])), f2_add(nr, one));
-                const f32x2 CI = f2_mul(f2_mul(f, u), f2_fma(ii, none, one));
-                f2_get(f2_mul(f, ii), w.CX[r0][v0], w.CX[r1][v1]);
-                f2_get(CI, w.CI[r0][v0], w.CI[r1][v1]);
-                f2_get(KR, w.KR[r0][v0], w.KR[r1][v1]);
-                f2_get(CR, w.CR[r0][v0], w.CR[r1][v1]);
-            }
+            f2_get(q, w.q[r0][v0], w.q[r1][v1]);
         }
-        const bool gen = emax > kGateMaxExp || xmin < kDecayMinX || !(qmin > 0.f);
-        bool any = gen || !(tc.cok && tc.t0 < g.T) || (p.h0 != nullptr && tc.t0 - (R - 1) <= 0);
-#pragma unroll
-        for (int r = 0; r < R; ++r) any = any || rg.rs[r] != 0;
-        if (any) {
+        w.gen = ft.gen || rg.rs != 0 || (p.h0 != nullptr && bk.t + ln.row(R - 1) == 0);
+        if (ft.gen || rg.rs != 0 || !ln.cok || !bk.full) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const int64_t t = tc.t0 - r;
-                const bool ok = tc.cok && t < g.T, reset = rg.rs[r] != 0;
-                const bool first = ok && t == 0 && p.h0 != nullptr;  // h0 is fp32
-                if (ok && !reset && !gen && !first) continue;
+                const bool ok = inside(ln, bk, sg, r), reset = (rg.rs >> r & 1u) != 0;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    float a = w.F[r][v], q;
+                    if (ft.gen) act_decay(ft.log_a(v, w.rr[r][v]), a, q);
+                    w.F[r][v] = ok ? (reset ? 0.f : a) : 1.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) { A[v] = w.F[0][v]; B[v] = w.F[0][v] * rg.dh[0].get(v); }
+#pragma unroll
+        for (int r = 1; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                B[v] = w.F[r][v] * (rg.dh[r].get(v) + B[v]);
+                A[v] *= w.F[r][v];
+            }
+    }
+    template <class L>
+    __device__ static __forceinline__ void finish(const Params& p, const SpanGeom& sg, const L& ln, const Block& bk,
+                                                  const Feat<VEC>& ft, const Regs& rg, const Work& w,
+                                                  float (&s)[VEC], float (&sum)[3][VEC]) {
+        float d[R][VEC];  // d_t
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                d[r][v] = rg.dh[r].get(v) + s[v];
+                s[v] = w.F[r][v] * d[r][v];
+            }
+        float dx[R][VEC], dzr[R][VEC], dzi[R][VEC], dl_[R][VEC];
+        if (!w.gen) {
+            const f32x2 one = f2(1.f), none = f2(-1.f), nl = f2(-kLog2e);
+#pragma unroll
+            for (int e = 0; e < R * VEC; e += 2) {
+                const int r0 = e / VEC, v0 = e % VEC, r1 = (e + 1) / VEC, v1 = (e + 1) % VEC;
+                float b0, b1, t0, t1;
+                f2_get(f2_fma(f2(rg.zi[r0].get(v0), rg.zi[r1].get(v1)), nl, f2(ft.b2i[v0], ft.b2i[v1])), b0, b1);
+                f2_get(f2_add(f2(ex2_ftz(b0), ex2_ftz(b1)), one), t0, t1);
+                const f32x2 ii = f2(rcp_ftz(t0), rcp_ftz(t1));
+                const f32x2 a = f2(w.F[r0][v0], w.F[r1][v1]);
+                const f32x2 rf = f2(rsqrt_ftz(w.q[r0][v0]), rsqrt_ftz(w.q[r1][v1]));  // 1/f
+                const f32x2 f = f2_mul(f2(w.q[r0][v0], w.q[r1][v1]), rf);
+                const f32x2 u = f2_mul(ii, f2(rg.x[r0].get(v0), rg.x[r1].get(v1)));
+                const f32x2 dd = f2(d[r0][v0], d[r1][v1]);
+                const f32x2 df = f2_mul(dd, f);
+                f2_get(f2_mul(df, ii), dx[r0][v0], dx[r1][v1]);
+                f2_get(f2_mul(f2_mul(df, u), f2_fma(ii, none, one)), dzi[r0][v0], dzi[r1][v1]);
+                // K = a (h - u a / f);  -d K r is lam's term, times lam (1 - r) zr's
+                const f32x2 nh = f2_mul(f2(rg.hp[r0].get(v0), rg.hp[r1].get(v1)), none);
+                const f32x2 nK = f2_mul(a, f2_fma(f2_mul(u, a), rf, nh));
+                const f32x2 rr = f2(w.rr[r0][v0], w.rr[r1][v1]);
+                const f32x2 dl = f2_mul(f2_mul(dd, nK), rr);
+                // l16 = -lam / 16: -16 l16 dl (1 - r), the 16 exact
+                const f32x2 lr = f2_mul(f2(ft.l16[v0], ft.l16[v1]), f2_fma(rr, f2(16.f), f2(-16.f)));
+                f2_get(f2_mul(dl, lr), dzr[r0][v0], dzr[r1][v1]);
+                f2_get(dl, dl_[r0][v0], dl_[r1][v1]);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const bool reset = (rg.rs >> r & 1u) != 0;
                 float hp[VEC];
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) hp[v] = rg.hp[r].get(v);
-                if (first) load_vec<float, VEC>(p.h0 + tc.c, hp);
+                if (p.h0 != nullptr && ln.cok && bk.t + ln.row(r) == 0) load_vec<float, VEC>(p.h0 + ln.c, hp);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
-                    const float rr = act_sigmoid(rg.zr[r].get(v) + br[v]);
-                    const float ii = act_sigmoid(rg.zi[r].get(v) + bi[v]);
+                    const float rr = w.rr[r][v];
+                    const float ii = ft.gate(rg.zi[r].get(v), ft.b2i[v]);
                     float a, q;
-                    act_decay(-lam[v] * rr, a, q);
+                    act_decay(ft.log_a(v, rr), a, q);
                     // where the decay is 1 to the last bit (q = 0) its gradient is
                     // 0: K's pole is cancelled by r (1-r) -> 0
                     const float rf = q > 0.f ? rsqrt_ftz(q) : q;
                     const float f = reset ? 1.f : q * rf;
                     const float u = ii * rg.x[r].get(v);
                     const float K = reset || q == 0.f ? 0.f : a * (hp[v] - u * a * rf);
-                    w.F[r][v] = ok ? (reset ? 0.f : a) : 1.f;
-                    w.CX[r][v] = f * ii;
-                    w.CI[r][v] = f * u * (1.f - ii);
-                    w.KR[r][v] = -K * rr;
-                    w.CR[r][v] = lam[v] * (w.KR[r][v] * (1.f - rr));
+                    const float dl = -d[r][v] * K * rr;
+                    dx[r][v] = d[r][v] * f * ii;
+                    dzi[r][v] = d[r][v] * f * u * (1.f - ii);
+                    dzr[r][v] = dl * (-16.f * ft.l16[v]) * (1.f - rr);
+                    dl_[r][v] = dl;
                 }
             }
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r)
+        S *ox = p.dx + bk.at, *or_ = p.dzr + bk.at, *oi = p.dzi + bk.at;
+        auto put = [&](int r) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                // rows outside hold dh = 0 and F = 1
-                B[v] = w.F[r][v] * (rg.dh[r].get(v) + B[v]);
-                A[v] *= w.F[r][v];
+                sum[0][v] += dl_[r][v];
+                sum[1][v] += dzr[r][v];
+                sum[2][v] += dzi[r][v];
             }
-    }
-    __device__ static void finish(const Params& p, const Geom& g, const TileCoord& tc,
-                                  const Regs& rg, Work& w, float (&s)[VEC], Smem& xs, Acc& acc) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        float sum[3][VEC];
+            store_row(ln.at(ox, r), dx[r]);
+            store_row(ln.at(or_, r), dzr[r]);
+            store_row(ln.at(oi, r), dzi[r]);
+        };
+        if (bk.full) {
+            if (ln.cok) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) sum[k][v] = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int64_t t = tc.t0 - r;
-            const bool ok = tc.cok && t < g.T;
-            float dx[VEC], dzr[VEC], dzi[VEC];
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float d = rg.dh[r].get(v) + s[v];
-                dx[v] = d * w.CX[r][v];
-                dzr[v] = d * w.CR[r][v];
-                dzi[v] = d * w.CI[r][v];
-                if (ok) {
-                    sum[0][v] += d * w.KR[r][v];
-                    sum[1][v] += dzr[v];
-                    sum[2][v] += dzi[v];
-                }
-                s[v] = w.F[r][v] * d;
+                for (int r = 0; r < R; ++r) put(r);
             }
-            if (ok) {
-                store_vec<S, VEC>(p.dx + t * g.C + tc.c, dx);
-                store_vec<S, VEC>(p.dzr + t * g.C + tc.c, dzr);
-                store_vec<S, VEC>(p.dzi + t * g.C + tc.c, dzi);
-            }
-        }
-        if (tc.tchunk == 0 && warp == NW - 1 && p.dh0 != nullptr && tc.cok)
-            store_vec<float, VEC>(p.dh0 + tc.c, s);
-        const int64_t arr = g.n_chunks * g.C;
-        float* out = p.partials + tc.tchunk * g.C + tc.c;
-        if (tc.acc_run) {
-            // a run of tiles of these channels through this CTA (see the SRU
-            // backward pass): zeros but for the run's last tile
+        } else {  // rows outside hold a neighbour's d
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) acc.s[k][v] += sum[k][v];
-            if (!tc.acc_flush) {
-                if (warp == 0 && tc.cok) {
-#pragma unroll
-                    for (int k = 0; k < 3; ++k)
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) out[k * arr + v] = 0.f;
-                }
-                return;
-            }
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    sum[k][v] = acc.s[k][v];
-                    acc.s[k][v] = 0.f;
-                }
-        }
-        csync<NW>();  // every warp is past its reads of the previous tile's sums
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) xs.ps[k][warp][lane][v] = sum[k][v];
-        csync<NW>();
-        if (warp == 0 && tc.cok) {
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    float t = 0.f;
-#pragma unroll
-                    for (int ww = 0; ww < NW; ++ww) t += xs.ps[k][ww][lane][v];
-                    out[k * arr + v] = t;
-                }
+            for (int r = 0; r < R; ++r)
+                if (inside(ln, bk, sg, r)) put(r);
         }
     }
-    __device__ static void at_exit(const Params&, Smem&, Acc&) {}
+    // the state after the last row of the scan: w_0
+    template <class L>
+    __device__ static __forceinline__ void last(const Params& p, const L& ln, const float (&s)[VEC]) {
+        if (p.dh0 != nullptr && ln.cok) store_vec<float, VEC>(p.dh0 + ln.c, s);
+    }
+    __device__ static float* sums(const Params& p) { return p.partials; }
 };
+
+// ------------------------------------------------------------------ kernels
+
+template <int VEC, int NW>
+struct SpanSmem {
+    float a[2][NW][32][VEC];
+    float b[2][NW][32][VEC];
+    float carry[2][32][VEC];
+};
+
+// The aggregate of span sp, strip j: (A, B) of its rows in scan order.  Warp w
+// folds the span's row groups [w cps, (w+1) cps), loading one group ahead.
+template <class Op>
+__global__ void __launch_bounds__(Op::NW * 32)
+    k_glr_agg(const typename Op::Params p, const SpanGeom sg, float2* __restrict__ agg) {
+    constexpr int NW = Op::NW, VEC = Op::VEC;
+    __shared__ float sa[NW][32][VEC], sb[NW][32][VEC];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sp = blockIdx.x / (uint32_t)sg.g.n_ct, j = blockIdx.x - sp * (uint32_t)sg.g.n_ct;
+    // row groups of R: the warp's run, in scan order
+    const int64_t g0 = ((int64_t)sp * NW + __shfl_sync(0xffffffffu, warp, 0)) * sg.cps;
+    const int64_t rows = sg.g.n_chunks * (NW * Op::R);
+    using L = Lane<Op, Op::R>;
+    const L ln(sg, j, 0);
+    auto place = [&](int64_t t) { return Block{t, t * sg.g.C, t + Op::R <= sg.g.T}; };
+    const int64_t tstep = Op::REV ? -Op::R : Op::R, estep = tstep * sg.g.C;
+    const bool one = one_sequence(ln);
+    Feat<VEC> ft;
+    ft.load(p.in, ln.cd, ln.cok);
+    float A[VEC], B[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) { A[v] = 1.f; B[v] = 0.f; }
+    typename Op::Regs rg[2];
+    auto fetch = [&](const Block& bk, typename Op::Regs& r) {
+        load_global<true, Op>(p, ln, bk, sg, r);
+        r.rs = resets<Op>(p.in, ln, bk, sg, one);
+    };
+    Block bk = place(Op::REV ? rows - Op::R - g0 * Op::R : g0 * Op::R);
+    fetch(bk, rg[0]);
+    for (uint32_t k = 0; k < sg.cps; k += 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (k + h >= sg.cps) break;
+            const int64_t t = bk.t + tstep;
+            const Block nx{t, bk.at + estep, t + Op::R <= sg.g.T};
+            if (k + h + 1 < sg.cps) fetch(nx, rg[h ^ 1]);
+            typename Op::Work w;
+            float a[VEC], b[VEC];
+            Op::gates(p, sg, ln, bk, ft, rg[h], w, a, b);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                B[v] = __fmaf_rn(a[v], B[v], b[v]);
+                A[v] *= a[v];
+            }
+            bk = nx;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) { sa[warp][lane][v] = A[v]; sb[warp][lane][v] = B[v]; }
+    __syncthreads();
+    if (warp != 0 || !ln.cok) return;
+#pragma unroll
+    for (int w = 1; w < NW; ++w)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            B[v] = __fmaf_rn(sa[w][lane][v], B[v], sb[w][lane][v]);
+            A[v] *= sa[w][lane][v];
+        }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) agg[(int64_t)sp * sg.g.C + ln.c + v] = make_float2(A[v], B[v]);
+}
+
+// Thread 0: stage `it % ST` <- the tile of chunk q (scan order), strip j.
+template <class Op, int ST>
+__device__ __forceinline__ void span_issue(const SpanGeom& sg, const TmaDesc& td, unsigned char* ring, uint64_t* full,
+                                           uint32_t it, uint32_t q, uint32_t j) {
+    constexpr int L = Op::NW * Op::R, CW = 32 * Op::VEC;
+    const int64_t tchunk = Op::REV ? sg.g.n_chunks - 1 - q : q;
+    const int32_t x = (int32_t)(j * CW), y0 = (int32_t)(tchunk * L);
+    const uint32_t st = it % ST;
+    mbar_arrive_tx(&full[st], td.tx_bytes);
+    unsigned char* dst = ring + st * tma_stage_bytes<Op>();
+#pragma unroll
+    for (int a = 0; a < Op::TMA_N; ++a)
+        tma_load_2d(dst + tma_off<Op>(a), &td.map[a], x, y0 + Op::tma_shift(a), &full[st]);
+}
+
+// Span sp of strip j.  ST > 0: tiles through a ring of ST stages filled by TMA;
+// ST = 0 (rows TMA cannot take): through registers, one tile ahead.  One barrier
+// per tile: the warps' aggregates alternate between two buffers, every warp folds
+// those before its own onto the carried state, and the last one carries on.
+template <class Op, int ST>
+__global__ void __launch_bounds__(Op::NW * 32, ST > 0 ? Op::MINB : Op::MINB - 2)
+    k_glr_span(const typename Op::Params p, const SpanGeom sg, const float2* __restrict__ agg, uint32_t* err,
+               const __grid_constant__ TmaDesc td) {
+    constexpr int NW = Op::NW, VEC = Op::VEC, L = NW * Op::R;
+    constexpr int NS = Op::NSUM > 0 ? Op::NSUM : 1;
+    extern __shared__ unsigned char dyn[];
+    unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dyn) + 127) & ~(uintptr_t)127);
+    __shared__ SpanSmem<VEC, NW> sm;
+    __shared__ __align__(8) uint64_t full[ST > 0 ? ST : 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sp = blockIdx.x / (uint32_t)sg.g.n_ct, j = blockIdx.x - sp * (uint32_t)sg.g.n_ct;
+    const uint32_t q0 = sp * sg.cps;
+    const uint32_t n = (uint32_t)sg.g.n_chunks - q0 < sg.cps ? (uint32_t)sg.g.n_chunks - q0 : sg.cps;
+    if (ST > 0 && threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) mbar_init(&full[i], 1);
+        mbar_init_fence();
+        for (uint32_t i = 0; i < (uint32_t)ST && i < n; ++i)
+            span_issue<Op, ST>(sg, td, ring, full, i, q0 + i, j);
+    }
+    using Ln = Lane<Op, L>;
+    const Ln ln(sg, j, warp * Op::R);
+    const int64_t tstep = Op::REV ? -L : L, estep = tstep * sg.g.C;
+    const bool one = one_sequence(ln);
+    Block bk;
+    bk.t = (Op::REV ? sg.g.n_chunks - 1 - q0 : (int64_t)q0) * L;
+    bk.at = bk.t * sg.g.C;
+    bk.full = bk.t + L <= sg.g.T;
+    typename Op::Regs rg, ahead;
+    if constexpr (ST == 0) load_global<false, Op>(p, ln, bk, sg, rg);
+    rg.rs = resets<Op>(p.in, ln, bk, sg, one);
+    Feat<VEC> ft;
+    ft.load(p.in, ln.cd, ln.cok);
+    const uint32_t mine = ln.row0 * (32 * VEC * (uint32_t)sizeof(typename Op::S)) + lane * (VEC * (uint32_t)sizeof(typename Op::S));
+    {  // the state entering the span: each warp folds its share of the spans before
+        griddep_wait();  // (launched while k_glr_agg runs)
+        float A[VEC], B[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) { A[v] = 1.f; B[v] = 0.f; }
+        const uint32_t lo = (uint32_t)((uint64_t)sp * warp / NW), hi = (uint32_t)((uint64_t)sp * (warp + 1) / NW);
+        if (ln.cok) {
+#pragma unroll 4
+            for (uint32_t k = lo; k < hi; ++k)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float2 e = agg[(int64_t)k * sg.g.C + ln.c + v];
+                    B[v] = __fmaf_rn(e.x, B[v], e.y);
+                    A[v] *= e.x;
+                }
+        }
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) { sm.a[1][warp][lane][v] = A[v]; sm.b[1][warp][lane][v] = B[v]; }
+        __syncthreads();
+        if (warp == 0) {
+            float s[VEC];
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) s[v] = 0.f;
+            const float* ip = Op::init_ptr(p);
+            if (ip != nullptr && ln.cok) load_vec<float, VEC>(ip + ln.c, s);
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) s[v] = __fmaf_rn(sm.a[1][w][lane][v], s[v], sm.b[1][w][lane][v]);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) sm.carry[0][lane][v] = s[v];
+        }
+        // carry[0] is read after the first tile's barrier
+    }
+    float sum[NS][VEC];
+#pragma unroll
+    for (int k = 0; k < NS; ++k)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) sum[k][v] = 0.f;
+    bool dead = false;
+    // one tile; PAR: its buffer (and stage: two), known to the compiler
+    auto tile = [&](auto par_, uint32_t it) {
+        constexpr int PAR = decltype(par_)::value;
+        const bool more = it + 1 < n;
+        const int64_t t = bk.t + tstep;
+        const Block nx{t, bk.at + estep, t + L <= sg.g.T};
+        if constexpr (ST > 0) {
+            if (!mbar_wait(&full[PAR], (it >> 1) & 1u, err)) {
+                dead = true;  // the states become NaN
+                atomicOr(err, ERRBIT_TIMEOUT);
+            }
+            Op::template load<false>(FromStage<Op>{ring + PAR * tma_stage_bytes<Op>() + mine}, p, rg);
+        } else if (more) {
+            load_global<false, Op>(p, ln, nx, sg, ahead);
+        }
+        if (more) ahead.rs = resets<Op>(p.in, ln, nx, sg, one);
+        float A[VEC], B[VEC];
+        typename Op::Work w;
+        Op::gates(p, sg, ln, bk, ft, rg, w, A, B);
+        if (ST > 0 && dead) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) B[v] = __int_as_float(0x7fc00000);
+        }
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) { sm.a[PAR][warp][lane][v] = A[v]; sm.b[PAR][warp][lane][v] = B[v]; }
+        csync<NW>();  // the tile's one barrier: its stage has been read too
+        if (ST > 0 && threadIdx.x == 0 && it + ST < n && !dead)
+            span_issue<Op, ST>(sg, td, ring, full, it + ST, q0 + it + ST, j);
+        float s[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) s[v] = sm.carry[PAR][lane][v];
+#pragma unroll
+        for (int w2 = 0; w2 < NW - 1; ++w2)
+            if (w2 < warp) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) s[v] = __fmaf_rn(sm.a[PAR][w2][lane][v], s[v], sm.b[PAR][w2][lane][v]);
+            }
+        Op::finish(p, sg, ln, bk, ft, rg, w, s, sum);
+        if (warp == NW - 1) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) sm.carry[PAR ^ 1][lane][v] = s[v];
+            if (!more && sp + 1 == sg.S) Op::last(p, ln, s);
+        }
+        if constexpr (ST == 0) rg = ahead;
+        else rg.rs = ahead.rs;
+        bk = nx;
+    };
+    static_assert(ST == 0 || ST == 2, "a stage per buffer");
+    for (uint32_t it = 0; it < n; it += 2) {
+        tile(std::integral_constant<int, 0>{}, it);
+        if (it + 1 < n) tile(std::integral_constant<int, 1>{}, it + 1);
+    }
+    if (ST > 0 && dead && threadIdx.x == 0) {  // copies still in flight land first
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(10000);
+    }
+    if constexpr (Op::NSUM > 0) {  // parameter sums of the span, the warps' in order
+        __syncthreads();
+        float(*ps)[32][VEC] = &sm.a[0][0];
+#pragma unroll
+        for (int k = 0; k < Op::NSUM; ++k) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) ps[warp][lane][v] = sum[k][v];
+            __syncthreads();
+            if (warp == 0 && ln.cok) {
+                float* out = Op::sums(p) + ((int64_t)k * sg.S + sp) * sg.g.C + ln.c;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    float t = ps[0][lane][v];
+#pragma unroll
+                    for (int w2 = 1; w2 < NW; ++w2) t += ps[w2][lane][v];
+                    out[v] = t;
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
 
 // One step of every row: four inputs and the state of the row's slot, each
 // element once.  A row is a few thousand elements at most and the rows few, so
@@ -516,54 +830,140 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-template <typename S, bool VP, int M>
-using GlrFwdOpT = GlrFwdOp<S, kvec(sizeof(S) == 2, VP), kcfg(OP_GLR_FWD, sizeof(S) == 2, M).NW,
-                           kcfg(OP_GLR_FWD, sizeof(S) == 2, M).R>;
-template <typename S, bool VP, int M>
-using GlrBwdOpT = GlrBwdOp<S, kvec(sizeof(S) == 2, VP), kcfg(OP_GLR_BWD, sizeof(S) == 2, M).NW,
-                           kcfg(OP_GLR_BWD, sizeof(S) == 2, M).R>;
 
-template <typename S, bool VP>
-static cudaError_t glr_fwd_t(const GlrIn& in, const float* h0, void* h, float* h_last,
-                             const Geom& g, const Carry& cr, cudaStream_t s) {
-    return launch_persist<GlrFwdOpT<S, VP, CARRY_CHAIN>, GlrFwdOpT<S, VP, CARRY_WALK>,
-                          GlrFwdOpT<S, VP, TILE_TMA>, kcfg(OP_GLR_FWD, sizeof(S) == 2, TILE_TMA).ST>(
-        {(const S*)in.x, (const S*)in.zr, (const S*)in.zi, in.lam, in.br, in.bi, in.reset, h0, (S*)h,
-         h_last, g.C / g.D},
-        g, cr, s);
+// --------------------------------------------------------------------- host
+
+constexpr int kSpanStages = 2;
+
+template <class Op, int ST>
+cudaError_t span_slots(int* slots) {  // CTAs resident on the GPU
+    static int known[64] = {0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int& n = known[dev & 63];
+    constexpr size_t smem = ST > 0 ? (size_t)ST * tma_stage_bytes<Op>() + 128 : 0;
+    if (n <= 0) {
+        if (ST > 0) {
+            cudaError_t e = cudaFuncSetAttribute(k_glr_span<Op, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            e = cudaFuncSetAttribute(k_glr_span<Op, ST>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     (int)cudaSharedmemCarveoutMaxShared);
+            if (e != cudaSuccess) return e;
+        }
+        int b = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, k_glr_span<Op, ST>, Op::NW * 32, smem) != cudaSuccess || b < 1)
+            b = 1;
+        n = b * sm_count();
+    }
+    *slots = n;
+    return cudaSuccess;
 }
 
-template <typename S, bool VP>
-static cudaError_t glr_bwd_t(const GlrIn& in, const float* h0, const void* h, const void* dh,
-                             const float* dh_last, void* dx, void* dzr, void* dzi, float* dh0,
-                             float* partials, const Geom& g, const Carry& cr, cudaStream_t s) {
-    return launch_persist<GlrBwdOpT<S, VP, CARRY_CHAIN>, GlrBwdOpT<S, VP, CARRY_WALK>,
-                          GlrBwdOpT<S, VP, TILE_TMA>, kcfg(OP_GLR_BWD, sizeof(S) == 2, TILE_TMA).ST>(
-        {(const S*)in.x, (const S*)in.zr, (const S*)in.zi, in.lam, in.br, in.bi, in.reset, h0,
-         (const S*)h, (const S*)dh, dh_last, (S*)dx, (S*)dzr, (S*)dzi, dh0, partials, g.C / g.D},
-        g, cr, s);
+template <class Op, int ST>
+cudaError_t span_run(const typename Op::Params& p, const GlrSpans& pl, const Geom& g, float2* agg, uint32_t* err,
+                     cudaStream_t s) {
+    int slots = 0;
+    const cudaError_t e = span_slots<Op, ST>(&slots);
+    if (e != cudaSuccess) return e;
+    const SpanGeom sg{g, (uint32_t)pl.cps, (uint32_t)pl.S, g.C / g.D};
+    TmaDesc td;
+    memset(&td, 0, sizeof td);
+    if (ST > 0) {
+        const void* ptr[TMA_MAX_ARR] = {};
+        Op::tma_arrays(p, ptr);
+        for (int a = 0; a < Op::TMA_N; ++a) {
+            if (!tma_encode(&td.map[a], ptr[a], sizeof(typename Op::S) == 2 ? 1 : 0, g.T, g.C, 32 * Op::VEC, Op::NW * Op::R))
+                return cudaErrorInvalidValue;
+            td.tx_bytes += tma_arr_bytes<Op>(a);
+        }
+    }
+    if (pl.S > 1) {
+        k_glr_agg<Op><<<(unsigned)((pl.S - 1) * g.n_ct), Op::NW * 32, 0, s>>>(p, sg, agg);
+        const cudaError_t e2 = cudaGetLastError();
+        if (e2 != cudaSuccess) return e2;
+    }
+    cudaLaunchConfig_t lc;
+    memset(&lc, 0, sizeof lc);
+    lc.gridDim = dim3((unsigned)(pl.S * g.n_ct));
+    lc.blockDim = dim3(Op::NW * 32);
+    lc.dynamicSmemBytes = ST > 0 ? (size_t)ST * tma_stage_bytes<Op>() + 128 : 0;
+    lc.stream = s;
+    return cudaLaunchKernelEx(&lc, k_glr_span<Op, ST>, p, sg, (const float2*)agg, err, td);
 }
 
-cudaError_t launch_glr_fwd(int dtype, bool vec, const GlrIn& in, const float* h0, void* h,
-                           float* h_last, const Geom& g, const Carry& cr, cudaStream_t s) {
-    if (dtype == 0)
-        return vec ? glr_fwd_t<float, true>(in, h0, h, h_last, g, cr, s)
-                   : glr_fwd_t<float, false>(in, h0, h, h_last, g, cr, s);
-    return vec ? glr_fwd_t<__nv_bfloat16, true>(in, h0, h, h_last, g, cr, s)
-               : glr_fwd_t<__nv_bfloat16, false>(in, h0, h, h_last, g, cr, s);
+template <template <typename, int> class Op, class Make>
+cudaError_t span_dispatch(int dtype, const GlrSpans& pl, const Geom& g, float2* agg, uint32_t* err, cudaStream_t s,
+                          const Make& make) {
+    if (dtype == 0) {
+        const auto p = make((float*)nullptr);
+        if (pl.tma) return span_run<Op<float, 2>, kSpanStages>(p, pl, g, agg, err, s);
+        return pl.vec ? span_run<Op<float, 2>, 0>(p, pl, g, agg, err, s) : span_run<Op<float, 1>, 0>(p, pl, g, agg, err, s);
+    }
+    const auto p = make((__nv_bfloat16*)nullptr);
+    if (pl.tma) return span_run<Op<__nv_bfloat16, 2>, kSpanStages>(p, pl, g, agg, err, s);
+    return pl.vec ? span_run<Op<__nv_bfloat16, 2>, 0>(p, pl, g, agg, err, s)
+                  : span_run<Op<__nv_bfloat16, 1>, 0>(p, pl, g, agg, err, s);
 }
 
-cudaError_t launch_glr_bwd(int dtype, bool vec, const GlrIn& in, const float* h0, const void* h,
-                           const void* dh, const float* dh_last, void* dx, void* dzr, void* dzi,
-                           float* dh0, float* partials, const Geom& g, const Carry& cr,
-                           cudaStream_t s) {
-    if (dtype == 0)
-        return vec ? glr_bwd_t<float, true>(in, h0, h, dh, dh_last, dx, dzr, dzi, dh0, partials, g, cr, s)
-                   : glr_bwd_t<float, false>(in, h0, h, dh, dh_last, dx, dzr, dzi, dh0, partials, g, cr, s);
-    return vec ? glr_bwd_t<__nv_bfloat16, true>(in, h0, h, dh, dh_last, dx, dzr, dzi, dh0, partials, g,
-                                                cr, s)
-               : glr_bwd_t<__nv_bfloat16, false>(in, h0, h, dh, dh_last, dx, dzr, dzi, dh0, partials, g,
-                                                 cr, s);
+Geom span_geom(const GlrSpans& pl, int64_t T, int64_t C, int64_t D) {
+    Geom g{};
+    g.T = T;
+    g.C = C;
+    g.D = D;
+    set_channel_div(g);
+    g.n_chunks = pl.n_chunks;
+    g.n_ct = (int)pl.n_ct;
+    return g;
+}
+
+}  // namespace
+
+// The spans of a problem.  vec: the 16-byte path's pointers and D a multiple of
+// 4.  One span while the strips alone keep the GPU busy -- a quarter of the CTAs
+// that fit, forward, where the aggregates would read every input again; half of
+// them backward, where they read two of five -- else as many as fill it, of at
+// least two chunks each.
+GlrSpans glr_spans(bool bwd, int dtype, bool vec, int64_t T, int64_t C) {
+    GlrSpans p{};
+    const int es = dtype == 1 ? 2 : 4;
+    p.rows = 16;
+    p.vec = vec;
+    p.tma = vec && (C * es) % 16 == 0 && C >= 64 && T < ((int64_t)1 << 30) && C < ((int64_t)1 << 30);
+    const int64_t cw = vec ? 64 : 32;
+    p.n_chunks = (T + p.rows - 1) / p.rows;
+    p.n_ct = (C + cw - 1) / cw;
+    const int64_t slots = (bwd ? 5 : 7) * (int64_t)kSpanSms;
+    p.S = 1;
+    if (p.n_ct < slots / (bwd ? 2 : 4)) {
+        p.S = slots / p.n_ct;
+        if (p.S > p.n_chunks / 2) p.S = p.n_chunks / 2;
+        if (p.S < 1) p.S = 1;
+    }
+    p.cps = (p.n_chunks + p.S - 1) / p.S;
+    p.S = (p.n_chunks + p.cps - 1) / p.cps;
+    return p;
+}
+
+cudaError_t launch_glr_fwd(int dtype, const GlrSpans& pl, const GlrIn& in, const float* h0, void* h, float* h_last,
+                           float* scratch, int64_t T, int64_t C, int64_t D, uint32_t* err, cudaStream_t s) {
+    const Geom g = span_geom(pl, T, C, D);
+    auto make = [&](auto* tag) {
+        using S = std::remove_pointer_t<decltype(tag)>;
+        return GlrFwdParams<S>{in, h0, (S*)h, h_last};
+    };
+    return span_dispatch<GlrFwdOp>(dtype, pl, g, (float2*)scratch, err, s, make);
+}
+
+cudaError_t launch_glr_bwd(int dtype, const GlrSpans& pl, const GlrIn& in, const float* h0, const void* h, const void* dh,
+                           const float* dh_last, void* dx, void* dzr, void* dzi, float* dh0, float* scratch, int64_t T,
+                           int64_t C, int64_t D, uint32_t* err, cudaStream_t s) {
+    const Geom g = span_geom(pl, T, C, D);
+    float* partials = scratch + 2 * pl.S * C;
+    auto make = [&](auto* tag) {
+        using S = std::remove_pointer_t<decltype(tag)>;
+        return GlrBwdParams<S>{in, h0, (const S*)h, (const S*)dh, dh_last, (S*)dx, (S*)dzr, (S*)dzi, dh0, partials};
+    };
+    return span_dispatch<GlrBwdOp>(dtype, pl, g, (float2*)scratch, err, s, make);
 }
 
 template <typename S, int VEC>

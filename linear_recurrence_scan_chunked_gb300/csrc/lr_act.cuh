@@ -152,25 +152,32 @@ __device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
     return r;
 }
 
-// act_decay for a pair, without a branch or the exponential: x = l / 8 in
-// [-1/4, 0], m = e^x - 1 by its series (the first omitted term is under
-// 5e-8 |x|), then three times e^2x - 1 = (e^x - 1)(2 + (e^x - 1)).  nq = -(1 - a^2).
-constexpr float kDecayMinX = -0.25f;  // below: act_decay
-__device__ __forceinline__ void act_decay2(f32x2 x, f32x2& a, f32x2& nq) {
-    const f32x2 one = f2(1.f), two = f2(2.f);
-    f32x2 p = f2_fma(x, f2(1.f / 720.f), f2(1.f / 120.f));
-    p = f2_fma(p, x, f2(1.f / 24.f));
-    p = f2_fma(p, x, f2(1.f / 6.f));
-    p = f2_fma(p, x, f2(0.5f));
-    p = f2_fma(p, x, one);
-    f32x2 m = f2_mul(p, x);
+// act_decay for a pair, without a branch or the exponential, for l in [-4, 0]:
+// x = l / 16, m = e^x - 1 by its series (the first omitted term is under
+// 5e-8 |x|), then four times e^2x - 1 = (e^x - 1)(2 + (e^x - 1)).  The series runs
+// on single values: its coefficients are immediate operands there, and as pairs
+// would take a register pair each.  q = 1 - a^2 + 1e-30: positive for every
+// decay, so that its root has no pole (1e-30 is below any q that a decay other
+// than 1 has, and its root, 1e-15, below any state's last bit).
+constexpr float kDecayMaxRate = 4.f;
+__device__ __forceinline__ float expm1_16th(float x) {
+    float p = fmaf(x, 1.f / 720.f, 1.f / 120.f);
+    p = fmaf(p, x, 1.f / 24.f);
+    p = fmaf(p, x, 1.f / 6.f);
+    p = fmaf(p, x, 0.5f);
+    return fmaf(p * x, x, x);
+}
+__device__ __forceinline__ void act_decay2(f32x2 x, f32x2& a, f32x2& q) {
+    const f32x2 one = f2(1.f), two = f2(2.f), none = f2(-1.f), ntwo = f2(-2.f), tiny = f2(1e-30f);
+    float x0, x1;
+    f2_get(x, x0, x1);
+    f32x2 m = f2(expm1_16th(x0), expm1_16th(x1));
+    m = f2_mul(m, f2_add(m, two));
     m = f2_mul(m, f2_add(m, two));
     m = f2_mul(m, f2_add(m, two));
     m = f2_mul(m, f2_add(m, two));
     a = f2_add(m, one);
-    nq = f2_mul(m, f2_add(m, two));
+    q = f2_fma(m, f2_fma(m, none, ntwo), tiny);
 }
-// Exponents of two above which a gate's 1 + 2^x is left to act_sigmoid.
-constexpr float kGateMaxExp = 60.f;
 
 }  // namespace lrs

@@ -519,12 +519,13 @@ int glr_fwd(const void* x, const void* zr, const void* zi, const float* lam, con
     GUARD;
     DevWS* ws;
     TRY(get_ws(&ws));
-    Geom g;
-    Carry cr;
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
-    TRY(plan(*ws, OP_GLR_FWD, dtype, vec, T, B * D, D, &g, &cr, s));
-    CK(launch_glr_fwd(dtype, vec, GlrIn{x, zr, zi, lam, br, bi, reset}, h0, h, h_last, g, cr, s));
+    const GlrSpans pl = glr_spans(false, dtype, vec, T, B * D);
+    if (pl.S * pl.n_ct > INT32_MAX || pl.n_chunks > INT32_MAX || B * D > kSpanMaxChannels) return LR_ERR_TOO_LARGE;
+    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(2 * pl.S * B * D), false, true));
+    CK(launch_glr_fwd(dtype, pl, GlrIn{x, zr, zi, lam, br, bi, reset}, h0, h, h_last, ws->partials, T, B * D, D,
+                      ws->words + kWordErr, s));
     return lv.done();
 }
 
@@ -556,16 +557,14 @@ int glr_bwd(const void* x, const void* zr, const void* zi, const float* lam, con
     GUARD;
     DevWS* ws;
     TRY(get_ws(&ws));
-    Geom g;
-    Carry cr;
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
-    TRY(plan(*ws, OP_GLR_BWD, dtype, vec, T, B * D, D, &g, &cr, s));
-    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(3 * g.n_chunks * g.C + 3 * g.C), false,
-             true));
-    CK(launch_glr_bwd(dtype, vec, GlrIn{x, zr, zi, lam, br, bi, reset}, h0, h, dh, dh_last, dx, dzr,
-                      dzi, dh0, ws->partials, g, cr, s));
-    CK(launch_bias_reduce(ws->partials, g.n_chunks, 3, B, D, BiasOut{{dlam, dbr, dbi, nullptr}}, s));
+    const GlrSpans pl = glr_spans(true, dtype, vec, T, B * D);
+    if (pl.S * pl.n_ct > INT32_MAX || pl.n_chunks > INT32_MAX || B * D > kSpanMaxChannels) return LR_ERR_TOO_LARGE;
+    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(5 * pl.S * B * D + 3 * B * D), false, true));
+    CK(launch_glr_bwd(dtype, pl, GlrIn{x, zr, zi, lam, br, bi, reset}, h0, h, dh, dh_last, dx, dzr, dzi, dh0,
+                      ws->partials, T, B * D, D, ws->words + kWordErr, s));
+    CK(launch_bias_reduce(ws->partials + 2 * pl.S * B * D, pl.S, 3, B, D, BiasOut{{dlam, dbr, dbi, nullptr}}, s));
     return lv.done();
 }
 
@@ -1235,8 +1234,7 @@ static_assert((int)LR_OP_SCAN_FWD == (int)OP_SCAN_FWD && (int)LR_OP_SCAN_BWD == 
                   (int)LR_OP_SRU_FWD == (int)OP_SRU_FWD && (int)LR_OP_SRU_BWD == (int)OP_SRU_BWD &&
                   (int)LR_OP_DEER == (int)OP_DEER && (int)LR_OP_DEER_BWD == (int)OP_DEER_BWD &&
                   (int)LR_OP_LSTM_FWD == (int)OP_LSTM_FWD && (int)LR_OP_LSTM_BWD == (int)OP_LSTM_BWD &&
-                  (int)LR_OP_DEER_ODE == (int)OP_DEER_ODE && (int)OP_DEER_ODE + 1 == (int)OP_GLR_FWD &&
-                  (int)OP_GLR_FWD + 1 == (int)OP_GLR_BWD && (int)OP_GLR_BWD + 1 == (int)OP_COUNT,
+                  (int)LR_OP_DEER_ODE == (int)OP_DEER_ODE && (int)OP_DEER_ODE + 1 == (int)OP_COUNT,
               "lr_op follows the library's operation order");
 static_assert(LR_PROTO_CHAIN == CARRY_CHAIN && LR_PROTO_WALK == CARRY_WALK &&
                   LR_PROTO_LOOK == CARRY_LOOK && LR_PROTO_CLUSTER == CARRY_CLUSTER,
@@ -1244,11 +1242,18 @@ static_assert(LR_PROTO_CHAIN == CARRY_CHAIN && LR_PROTO_WALK == CARRY_WALK &&
 
 int lr_plan_info(int op, int dtype, int vec, int64_t T, int64_t C, int* protocol, int* tma,
                  int64_t* tile_rows, int64_t* n_chunks) {
-    if (op == LR_OP_GLR_FWD || op == LR_OP_GLR_BWD) op = (int)OP_GLR_FWD + (op - LR_OP_GLR_FWD);
-    else if (op > LR_OP_DEER_ODE) return LR_ERR_INVALID_ARG;
-    if (op < 0 || (dtype != LR_F32 && dtype != LR_BF16) || T < 1 || C < 1)
+    const bool glr = op == LR_OP_GLR_FWD || op == LR_OP_GLR_BWD;
+    if (op < 0 || (op >= (int)OP_COUNT && !glr) || (dtype != LR_F32 && dtype != LR_BF16) || T < 1 || C < 1)
         return LR_ERR_INVALID_ARG;
     const bool v = vec != 0;
+    if (glr) {
+        const GlrSpans sp = glr_spans(op == LR_OP_GLR_BWD, dtype, v, T, C);
+        if (protocol) *protocol = sp.S > 1 ? LR_PROTO_SPANS : LR_PROTO_CHAIN;
+        if (tma) *tma = sp.tma ? 1 : 0;
+        if (tile_rows) *tile_rows = sp.rows;
+        if (n_chunks) *n_chunks = sp.n_chunks;
+        return LR_OK;
+    }
     // the same plan the entry points make (plan(), onepass_begin)
     const CarryPlan cp = carry_plan((Op)op, dtype, v, use_tma(dtype, v, T, C), T, C);
     if (protocol) *protocol = cp.mode;

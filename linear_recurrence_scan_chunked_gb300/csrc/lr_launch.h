@@ -68,8 +68,6 @@ enum Op {
     OP_LSTM_FWD,
     OP_LSTM_BWD,
     OP_DEER_ODE,
-    OP_GLR_FWD,
-    OP_GLR_BWD,
     OP_COUNT
 };
 
@@ -96,14 +94,10 @@ constexpr KCfg kcfg(Op op, int dtype, int mode) {
     // both storage types).  The LSTM cell stages as many arrays per direction
     // as the SRU cell and takes its rows; DEER's ODE form takes the tanh
     // form's rows at eight warps per CTA (its heavier producer measured slower
-    // with four).  The gated linear recurrence takes the SRU cell's rows, and
-    // the TMA-staged kernels' rows for its walker protocol too, so that long,
-    // narrow problems run the segmented walker kernel.
+    // with four).
     return mode == TILE_CLUSTER ? KCfg{8, 16, 0}  // 16 rows of 32 channels per warp, 128 per CTA
            : op == OP_DEER_ODE   ? KCfg{8, mode == CARRY_CHAIN ? 2 : 4, mode == TILE_TMA ? 3 : 0}
            : op == OP_DEER && dtype == 1 ? kcfg(OP_DEER, 0, mode)
-           : op == OP_GLR_FWD || op == OP_GLR_BWD
-               ? KCfg{8, op == OP_GLR_FWD && dtype == 1 ? 4 : 2, mode != TILE_TMA ? 0 : op == OP_GLR_FWD ? 3 : 2}
            : op == OP_LSTM_FWD ? kcfg(OP_SRU_FWD, dtype, mode)
            : op == OP_LSTM_BWD ? kcfg(OP_SRU_BWD, dtype, mode)
            : op == OP_DEER_BWD ? KCfg{8, mode == CARRY_CHAIN ? 2 : 4, mode == TILE_TMA ? 3 : 0}
@@ -390,14 +384,22 @@ struct GlrIn {
     const float* bi;
     const uint8_t* reset;
 };
-cudaError_t launch_glr_fwd(int dtype, bool vec, const GlrIn& in, const float* h0, void* h,
-                           float* h_last, const Geom& g, const Carry& cr, cudaStream_t s);
-// partials: [3][n_chunks][C] fp32 scratch (rate, decay bias, input bias),
-// followed by 3*C floats for launch_bias_reduce
-cudaError_t launch_glr_bwd(int dtype, bool vec, const GlrIn& in, const float* h0, const void* h,
-                           const void* dh, const float* dh_last, void* dx, void* dzr, void* dzi,
-                           float* dh0, float* partials, const Geom& g, const Carry& cr,
-                           cudaStream_t s);
+// The spans that a problem is cut into: S spans of cps chunks of `rows` time rows,
+// n_ct channel strips (64 channels on the vector path, 32 on the scalar one).
+constexpr int kSpanSms = 152;  // GB300: the plan depends on the shape alone
+struct GlrSpans {
+    int64_t rows, n_chunks, n_ct, cps, S;
+    bool vec, tma;
+};
+constexpr int64_t kSpanMaxChannels = (int64_t)1 << 25;  // 32-bit offsets within a tile of 16 rows
+GlrSpans glr_spans(bool bwd, int dtype, bool vec, int64_t T, int64_t C);
+// scratch: forward 2*S*C floats (the spans' aggregates); backward 5*S*C + 3*C (the
+// aggregates, the parameters' partial sums [3][S][C] and launch_bias_reduce's)
+cudaError_t launch_glr_fwd(int dtype, const GlrSpans& pl, const GlrIn& in, const float* h0, void* h, float* h_last,
+                           float* scratch, int64_t T, int64_t C, int64_t D, uint32_t* err, cudaStream_t s);
+cudaError_t launch_glr_bwd(int dtype, const GlrSpans& pl, const GlrIn& in, const float* h0, const void* h, const void* dh,
+                           const float* dh_last, void* dx, void* dzr, void* dzi, float* dh0, float* scratch, int64_t T,
+                           int64_t C, int64_t D, uint32_t* err, cudaStream_t s);
 // One step of `rows` sequences: h and the states of their slots (slots ==
 // nullptr: slot b is row b; a negative slot is padding).  in.reset: [rows].
 cudaError_t launch_glr_step(int dtype, bool vec, const GlrIn& in, const int32_t* slots, float* state,

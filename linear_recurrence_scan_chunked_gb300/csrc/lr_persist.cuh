@@ -23,7 +23,7 @@
 //                                 thread, values passed from aggregate() to
 //                                 finish(), extra shared memory, per-thread
 //                                 accumulators kept across tiles
-//   init_ptr(p)                   state before the scan (nullable; storage type or fp32)
+//   init_ptr(p)                   state before the scan (nullable)
 //   skip(p)                       the whole launch has nothing to do (checked
 //                                 first by every CTA)
 //   load(src, p, g, tc, regs)     the loads of one tile, from global memory or
@@ -46,7 +46,6 @@
 #include <algorithm>
 
 #include <type_traits>
-#include <utility>
 
 #include "lr_launch.h"
 #include "lr_tma.cuh"
@@ -58,12 +57,6 @@ namespace lrs {
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-
-// The type of the state before the scan, as Op::init_ptr gives it: the storage
-// type, or fp32 for the operations that keep their states in 32 bits.
-template <class Op>
-using init_t = typename std::remove_const<typename std::remove_pointer<decltype(
-    Op::init_ptr(std::declval<const typename Op::Params&>()))>::type>::type;
 
 struct TileCoord {
     int64_t q;       // chunk index in scan order
@@ -159,7 +152,7 @@ __global__ void __launch_bounds__(Op::NW * 32, Op::MINB * 8 / Op::NW)
         const bool draw = tk >= cr.n_walk && tk < limit;
         if (draw && threadIdx.x == 0) next = draw_ticket(cr);
         if (tk < cr.n_walk) {  // walker role
-            walker<init_t<Op>, Op::NW>(cr, g, tk, Op::init_ptr(p));
+            walker<typename Op::S, Op::NW>(cr, g, tk, Op::init_ptr(p));
             return;
         }
         if (tk >= limit) break;
@@ -194,9 +187,9 @@ __global__ void __launch_bounds__(Op::NW * 32, Op::MINB * 8 / Op::NW)
             float init[VEC];
 #pragma unroll
             for (int v = 0; v < VEC; ++v) init[v] = 0.f;
-            const init_t<Op>* ip = Op::init_ptr(p);
+            const typename Op::S* ip = Op::init_ptr(p);
             if (tc.q == 0 && (threadIdx.x >> 5) == 0 && ip != nullptr && tc.cok)
-                load_vec<init_t<Op>, VEC>(ip + tc.c, init);
+                load_vec<typename Op::S, VEC>(ip + tc.c, init);
             float s[VEC];
             tile_carry<VEC, Op::NW>(sm, A, B, init, s, cr, g, tc.q, tc.c, tc.cok, pre);
             Op::finish(p, g, tc, regs, w, s, xs, acc);
@@ -397,7 +390,7 @@ __global__ void __launch_bounds__(WsLayout<Op>::NWARPS * 32, 1)
     const uint32_t first = s_first;
 
     if (warp == Ly::W_WALK) {
-        if (first < cr.n_walk) walker_warp<init_t<Op>>(cr, g, first, Op::init_ptr(p));
+        if (first < cr.n_walk) walker_warp<typename Op::S>(cr, g, first, Op::init_ptr(p));
         return;
     }
 
@@ -577,7 +570,7 @@ __global__ void __launch_bounds__(WsLayout<Op>::NWARPS * 32, 1)
     // consumer warps: warp w's rows are in stage w / WPS of a tile
     typename Op::Acc acc;
     Op::acc_init(acc);
-    const init_t<Op>* ip = Op::init_ptr(p);
+    const typename Op::S* ip = Op::init_ptr(p);
     const int h = warp / WPS;
     bool any = false;
     uint32_t par = 0;
@@ -634,7 +627,7 @@ __global__ void __launch_bounds__(WsLayout<Op>::NWARPS * 32, 1)
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) cin[v] = 0.f;
                 if (tc.q == 0) {
-                    if (ip != nullptr && tc.cok) load_vec<init_t<Op>, VEC>(ip + tc.c, cin);
+                    if (ip != nullptr && tc.cok) load_vec<typename Op::S, VEC>(ip + tc.c, cin);
                 } else {
                     bool ok = true;
 #pragma unroll
@@ -699,9 +692,9 @@ __device__ __forceinline__ void tile_process(const typename Op::Params& p, const
     float init[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) init[v] = 0.f;
-    const init_t<Op>* ip = Op::init_ptr(p);
+    const typename Op::S* ip = Op::init_ptr(p);
     if (tc.q == 0 && (threadIdx.x >> 5) == 0 && ip != nullptr && tc.cok)
-        load_vec<init_t<Op>, VEC>(ip + tc.c, init);
+        load_vec<typename Op::S, VEC>(ip + tc.c, init);
     float s[VEC];
     tile_carry<VEC, Op::NW>(sm, A, B, init, s, cr, g, tc.q, tc.c, tc.cok);
     Op::finish(p, g, tc, regs, w, s, xs, acc);
@@ -1156,8 +1149,8 @@ __global__ void __launch_bounds__(Op::NW * 32, Op::MINB * 8 / Op::NW)
         float s[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) s[v] = 0.f;
-        const init_t<Op>* ip = Op::init_ptr(p);
-        if (ip != nullptr && tc.cok) load_vec<init_t<Op>, VEC>(ip + tc.c, s);
+        const typename Op::S* ip = Op::init_ptr(p);
+        if (ip != nullptr && tc.cok) load_vec<typename Op::S, VEC>(ip + tc.c, s);
         csync<NW>();  // sm is free for the look-back
         // 2. this warp's share of the preceding chunks
         const uint32_t q = (uint32_t)tc.q;
@@ -1284,8 +1277,8 @@ __global__ void __launch_bounds__(Op::NW * 32, Op::MINB)
     float s[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; ++v) s[v] = 0.f;
-    const init_t<Op>* ip = Op::init_ptr(p);
-    if (ip != nullptr && tc.cok) load_vec<init_t<Op>, VEC>(ip + tc.c, s);
+    const typename Op::S* ip = Op::init_ptr(p);
+    if (ip != nullptr && tc.cok) load_vec<typename Op::S, VEC>(ip + tc.c, s);
     typename Op::Regs regs;
     typename Op::Work w;
     typename Op::Acc acc;
@@ -1527,8 +1520,8 @@ __global__ void __launch_bounds__(Op::NW * 32, Op::MINB * 8 / Op::NW)
         float init[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) init[v] = 0.f;
-        const init_t<Op>* ip = Op::init_ptr(p);
-        if (tc.q == 0 && ip != nullptr && tc.cok) load_vec<init_t<Op>, VEC>(ip + tc.c, init);
+        const typename Op::S* ip = Op::init_ptr(p);
+        if (tc.q == 0 && ip != nullptr && tc.cok) load_vec<typename Op::S, VEC>(ip + tc.c, init);
         float s[VEC];
         if constexpr (ONEB) {
             const int pb = (int)(it & 1u);
@@ -1785,7 +1778,7 @@ __global__ void __launch_bounds__(Op::NW * 32, Op::MINB * 8 / Op::NW)
     if (cur < cr.n_walk) {  // walker role: its chunks are the segments
         Geom gw = g;
         gw.n_chunks = sg.n_seg;
-        walker<init_t<Op>, NW>(cr, gw, cur, Op::init_ptr(p));
+        walker<typename Op::S, NW>(cr, gw, cur, Op::init_ptr(p));
         return;
     }
     if (cur >= limit) return;
@@ -1944,9 +1937,9 @@ __global__ void __launch_bounds__(Op::NW * 32, Op::MINB * 8 / Op::NW)
             float cin[VEC];
 #pragma unroll
             for (int v = 0; v < VEC; ++v) cin[v] = 0.f;
-            const init_t<Op>* ip = Op::init_ptr(p);
+            const typename Op::S* ip = Op::init_ptr(p);
             if (seg_c == 0) {
-                if (tc.cok && ip != nullptr) load_vec<init_t<Op>, VEC>(ip + tc.c, cin);
+                if (tc.cok && ip != nullptr) load_vec<typename Op::S, VEC>(ip + tc.c, cin);
             } else {
                 uint32_t spins = 0, sleep_ns = 0;
                 while (true) {
@@ -2088,7 +2081,7 @@ __global__ void __launch_bounds__(Op::NW * 32, Op::MINB * 8 / Op::NW)
     if (cur < cr.n_walk) {  // walker role: its chunks are the segments
         Geom gw = g;
         gw.n_chunks = sg.n_seg;
-        walker<init_t<Op>, NW>(cr, gw, cur, Op::init_ptr(p));
+        walker<typename Op::S, NW>(cr, gw, cur, Op::init_ptr(p));
         return;
     }
     if (cur >= limit) return;
@@ -2144,9 +2137,9 @@ __global__ void __launch_bounds__(Op::NW * 32, Op::MINB * 8 / Op::NW)
             float cin[VEC];
 #pragma unroll
             for (int v = 0; v < VEC; ++v) cin[v] = 0.f;
-            const init_t<Op>* ip = Op::init_ptr(p);
+            const typename Op::S* ip = Op::init_ptr(p);
             if (seg_c == 0) {
-                if (tc.cok && ip != nullptr) load_vec<init_t<Op>, VEC>(ip + tc.c, cin);
+                if (tc.cok && ip != nullptr) load_vec<typename Op::S, VEC>(ip + tc.c, cin);
             } else {
                 uint32_t spins = 0, sleep_ns = 0;
                 while (true) {

@@ -371,10 +371,14 @@ def test_refusals_on_device_tensors(cuda):
         cuda.glr_fwd(*[a.half() if a.dim() == 3 else a for a in args])
 
 
-def test_shapes_cover_every_protocol():
-    """The parity shapes above reach each carry protocol of both directions on
-    both paths; the recurrence never takes the cluster kernel (CPU)."""
+def test_shapes_cover_every_plan():
+    """The parity shapes above reach one span and several, staged by TMA, through
+    registers in vectors and element by element, in both directions (CPU)."""
     for op in ("glr_fwd", "glr_bwd"):
-        seen = {(lrs.plan_info(op, dt, D % 4 == 0, T, B * D)["protocol"], D % 4 == 0)
-                for T, B, D in SHAPES for dt in ("f32", "bf16")}
-        assert seen == {("look", True), ("chain", True), ("walk", True), ("chain", False), ("walk", False)}, seen
+        seen = set()
+        for T, B, D in SHAPES:
+            for dt in ("f32", "bf16"):
+                p = lrs.plan_info(op, dt, D % 4 == 0, T, B * D)
+                seen.add((p["protocol"], p["tma"], D % 4 == 0))
+        assert seen == {(pr, *kind) for pr in ("chain", "spans")
+                        for kind in ((True, True), (False, True), (False, False))}, seen

@@ -330,7 +330,9 @@ __device__ __forceinline__ uint32_t bf_bits(float x) {
     return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(x));
 }
 __device__ __forceinline__ uint32_t bf_pack(float lo, float hi) {
-    return bf_bits(lo) | (bf_bits(hi) << 16);
+    uint32_t w;  // both roundings in one instruction
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
 }
 
 // --------------------------------------------------------- storage packs

@@ -18,6 +18,8 @@
 // and a second kernel adds them in a fixed order (bitwise reproducible).
 #include "lr_launch.h"
 
+#include <type_traits>
+
 namespace lrs {
 
 // Sum of `v` over the T = 32*W threads of a row (blockDim.x), to all of them.
@@ -47,60 +49,105 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* sm) {
     }
 }
 
-template <typename S, int VEC, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+// A thread's columns: vector k starts at column (k T + threadIdx.x) VEC.  Rows are
+// addressed by the CTA's first row, the same for all its threads, plus a 32-bit
+// offset that no row changes.  Only the last vectors can lie outside (T is rounded
+// up to a warp); their offset is the row's last vector, whose data they read and
+// whose results they drop.
+template <typename S, int VEC, int NV>
+struct Cols {
+    static constexpr int kMasked = NV >= 16 ? 4 : NV == 8 ? 2 : 1;
+    uint32_t off[NV];  // bytes
+    int d[NV];
+    bool in_[kMasked];
+    __device__ __forceinline__ Cols(int D) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            d[k] = (k * (int)blockDim.x + (int)threadIdx.x) * VEC;
+            if (k >= NV - kMasked) {
+                in_[k - (NV - kMasked)] = d[k] < D;
+                if (d[k] >= D) d[k] = D - VEC;
+            }
+            off[k] = (uint32_t)((threadIdx.y * D + d[k]) * (int)sizeof(S));
+        }
+    }
+    __device__ __forceinline__ bool in(int k) const {
+        return k < NV - kMasked ? true : in_[k < NV - kMasked ? 0 : k - (NV - kMasked)];
+    }
+    template <typename T>
+    __device__ __forceinline__ T* at(T* row, int k) const {
+        using B = typename std::conditional<std::is_const<T>::value, const char, char>::type;
+        return reinterpret_cast<T*>(reinterpret_cast<B*>(row) + off[k]);
+    }
+};
+
+// The next row's vectors are loaded before the current row's sums: a row's two
+// reductions and its output then cover the next one's way from memory.
+template <typename S, int VEC, int NV, int MAXT, bool RES>
+__global__ void __launch_bounds__(MAXT, 1)
     k_ln_fwd(const S* __restrict__ x, const S* __restrict__ res, const float* __restrict__ w,
              const float* __restrict__ b, S* __restrict__ y, S* __restrict__ sum,
              float* __restrict__ mean, float* __restrict__ rstd, int64_t N, int D, float eps) {
     __shared__ float sm[2][8][32];  // at most 8 rows a CTA (256 threads of 32)
-    const int T = blockDim.x;
     const float inv_d = 1.f / (float)D;
-    bool in[NV];
+    const Cols<S, VEC, NV> cl(D);
     float wv[NV][VEC], bv[NV][VEC];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int d = (k * T + (int)threadIdx.x) * VEC;
-        in[k] = d < D;
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) { wv[k][v] = 0.f; bv[k][v] = 0.f; }
-        if (in[k]) {
-            load_param<VEC>(w + d, wv[k]);
-            if (b != nullptr) load_param<VEC>(b + d, bv[k]);
-        }
+        for (int v = 0; v < VEC; ++v) bv[k][v] = 0.f;
+        load_param<VEC>(w + cl.d[k], wv[k]);
+        if (b != nullptr) load_param<VEC>(b + cl.d[k], bv[k]);
     }
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
+    Pack<S, VEC> px[NV], pr[NV];
+    auto fetch = [&](int64_t r0) {
+        if (r0 + threadIdx.y >= N) return;
+        const S *xr = x + r0 * D, *rr = res + r0 * D;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            px[k].load(cl.at(xr, k));
+            if constexpr (RES) pr[k].load(cl.at(rr, k));
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < NV; ++k) { px[k].ident(0.f); pr[k].ident(0.f); }
+    fetch((int64_t)blockIdx.x * blockDim.y);
     // every row of a CTA runs the same number of rounds (the barriers)
     for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < N; r0 += step) {
-        const int64_t r = r0 + threadIdx.y;
-        const bool live = r < N;
-        const int64_t base = r * D;
+        const bool live = r0 + threadIdx.y < N;
+        S *yr = y + r0 * D, *sr = sum + r0 * D;
         float e[NV][VEC];
         float t[1] = {0.f};
-        Pack<S, VEC> px[NV], pr[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int d = (k * T + (int)threadIdx.x) * VEC;
-            px[k].ident(0.f);
-            pr[k].ident(0.f);
-            if (live && in[k]) {
-                px[k].load(x + base + d);
-                if (res != nullptr) pr[k].load(res + base + d);
-            }
-        }
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int d = (k * T + (int)threadIdx.x) * VEC;
+            for (int v = 0; v < VEC; ++v) e[k][v] = px[k].get(v);
+            if constexpr (RES) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                e[k][v] = px[k].get(v);
-                if (res != nullptr) {
-                    e[k][v] += pr[k].get(v);
-                    if constexpr (sizeof(S) == 2) e[k][v] = bf_lo(bf_bits(e[k][v]));
+                for (int v = 0; v < VEC; ++v) e[k][v] += pr[k].get(v);
+                if constexpr (sizeof(S) == 2 && VEC > 1) {
+                    // rounded once, stored and carried on
+#pragma unroll
+                    for (int v = 0; v < VEC; v += 2) {
+                        px[k].w[v / 2] = bf_pack(e[k][v], e[k][v + 1]);
+                        e[k][v] = bf_lo(px[k].w[v / 2]);
+                        e[k][v + 1] = bf_hi(px[k].w[v / 2]);
+                    }
+                    if (live && cl.in(k))
+                        st_u4(cl.at(sr, k), make_uint4(px[k].w[0], px[k].w[1], px[k].w[2], px[k].w[3]));
+                } else {
+                    if constexpr (sizeof(S) == 2) {
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) e[k][v] = bf_lo(bf_bits(e[k][v]));
+                    }
+                    if (live && cl.in(k)) store_vec<S, VEC>(cl.at(sr, k), e[k]);
                 }
-                t[0] += e[k][v];
             }
-            if (res != nullptr && live && in[k]) store_vec<S, VEC>(sum + base + d, e[k]);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) t[0] += cl.in(k) ? e[k][v] : 0.f;
         }
+        fetch(r0 + step);
         row_sum(t, &sm[0][0][0]);
         const float mu = t[0] * inv_d;
         t[0] = 0.f;
@@ -108,31 +155,31 @@ __global__ void __launch_bounds__(MAXT)
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                const float c = in[k] ? e[k][v] - mu : 0.f;
+                e[k][v] -= mu;
+                const float c = cl.in(k) ? e[k][v] : 0.f;
                 t[0] = fmaf(c, c, t[0]);
             }
         row_sum(t, &sm[1][0][0]);
         const float rs = 1.f / sqrtf(fmaf(t[0], inv_d, eps));
         if (live) {
             if (threadIdx.x == 0) {
-                mean[r] = mu;
-                rstd[r] = rs;
+                mean[r0 + threadIdx.y] = mu;
+                rstd[r0 + threadIdx.y] = rs;
             }
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int d = (k * T + (int)threadIdx.x) * VEC;
                 float o[VEC];
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) o[v] = fmaf((e[k][v] - mu) * rs, wv[k][v], bv[k][v]);
-                if (in[k]) store_vec<S, VEC>(y + base + d, o);
+                for (int v = 0; v < VEC; ++v) o[v] = fmaf(e[k][v] * rs, wv[k][v], bv[k][v]);
+                if (cl.in(k)) store_vec<S, VEC>(cl.at(yr, k), o);
             }
         }
     }
 }
 
 // partials: [2][gridDim.x][D] (dw, db).
-template <typename S, int VEC, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+template <typename S, int VEC, int NV, int MAXT, bool RES>
+__global__ void __launch_bounds__(MAXT, 1)
     k_ln_bwd(const S* __restrict__ x, const float* __restrict__ w, const float* __restrict__ mean,
              const float* __restrict__ rstd, const S* __restrict__ dy, const S* __restrict__ dres,
              S* __restrict__ dx, float* __restrict__ partials, int64_t N, int D) {
@@ -140,62 +187,69 @@ __global__ void __launch_bounds__(MAXT)
     extern __shared__ float cols[];  // [blockDim.y - 1][T * NV * VEC] when a CTA holds several rows
     const int T = blockDim.x;
     const float inv_d = 1.f / (float)D;
-    bool in[NV];
+    const Cols<S, VEC, NV> cl(D);
     float wv[NV][VEC], aw[NV][VEC], ab[NV][VEC];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int d = (k * T + (int)threadIdx.x) * VEC;
-        in[k] = d < D;
+        load_param<VEC>(w + cl.d[k], wv[k]);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) wv[k][v] = aw[k][v] = ab[k][v] = 0.f;
-        if (in[k]) load_param<VEC>(w + d, wv[k]);
+        for (int v = 0; v < VEC; ++v) {
+            aw[k][v] = ab[k][v] = 0.f;
+            if (!cl.in(k)) wv[k][v] = 0.f;
+        }
     }
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    int par = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < N; r0 += step, par ^= 1) {
-        const int64_t r = r0 + threadIdx.y;
-        const bool live = r < N;
-        const int64_t base = r * D;
-        Pack<S, VEC> px[NV], pd[NV], pr[NV];
+    Pack<S, VEC> px[NV], pd[NV], pr[NV];
+    float mu = 0.f, rs = 0.f;
+    auto fetch = [&](int64_t r0) {
+        if (r0 + threadIdx.y >= N) {  // past the end: rows of zeros
+#pragma unroll
+            for (int k = 0; k < NV; ++k) { px[k].ident(0.f); pd[k].ident(0.f); pr[k].ident(0.f); }
+            mu = rs = 0.f;
+            return;
+        }
+        const S *xr = x + r0 * D, *gr = dy + r0 * D, *rr = dres + r0 * D;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int d = (k * T + (int)threadIdx.x) * VEC;
-            px[k].ident(0.f);
-            pd[k].ident(0.f);
-            pr[k].ident(0.f);
-            if (live && in[k]) {
-                px[k].load(x + base + d);
-                pd[k].load(dy + base + d);
-                if (dres != nullptr) pr[k].load(dres + base + d);
-            }
+            px[k].load(cl.at(xr, k));
+            pd[k].load(cl.at(gr, k));
+            if constexpr (RES) pr[k].load(cl.at(rr, k));
         }
-        const float mu = live ? __ldg(mean + r) : 0.f, rs = live ? __ldg(rstd + r) : 0.f;
+        mu = __ldg(mean + r0 + threadIdx.y);
+        rs = __ldg(rstd + r0 + threadIdx.y);
+    };
+    fetch((int64_t)blockIdx.x * blockDim.y);
+    int par = 0;
+    for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < N; r0 += step, par ^= 1) {
+        const bool live = r0 + threadIdx.y < N;
+        S* xr = dx + r0 * D;
+        // xh, and t = dy w with what dx adds to it: rs t + dres
+        float xh[NV][VEC], q[NV][VEC], o[NV][VEC];
         float t[2] = {0.f, 0.f};
+        const float r_s = rs;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                const float xh = in[k] ? (px[k].get(v) - mu) * rs : 0.f;
+                xh[k][v] = (px[k].get(v) - mu) * r_s;
                 const float g = pd[k].get(v);
-                aw[k][v] = fmaf(g, xh, aw[k][v]);
+                aw[k][v] = fmaf(g, xh[k][v], aw[k][v]);
                 ab[k][v] += g;
-                const float q = g * wv[k][v];
-                t[0] += q;
-                t[1] = fmaf(q, xh, t[1]);
+                q[k][v] = g * wv[k][v];
+                t[0] += q[k][v];
+                t[1] = fmaf(q[k][v], xh[k][v], t[1]);
+                if constexpr (RES) o[k][v] = pr[k].get(v);
+                else o[k][v] = 0.f;
             }
+        fetch(r0 + step);
         row_sum(t, &sm[par][0][0]);
         const float c0 = t[0] * inv_d, c1 = t[1] * inv_d;
         if (live) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int d = (k * T + (int)threadIdx.x) * VEC;
-                float o[VEC];
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float xh = (px[k].get(v) - mu) * rs;
-                    o[v] = fmaf(rs, pd[k].get(v) * wv[k][v] - c0 - xh * c1, pr[k].get(v));
-                }
-                if (in[k]) store_vec<S, VEC>(dx + base + d, o);
+                for (int v = 0; v < VEC; ++v) o[k][v] = fmaf(r_s, fmaf(-xh[k][v], c1, q[k][v] - c0), o[k][v]);
+                if (cl.in(k)) store_vec<S, VEC>(cl.at(xr, k), o[k]);
             }
         }
     }
@@ -218,12 +272,12 @@ __global__ void __launch_bounds__(MAXT)
             float* out = partials + ((int64_t)a * gridDim.x + blockIdx.x) * D;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int d = (k * T + (int)threadIdx.x) * VEC;
+                const int d = cl.d[k];
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     float s = a == 0 ? aw[k][v] : ab[k][v];
                     for (int j = 0; j + 1 < (int)blockDim.y; ++j) s += cols[j * pitch + (k * VEC + v) * T + threadIdx.x];
-                    if (in[k]) out[d + v] = s;
+                    if (cl.in(k)) out[d + v] = s;
                 }
             }
         }
@@ -276,27 +330,42 @@ static int ln_grid(K kernel, int threads, size_t smem, int64_t groups) {
     return (int)(groups < cap ? groups : cap);
 }
 
-template <typename S, int VEC, int NV, int MAXT>
-static cudaError_t ln_fwd_k(const LnShape& sh, const void* x, const void* res, const float* w,
+template <typename S, int VEC, int NV, int MAXT, bool RES>
+static cudaError_t ln_fwd_r(const LnShape& sh, const void* x, const void* res, const float* w,
                             const float* b, void* y, void* sum, float* mean, float* rstd, int64_t N,
                             int64_t D, float eps, cudaStream_t s) {
-    const int grid = ln_grid(k_ln_fwd<S, VEC, NV, MAXT>, sh.t * sh.rows, 0, (N + sh.rows - 1) / sh.rows);
-    k_ln_fwd<S, VEC, NV, MAXT><<<grid, dim3(sh.t, sh.rows), 0, s>>>(
+    const int grid = ln_grid(k_ln_fwd<S, VEC, NV, MAXT, RES>, sh.t * sh.rows, 0, (N + sh.rows - 1) / sh.rows);
+    k_ln_fwd<S, VEC, NV, MAXT, RES><<<grid, dim3(sh.t, sh.rows), 0, s>>>(
         (const S*)x, (const S*)res, w, b, (S*)y, (S*)sum, mean, rstd, N, (int)D, eps);
     return cudaGetLastError();
 }
 
+template <typename S, int VEC, int NV, int MAXT, bool RES>
+static cudaError_t ln_bwd_r(const LnShape& sh, const void* x, const float* w, const float* mean,
+                            const float* rstd, const void* dy, const void* dres, void* dx, float* dw,
+                            float* db, float* partials, int64_t N, int64_t D, cudaStream_t s) {
+    const size_t smem = (size_t)(sh.rows - 1) * sh.t * NV * VEC * sizeof(float);
+    int grid = ln_grid(k_ln_bwd<S, VEC, NV, MAXT, RES>, sh.t * sh.rows, smem, (N + sh.rows - 1) / sh.rows);
+    if (grid > kLnMaxPartials) grid = kLnMaxPartials;
+    k_ln_bwd<S, VEC, NV, MAXT, RES><<<grid, dim3(sh.t, sh.rows), smem, s>>>(
+        (const S*)x, w, mean, rstd, (const S*)dy, (const S*)dres, (S*)dx, partials, N, (int)D);
+    k_ln_colsum<<<dim3((unsigned)((D + 31) / 32), 2), dim3(32, 32), 0, s>>>(partials, grid, D, dw, db);
+    return cudaGetLastError();
+}
+
+template <typename S, int VEC, int NV, int MAXT>
+static cudaError_t ln_fwd_k(const LnShape& sh, const void* x, const void* res, const float* w,
+                            const float* b, void* y, void* sum, float* mean, float* rstd, int64_t N,
+                            int64_t D, float eps, cudaStream_t s) {
+    return res ? ln_fwd_r<S, VEC, NV, MAXT, true>(sh, x, res, w, b, y, sum, mean, rstd, N, D, eps, s)
+               : ln_fwd_r<S, VEC, NV, MAXT, false>(sh, x, res, w, b, y, sum, mean, rstd, N, D, eps, s);
+}
 template <typename S, int VEC, int NV, int MAXT>
 static cudaError_t ln_bwd_k(const LnShape& sh, const void* x, const float* w, const float* mean,
                             const float* rstd, const void* dy, const void* dres, void* dx, float* dw,
                             float* db, float* partials, int64_t N, int64_t D, cudaStream_t s) {
-    const size_t smem = (size_t)(sh.rows - 1) * sh.t * NV * VEC * sizeof(float);
-    int grid = ln_grid(k_ln_bwd<S, VEC, NV, MAXT>, sh.t * sh.rows, smem, (N + sh.rows - 1) / sh.rows);
-    if (grid > kLnMaxPartials) grid = kLnMaxPartials;
-    k_ln_bwd<S, VEC, NV, MAXT><<<grid, dim3(sh.t, sh.rows), smem, s>>>(
-        (const S*)x, w, mean, rstd, (const S*)dy, (const S*)dres, (S*)dx, partials, N, (int)D);
-    k_ln_colsum<<<dim3((unsigned)((D + 31) / 32), 2), dim3(32, 32), 0, s>>>(partials, grid, D, dw, db);
-    return cudaGetLastError();
+    return dres ? ln_bwd_r<S, VEC, NV, MAXT, true>(sh, x, w, mean, rstd, dy, dres, dx, dw, db, partials, N, D, s)
+                : ln_bwd_r<S, VEC, NV, MAXT, false>(sh, x, w, mean, rstd, dy, dres, dx, dw, db, partials, N, D, s);
 }
 
 // The instance of a shape.

@@ -81,10 +81,22 @@ struct Cols {
     }
 };
 
+// CTAs per SM to compile for (256 threads; a row of up to 512 takes what it
+// gets): enough rows in flight to cover the memory's latency.  Left to itself the
+// compiler spends 128 registers on five elements a thread, and the backward pass
+// of 30011 x 1111 took 10% longer.
+constexpr int ln_min_ctas(bool bwd, bool res, int elems, int maxt) {
+    return maxt > 256 || elems > 16 ? 1
+           : elems > 8              ? 2
+           : bwd || res             ? (elems <= 2 ? 5 : elems <= 4 ? 4 : elems <= 6 && bwd ? 4 : 3)
+           : elems <= 4             ? 6
+                                    : 4;
+}
+
 // The next row's vectors are loaded before the current row's sums: a row's two
 // reductions and its output then cover the next one's way from memory.
 template <typename S, int VEC, int NV, int MAXT, bool RES>
-__global__ void __launch_bounds__(MAXT, 1)
+__global__ void __launch_bounds__(MAXT, ln_min_ctas(false, RES, VEC * NV, MAXT))
     k_ln_fwd(const S* __restrict__ x, const S* __restrict__ res, const float* __restrict__ w,
              const float* __restrict__ b, S* __restrict__ y, S* __restrict__ sum,
              float* __restrict__ mean, float* __restrict__ rstd, int64_t N, int D, float eps) {
@@ -179,7 +191,7 @@ __global__ void __launch_bounds__(MAXT, 1)
 
 // partials: [2][gridDim.x][D] (dw, db).
 template <typename S, int VEC, int NV, int MAXT, bool RES>
-__global__ void __launch_bounds__(MAXT, 1)
+__global__ void __launch_bounds__(MAXT, ln_min_ctas(true, RES, VEC * NV, MAXT))
     k_ln_bwd(const S* __restrict__ x, const float* __restrict__ w, const float* __restrict__ mean,
              const float* __restrict__ rstd, const S* __restrict__ dy, const S* __restrict__ dres,
              S* __restrict__ dx, float* __restrict__ partials, int64_t N, int D) {
@@ -315,17 +327,27 @@ struct LnShape {
 static LnShape ln_shape(int64_t D, int vec) {
     LnShape s{1, 0, 1};
     auto lanes = [&](int nv) { return (D + (int64_t)vec * nv - 1) / ((int64_t)vec * nv); };
-    while (vec * s.nv < 16 && lanes(s.nv) > 256) s.nv *= 2;
+    // (element by element: 1, 2, 3, 4, 5, 6, 8 or 16 of them, so that an odd width
+    // leaves few threads without one)
+    while (vec * s.nv < 16 && lanes(s.nv) > 256) s.nv = vec > 1 ? 2 * s.nv : s.nv < 6 ? s.nv + 1 : s.nv == 6 ? 8 : 16;
     if (lanes(s.nv) > 512) s.nv *= 2;
     s.t = (int)((lanes(s.nv) + 31) / 32 * 32);
     s.rows = s.t >= 256 ? 1 : 256 / s.t;
     return s;
 }
 
+// CTAs of a launch: the groups of rows, at most as many as are resident at once
+// (asked once per kernel, device and block size: `known`, one entry per warp count).
 template <class K>
-static int ln_grid(K kernel, int threads, size_t smem, int64_t groups) {
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n <= 0) n = 1;
+static int ln_grid(K kernel, int threads, size_t smem, int64_t groups, int (&known)[64][17]) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int& n = known[dev & 63][threads / 32];
+    if (n <= 0) {
+        int b = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, threads, smem) != cudaSuccess || b <= 0) b = 1;
+        n = b;
+    }
     const int64_t cap = (int64_t)n * sm_count();
     return (int)(groups < cap ? groups : cap);
 }
@@ -334,7 +356,8 @@ template <typename S, int VEC, int NV, int MAXT, bool RES>
 static cudaError_t ln_fwd_r(const LnShape& sh, const void* x, const void* res, const float* w,
                             const float* b, void* y, void* sum, float* mean, float* rstd, int64_t N,
                             int64_t D, float eps, cudaStream_t s) {
-    const int grid = ln_grid(k_ln_fwd<S, VEC, NV, MAXT, RES>, sh.t * sh.rows, 0, (N + sh.rows - 1) / sh.rows);
+    static int known[64][17] = {};
+    const int grid = ln_grid(k_ln_fwd<S, VEC, NV, MAXT, RES>, sh.t * sh.rows, 0, (N + sh.rows - 1) / sh.rows, known);
     k_ln_fwd<S, VEC, NV, MAXT, RES><<<grid, dim3(sh.t, sh.rows), 0, s>>>(
         (const S*)x, (const S*)res, w, b, (S*)y, (S*)sum, mean, rstd, N, (int)D, eps);
     return cudaGetLastError();
@@ -345,7 +368,8 @@ static cudaError_t ln_bwd_r(const LnShape& sh, const void* x, const float* w, co
                             const float* rstd, const void* dy, const void* dres, void* dx, float* dw,
                             float* db, float* partials, int64_t N, int64_t D, cudaStream_t s) {
     const size_t smem = (size_t)(sh.rows - 1) * sh.t * NV * VEC * sizeof(float);
-    int grid = ln_grid(k_ln_bwd<S, VEC, NV, MAXT, RES>, sh.t * sh.rows, smem, (N + sh.rows - 1) / sh.rows);
+    static int known[64][17] = {};
+    int grid = ln_grid(k_ln_bwd<S, VEC, NV, MAXT, RES>, sh.t * sh.rows, smem, (N + sh.rows - 1) / sh.rows, known);
     if (grid > kLnMaxPartials) grid = kLnMaxPartials;
     k_ln_bwd<S, VEC, NV, MAXT, RES><<<grid, dim3(sh.t, sh.rows), smem, s>>>(
         (const S*)x, w, mean, rstd, (const S*)dy, (const S*)dres, (S*)dx, partials, N, (int)D);
@@ -375,7 +399,10 @@ static cudaError_t ln_bwd_k(const LnShape& sh, const void* x, const float* w, co
         if (sh.nv == 2) return CALL(2, 256);                              \
     }                                                                     \
     if constexpr (VEC < 4) {                                              \
+        if (sh.nv == 3) return CALL(3, 256);                              \
         if (sh.nv == 4) return CALL(4, 256);                              \
+        if (sh.nv == 5) return CALL(5, 256);                              \
+        if (sh.nv == 6) return CALL(6, 256);                              \
         if (sh.nv == 8) return CALL(8, 256);                              \
     }                                                                     \
     if (sh.nv * VEC == 16) return sh.t <= 256 ? CALL((16 / VEC), 256) : CALL((16 / VEC), 512); \

@@ -495,8 +495,7 @@ def layer_norm_fwd(x, w, b=None, res=None, eps=1e-5, y=None, s=None, stream=None
     elif s is not None:
         raise ValueError("s is an output of the residual add: give res with it")
     y = torch.empty_like(x) if y is None else y
-    mean = torch.empty(row, dtype=f32, device=x.device)
-    rstd = torch.empty_like(mean)
+    mean, rstd = w.new_empty(row), w.new_empty(row)
     _check(load().layer_norm_fwd(x.data_ptr(), _opt("res", res, shape, dt, dev), _like("w", w, D, f32, dev),
                                  _opt("b", b, D, f32, dev), _like("y", y, shape, dt, dev),
                                  _opt("s", s, shape, dt, dev), mean.data_ptr(), rstd.data_ptr(), mean.numel(),

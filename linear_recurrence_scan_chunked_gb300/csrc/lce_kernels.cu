@@ -92,32 +92,33 @@ __device__ __forceinline__ float pick32(const float (&v)[32], int j) {
 // multiply-add rounds nothing but the result, and no common error enters the sum.
 template <bool CHUNKED>
 struct StatsEpi {
-    static constexpr bool kChunked = CHUNKED;
+    static constexpr bool kChunked = CHUNKED, kStaged = false;
     float2* part;           // [half tiles][rows]
     float* tl;              // the targets' logits
     const int64_t* target;
     int64_t rows, V;
+    int tn;                 // columns of a tile
     struct Row {
         int64_t n, slot;
         int width, at;
         float M, s;
     };
     __device__ int width(const Tile& t, int half) const {
-        const int64_t w = V - (int64_t)t.n * kTile - half * mm::kHalf;
-        return (int)(w < mm::kHalf ? w : mm::kHalf);
+        const int64_t w = V - ((int64_t)t.n * 2 + half) * (tn / 2);
+        return (int)(w < tn / 2 ? w : tn / 2);
     }
     __device__ Row begin(const Tile& t, int row, int half) const {
         Row r;
         r.n = (int64_t)t.m * kTile + row;
         r.slot = (int64_t)t.n * 2 + half;
         r.width = width(t, half);
-        const int64_t tg = r.n < rows ? __ldg(target + r.n) - r.slot * mm::kHalf : -1;
+        const int64_t tg = r.n < rows ? __ldg(target + r.n) - r.slot * (tn / 2) : -1;
         r.at = tg >= 0 && tg < r.width ? (int)tg : -1;
         r.M = -INFINITY;
         r.s = 0.f;
         return r;
     }
-    __device__ void cols(Row& r, int c, float (&v)[32]) const {
+    __device__ void cols(Row& r, int c, float (&v)[32], float*) const {
         if (r.width < c * 32 + 32) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = c * 32 + i < r.width ? v[i] : -INFINITY;
@@ -175,20 +176,6 @@ __global__ void __launch_bounds__(1024)
     loss[n] = t == ignore || !in ? 0.f : z - tl[n];
 }
 
-// max |dloss| over the rows that count (finite ones), as float bits: the maximum
-// of non-negative floats is the maximum of their bits, in any order.
-__global__ void __launch_bounds__(256)
-    k_lce_scale(const float* __restrict__ dloss, const int64_t* __restrict__ target, int64_t ignore, int64_t N, int64_t V,
-                uint32_t* __restrict__ top) {
-    uint32_t m = 0;
-    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < N; n += (int64_t)gridDim.x * 256) {
-        const int64_t t = target[n];
-        const float a = fabsf(dloss[n]);
-        if (t != ignore && t >= 0 && t < V && a < INFINITY) m = max(m, __float_as_uint(a));
-    }
-    m = __reduce_max_sync(0xffffffffu, m);
-    if ((threadIdx.x & 31) == 0 && m) atomicMax(top, m);
-}
 __device__ __forceinline__ float scale_of(const uint32_t* top) {
     const float s = __uint_as_float(__ldg(top));
     return s > 0.f ? s : 1.f;
@@ -197,7 +184,7 @@ __device__ __forceinline__ float scale_of(const uint32_t* top) {
 // Backward: g / max|dloss| of a tile, in P bf16 planes.
 template <int P>
 struct GradEpi {
-    static constexpr bool kChunked = P > 1;
+    static constexpr bool kChunked = P > 1, kStaged = false;
     __nv_bfloat16* g;  // [P][rows][pitch]
     int64_t pitch;     // a multiple of 16
     int64_t plane;     // elements of a plane
@@ -206,6 +193,7 @@ struct GradEpi {
     const int64_t* target;
     const uint32_t* top;
     int64_t ignore, rows, v0, vc, V;
+    int tn;
     struct Row {
         int64_t n;
         __nv_bfloat16* out;
@@ -213,13 +201,13 @@ struct GradEpi {
         float f, ds, hi, z;
     };
     __device__ int width(const Tile& t, int half) const {
-        const int64_t w = vc - (int64_t)t.n * kTile - half * mm::kHalf;
-        return (int)(w < mm::kHalf ? w : mm::kHalf);
+        const int64_t w = vc - ((int64_t)t.n * 2 + half) * (tn / 2);
+        return (int)(w < tn / 2 ? w : tn / 2);
     }
     __device__ Row begin(const Tile& t, int row, int half) const {
         Row r;
         r.n = (int64_t)t.m * kTile + row;
-        const int64_t c0 = (int64_t)t.n * kTile + half * mm::kHalf;
+        const int64_t c0 = ((int64_t)t.n * 2 + half) * (tn / 2);
         r.width = width(t, half);
         r.out = g + r.n * pitch + c0;
         r.f = r.ds = r.z = 0.f;
@@ -240,7 +228,7 @@ struct GradEpi {
         }
         return r;
     }
-    __device__ void cols(Row& r, int c, float (&v)[32]) const {
+    __device__ void cols(Row& r, int c, float (&v)[32], float*) const {
         const bool mine = r.at >> 5 == c, any = __any_sync(0xffffffffu, mine);
         float gt = 0.f;
         // the target's p - 1 without cancellation where p is near 1
@@ -268,12 +256,13 @@ struct GradEpi {
 // the k loop, fp32.
 template <typename S>
 struct OutEpi {
-    static constexpr bool kChunked = sizeof(S) == 4;
+    static constexpr bool kChunked = sizeof(S) == 4, kStaged = true;
     S* out;         // nullptr: parts
     float* part;    // [splits][rows x cols]
     int64_t pitch;  // elements of a part
     const uint32_t* top;
     int64_t rows, cols_n;
+    int tn;
     bool wide;      // rows of the destination are 32-byte aligned
     struct Row {
         int64_t m, at;
@@ -281,26 +270,44 @@ struct OutEpi {
         float a;
     };
     __device__ int width(const Tile& t, int half) const {
-        const int64_t w = cols_n - (int64_t)t.n * kTile - half * mm::kHalf;
-        return (int)(w < mm::kHalf ? w : mm::kHalf);
+        const int64_t w = cols_n - ((int64_t)t.n * 2 + half) * (tn / 2);
+        return (int)(w < tn / 2 ? w : tn / 2);
     }
     __device__ Row begin(const Tile& t, int row, int half) const {
         Row r;
         r.m = (int64_t)t.m * kTile + row;
         r.width = width(t, half);
-        r.at = (out ? 0 : t.split * pitch) + r.m * cols_n + (int64_t)t.n * kTile + half * mm::kHalf;
+        r.at = (out ? 0 : t.split * pitch) + r.m * cols_n + ((int64_t)t.n * 2 + half) * (tn / 2);
         r.a = out ? scale_of(top) : 1.f;
         return r;
     }
-    __device__ void cols(Row& r, int c, float (&v)[32]) const {
-        if (r.m >= rows) return;
+    __device__ void cols(Row& r, int c, float (&v)[32], float* scratch) const {
         if (out) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= r.a;
-            st_row32(out + r.at + c * 32, v, r.width - c * 32, wide);
-        } else {
-            st_row32(part + r.at + c * 32, v, r.width - c * 32, wide);
         }
+        if (wide && r.width - c * 32 >= 32) {  // 32 bytes a lane, whole sectors
+            if (r.m >= rows) return;
+            if (out) st_row32(out + r.at + c * 32, v, 32, true);
+            else st_row32(part + r.at + c * 32, v, 32, true);
+            return;
+        }
+        // unaligned rows: through shared memory, so that a store writes 32
+        // neighbouring elements of one row
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) scratch[lane * 33 + i] = v[i];
+        __syncwarp();
+        const int64_t m0 = r.m - lane, at0 = r.at - lane * cols_n + c * 32 + lane;
+        const int n = (int)(rows - m0 < 32 ? rows - m0 : 32);
+        if (lane < r.width - c * 32) {
+            for (int i = 0; i < n; ++i) {
+                const float o[1] = {scratch[i * 33 + lane]};
+                if (out) store_vec<S, 1>(out + at0 + i * cols_n, o);
+                else store_vec<float, 1>(part + at0 + i * cols_n, o);
+            }
+        }
+        __syncwarp();
     }
     __device__ void end(Row&) const {}
 };
@@ -315,11 +322,16 @@ __global__ void __launch_bounds__(256)
     if (vec) {
         for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n / 4; i += step) {
             float s[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int64_t k = 0; k < parts; ++k) {
-                Pack<float, 4> p;
-                p.load(part + k * pitch + 4 * i);
+            for (int64_t k = 0; k < parts; k += 8) {  // eight loads in flight, added in order
+                Pack<float, 4> p[8];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[j] += p.get(j);
+                for (int u = 0; u < 8; ++u)
+                    if (k + u < parts) p[u].load(part + (k + u) * pitch + 4 * i);
+                    else p[u].ident(0.f);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[j] += p[u].get(j);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[j] *= a;
@@ -334,25 +346,72 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// [rows][D] into P bf16 planes of pitch ld (a multiple of 8): fp32 data split into
-// three, bf16 data whose rows TMA cannot read (odd widths, unaligned views) copied.
+// A matrix on its way into planes: [rows][D] into P bf16 planes of pitch ld (a
+// multiple of 8; the columns past D are never read).
+struct PackJob {
+    const void* src;
+    __nv_bfloat16* dst;
+    int64_t rows, D, ld;
+};
+
+// Before the products, one launch: block 0 takes max |dloss| over the rows that
+// count (finite ones) into `top`, as float bits; the other blocks pack x and W --
+// fp32 data split into three planes, bf16 data whose rows TMA cannot read (odd
+// widths, unaligned views) copied.  A warp takes a row, four elements a lane.
 template <typename S, int P>
 __global__ void __launch_bounds__(256)
-    k_lce_pack(const S* __restrict__ src, __nv_bfloat16* __restrict__ dst, int64_t rows, int64_t D, int64_t ld) {
-    const int64_t plane = rows * ld, n = rows * ld;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / ld, d = i - r * ld;
-        float v = 0.f;
-        if (d < D) {
-            Pack<S, 1> p;
-            p.load(src + r * D + d);
-            v = p.get(0);
-        }
+    k_lce_prep(const PackJob jx, const PackJob jw, const float* __restrict__ dloss, const int64_t* __restrict__ target,
+               int64_t ignore, int64_t N, int64_t V, uint32_t* __restrict__ top) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x == 0) {
+        __shared__ uint32_t sm[8];
+        if (top == nullptr) return;
+        uint32_t m = 0;
+        for (int64_t n0 = threadIdx.x; n0 < N; n0 += 1024) {
+            float a[4];
+            int64_t t[4];
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-            const __nv_bfloat16 b = __float2bfloat16_rn(v);
-            dst[k * plane + i] = b;
-            v -= __bfloat162float(b);
+            for (int u = 0; u < 4; ++u) {
+                const int64_t n = n0 + 256 * u;
+                a[u] = n < N ? fabsf(__ldg(dloss + n)) : 0.f;
+                t[u] = n < N ? __ldg(target + n) : ignore;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (t[u] != ignore && t[u] >= 0 && t[u] < V && a[u] < INFINITY) m = max(m, __float_as_uint(a[u]));
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) sm[warp] = m;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 8; ++w) m = max(m, sm[w]);
+            *top = m;
+        }
+        return;
+    }
+    const int64_t warps = (int64_t)(gridDim.x - 1) * 8;
+    for (int64_t row = (int64_t)(blockIdx.x - 1) * 8 + warp; row < jx.rows + jw.rows; row += warps) {
+        const bool first = row < jx.rows;
+        const PackJob& j = first ? jx : jw;
+        const int64_t r = first ? row : row - jx.rows;
+        const S* src = (const S*)j.src + r * j.D;
+        __nv_bfloat16* dst = j.dst + r * j.ld;
+        const int64_t plane = j.rows * j.ld;
+        for (int64_t d = lane * 4; d < j.D; d += 128) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                Pack<S, 1> p;
+                p.ident(0.f);
+                if (d + i < j.D) p.load(src + d + i);
+                v[i] = p.get(0);
+            }
+#pragma unroll
+            for (int k = 0; k < P; ++k) {  // rows are padded to 8: 8-byte stores stay inside
+                const uint32_t a = bf_pack(v[0], v[1]), b = bf_pack(v[2], v[3]);
+                *reinterpret_cast<uint2*>(dst + k * plane + d) = make_uint2(a, b);
+                v[0] -= bf_lo(a); v[1] -= bf_hi(a); v[2] -= bf_lo(b); v[3] -= bf_hi(b);
+            }
         }
     }
 }
@@ -368,25 +427,26 @@ struct Operand {
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// mn: the product takes it MN-major (boxes of 64 x 64), else K-major (64 x 128).
-bool operand_map(CUtensorMap* m, const Operand& o, bool mn) {
-    return tma_encode_planes(m, o.p, o.cols, o.rows, o.planes, o.ld, o.plane, mm::kBlockK, mn ? mm::kBlockK : mm::kHalf);
+// mn: the product takes it MN-major (boxes of 64 x 64), else K-major (64 x box_rows).
+bool operand_map(CUtensorMap* m, const Operand& o, bool mn, int box_rows) {
+    return tma_encode_planes(m, o.p, o.cols, o.rows, o.planes, o.ld, o.plane, mm::kBlockK, mn ? mm::kBlockK : box_rows);
 }
 
 // Pairs of CTAs resident at once.
-template <class Epi>
+template <class Epi, int TN>
 cudaError_t mm_pairs(int* pairs) {
     static int known[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);
     int& n = known[dev & 63];
+    constexpr int smem = mm::Cfg<TN>::smem(Epi::kStaged);
     if (n <= 0) {
-        cudaError_t e = cudaFuncSetAttribute(mm::k_mm<Epi>, cudaFuncAttributeMaxDynamicSharedMemorySize, mm::kSmem);
+        cudaError_t e = cudaFuncSetAttribute(mm::k_mm<Epi, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t lc{};
         lc.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
         lc.blockDim = dim3(mm::kThreads);
-        lc.dynamicSmemBytes = mm::kSmem;
+        lc.dynamicSmemBytes = smem;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeClusterDimension;
         at[0].val.clusterDim.x = 2;
@@ -394,33 +454,39 @@ cudaError_t mm_pairs(int* pairs) {
         lc.attrs = at;
         lc.numAttrs = 1;
         int c = 0;
-        if (cudaOccupancyMaxActiveClusters(&c, mm::k_mm<Epi>, &lc) != cudaSuccess || c < 1) c = 1;
+        if (cudaOccupancyMaxActiveClusters(&c, mm::k_mm<Epi, TN>, &lc) != cudaSuccess || c < 1) c = 1;
         n = c < sm_count() / 2 ? c : sm_count() / 2;
     }
     *pairs = n;
     return cudaSuccess;
 }
 
-template <class Epi>
-cudaError_t mm_run(const Operand& a, const Operand& b, Shape sh, const Epi& epi, uint32_t* err, cudaStream_t s) {
+template <class Epi, int TN>
+cudaError_t mm_launch(const Operand& a, const Operand& b, const Shape& sh, const Epi& epi, uint32_t* err, cudaStream_t s) {
     CUtensorMap ma, mb;
-    if (!operand_map(&ma, a, sh.a_mn) || !operand_map(&mb, b, sh.b_mn)) return cudaErrorInvalidValue;
+    if (!operand_map(&ma, a, sh.a_mn, mm::kHalf) || !operand_map(&mb, b, sh.b_mn, TN / 2)) return cudaErrorInvalidValue;
     int pairs = 1;
-    const cudaError_t e = mm_pairs<Epi>(&pairs);
+    const cudaError_t e = mm_pairs<Epi, TN>(&pairs);
     if (e != cudaSuccess) return e;
     const uint64_t tiles = (uint64_t)sh.tm * sh.tn * sh.splits;
     if (tiles > 0x7fffffffull) return cudaErrorInvalidValue;
     const unsigned grid = 2 * (unsigned)std::min<uint64_t>(tiles, (uint64_t)pairs);
-    mm::k_mm<Epi><<<grid, mm::kThreads, mm::kSmem, s>>>(ma, mb, sh, epi, err);
+    mm::k_mm<Epi, TN><<<grid, mm::kThreads, mm::Cfg<TN>::smem(Epi::kStaged), s>>>(ma, mb, sh, epi, err);
     return cudaGetLastError();
 }
 
-Shape mm_shape(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, bool n_fast, int64_t splits) {
+// How a product M x N x K is cut: tiles of 256 x tn, the k loop in `splits` parts.
+struct MmPlan {
+    int tn;
+    int64_t splits;
+};
+
+Shape mm_shape(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, bool n_fast, const MmPlan& pl) {
     Shape s{};
     s.tm = (uint32_t)((M + kTile - 1) / kTile);
-    s.tn = (uint32_t)((N + kTile - 1) / kTile);
+    s.tn = (uint32_t)((N + pl.tn - 1) / pl.tn);
     s.kb = (uint32_t)((K + mm::kBlockK - 1) / mm::kBlockK);
-    s.kb_split = (uint32_t)((s.kb + splits - 1) / splits);
+    s.kb_split = (uint32_t)((s.kb + pl.splits - 1) / pl.splits);
     s.splits = (s.kb + s.kb_split - 1) / s.kb_split;
     s.pairs = planes == 1 ? 1 : 6;
     s.n_fast = n_fast;
@@ -429,25 +495,34 @@ Shape mm_shape(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn
     return s;
 }
 
-// Parts of the k loop of a product M x N x K: the number that gives the shortest
-// time in a simple model, rounds of tiles over the pairs at a pair's rate (a
-// k-block of 64 takes about 512 cycles) plus the parts' way to memory and back
-// (about 3.5 KB a cycle over the GPU).  With few tiles the parts fill the GPU;
-// with many they even out its last round.
-int64_t mm_splits(int64_t M, int64_t N, int64_t K, int planes) {
-    const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-    const int64_t kb = (K + mm::kBlockK - 1) / mm::kBlockK, pairs = sm_count() / 2;
-    int64_t best = 1;
+template <class Epi>
+cudaError_t mm_run(const Operand& a, const Operand& b, const Shape& sh, Epi epi, int tn, uint32_t* err, cudaStream_t s) {
+    epi.tn = tn;
+    return tn == 256 ? mm_launch<Epi, 256>(a, b, sh, epi, err, s) : mm_launch<Epi, 128>(a, b, sh, epi, err, s);
+}
+
+// The cut of a product that takes the shortest time in a simple model: rounds of
+// tiles over the pairs, each at a pair's rate (a k-block of 64 by 256 columns takes
+// about 512 cycles, by 128 about 300: its operands come from L2 twice as often)
+// plus about 1500 cycles of latency, plus, with more than one part, the parts' way
+// to memory and back (about 3.5 KB a cycle over the GPU).  With few tiles narrow ones
+// and parts fill the GPU; with many, parts even out its last round.
+MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int planes, bool may_split) {
+    const int64_t kb = (K + mm::kBlockK - 1) / mm::kBlockK, pairs = kSpanSms / 2;
+    MmPlan best{256, 1};
     double best_t = 0;
-    for (int64_t s = 1; s <= 64 && s <= kb; ++s) {
-        const int64_t per = (kb + s - 1) / s, real = (kb + per - 1) / per;
-        if (real != s) continue;
-        const double rounds = (double)((tiles * s + pairs - 1) / pairs);
-        double t = rounds * (double)per * (planes == 1 ? 1 : 6) * 512 + rounds * 1500;
-        if (s > 1) t += (double)(s * M * N) * 8 / 3500 + 4000;
-        if (best_t == 0 || t < 0.98 * best_t) {
-            best = s;
-            best_t = t;
+    for (int tn : {256, 128}) {
+        const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + tn - 1) / tn);
+        for (int64_t s = 1; s <= (may_split ? 64 : 1) && s <= kb; ++s) {
+            const int64_t per = (kb + s - 1) / s, real = (kb + per - 1) / per;
+            if (real != s) continue;
+            const double rounds = (double)((tiles * s + pairs - 1) / pairs);
+            double t = rounds * ((double)per * (planes == 1 ? 1 : 6) * (tn == 256 ? 512 : 300) + 1500);
+            if (s > 1) t += (double)(s * M * N) * 8 / 3500 + 4000;
+            if (best_t == 0 || t < 0.98 * best_t) {
+                best = MmPlan{tn, s};
+                best_t = t;
+            }
         }
     }
     return best;
@@ -485,16 +560,25 @@ Layout layout(int dtype, const void* x, const void* w, int64_t N, int64_t V, int
     return l;
 }
 
-// The operand of a caller's matrix, packed into the scratch where it has to be.
+// The operand of a caller's matrix, and the job that packs it into the scratch
+// where it has to be (rows = 0: it need not).
 template <typename S>
-cudaError_t operand(const void* src, int64_t rows, int64_t D, void* scratch, Operand* o, cudaStream_t s) {
+Operand operand(const void* src, int64_t rows, int64_t D, void* scratch, PackJob* job) {
     constexpr int P = sizeof(S) == 4 ? 3 : 1;
-    *o = Operand{(const __nv_bfloat16*)src, rows, D, D, rows * D, P};
-    if (!packed(sizeof(S) == 4 ? 0 : 1, src, D)) return cudaSuccess;
+    *job = PackJob{nullptr, nullptr, 0, 0, 0};
+    if (!packed(sizeof(S) == 4 ? 0 : 1, src, D)) return Operand{(const __nv_bfloat16*)src, rows, D, D, rows * D, P};
     const int64_t ld = round_up(D, 8);
-    const int64_t blocks = std::min<int64_t>((rows * ld + 255) / 256, (int64_t)sm_count() * 16);
-    k_lce_pack<S, P><<<(unsigned)blocks, 256, 0, s>>>((const S*)src, (__nv_bfloat16*)scratch, rows, D, ld);
-    *o = Operand{(const __nv_bfloat16*)scratch, rows, D, ld, rows * ld, P};
+    *job = PackJob{src, (__nv_bfloat16*)scratch, rows, D, ld};
+    return Operand{(const __nv_bfloat16*)scratch, rows, D, ld, rows * ld, P};
+}
+
+template <typename S>
+cudaError_t prepare(const PackJob& jx, const PackJob& jw, const float* dloss, const int64_t* target, int64_t ignore,
+                    int64_t N, int64_t V, uint32_t* top, cudaStream_t s) {
+    const int64_t rows = jx.rows + jw.rows;
+    if (rows == 0 && top == nullptr) return cudaSuccess;
+    const int64_t blocks = 1 + std::min<int64_t>((rows + 7) / 8, (int64_t)sm_count() * 8);
+    k_lce_prep<S, sizeof(S) == 4 ? 3 : 1><<<(unsigned)blocks, 256, 0, s>>>(jx, jw, dloss, target, ignore, N, V, top);
     return cudaGetLastError();
 }
 
@@ -508,9 +592,9 @@ template <typename S>
 cudaError_t lce_fwd_t(const void* x, const void* w, const int64_t* target, int64_t ignore, float* loss, float* lse,
                       int64_t N, int64_t V, int64_t D, const LcePlan& pl, char* sc, uint32_t* err, cudaStream_t s) {
     const Layout l = layout(sizeof(S) == 4 ? 0 : 1, x, w, N, V, D, pl, false);
-    Operand ox, ow;
-    LCE_TRY(operand<S>(x, N, D, sc + l.x, &ox, s));
-    LCE_TRY(operand<S>(w, V, D, sc + l.w, &ow, s));
+    PackJob jx, jw;
+    const Operand ox = operand<S>(x, N, D, sc + l.x, &jx), ow = operand<S>(w, V, D, sc + l.w, &jw);
+    LCE_TRY(prepare<S>(jx, jw, nullptr, target, ignore, N, V, nullptr, s));
     float2* part = (float2*)(sc + l.part);
     float* tl = (float*)(sc + l.tl);
     for (int64_t r = 0; r < N; r += pl.rows) {
@@ -518,11 +602,11 @@ cudaError_t lce_fwd_t(const void* x, const void* w, const int64_t* target, int64
         Operand a = ox;
         a.p += r * a.ld;
         a.rows = n;
-        const Shape sh = mm_shape(n, V, D, ox.planes, false, false, false, 1);
+        const Shape sh = mm_shape(n, V, D, ox.planes, false, false, false, MmPlan{pl.tn_logits, 1});
         if (sh.kb * sh.pairs > mm::kChunk)
-            LCE_TRY(mm_run(a, ow, sh, StatsEpi<true>{part, tl, target + r, n, V}, err, s));
+            LCE_TRY(mm_run(a, ow, sh, StatsEpi<true>{part, tl, target + r, n, V, 0}, pl.tn_logits, err, s));
         else
-            LCE_TRY(mm_run(a, ow, sh, StatsEpi<false>{part, tl, target + r, n, V}, err, s));
+            LCE_TRY(mm_run(a, ow, sh, StatsEpi<false>{part, tl, target + r, n, V, 0}, pl.tn_logits, err, s));
         k_lce_join<<<(unsigned)((n + 31) / 32), dim3(32, 32), 0, s>>>(part, pl.tiles, tl, target + r, ignore, loss + r,
                                                                      lse + r, n, V, err);
         LCE_TRY(cudaGetLastError());
@@ -546,12 +630,9 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
     constexpr int P = sizeof(S) == 4 ? 3 : 1;
     const Layout l = layout(sizeof(S) == 4 ? 0 : 1, x, w, N, V, D, pl, true);
     uint32_t* top = (uint32_t*)(sc + l.top);
-    LCE_TRY(cudaMemsetAsync(top, 0, 4, s));
-    k_lce_scale<<<(unsigned)std::min<int64_t>((N + 255) / 256, sm_count()), 256, 0, s>>>(dloss, target, ignore, N, V, top);
-    LCE_TRY(cudaGetLastError());
-    Operand ox, ow;
-    LCE_TRY(operand<S>(x, N, D, sc + l.x, &ox, s));
-    LCE_TRY(operand<S>(w, V, D, sc + l.w, &ow, s));
+    PackJob jx, jw;
+    const Operand ox = operand<S>(x, N, D, sc + l.x, &jx), ow = operand<S>(w, V, D, sc + l.w, &jw);
+    LCE_TRY(prepare<S>(jx, jw, dloss, target, ignore, N, V, top, s));
     __nv_bfloat16* g = (__nv_bfloat16*)(sc + l.g);
     float* px = (float*)(sc + l.px);
     float* pw = (float*)(sc + l.pw);
@@ -564,24 +645,24 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
         wp.p += v0 * ow.ld;
         wp.rows = vc;
         const Operand og{g, N, vc, pitch, N * pitch, P};
-        LCE_TRY(mm_run(ox, wp, mm_shape(N, vc, D, P, false, false, false, 1),
-                       GradEpi<P>{g, pitch, N * pitch, lse, dloss, target, top, ignore, N, v0, vc, V}, err, s));
+        LCE_TRY(mm_run(ox, wp, mm_shape(N, vc, D, P, false, false, false, MmPlan{pl.tn_logits, 1}),
+                       GradEpi<P>{g, pitch, N * pitch, lse, dloss, target, top, ignore, N, v0, vc, V, 0}, pl.tn_logits, err, s));
         // dx: rows of x by features, over the words of the piece
-        const Shape sx = mm_shape(N, D, vc, P, false, true, true, pl.dx_splits);
+        const Shape sx = mm_shape(N, D, vc, P, false, true, true, MmPlan{pl.tn_dx, pl.dx_splits});
         const bool dx_direct = pl.dx_parts == 1;
         LCE_TRY(mm_run(og, wp, sx,
-                       OutEpi<S>{dx_direct ? (S*)dx : nullptr, px + part * xpitch, xpitch, top, N, D,
+                       OutEpi<S>{dx_direct ? (S*)dx : nullptr, px + part * xpitch, xpitch, top, N, D, 0,
                                  dx_direct ? wide_s && ((uintptr_t)dx & 31) == 0 : wide_f},
-                       err, s));
+                       pl.tn_dx, err, s));
         part += sx.splits;
         // dw: words of the piece by features, over the rows of x
-        const Shape sw = mm_shape(vc, D, N, P, true, true, true, pl.dw_splits);
+        const Shape sw = mm_shape(vc, D, N, P, true, true, true, MmPlan{pl.tn_dw, pl.dw_splits});
         const bool dw_direct = pl.dw_splits == 1;
         S* dwp = (S*)dw + v0 * D;
         LCE_TRY(mm_run(og, ox, sw,
-                       OutEpi<S>{dw_direct ? dwp : nullptr, pw, wpitch, top, vc, D,
+                       OutEpi<S>{dw_direct ? dwp : nullptr, pw, wpitch, top, vc, D, 0,
                                  dw_direct ? wide_s && ((uintptr_t)dwp & 31) == 0 : wide_f},
-                       err, s));
+                       pl.tn_dw, err, s));
         if (!dw_direct) LCE_TRY(sum_parts<S>(pw, sw.splits, wpitch, vc * D, top, dwp, s));
     }
     if (pl.dx_parts > 1) LCE_TRY(sum_parts<S>(px, part, xpitch, N * D, top, (S*)dx, s));
@@ -594,16 +675,21 @@ LcePlan lce_plan(int dtype, const void* x, const void* w, int64_t N, int64_t V, 
     LcePlan p{};
     const int planes = dtype == 0 ? 3 : 1;
     if (!bwd) {
-        p.tiles = (V + mm::kHalf - 1) / mm::kHalf;
         p.rows = std::min<int64_t>(N, 16384);
+        p.tn_logits = mm_plan(p.rows, V, D, planes, false).tn;
+        p.tiles = (V + p.tn_logits / 2 - 1) / (p.tn_logits / 2);
     } else {
         p.piece = std::max<int64_t>(kPieceBytes / (N * 2 * planes) / kTile, 1) * kTile;
         if (p.piece >= V) p.piece = V;
-        p.dx_splits = mm_splits(N, D, p.piece, planes);
-        p.dw_splits = mm_splits(p.piece, D, N, planes);
+        p.tn_logits = mm_plan(N, p.piece, D, planes, false).tn;
+        const MmPlan dx = mm_plan(N, D, p.piece, planes, true), dw = mm_plan(p.piece, D, N, planes, true);
+        p.tn_dx = dx.tn;
+        p.dx_splits = dx.splits;
+        p.tn_dw = dw.tn;
+        p.dw_splits = dw.splits;
         p.dx_parts = 0;
         for (int64_t v0 = 0; v0 < V; v0 += p.piece)
-            p.dx_parts += mm_shape(N, D, std::min(p.piece, V - v0), planes, false, true, true, p.dx_splits).splits;
+            p.dx_parts += mm_shape(N, D, std::min(p.piece, V - v0), planes, false, true, true, dx).splits;
     }
     p.bytes = layout(dtype, x, w, N, V, D, p, bwd).bytes;
     return p;

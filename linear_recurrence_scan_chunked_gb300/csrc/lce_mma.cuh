@@ -2,11 +2,12 @@
 // (tcgen05.mma, bf16 operands, fp32 accumulators in TMEM).
 //
 // One kernel, three products: logits x W^T, g W and g^T x.  A pair of CTAs
-// (cta_group::2, a cluster of two on neighbouring SMs) owns a 256 x 256 tile of
+// (cta_group::2, a cluster of two on neighbouring SMs) owns a 256 x TN tile of
 // the result: each holds 128 rows of A, half of B and the accumulators of its
 // 128 rows, so an operand byte in shared memory feeds twice the arithmetic of a
-// single CTA's tile.  Per CTA: a producer thread keeps a ring of kStages k-blocks
-// of 64 in flight by TMA (128-byte swizzle), one thread of the pair's first CTA
+// single CTA's tile.  TN is 256; 128 where tiles of 256 would leave pairs idle.
+// Per CTA: a producer thread keeps a ring of k-blocks of 64 in flight by TMA
+// (128-byte swizzle), one thread of the pair's first CTA
 // issues the MMAs, and eight warps read finished accumulators back and run the
 // epilogue while the next tile accumulates in the other half of TMEM.
 //
@@ -32,15 +33,23 @@
 namespace lrs {
 namespace mm {
 
-constexpr int kTile = 256;       // rows and columns of a pair's tile
-constexpr int kHalf = 128;       // rows of A and of B that a CTA holds
+constexpr int kTile = 256;       // rows of a pair's tile
+constexpr int kHalf = 128;       // rows of A that a CTA holds
 constexpr int kBlockK = 64;      // k-block: 128 bytes of bf16, the swizzle's width
-constexpr int kStages = 6;
-constexpr int kOperand = kHalf * kBlockK * 2;  // 16 KB: one operand of a stage
-constexpr int kStageBytes = 2 * kOperand;
+constexpr int kOperandA = kHalf * kBlockK * 2;  // 16 KB: A of a stage
 constexpr int kThreads = 320;    // producer warp, MMA warp, 8 epilogue warps
 constexpr uint32_t kChunk = 16;  // k-blocks of a chunk: k = 1024, a shrinkage of 3e-7
-constexpr int kSmem = kStages * kStageBytes + 1024;  // + alignment to 1024
+constexpr int kScratch = 32 * 33 * 4;  // bytes an epilogue warp may use
+
+template <int TN>
+struct Cfg {
+    static constexpr int kHalfN = TN / 2;                      // rows of B that a CTA holds; columns of an epilogue warp
+    static constexpr int kOperandB = kHalfN * kBlockK * 2;
+    static constexpr int kStageBytes = kOperandA + kOperandB;  // of one CTA
+    static constexpr int kStages = TN == 256 ? 6 : 8;          // 192 KB
+    static constexpr int kRing = kStages * kStageBytes;
+    static constexpr int smem(bool scratch) { return kRing + 1024 + (scratch ? 8 * kScratch : 0); }
+};
 
 // What the products share: the tile grid and the k loop.
 struct Shape {
@@ -136,9 +145,9 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool mn) {
     return (uint64_t)((addr >> 4) & 0x3fff) | lead << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
            (uint64_t)2 << 61;
 }
-// bf16 x bf16 -> fp32, 256 x 256.
-__device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn) {
-    return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 | (uint32_t)(kTile >> 3) << 17 |
+// bf16 x bf16 -> fp32, 256 x tn.
+__device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int tn) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 | (uint32_t)(tn >> 3) << 17 |
            (uint32_t)(kTile >> 4) << 24;
 }
 
@@ -173,15 +182,18 @@ __device__ __forceinline__ uint32_t tile_steps(const Shape& s, const Tile& t) {
 
 // Epilogue: a struct with
 //   kChunked                       sum the k loop in chunks
+//   kStaged                        cols() uses the warp's scratch
 //   Row                            what a thread keeps of its row of a tile
 //   begin(tile, row, half) -> Row  row 0 .. 255 of the tile, half 0 / 1 of its columns
 //   width(tile, half)              columns of the half inside the result (may be <= 0)
-//   cols(Row&, c, v[32])           columns 32c .. 32c + 31 of the half (whole warps)
+//   cols(Row&, c, v[32], scratch)  columns 32c .. 32c + 31 of the half (whole warps)
 //   end(Row&)
-template <class Epi>
+template <class Epi, int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_mm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const Shape sh,
          const Epi epi, uint32_t* err) {
+    using C = Cfg<TN>;
+    constexpr uint32_t kStages = C::kStages, kStageBytes = C::kStageBytes;
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2];
     __shared__ uint32_t tmem_base;
@@ -192,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t n_tiles = sh.tm * sh.tn * sh.splits;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (uint32_t i = 0; i < kStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
@@ -202,7 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         mbar_init_fence();
     }
-    if (warp == 1) tmem_alloc(&tmem_base, 512);
+    if (warp == 1) tmem_alloc(&tmem_base, 2 * TN);
     fence_before();
     __syncthreads();
     pair_sync();
@@ -215,7 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t it = 0;
             for (uint32_t t = pair; t < n_tiles && ok; t += n_pairs) {
                 const Tile tl = tile_of(sh, t);
-                const int32_t m0 = (int32_t)(tl.m * kTile + rank * kHalf), n0 = (int32_t)(tl.n * kTile + rank * kHalf);
+                const int32_t m0 = (int32_t)(tl.m * kTile + rank * kHalf), n0 = (int32_t)(tl.n * TN + rank * C::kHalfN);
                 const uint32_t k0 = tl.split * sh.kb_split;
                 const uint32_t k1 = k0 + sh.kb_split < sh.kb ? k0 + sh.kb_split : sh.kb;
                 for (uint32_t p = 0; p < sh.pairs && ok; ++p) {
@@ -229,17 +241,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         if (rank == 0) mbar_arrive_tx(&full[st], 2 * kStageBytes);
                         const uint32_t bar = cluster_addr(&full[st], 0);
                         unsigned char* a = ring + st * kStageBytes;
-                        unsigned char* b = a + kOperand;
+                        unsigned char* b = a + kOperandA;
                         const int32_t kk = (int32_t)(k * kBlockK);
                         if (sh.a_mn) {
                             tma_load_pair(a, &map_a, m0, kk, pa, bar);
-                            tma_load_pair(a + kOperand / 2, &map_a, m0 + 64, kk, pa, bar);
+                            tma_load_pair(a + kOperandA / 2, &map_a, m0 + 64, kk, pa, bar);
                         } else {
                             tma_load_pair(a, &map_a, kk, m0, pa, bar);
                         }
                         if (sh.b_mn) {
                             tma_load_pair(b, &map_b, n0, kk, pb, bar);
-                            tma_load_pair(b + kOperand / 2, &map_b, n0 + 64, kk, pb, bar);
+                            if constexpr (TN == 256) tma_load_pair(b + 8192, &map_b, n0 + 64, kk, pb, bar);
                         } else {
                             tma_load_pair(b, &map_b, kk, n0, pb, bar);
                         }
@@ -254,7 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {  // MMA issue
-            const uint32_t idesc = instr_desc(sh.a_mn, sh.b_mn);
+            const uint32_t idesc = instr_desc(sh.a_mn, sh.b_mn, TN);
             const uint32_t step_a = sh.a_mn ? 2048 >> 4 : 32 >> 4, step_b = sh.b_mn ? 2048 >> 4 : 32 >> 4;
             uint32_t it = 0, seq = 0;
             for (uint32_t t = pair; t < n_tiles && ok; t += n_pairs) {
@@ -267,7 +279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         break;
                     }
                     fence_after();
-                    const uint32_t d = tmem + buf * kTile;
+                    const uint32_t d = tmem + buf * TN;
                     const uint32_t n = steps - c0 < chunk ? steps - c0 : chunk;
                     for (uint32_t k = 0; k < n; ++k, ++it) {
                         const uint32_t st = it % kStages;
@@ -277,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                         fence_after();
                         const uint32_t a = smem_u32(ring + st * kStageBytes);
-                        const uint64_t da = smem_desc(a, sh.a_mn), db = smem_desc(a + kOperand, sh.b_mn);
+                        const uint64_t da = smem_desc(a, sh.a_mn), db = smem_desc(a + kOperandA, sh.b_mn);
 #pragma unroll
                         for (uint32_t j = 0; j < kBlockK / 16; ++j)
                             mma(d, da + j * step_a, db + j * step_b, idesc, k > 0 || j > 0);
@@ -290,7 +302,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {  // epilogue: a quarter of the rows, a half of the columns a warp
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         const int row = (int)rank * kHalf + quarter * 32 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + half * C::kHalfN;
+        float* scratch = reinterpret_cast<float*>(ring + C::kRing + (warp - 2) * kScratch);  // with Epi::kStaged
         uint32_t seq = 0;
         auto wait = [&](uint32_t buf) {
             const bool good = __all_sync(0xffffffffu, wait_cluster(&tfull[buf], (seq / 2) & 1, err));
@@ -307,18 +320,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int width = epi.width(tl, half);
             if constexpr (Epi::kChunked) {
                 const uint32_t chunks = (tile_steps(sh, tl) + kChunk - 1) / kChunk;
-                float acc[kHalf];
+                float acc[C::kHalfN];
 #pragma unroll
-                for (int i = 0; i < kHalf; ++i) acc[i] = 0.f;
+                for (int i = 0; i < C::kHalfN; ++i) acc[i] = 0.f;
                 for (uint32_t c = 0; c < chunks && ok; ++c, ++seq) {
                     const uint32_t buf = seq & 1;
                     ok = wait(buf);
                     if (!ok) break;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
+                    for (int g = 0; g < C::kHalfN / 32; ++g) {
                         float v[32];
                         __syncwarp();
-                        tmem_load32(lanes + buf * kTile + g * 32, v);
+                        tmem_load32(lanes + buf * TN + g * 32, v);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) acc[32 * g + i] += v[i];
                     }
@@ -327,13 +340,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 typename Epi::Row r = epi.begin(tl, row, half);
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+                for (int g = 0; g < C::kHalfN / 32; ++g) {
                     if (g * 32 >= width) continue;
                     float v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = acc[32 * g + i];
                     __syncwarp();
-                    epi.cols(r, g, v);
+                    epi.cols(r, g, v, scratch);
                 }
                 epi.end(r);
             } else {
@@ -341,11 +354,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 typename Epi::Row r = epi.begin(tl, row, half);
                 ok = wait(buf);
                 if (!ok) break;
-                for (int g = 0; g < 4 && g * 32 < width; ++g) {
+                for (int g = 0; g < C::kHalfN / 32 && g * 32 < width; ++g) {
                     float v[32];
                     __syncwarp();  // the load is one instruction of the whole warp
-                    tmem_load32(lanes + buf * kTile + g * 32, v);
-                    epi.cols(r, g, v);
+                    tmem_load32(lanes + buf * TN + g * 32, v);
+                    epi.cols(r, g, v, scratch);
                 }
                 epi.end(r);
                 __syncwarp();
@@ -365,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncthreads();
     pair_sync();  // the peer's arrivals on this CTA's barriers have landed
     fence_after();
-    if (warp == 1) tmem_free(tmem, 512);
+    if (warp == 1) tmem_free(tmem, 2 * TN);
 }
 
 }  // namespace mm

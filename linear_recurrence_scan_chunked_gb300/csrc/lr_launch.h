@@ -450,6 +450,8 @@ cudaError_t launch_adamw(AdamKind kind, int gdtype, const AdamTensor* t, int64_t
 struct LcePlan {
     int64_t tiles;      // forward: half tiles of the vocabulary (a pair of statistics each, per row)
     int64_t rows;       // forward: rows per round
+    int tn_logits;      // columns of the products' tiles, 256 or 128
+    int tn_dx, tn_dw;
     int64_t piece;      // backward: vocabulary rows per piece
     int64_t dx_splits;  // backward: parts of the k loops
     int64_t dw_splits;

@@ -90,9 +90,10 @@ __device__ __forceinline__ float pick32(const float (&v)[32], int j) {
 // Forward: the pair of a tile and a row.  With M = ceil(max l log2 e), the sum
 // of 2^(l log2 e - M): M is an integer, so its subtraction inside the
 // multiply-add rounds nothing but the result, and no common error enters the sum.
-template <bool CHUNKED>
+template <bool CHUNKED, int P>
 struct StatsEpi {
     static constexpr bool kChunked = CHUNKED, kStaged = false;
+    static constexpr int kPlanes = P;
     float2* part;           // [half tiles][rows]
     float* tl;              // the targets' logits
     const int64_t* target;
@@ -185,6 +186,7 @@ __device__ __forceinline__ float scale_of(const uint32_t* top) {
 template <int P>
 struct GradEpi {
     static constexpr bool kChunked = P > 1, kStaged = false;
+    static constexpr int kPlanes = P;
     __nv_bfloat16* g;  // [P][rows][pitch]
     int64_t pitch;     // a multiple of 16
     int64_t plane;     // elements of a plane
@@ -257,6 +259,7 @@ struct GradEpi {
 template <typename S>
 struct OutEpi {
     static constexpr bool kChunked = sizeof(S) == 4, kStaged = true;
+    static constexpr int kPlanes = sizeof(S) == 4 ? 3 : 1;
     S* out;         // nullptr: parts
     float* part;    // [splits][rows x cols]
     int64_t pitch;  // elements of a part
@@ -481,14 +484,13 @@ struct MmPlan {
     int64_t splits;
 };
 
-Shape mm_shape(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, bool n_fast, const MmPlan& pl) {
+Shape mm_shape(int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn, bool n_fast, const MmPlan& pl) {
     Shape s{};
     s.tm = (uint32_t)((M + kTile - 1) / kTile);
     s.tn = (uint32_t)((N + pl.tn - 1) / pl.tn);
     s.kb = (uint32_t)((K + mm::kBlockK - 1) / mm::kBlockK);
     s.kb_split = (uint32_t)((s.kb + pl.splits - 1) / pl.splits);
     s.splits = (s.kb + s.kb_split - 1) / s.kb_split;
-    s.pairs = planes == 1 ? 1 : 6;
     s.n_fast = n_fast;
     s.a_mn = a_mn;
     s.b_mn = b_mn;
@@ -602,11 +604,12 @@ cudaError_t lce_fwd_t(const void* x, const void* w, const int64_t* target, int64
         Operand a = ox;
         a.p += r * a.ld;
         a.rows = n;
-        const Shape sh = mm_shape(n, V, D, ox.planes, false, false, false, MmPlan{pl.tn_logits, 1});
-        if (sh.kb * sh.pairs > mm::kChunk)
-            LCE_TRY(mm_run(a, ow, sh, StatsEpi<true>{part, tl, target + r, n, V, 0}, pl.tn_logits, err, s));
+        const Shape sh = mm_shape(n, V, D, false, false, false, MmPlan{pl.tn_logits, 1});
+        constexpr int P = sizeof(S) == 4 ? 3 : 1;
+        if (sh.kb > mm::chunk_of(P))
+            LCE_TRY(mm_run(a, ow, sh, StatsEpi<true, P>{part, tl, target + r, n, V, 0}, pl.tn_logits, err, s));
         else
-            LCE_TRY(mm_run(a, ow, sh, StatsEpi<false>{part, tl, target + r, n, V, 0}, pl.tn_logits, err, s));
+            LCE_TRY(mm_run(a, ow, sh, StatsEpi<false, P>{part, tl, target + r, n, V, 0}, pl.tn_logits, err, s));
         k_lce_join<<<(unsigned)((n + 31) / 32), dim3(32, 32), 0, s>>>(part, pl.tiles, tl, target + r, ignore, loss + r,
                                                                      lse + r, n, V, err);
         LCE_TRY(cudaGetLastError());
@@ -645,10 +648,10 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
         wp.p += v0 * ow.ld;
         wp.rows = vc;
         const Operand og{g, N, vc, pitch, N * pitch, P};
-        LCE_TRY(mm_run(ox, wp, mm_shape(N, vc, D, P, false, false, false, MmPlan{pl.tn_logits, 1}),
+        LCE_TRY(mm_run(ox, wp, mm_shape(N, vc, D, false, false, false, MmPlan{pl.tn_logits, 1}),
                        GradEpi<P>{g, pitch, N * pitch, lse, dloss, target, top, ignore, N, v0, vc, V, 0}, pl.tn_logits, err, s));
         // dx: rows of x by features, over the words of the piece
-        const Shape sx = mm_shape(N, D, vc, P, false, true, true, MmPlan{pl.tn_dx, pl.dx_splits});
+        const Shape sx = mm_shape(N, D, vc, false, true, true, MmPlan{pl.tn_dx, pl.dx_splits});
         const bool dx_direct = pl.dx_parts == 1;
         LCE_TRY(mm_run(og, wp, sx,
                        OutEpi<S>{dx_direct ? (S*)dx : nullptr, px + part * xpitch, xpitch, top, N, D, 0,
@@ -656,7 +659,7 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
                        pl.tn_dx, err, s));
         part += sx.splits;
         // dw: words of the piece by features, over the rows of x
-        const Shape sw = mm_shape(vc, D, N, P, true, true, true, MmPlan{pl.tn_dw, pl.dw_splits});
+        const Shape sw = mm_shape(vc, D, N, true, true, true, MmPlan{pl.tn_dw, pl.dw_splits});
         const bool dw_direct = pl.dw_splits == 1;
         S* dwp = (S*)dw + v0 * D;
         LCE_TRY(mm_run(og, ox, sw,
@@ -689,7 +692,7 @@ LcePlan lce_plan(int dtype, const void* x, const void* w, int64_t N, int64_t V, 
         p.dw_splits = dw.splits;
         p.dx_parts = 0;
         for (int64_t v0 = 0; v0 < V; v0 += p.piece)
-            p.dx_parts += mm_shape(N, D, std::min(p.piece, V - v0), planes, false, true, true, dx).splits;
+            p.dx_parts += mm_shape(N, D, std::min(p.piece, V - v0), false, true, true, dx).splits;
     }
     p.bytes = layout(dtype, x, w, N, V, D, p, bwd).bytes;
     return p;

@@ -38,7 +38,7 @@ constexpr int kHalf = 128;       // rows of A that a CTA holds
 constexpr int kBlockK = 64;      // k-block: 128 bytes of bf16, the swizzle's width
 constexpr int kOperandA = kHalf * kBlockK * 2;  // 16 KB: A of a stage
 constexpr int kThreads = 320;    // producer warp, MMA warp, 8 epilogue warps
-constexpr uint32_t kChunk = 16;  // k-blocks of a chunk: k = 1024, a shrinkage of 3e-7
+constexpr uint32_t kChunk = 16;  // k-blocks of a chunk: k = 1024, a shrinkage of 3e-7 (fp32 planes: 3, of six products)
 constexpr int kScratch = 32 * 33 * 4;  // bytes an epilogue warp may use
 
 template <int TN>
@@ -55,9 +55,8 @@ struct Cfg {
 struct Shape {
     uint32_t tm, tn;        // tiles along the result's rows and columns
     uint32_t splits;        // parts of the k loop, each a tile of its own
-    uint32_t kb;            // k-blocks of the whole loop (of one plane pair)
+    uint32_t kb;            // k-blocks of the whole loop
     uint32_t kb_split;      // k-blocks of a part
-    uint32_t pairs;         // plane pairs: 1 or 6
     uint32_t n_fast;        // neighbouring tiles along the columns (else along the rows)
     uint32_t a_mn, b_mn;    // MN-major operands
 };
@@ -151,9 +150,10 @@ __device__ __forceinline__ uint32_t instr_desc(bool a_mn, bool b_mn, int tn) {
            (uint32_t)(kTile >> 4) << 24;
 }
 
-// The plane pairs of fp32 data, smallest products first.
-__device__ __forceinline__ int pair_a(uint32_t p, uint32_t pairs) { return pairs == 1 ? 0 : (0x001012 >> (4 * p)) & 3; }
-__device__ __forceinline__ int pair_b(uint32_t p, uint32_t pairs) { return pairs == 1 ? 0 : (0x010210 >> (4 * p)) & 3; }
+// The plane pairs of fp32 data, smallest products first.  A k-block's planes take
+// a stage each and are loaded once for the six products.
+__device__ constexpr int pair_a(int p) { return (0x001012 >> (4 * p)) & 3; }
+__device__ constexpr int pair_b(int p) { return (0x010210 >> (4 * p)) & 3; }
 
 struct Tile {
     uint32_t m, n, split;
@@ -173,16 +173,18 @@ __device__ __forceinline__ Tile tile_of(const Shape& s, uint32_t t) {
     return r;
 }
 
-// k-blocks of a tile, all plane pairs.
+// k-blocks of a tile, and of a chunk.
+__host__ __device__ constexpr uint32_t chunk_of(int planes) { return planes == 1 ? kChunk : 3; }
 __device__ __forceinline__ uint32_t tile_steps(const Shape& s, const Tile& t) {
     const uint32_t k0 = t.split * s.kb_split;
     const uint32_t k1 = k0 + s.kb_split < s.kb ? k0 + s.kb_split : s.kb;
-    return (k1 - k0) * s.pairs;
+    return k1 - k0;
 }
 
 // Epilogue: a struct with
 //   kChunked                       sum the k loop in chunks
 //   kStaged                        cols() uses the warp's scratch
+//   kPlanes                        planes of the operands: 1, or 3 (six products a k-block)
 //   Row                            what a thread keeps of its row of a tile
 //   begin(tile, row, half) -> Row  row 0 .. 255 of the tile, half 0 / 1 of its columns
 //   width(tile, half)              columns of the half inside the result (may be <= 0)
@@ -194,6 +196,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
          const Epi epi, uint32_t* err) {
     using C = Cfg<TN>;
     constexpr uint32_t kStages = C::kStages, kStageBytes = C::kStageBytes;
+    constexpr int kPlanes = Epi::kPlanes;
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2];
     __shared__ uint32_t tmem_base;
@@ -230,9 +233,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const int32_t m0 = (int32_t)(tl.m * kTile + rank * kHalf), n0 = (int32_t)(tl.n * TN + rank * C::kHalfN);
                 const uint32_t k0 = tl.split * sh.kb_split;
                 const uint32_t k1 = k0 + sh.kb_split < sh.kb ? k0 + sh.kb_split : sh.kb;
-                for (uint32_t p = 0; p < sh.pairs && ok; ++p) {
-                    const int pa = pair_a(p, sh.pairs), pb = pair_b(p, sh.pairs);
-                    for (uint32_t k = k0; k < k1; ++k, ++it) {
+                for (uint32_t k = k0; k < k1 && ok; ++k) {
+                    const int32_t kk = (int32_t)(k * kBlockK);
+                    for (int32_t p = 0; p < kPlanes; ++p, ++it) {
                         const uint32_t st = it % kStages;
                         if (it >= kStages && !wait_cluster(&empty[st], (it / kStages - 1) & 1, err)) {
                             ok = false;
@@ -242,18 +245,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         const uint32_t bar = cluster_addr(&full[st], 0);
                         unsigned char* a = ring + st * kStageBytes;
                         unsigned char* b = a + kOperandA;
-                        const int32_t kk = (int32_t)(k * kBlockK);
                         if (sh.a_mn) {
-                            tma_load_pair(a, &map_a, m0, kk, pa, bar);
-                            tma_load_pair(a + kOperandA / 2, &map_a, m0 + 64, kk, pa, bar);
+                            tma_load_pair(a, &map_a, m0, kk, p, bar);
+                            tma_load_pair(a + kOperandA / 2, &map_a, m0 + 64, kk, p, bar);
                         } else {
-                            tma_load_pair(a, &map_a, kk, m0, pa, bar);
+                            tma_load_pair(a, &map_a, kk, m0, p, bar);
                         }
                         if (sh.b_mn) {
-                            tma_load_pair(b, &map_b, n0, kk, pb, bar);
-                            if constexpr (TN == 256) tma_load_pair(b + 8192, &map_b, n0 + 64, kk, pb, bar);
+                            tma_load_pair(b, &map_b, n0, kk, p, bar);
+                            if constexpr (TN == 256) tma_load_pair(b + 8192, &map_b, n0 + 64, kk, p, bar);
                         } else {
-                            tma_load_pair(b, &map_b, kk, n0, pb, bar);
+                            tma_load_pair(b, &map_b, kk, n0, p, bar);
                         }
                     }
                 }
@@ -271,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t it = 0, seq = 0;
             for (uint32_t t = pair; t < n_tiles && ok; t += n_pairs) {
                 const uint32_t steps = tile_steps(sh, tile_of(sh, t));
-                const uint32_t chunk = Epi::kChunked ? kChunk : steps;
+                const uint32_t chunk = Epi::kChunked ? chunk_of(kPlanes) : steps;
                 for (uint32_t c0 = 0; c0 < steps && ok; c0 += chunk, ++seq) {
                     const uint32_t buf = seq & 1;
                     if (seq >= 2 && !wait_cluster(&tempty[buf], (seq / 2 - 1) & 1, err)) {
@@ -281,19 +283,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     fence_after();
                     const uint32_t d = tmem + buf * TN;
                     const uint32_t n = steps - c0 < chunk ? steps - c0 : chunk;
-                    for (uint32_t k = 0; k < n; ++k, ++it) {
-                        const uint32_t st = it % kStages;
-                        if (!wait_cluster(&full[st], (it / kStages) & 1, err)) {
-                            ok = false;
-                            break;
-                        }
-                        fence_after();
-                        const uint32_t a = smem_u32(ring + st * kStageBytes);
-                        const uint64_t da = smem_desc(a, sh.a_mn), db = smem_desc(a + kOperandA, sh.b_mn);
+                    for (uint32_t k = 0; k < n; ++k, it += kPlanes) {
+                        uint64_t da[kPlanes], db[kPlanes];
 #pragma unroll
-                        for (uint32_t j = 0; j < kBlockK / 16; ++j)
-                            mma(d, da + j * step_a, db + j * step_b, idesc, k > 0 || j > 0);
-                        commit_pair(&empty[st]);
+                        for (uint32_t p = 0; p < (uint32_t)kPlanes; ++p) {
+                            const uint32_t st = (it + p) % kStages;
+                            ok = ok && wait_cluster(&full[st], ((it + p) / kStages) & 1, err);
+                            const uint32_t a = smem_u32(ring + st * kStageBytes);
+                            da[p] = smem_desc(a, sh.a_mn);
+                            db[p] = smem_desc(a + kOperandA, sh.b_mn);
+                        }
+                        if (!ok) break;
+                        fence_after();
+                        if constexpr (kPlanes == 1) {
+#pragma unroll
+                            for (uint32_t j = 0; j < kBlockK / 16; ++j)
+                                mma(d, da[0] + j * step_a, db[0] + j * step_b, idesc, k > 0 || j > 0);
+                        } else {
+#pragma unroll
+                            for (int p = 0; p < 6; ++p)
+#pragma unroll
+                                for (uint32_t j = 0; j < kBlockK / 16; ++j)
+                                    mma(d, da[pair_a(p)] + j * step_a, db[pair_b(p)] + j * step_b, idesc,
+                                        k > 0 || p > 0 || j > 0);
+                        }
+                        for (uint32_t p = 0; p < (uint32_t)kPlanes; ++p) commit_pair(&empty[(it + p) % kStages]);
                     }
                     if (ok) commit_pair(&tfull[buf]);
                 }
@@ -319,7 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Tile tl = tile_of(sh, t);
             const int width = epi.width(tl, half);
             if constexpr (Epi::kChunked) {
-                const uint32_t chunks = (tile_steps(sh, tl) + kChunk - 1) / kChunk;
+                const uint32_t chunks = (tile_steps(sh, tl) + chunk_of(kPlanes) - 1) / chunk_of(kPlanes);
                 float acc[C::kHalfN];
 #pragma unroll
                 for (int i = 0; i < C::kHalfN; ++i) acc[i] = 0.f;

@@ -109,17 +109,40 @@ __device__ __forceinline__ uint32_t adam_hash(uint32_t i, uint32_t key) {
     x = (x ^ (x >> 15)) * 0x3C6EF373u;
     return x ^ (x >> 16);
 }
-__device__ __forceinline__ float adam_decode_m(int q, float scale) {
-    const float t = __fmul_rn((float)q, 1.f / 127.f);
-    return __fmul_rn(__fmul_rn(t, fabsf(t)), scale);
+// Small integers as floats and back without the conversion instructions, which
+// issue at a quarter of the rate of the others and were what bound this kernel: a
+// byte b under the exponent of 2^23 is the float 2^23 + b; 16 bits under that of
+// 1 are 1 + u / 2^16; and adding 2^23 rounding towards zero leaves floor(x) in the
+// low bits of the sum (0 <= x < 2^23).
+__device__ __forceinline__ float byte_float(uint32_t w, int k, float bias) {
+    return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u + (uint32_t)k)) - bias;
 }
-__device__ __forceinline__ float adam_decode_v(int q, float scale) {
-    float t = __fmul_rn((float)q, 1.f / 255.f);
-    t = __fmul_rn(t, t);
-    return __fmul_rn(__fmul_rn(t, t), scale);
+__device__ __forceinline__ float unit16(uint32_t u16) { return __uint_as_float(0x3F800000u | u16 << 7) - 1.f; }
+__device__ __forceinline__ uint32_t floor_bits(float x) { return __float_as_uint(__fadd_rz(x, 8388608.f)) & 0x3ffu; }
+
+// A sum of pairs, each of its terms rounded by itself: the compiler fuses
+// mul.rn.f32x2 into an add.f32x2 that follows (seen in the results), so the
+// additions after products are single ones.
+__device__ __forceinline__ void add_apart(f32x2 a, f32x2 b, float& x, float& y) {
+    float a0, a1, b0, b1;
+    f2_get(a, a0, a1);
+    f2_get(b, b0, b1);
+    x = __fadd_rn(a0, b0);
+    y = __fadd_rn(a1, b1);
 }
 
-// One warp per block of 256 elements, 8 consecutive ones a lane.
+__device__ __forceinline__ f32x2 adam_decode_m(float q0, float q1, f32x2 scale) {
+    float t0, t1;
+    f2_get(f2_mul(f2(q0, q1), f2(1.f / 127.f)), t0, t1);
+    return f2_mul(f2(__fmul_rn(t0, fabsf(t0)), __fmul_rn(t1, fabsf(t1))), scale);
+}
+__device__ __forceinline__ f32x2 adam_decode_v(float q0, float q1, f32x2 scale) {
+    f32x2 t = f2_mul(f2(q0, q1), f2(1.f / 255.f));
+    t = f2_mul(t, t);
+    return f2_mul(f2_mul(t, t), scale);
+}
+
+// One warp per block of 256 elements, 8 consecutive ones a lane, in pairs.
 template <typename G, bool VP>
 __device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, const AdamHyper& h,
                                             float gs, uint32_t key) {
@@ -127,48 +150,51 @@ __device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, co
     const int64_t i0 = blk * 256 + lane * 8;
     const int n = t.n - i0 >= 8 ? 8 : t.n > i0 ? (int)(t.n - i0) : 0;
     const G* gp = (const G*)t.g;
-    int8_t* mq = (int8_t*)t.m;
+    uint8_t* mq = (uint8_t*)t.m;  // int8 codes
     uint8_t* vq = (uint8_t*)t.v;
     const float sm = t.ms[blk], sv = t.vs[blk];
-    float p[8], m[8], v[8];
+    float p[8], g[8];
+    uint2 cm = make_uint2(0u, 0u), cv = make_uint2(0u, 0u);
     if (VP && n == 8) {
         const float4 a = *reinterpret_cast<const float4*>(t.p + i0);
         const float4 b = *reinterpret_cast<const float4*>(t.p + i0 + 4);
         p[0] = a.x; p[1] = a.y; p[2] = a.z; p[3] = a.w;
         p[4] = b.x; p[5] = b.y; p[6] = b.z; p[7] = b.w;
-        const uint2 cm = *reinterpret_cast<const uint2*>(mq + i0);
-        const uint2 cv = *reinterpret_cast<const uint2*>(vq + i0);
+        cm = *reinterpret_cast<const uint2*>(mq + i0);
+        cv = *reinterpret_cast<const uint2*>(vq + i0);
         Pack<G, 4> g0, g1;
         g0.load(gp + i0);
         g1.load(gp + i0 + 4);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t wm = k < 4 ? cm.x : cm.y, wv = k < 4 ? cv.x : cv.y;
-            m[k] = adam_decode_m((int)(int8_t)(wm >> (8 * (k & 3))), sm);
-            v[k] = adam_decode_v((int)((wv >> (8 * (k & 3))) & 255u), sv);
-            const float g = __fmul_rn(k < 4 ? g0.get(k & 3) : g1.get(k & 3), gs);
-            m[k] = __fadd_rn(__fmul_rn(h.b1, m[k]), __fmul_rn(h.c1, g));
-            v[k] = __fadd_rn(__fmul_rn(h.b2, v[k]), __fmul_rn(h.c2, __fmul_rn(g, g)));
-        }
+        for (int k = 0; k < 8; ++k) g[k] = k < 4 ? g0.get(k & 3) : g1.get(k & 3);
     } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            p[k] = m[k] = v[k] = 0.f;
+            p[k] = g[k] = 0.f;
             if (k >= n) continue;
             p[k] = t.p[i0 + k];
             Pack<G, 1> g1;
             g1.load(gp + i0 + k);
-            const float g = __fmul_rn(g1.get(0), gs);
-            m[k] = __fadd_rn(__fmul_rn(h.b1, adam_decode_m((int)mq[i0 + k], sm)), __fmul_rn(h.c1, g));
-            v[k] = __fadd_rn(__fmul_rn(h.b2, adam_decode_v((int)vq[i0 + k], sv)),
-                             __fmul_rn(h.c2, __fmul_rn(g, g)));
+            g[k] = g1.get(0);
+            (k < 4 ? cm.x : cm.y) |= (uint32_t)mq[i0 + k] << (8 * (k & 3));
+            (k < 4 ? cv.x : cv.y) |= (uint32_t)vq[i0 + k] << (8 * (k & 3));
         }
     }
+    // the new moments
+    cm.x ^= 0x80808080u;  // signed codes, biased
+    cm.y ^= 0x80808080u;
+    float m[8], v[8];
     float tm = 0.f, tv = 0.f;  // the block's new scales
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        tm = fmaxf(tm, fabsf(m[k]));
-        tv = fmaxf(tv, v[k]);
+    for (int k = 0; k < 8; k += 2) {
+        const uint32_t wm = k < 4 ? cm.x : cm.y, wv = k < 4 ? cv.x : cv.y;
+        const f32x2 m0 = adam_decode_m(byte_float(wm, k & 3, 8388736.f), byte_float(wm, (k & 3) + 1, 8388736.f), f2(sm));
+        const f32x2 v0 = adam_decode_v(byte_float(wv, k & 3, 8388608.f), byte_float(wv, (k & 3) + 1, 8388608.f), f2(sv));
+        const f32x2 gg = f2_mul(f2(g[k], g[k + 1]), f2(gs));
+        add_apart(f2_mul(m0, f2(h.b1)), f2_mul(gg, f2(h.c1)), m[k], m[k + 1]);
+        add_apart(f2_mul(v0, f2(h.b2)), f2_mul(f2_mul(gg, gg), f2(h.c2)), v[k], v[k + 1]);
+        tm = fmaxf(tm, fmaxf(fabsf(m[k]), fabsf(m[k + 1])));
+        tv = fmaxf(tv, fmaxf(v[k], v[k + 1]));
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -176,28 +202,41 @@ __device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, co
         tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, off));
     }
     const float im = tm > 0.f ? __fdiv_rn(1.f, tm) : 0.f, iv = tv > 0.f ? __fdiv_rn(1.f, tv) : 0.f;
-    uint32_t qm[8], qv[8];
+    // sqrt(v) = sqrt(v / scale) sqrt(scale): the first root is the code's too
+    const float rv = sqrtf(tv) * h.rk2;
+    uint32_t qm[2] = {0u, 0u}, qv[2] = {0u, 0u};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        p[k] = fmaf(-h.step, __fdividef(m[k], fmaf(sqrtf(v[k]), h.rk2, h.eps)), h.decay * p[k]);
-        const uint32_t u = adam_hash((uint32_t)(i0 + k), key);
-        const float um = (float)(u >> 16) * (1.f / 65536.f), uv = (float)(u & 0xffffu) * (1.f / 65536.f);
-        float a = __fsqrt_rn(__fmul_rn(fabsf(m[k]), im));
-        a = fminf(floorf(__fadd_rn(__fmul_rn(a, 127.f), um)), 127.f);
-        float b = __fsqrt_rn(__fsqrt_rn(__fmul_rn(v[k], iv)));
-        b = fminf(floorf(__fadd_rn(__fmul_rn(b, 255.f), uv)), 255.f);
-        if (v[k] > 0.f && b < 1.f) b = 1.f;
-        const int q = (int)a;
-        qm[k] = (uint32_t)(m[k] < 0.f ? -q : q) & 255u;
-        qv[k] = (uint32_t)(int)b & 255u;
+    for (int k = 0; k < 8; k += 2) {
+        float rm[2], r2[2], a[2], b[2], um[2], uv[2];
+        f2_get(f2_mul(f2(fabsf(m[k]), fabsf(m[k + 1])), f2(im)), rm[0], rm[1]);
+        f2_get(f2_mul(f2(v[k], v[k + 1]), f2(iv)), r2[0], r2[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t u = adam_hash((uint32_t)(i0 + k + e), key);
+            um[e] = unit16(u >> 16);
+            uv[e] = unit16(u & 0xffffu);
+            rm[e] = __fsqrt_rn(rm[e]);
+            r2[e] = __fsqrt_rn(r2[e]);
+            b[e] = __fsqrt_rn(r2[e]);
+        }
+        add_apart(f2_mul(f2(rm[0], rm[1]), f2(127.f)), f2(um[0], um[1]), a[0], a[1]);
+        add_apart(f2_mul(f2(b[0], b[1]), f2(255.f)), f2(uv[0], uv[1]), b[0], b[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            p[k + e] = fmaf(-h.step, __fdividef(m[k + e], fmaf(r2[e], rv, h.eps)), h.decay * p[k + e]);
+            int q = (int)min(floor_bits(a[e]), 127u);
+            q = m[k + e] < 0.f ? -q : q;
+            uint32_t w = min(floor_bits(b[e]), 255u);
+            if (w == 0u && v[k + e] > 0.f) w = 1u;
+            qm[k >> 2] |= ((uint32_t)q & 255u) << (8 * ((k + e) & 3));
+            qv[k >> 2] |= w << (8 * ((k + e) & 3));
+        }
     }
     if (VP && n == 8) {
         *reinterpret_cast<float4*>(t.p + i0) = make_float4(p[0], p[1], p[2], p[3]);
         *reinterpret_cast<float4*>(t.p + i0 + 4) = make_float4(p[4], p[5], p[6], p[7]);
-        *reinterpret_cast<uint2*>(mq + i0) =
-            make_uint2(qm[0] | qm[1] << 8 | qm[2] << 16 | qm[3] << 24, qm[4] | qm[5] << 8 | qm[6] << 16 | qm[7] << 24);
-        *reinterpret_cast<uint2*>(vq + i0) =
-            make_uint2(qv[0] | qv[1] << 8 | qv[2] << 16 | qv[3] << 24, qv[4] | qv[5] << 8 | qv[6] << 16 | qv[7] << 24);
+        *reinterpret_cast<uint2*>(mq + i0) = make_uint2(qm[0], qm[1]);
+        *reinterpret_cast<uint2*>(vq + i0) = make_uint2(qv[0], qv[1]);
         if (t.copy)
             *reinterpret_cast<uint4*>((__nv_bfloat16*)t.copy + i0) =
                 make_uint4(bf_pack(p[0], p[1]), bf_pack(p[2], p[3]), bf_pack(p[4], p[5]), bf_pack(p[6], p[7]));
@@ -206,8 +245,8 @@ __device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, co
         for (int k = 0; k < 8; ++k) {
             if (k >= n) continue;
             t.p[i0 + k] = p[k];
-            mq[i0 + k] = (int8_t)qm[k];
-            vq[i0 + k] = (uint8_t)qv[k];
+            mq[i0 + k] = (uint8_t)(qm[k >> 2] >> (8 * (k & 3)));
+            vq[i0 + k] = (uint8_t)(qv[k >> 2] >> (8 * (k & 3)));
             if (t.copy) ((__nv_bfloat16*)t.copy)[i0 + k] = __float2bfloat16_rn(p[k]);
         }
     }
@@ -246,30 +285,30 @@ __global__ void __launch_bounds__(256) k_adamw8_values(const __grid_constant__ A
     const int8_t* mq = (const int8_t*)t.m;
     const uint8_t* vq = (const uint8_t*)t.v;
     float* vo = (float*)t.copy;
+    auto one = [&](int64_t i) {
+        float x;
+        f2_get(adam_decode_m((float)mq[i], 0.f, f2(__ldg(t.ms + (i >> 8)))), t.p[i], x);
+        f2_get(adam_decode_v((float)vq[i], 0.f, f2(__ldg(t.vs + (i >> 8)))), vo[i], x);
+    };
     if (t.vec) {
         const int64_t mid = lo + ((hi - lo) & ~(int64_t)3);
         for (int64_t i = lo + (int64_t)threadIdx.x * 4; i < mid; i += 1024) {
             const uint32_t cm = *reinterpret_cast<const uint32_t*>(mq + i);
             const uint32_t cv = *reinterpret_cast<const uint32_t*>(vq + i);
             const float sm = __ldg(t.ms + (i >> 8)), sv = __ldg(t.vs + (i >> 8));
+            const uint32_t wm = cm ^ 0x80808080u;
             float m[4], v[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                m[k] = adam_decode_m((int)(int8_t)(cm >> (8 * k)), sm);
-                v[k] = adam_decode_v((int)((cv >> (8 * k)) & 255u), sv);
+            for (int k = 0; k < 4; k += 2) {
+                f2_get(adam_decode_m(byte_float(wm, k, 8388736.f), byte_float(wm, k + 1, 8388736.f), f2(sm)), m[k], m[k + 1]);
+                f2_get(adam_decode_v(byte_float(cv, k, 8388608.f), byte_float(cv, k + 1, 8388608.f), f2(sv)), v[k], v[k + 1]);
             }
             store_vec<float, 4>(t.p + i, m);
             store_vec<float, 4>(vo + i, v);
         }
-        for (int64_t i = mid + threadIdx.x; i < hi; i += 256) {
-            t.p[i] = adam_decode_m((int)mq[i], __ldg(t.ms + (i >> 8)));
-            vo[i] = adam_decode_v((int)vq[i], __ldg(t.vs + (i >> 8)));
-        }
+        for (int64_t i = mid + threadIdx.x; i < hi; i += 256) one(i);
     } else {
-        for (int64_t i = lo + threadIdx.x; i < hi; i += 256) {
-            t.p[i] = adam_decode_m((int)mq[i], __ldg(t.ms + (i >> 8)));
-            vo[i] = adam_decode_v((int)vq[i], __ldg(t.vs + (i >> 8)));
-        }
+        for (int64_t i = lo + threadIdx.x; i < hi; i += 256) one(i);
     }
 }
 

@@ -52,11 +52,11 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* sm) {
 // A thread's columns: vector k starts at column (k T + threadIdx.x) VEC.  Rows are
 // addressed by the CTA's first row, the same for all its threads, plus a 32-bit
 // offset that no row changes.  Only the last vectors can lie outside (T is rounded
-// up to a warp); their offset is the row's last vector, whose data they read and
-// whose results they drop.
+// up to a warp, NV to an instance); their offset is the row's last vector, whose
+// data they read and whose results they drop.
 template <typename S, int VEC, int NV>
 struct Cols {
-    static constexpr int kMasked = NV >= 16 ? 4 : NV == 8 ? 2 : 1;
+    static constexpr int kMasked = NV >= 8 && VEC == 1 ? 2 : 1;
     uint32_t off[NV];  // bytes
     int d[NV];
     bool in_[kMasked];
@@ -86,12 +86,15 @@ struct Cols {
 // compiler spends 128 registers on five elements a thread, and the backward pass
 // of 30011 x 1111 took 10% longer.
 constexpr int ln_min_ctas(bool bwd, bool res, int elems, int maxt) {
-    return maxt > 256 || elems > 16 ? 1
-           : elems > 8              ? 2
-           : bwd || res             ? (elems <= 2 ? 5 : elems <= 4 ? 4 : elems <= 6 && bwd ? 4 : 3)
-           : elems <= 4             ? 6
-                                    : 4;
+    return maxt > 256       ? 1
+           : elems > 8      ? 2
+           : bwd || res     ? (elems <= 2 ? 5 : elems <= 4 ? 4 : elems <= 6 && bwd ? 4 : 3)
+           : elems <= 4     ? 6
+                            : 4;
 }
+// Rows past 8192 columns (1024 threads, 64 registers each) keep w and b in L1 and,
+// backward, the column sums in shared memory, and load no row ahead.
+__host__ __device__ constexpr bool ln_wide(int maxt) { return maxt > 512; }
 
 // The next row's vectors are loaded before the current row's sums: a row's two
 // reductions and its output then cover the next one's way from memory.
@@ -103,13 +106,17 @@ __global__ void __launch_bounds__(MAXT, ln_min_ctas(false, RES, VEC * NV, MAXT))
     __shared__ float sm[2][8][32];  // at most 8 rows a CTA (256 threads of 32)
     const float inv_d = 1.f / (float)D;
     const Cols<S, VEC, NV> cl(D);
+    constexpr bool WIDE = ln_wide(MAXT);
     float wv[NV][VEC], bv[NV][VEC];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
+    auto params = [&](int k) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) bv[k][v] = 0.f;
         load_param<VEC>(w + cl.d[k], wv[k]);
         if (b != nullptr) load_param<VEC>(b + cl.d[k], bv[k]);
+    };
+    if constexpr (!WIDE) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) params(k);
     }
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
     Pack<S, VEC> px[NV], pr[NV];
@@ -129,6 +136,9 @@ __global__ void __launch_bounds__(MAXT, ln_min_ctas(false, RES, VEC * NV, MAXT))
     for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < N; r0 += step) {
         const bool live = r0 + threadIdx.y < N;
         S *yr = y + r0 * D, *sr = sum + r0 * D;
+        if constexpr (WIDE) {
+            if (r0 != (int64_t)blockIdx.x * blockDim.y) fetch(r0);
+        }
         float e[NV][VEC];
         float t[1] = {0.f};
 #pragma unroll
@@ -159,7 +169,7 @@ __global__ void __launch_bounds__(MAXT, ln_min_ctas(false, RES, VEC * NV, MAXT))
 #pragma unroll
             for (int v = 0; v < VEC; ++v) t[0] += cl.in(k) ? e[k][v] : 0.f;
         }
-        fetch(r0 + step);
+        if constexpr (!WIDE) fetch(r0 + step);
         row_sum(t, &sm[0][0][0]);
         const float mu = t[0] * inv_d;
         t[0] = 0.f;
@@ -181,6 +191,7 @@ __global__ void __launch_bounds__(MAXT, ln_min_ctas(false, RES, VEC * NV, MAXT))
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 float o[VEC];
+                if constexpr (WIDE) params(k);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) o[v] = fmaf(e[k][v] * rs, wv[k][v], bv[k][v]);
                 if (cl.in(k)) store_vec<S, VEC>(cl.at(yr, k), o);
@@ -196,18 +207,28 @@ __global__ void __launch_bounds__(MAXT, ln_min_ctas(true, RES, VEC * NV, MAXT))
              const float* __restrict__ rstd, const S* __restrict__ dy, const S* __restrict__ dres,
              S* __restrict__ dx, float* __restrict__ partials, int64_t N, int D) {
     __shared__ float sm[2][8][64];
-    extern __shared__ float cols[];  // [blockDim.y - 1][T * NV * VEC] when a CTA holds several rows
+    constexpr bool WIDE = ln_wide(MAXT);
+    // several rows a CTA: [blockDim.y - 1][T * NV * VEC] at the end; WIDE: the
+    // column sums, [2][NV * VEC][T]
+    extern __shared__ float cols[];
     const int T = blockDim.x;
     const float inv_d = 1.f / (float)D;
     const Cols<S, VEC, NV> cl(D);
     float wv[NV][VEC], aw[NV][VEC], ab[NV][VEC];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
+    auto params = [&](int k) {
         load_param<VEC>(w + cl.d[k], wv[k]);
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            aw[k][v] = ab[k][v] = 0.f;
+        for (int v = 0; v < VEC; ++v)
             if (!cl.in(k)) wv[k][v] = 0.f;
+    };
+    auto slot = [&](int a, int k, int v) -> float& { return cols[((a * NV + k) * VEC + v) * T + threadIdx.x]; };
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        if constexpr (!WIDE) params(k);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            if constexpr (WIDE) slot(0, k, v) = slot(1, k, v) = 0.f;
+            else aw[k][v] = ab[k][v] = 0.f;
         }
     }
     const int64_t step = (int64_t)gridDim.x * blockDim.y;
@@ -235,25 +256,35 @@ __global__ void __launch_bounds__(MAXT, ln_min_ctas(true, RES, VEC * NV, MAXT))
     for (int64_t r0 = (int64_t)blockIdx.x * blockDim.y; r0 < N; r0 += step, par ^= 1) {
         const bool live = r0 + threadIdx.y < N;
         S* xr = dx + r0 * D;
+        if constexpr (WIDE) {
+            if (r0 != (int64_t)blockIdx.x * blockDim.y) fetch(r0);
+        }
         // xh, and t = dy w with what dx adds to it: rs t + dres
         float xh[NV][VEC], q[NV][VEC], o[NV][VEC];
         float t[2] = {0.f, 0.f};
         const float r_s = rs;
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+        for (int k = 0; k < NV; ++k) {
+            if constexpr (WIDE) params(k);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 xh[k][v] = (px[k].get(v) - mu) * r_s;
                 const float g = pd[k].get(v);
-                aw[k][v] = fmaf(g, xh[k][v], aw[k][v]);
-                ab[k][v] += g;
+                if constexpr (WIDE) {
+                    slot(0, k, v) = fmaf(g, xh[k][v], slot(0, k, v));
+                    slot(1, k, v) += g;
+                } else {
+                    aw[k][v] = fmaf(g, xh[k][v], aw[k][v]);
+                    ab[k][v] += g;
+                }
                 q[k][v] = g * wv[k][v];
                 t[0] += q[k][v];
                 t[1] = fmaf(q[k][v], xh[k][v], t[1]);
                 if constexpr (RES) o[k][v] = pr[k].get(v);
                 else o[k][v] = 0.f;
             }
-        fetch(r0 + step);
+        }
+        if constexpr (!WIDE) fetch(r0 + step);
         row_sum(t, &sm[par][0][0]);
         const float c0 = t[0] * inv_d, c1 = t[1] * inv_d;
         if (live) {
@@ -276,7 +307,8 @@ __global__ void __launch_bounds__(MAXT, ln_min_ctas(true, RES, VEC * NV, MAXT))
                 for (int k = 0; k < NV; ++k)
 #pragma unroll
                     for (int v = 0; v < VEC; ++v)
-                        cols[(threadIdx.y - 1) * pitch + (k * VEC + v) * T + threadIdx.x] = a == 0 ? aw[k][v] : ab[k][v];
+                        if constexpr (!WIDE)
+                            cols[(threadIdx.y - 1) * pitch + (k * VEC + v) * T + threadIdx.x] = a == 0 ? aw[k][v] : ab[k][v];
             }
             __syncthreads();
         }
@@ -287,7 +319,9 @@ __global__ void __launch_bounds__(MAXT, ln_min_ctas(true, RES, VEC * NV, MAXT))
                 const int d = cl.d[k];
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
-                    float s = a == 0 ? aw[k][v] : ab[k][v];
+                    float s;
+                    if constexpr (WIDE) s = slot(a, k, v);
+                    else s = a == 0 ? aw[k][v] : ab[k][v];
                     for (int j = 0; j + 1 < (int)blockDim.y; ++j) s += cols[j * pitch + (k * VEC + v) * T + threadIdx.x];
                     if (cl.in(k)) out[d + v] = s;
                 }
@@ -317,21 +351,28 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == 0 && dj < D) (blockIdx.y == 0 ? dw : db)[dj] = s;
 }
 
-// Threads of a row and vectors of a thread: the fewest vectors that keep a row
-// within 256 threads, up to 16 elements a thread (rows short of 256 threads
-// share a CTA); wider rows take up to 512 threads, and past 16 x 512 elements
-// 32 a thread.
+// Threads of a row and vectors of a thread.  Up to 2048 columns about 8 elements a
+// thread in 32 to 256 threads -- a warp to a row of up to 256 columns, so that its
+// sums need no barrier; rows short of 256 threads share a CTA.  Up to 4096 columns
+// 16 elements (8 one by one, in up to 512 threads), up to 8192 16 in 512 threads,
+// beyond 16 in 1024.
 struct LnShape {
-    int nv, t, rows;
+    int nv, t, rows, maxt;
 };
 static LnShape ln_shape(int64_t D, int vec) {
-    LnShape s{1, 0, 1};
-    auto lanes = [&](int nv) { return (D + (int64_t)vec * nv - 1) / ((int64_t)vec * nv); };
-    // (element by element: 1, 2, 3, 4, 5, 6, 8 or 16 of them, so that an odd width
-    // leaves few threads without one)
-    while (vec * s.nv < 16 && lanes(s.nv) > 256) s.nv = vec > 1 ? 2 * s.nv : s.nv < 6 ? s.nv + 1 : s.nv == 6 ? 8 : 16;
-    if (lanes(s.nv) > 512) s.nv *= 2;
-    s.t = (int)((lanes(s.nv) + 31) / 32 * 32);
+    LnShape s{1, 0, 1, 256};
+    auto per = [&](int64_t n) { return (D + n - 1) / n; };
+    if (D <= 2048) {
+        int tm = 32;
+        while (tm < 256 && D > 8 * (int64_t)tm) tm *= 2;
+        s.nv = (int)per((int64_t)vec * tm);
+    } else if (D <= 4096) {
+        s.nv = vec > 1 ? 16 / vec : 8;
+    } else {
+        s.nv = 16 / vec;
+    }
+    s.t = (int)((per((int64_t)vec * s.nv) + 31) / 32 * 32);
+    s.maxt = s.t <= 256 ? 256 : s.t <= 512 ? 512 : 1024;
     s.rows = s.t >= 256 ? 1 : 256 / s.t;
     return s;
 }
@@ -339,7 +380,7 @@ static LnShape ln_shape(int64_t D, int vec) {
 // CTAs of a launch: the groups of rows, at most as many as are resident at once
 // (asked once per kernel, device and block size: `known`, one entry per warp count).
 template <class K>
-static int ln_grid(K kernel, int threads, size_t smem, int64_t groups, int (&known)[64][17]) {
+static int ln_grid(K kernel, int threads, size_t smem, int64_t groups, int (&known)[64][33]) {
     int dev = 0;
     cudaGetDevice(&dev);
     int& n = known[dev & 63][threads / 32];
@@ -356,7 +397,7 @@ template <typename S, int VEC, int NV, int MAXT, bool RES>
 static cudaError_t ln_fwd_r(const LnShape& sh, const void* x, const void* res, const float* w,
                             const float* b, void* y, void* sum, float* mean, float* rstd, int64_t N,
                             int64_t D, float eps, cudaStream_t s) {
-    static int known[64][17] = {};
+    static int known[64][33] = {};
     const int grid = ln_grid(k_ln_fwd<S, VEC, NV, MAXT, RES>, sh.t * sh.rows, 0, (N + sh.rows - 1) / sh.rows, known);
     k_ln_fwd<S, VEC, NV, MAXT, RES><<<grid, dim3(sh.t, sh.rows), 0, s>>>(
         (const S*)x, (const S*)res, w, b, (S*)y, (S*)sum, mean, rstd, N, (int)D, eps);
@@ -367,8 +408,13 @@ template <typename S, int VEC, int NV, int MAXT, bool RES>
 static cudaError_t ln_bwd_r(const LnShape& sh, const void* x, const float* w, const float* mean,
                             const float* rstd, const void* dy, const void* dres, void* dx, float* dw,
                             float* db, float* partials, int64_t N, int64_t D, cudaStream_t s) {
-    const size_t smem = (size_t)(sh.rows - 1) * sh.t * NV * VEC * sizeof(float);
-    static int known[64][17] = {};
+    const size_t smem = (size_t)(ln_wide(MAXT) ? 2 : sh.rows - 1) * sh.t * NV * VEC * sizeof(float);
+    if (ln_wide(MAXT)) {
+        const cudaError_t e = cudaFuncSetAttribute(k_ln_bwd<S, VEC, NV, MAXT, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   2 * 1024 * 16 * (int)sizeof(float));
+        if (e != cudaSuccess) return e;
+    }
+    static int known[64][33] = {};
     int grid = ln_grid(k_ln_bwd<S, VEC, NV, MAXT, RES>, sh.t * sh.rows, smem, (N + sh.rows - 1) / sh.rows, known);
     if (grid > kLnMaxPartials) grid = kLnMaxPartials;
     k_ln_bwd<S, VEC, NV, MAXT, RES><<<grid, dim3(sh.t, sh.rows), smem, s>>>(
@@ -394,19 +440,30 @@ static cudaError_t ln_bwd_k(const LnShape& sh, const void* x, const float* w, co
 
 // The instance of a shape.
 #define LN_PICK(CALL)                                                     \
-    if (sh.nv == 1) return CALL(1, 256);                                  \
-    if constexpr (VEC < 8) {                                              \
-        if (sh.nv == 2) return CALL(2, 256);                              \
+    if (sh.maxt == 1024) return CALL((16 / VEC), 1024);                   \
+    if (sh.maxt == 512) {                                                 \
+        if constexpr (VEC == 1) {                                         \
+            if (sh.nv == 8) return CALL(8, 512);                          \
+        }                                                                 \
+        return CALL((16 / VEC), 512);                                     \
     }                                                                     \
-    if constexpr (VEC < 4) {                                              \
-        if (sh.nv == 3) return CALL(3, 256);                              \
-        if (sh.nv == 4) return CALL(4, 256);                              \
-        if (sh.nv == 5) return CALL(5, 256);                              \
-        if (sh.nv == 6) return CALL(6, 256);                              \
-        if (sh.nv == 8) return CALL(8, 256);                              \
+    switch (sh.nv) {                                                      \
+        case 1: return CALL(1, 256);                                      \
+        case 2: return CALL(2, 256);                                      \
+        default: break;                                                   \
     }                                                                     \
-    if (sh.nv * VEC == 16) return sh.t <= 256 ? CALL((16 / VEC), 256) : CALL((16 / VEC), 512); \
-    if (sh.nv * VEC == 32) return CALL((32 / VEC), 512);                  \
+    if constexpr (VEC == 4) return CALL(4, 256);                          \
+    if constexpr (VEC == 1) {                                             \
+        switch (sh.nv) {                                                  \
+            case 3: return CALL(3, 256);                                  \
+            case 4: return CALL(4, 256);                                  \
+            case 5: return CALL(5, 256);                                  \
+            case 6: return CALL(6, 256);                                  \
+            case 7: return CALL(7, 256);                                  \
+            case 8: return CALL(8, 256);                                  \
+            default: break;                                               \
+        }                                                                 \
+    }                                                                     \
     return cudaErrorInvalidValue;
 
 template <typename S, int VEC>

@@ -188,3 +188,20 @@ def test_refusals_on_device_tensors(cuda):
                  lambda: cuda.layer_norm_bwd(d["x"], d["w"], d["x"][:, 0], d["w"], d["dy"])):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [31, 32, 65, 119, 128, 250, 255, 257, 511, 520, 900, 1500, 1792, 2047, 3000, 5000, 10995, 16383])
+def test_every_instance(cuda, D, dtype):
+    """The row shapes between the sizes above: each number of elements a thread, the wide rows."""
+    c = make(67, D, dtype, seed=D)
+    d = {k: v.cuda() for k, v in c.items()}
+    y, mean, rstd = cuda.layer_norm_fwd(d["x"], d["w"], d["b"])
+    ry, rm, _ = ref_fwd(c["x"], c["w"], c["b"], 1e-5)
+    assert err(y, ry) <= TOL[dtype] and err(mean, rm) <= 2e-6
+    got = cuda.layer_norm_bwd(d["x"], d["w"], mean, rstd, d["dy"], dres=d["dres"])
+    dx, tw, tb = ref_bwd(c["x"], c["w"], mean.cpu(), rstd.cpu(), c["dy"], c["dres"])
+    assert err(got["dx"], dx) <= 2 * TOL[dtype]
+    for k, t in (("dw", tw), ("db", tb)):
+        assert float(((got[k].double().cpu() - t.sum(0)).abs() / t.abs().sum(0).clamp(min=1.0)).max()) <= 2e-6, k

@@ -1,7 +1,8 @@
 """Python binding of the GB300 chunked linear-recurrence library (liblrscan.so).
 
-Argument marshalling only: every step of every operation runs in the CUDA
-kernels behind the C ABI declared in ``include/lrscan.h``.  PyTorch provides
+Argument marshalling only (for the newer calls in a small native module,
+``csrc/binding.cpp``): every step of every operation runs in the CUDA kernels
+behind the C ABI declared in ``include/lrscan.h``.  PyTorch provides
 device memory (output tensors are allocated with ``torch.empty`` when not
 given) and the current CUDA stream.  There is no CPU fallback: if the shared
 library has not been built, every call raises.
@@ -11,9 +12,8 @@ Tensors are CUDA, contiguous, [T, B, D] for sequences, [B, D] for states and
 """
 from __future__ import annotations
 
-import array
 import ctypes
-import operator
+import importlib.util
 import os
 import re
 
@@ -371,51 +371,23 @@ def deer_diag_bwd(w, y, dy, h0=None, du=None, dw=None, dh0=None, want_dh0=True, 
     return du, dw, dh0
 
 
-# The calls below may be a few microseconds of work on the device: their checks
-# take one look at each tensor (a host tensor's get_device() is -1), and the
-# addresses go to ctypes as plain integers.
-def _like(name, t, shape, dtype, dev):
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on cuda:{dev}, got "
-                         f"{t.dtype} {list(t.shape)} on {t.device}"
-                         + ("" if t.is_contiguous() else ", not contiguous"))
-    return t.data_ptr()
+_native = None
 
 
-def _opt(name, t, shape, dtype, dev):
-    return None if t is None else _like(name, t, shape, dtype, dev)
-
-
-def _first(name, t, dims):
-    """The device index of a call's first tensor."""
-    dev = t.get_device()
-    if dev < 0 or not t.is_contiguous() or (t.dim() < 1 if dims is None else t.dim() != len(dims)):
-        raise ValueError(f"{name} must be a contiguous [{', '.join(dims or ('...', 'D'))}] CUDA tensor, got "
-                         f"{list(t.shape)} on {t.device}")
-    return dev
-
-
-def _reset_flags(t, shape, dev):
-    return None if t is None else _like("reset", t, shape, torch.bool if t.dtype is torch.bool else torch.uint8, dev)
-
-
-def _stream_on(stream, dev):
-    """The stream handle for a call on tensors of device `dev`, as _stream."""
-    if dev != torch._C._cuda_getDevice():
-        raise ValueError(f"the tensors are on cuda:{dev} but the current CUDA device is "
-                         f"cuda:{torch.cuda.current_device()}: call under torch.cuda.device({dev})")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    if stream.device.index != dev:
-        raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{dev}")
-    return stream.cuda_stream
-
-
-def _glr_inputs(x, zr, zi, lam, br, bi, dev):
-    shape, dt, D = x.shape, x.dtype, x.shape[-1:]
-    f32 = torch.float32
-    return (x.data_ptr(), _like("zr", zr, shape, dt, dev), _like("zi", zi, shape, dt, dev),
-            _like("lam", lam, D, f32, dev), _like("br", br, D, f32, dev), _like("bi", bi, D, f32, dev))
+def native():
+    """The marshalling module of the calls below (raises if it was not built)."""
+    global _native
+    if _native is None:
+        load()
+        path = os.path.join(os.path.dirname(LIB_PATH), "_lrs_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build the library first "
+                               "(linear_recurrence_scan_chunked_gb300.build())")
+        spec = importlib.util.spec_from_file_location("_lrs_binding", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        _native = mod
+    return _native
 
 
 def glr_fwd(x, zr, zi, lam, br, bi, h0=None, reset=None, h=None, h_last=None, want_last=True,
@@ -425,42 +397,17 @@ def glr_fwd(x, zr, zi, lam, br, bi, h0=None, reset=None, h=None, h_last=None, wa
     lam, br, bi [D] fp32; h0 [B, D] fp32; reset [T, B] uint8 or bool, nonzero
     where a new document starts). Returns (h, h_last), h_last the fp32 state
     after the last step (None with want_last=False)."""
-    dev = _first("x", x, ("T", "B", "D"))
-    T, B, D = x.shape
-    f32, st = torch.float32, x.shape[1:]
-    args = _glr_inputs(x, zr, zi, lam, br, bi, dev)
-    args += (_opt("h0", h0, st, f32, dev), _reset_flags(reset, x.shape[:2], dev))
-    h = torch.empty_like(x) if h is None else h
-    if h_last is None and want_last:
-        h_last = torch.empty(st, dtype=f32, device=x.device)
-    _check(load().glr_fwd(*args, _like("h", h, x.shape, x.dtype, dev), _opt("h_last", h_last, st, f32, dev), B, T, D,
-                          _code(x), _stream_on(stream, dev)))
-    return h, h_last
+    return native().glr_fwd(x, zr, zi, lam, br, bi, h0, reset, h, h_last, want_last, stream)
 
 
 def glr_bwd(x, zr, zi, lam, br, bi, h, dh, h0=None, reset=None, dh_last=None, out=None,
             want_dh0=True, stream=None):
     """Backward of glr_fwd for the upstream dh [T, B, D] and dh_last [B, D] fp32
     (the gradient of h_last). Returns dict dx, dzr, dzi, dlam, dbr, dbi, dh0."""
-    dev = _first("x", x, ("T", "B", "D"))
-    T, B, D = x.shape
-    f32, st, dt = torch.float32, x.shape[1:], x.dtype
-    args = _glr_inputs(x, zr, zi, lam, br, bi, dev)
-    args += (_opt("h0", h0, st, f32, dev), _reset_flags(reset, x.shape[:2], dev),
-             _like("h", h, x.shape, dt, dev), _like("dh", dh, x.shape, dt, dev),
-             _opt("dh_last", dh_last, st, f32, dev))
-    o = dict(out or {})
-    for k in ("dx", "dzr", "dzi"):
-        o[k] = torch.empty_like(x) if o.get(k) is None else o[k]
-    for k in ("dlam", "dbr", "dbi"):
-        o[k] = torch.empty_like(lam) if o.get(k) is None else o[k]
-    if o.get("dh0") is None and want_dh0:
-        o["dh0"] = torch.empty(st, dtype=f32, device=x.device)
-    args += tuple(_like(k, o[k], x.shape, dt, dev) for k in ("dx", "dzr", "dzi"))
-    args += tuple(_like(k, o[k], lam.shape, f32, dev) for k in ("dlam", "dbr", "dbi"))
-    _check(load().glr_bwd(*args, _opt("dh0", o.get("dh0"), st, f32, dev), B, T, D, _code(x),
-                          _stream_on(stream, dev)))
-    return o
+    names = ("dx", "dzr", "dzi", "dlam", "dbr", "dbi", "dh0")
+    o = out or {}
+    return dict(zip(names, native().glr_bwd(x, zr, zi, lam, br, bi, h, dh, h0, reset, dh_last,
+                                            tuple(o.get(k) for k in names), want_dh0, stream)))
 
 
 def glr_step(x, zr, zi, lam, br, bi, state, slots=None, reset=None, h=None, stream=None):
@@ -469,63 +416,22 @@ def glr_step(x, zr, zi, lam, br, bi, state, slots=None, reset=None, h=None, stre
     updated in place. slots [B] int32: the slot of each row, negative for a
     padding row (None: slot b for row b); no slot twice. A slot past the pool
     counts as padding and sets LR_ERR_INDEX (last_error). Returns h [B, D]."""
-    dev = _first("x", x, ("B", "D"))
-    B, D = x.shape
-    args = _glr_inputs(x, zr, zi, lam, br, bi, dev)
-    n_slots = state.shape[0]
-    if slots is None and n_slots < B:
-        raise ValueError(f"state has {n_slots} slots for {B} rows")
-    h = torch.empty_like(x) if h is None else h
-    _check(load().glr_step(*args, _reset_flags(reset, x.shape[:1], dev),
-                           _opt("slots", slots, x.shape[:1], torch.int32, dev),
-                           _like("state", state, (n_slots, D), torch.float32, dev),
-                           _like("h", h, x.shape, x.dtype, dev), B, n_slots, D, _code(x), _stream_on(stream, dev)))
-    return h
+    return native().glr_step(x, zr, zi, lam, br, bi, state, slots, reset, h, stream)
 
 
 def layer_norm_fwd(x, w, b=None, res=None, eps=1e-5, y=None, s=None, stream=None):
     """Layer norm over the last axis (x [..., D]; w, b [D] fp32), of x or, with
     res, of s = x + res. Returns (y, mean, rstd), with res (y, mean, rstd, s);
     mean and rstd are fp32 [...]."""
-    dev = _first("x", x, None)
-    shape, dt, f32 = x.shape, x.dtype, torch.float32
-    row, D = shape[:-1], shape[-1:]
-    if res is not None:
-        s = torch.empty_like(x) if s is None else s
-    elif s is not None:
-        raise ValueError("s is an output of the residual add: give res with it")
-    y = torch.empty_like(x) if y is None else y
-    mean, rstd = w.new_empty(row), w.new_empty(row)
-    _check(load().layer_norm_fwd(x.data_ptr(), _opt("res", res, shape, dt, dev), _like("w", w, D, f32, dev),
-                                 _opt("b", b, D, f32, dev), _like("y", y, shape, dt, dev),
-                                 _opt("s", s, shape, dt, dev), mean.data_ptr(), rstd.data_ptr(), mean.numel(),
-                                 D[0], eps, _code(x), _stream_on(stream, dev)))
-    return (y, mean, rstd) if res is None else (y, mean, rstd, s)
+    return native().layer_norm_fwd(x, w, b, res, eps, y, s, stream)
 
 
 def layer_norm_bwd(x, w, mean, rstd, dy, dres=None, out=None, stream=None):
     """Layer norm backward (x: what the norm was taken of; dres: the gradient
     that reaches it along the residual stream). Returns dict dx, dw, db."""
-    dev = _first("x", x, None)
-    shape, dt, f32 = x.shape, x.dtype, torch.float32
-    row, D = shape[:-1], shape[-1:]
-    o = dict(out or {})
-    o["dx"] = torch.empty_like(x) if o.get("dx") is None else o["dx"]
-    for k in ("dw", "db"):
-        o[k] = torch.empty_like(w) if o.get(k) is None else o[k]
-    _check(load().layer_norm_bwd(x.data_ptr(), _like("w", w, D, f32, dev), _like("mean", mean, row, f32, dev),
-                                 _like("rstd", rstd, row, f32, dev), _like("dy", dy, shape, dt, dev),
-                                 _opt("dres", dres, shape, dt, dev), _like("dx", o["dx"], shape, dt, dev),
-                                 _like("dw", o["dw"], D, f32, dev), _like("db", o["db"], D, f32, dev),
-                                 mean.numel(), D[0], _code(x), _stream_on(stream, dev)))
-    return o
-
-
-def _lce_inputs(x, w, target):
-    dev = _first("x", x, None)
-    V = w.shape[0] if w.dim() else 0
-    return dev, V, (x.data_ptr(), _like("w", w, (V, x.shape[-1]), x.dtype, dev),
-                    _like("target", target, x.shape[:-1], torch.int64, dev))
+    o = out or {}
+    return dict(zip(("dx", "dw", "db"), native().layer_norm_bwd(x, w, mean, rstd, dy, dres, o.get("dx"), o.get("dw"),
+                                                                o.get("db"), stream)))
 
 
 def lce_fwd(x, w, target, ignore=-100, loss=None, lse=None, stream=None):
@@ -533,67 +439,13 @@ def lce_fwd(x, w, target, ignore=-100, loss=None, lse=None, stream=None):
     target [...] int64, without keeping the logits. Returns (loss, lse), fp32
     [...]; loss is 0 where target == ignore. A target outside 0 .. V-1 counts
     as ignored and sets LR_ERR_INDEX (last_error)."""
-    dev, V, args = _lce_inputs(x, w, target)
-    row, f32 = x.shape[:-1], torch.float32
-    loss = torch.empty(row, dtype=f32, device=x.device) if loss is None else loss
-    lse = torch.empty_like(loss) if lse is None else lse
-    _check(load().lce_fwd(*args, ignore, _like("loss", loss, row, f32, dev), _like("lse", lse, row, f32, dev),
-                          target.numel(), V, x.shape[-1], _code(x), _stream_on(stream, dev)))
-    return loss, lse
+    return native().lce_fwd(x, w, target, ignore, loss, lse, stream)
 
 
 def lce_bwd(x, w, target, lse, dloss, ignore=-100, dx=None, dw=None, stream=None):
     """Gradient of lce_fwd for the upstream dloss [...] fp32 (lse: lce_fwd's).
     Returns (dx, dw)."""
-    dev, V, args = _lce_inputs(x, w, target)
-    row, f32 = x.shape[:-1], torch.float32
-    dx = torch.empty_like(x) if dx is None else dx
-    dw = torch.empty_like(w) if dw is None else dw
-    _check(load().lce_bwd(*args, ignore, _like("lse", lse, row, f32, dev), _like("dloss", dloss, row, f32, dev),
-                          _like("dx", dx, x.shape, x.dtype, dev), _like("dw", dw, w.shape, x.dtype, dev),
-                          target.numel(), V, x.shape[-1], _code(x), _stream_on(stream, dev)))
-    return dx, dw
-
-
-_T = torch.Tensor
-_dtype_of = operator.attrgetter("dtype")
-
-
-def _addresses(name, ts, dtype, numels, dev):
-    """The addresses of a list of contiguous CUDA tensors of one dtype on device
-    `dev`, with the given numbers of elements (one C loop per property: a call
-    may hold hundreds of tensors)."""
-    if list(map(_T.numel, ts)) != numels or set(map(_dtype_of, ts)) != {dtype} \
-            or set(map(_T.get_device, ts)) != {dev} or not all(map(_T.is_contiguous, ts)):
-        raise ValueError(f"{name} must hold one contiguous {dtype} tensor on cuda:{dev} per parameter, of as many "
-                         "elements (the scales: one per 256)")
-    return array.array("Q", map(_T.data_ptr, ts))
-
-
-def _adamw_call(fn, params, grads, moments, scales, copies, grad_scale, step, hyper, extra, stream):
-    dev = params[0].get_device()
-    if dev < 0:
-        raise ValueError("params must be CUDA tensors")
-    numels = list(map(_T.numel, params))
-    nb = [(k + ADAMW8_BLOCK - 1) // ADAMW8_BLOCK for k in numels]
-    gd = grads[0].dtype if len(grads) else torch.float32
-    if gd not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"gradients must be float32 or bfloat16, got {gd}")
-    keep = [array.array("q", numels), _addresses("params", params, torch.float32, numels, dev),
-            _addresses("grads", grads, gd, numels, dev)]
-    keep += [_addresses(name, ts, dt, numels, dev) for name, ts, dt in moments]
-    keep += [_addresses(name, ts, torch.float32, nb, dev) for name, ts in scales]
-    args = [a.buffer_info()[0] for a in keep]
-    if copies is not None:
-        keep.append(_addresses("copies", copies, torch.bfloat16, numels, dev))
-        args.append(keep[-1].buffer_info()[0])
-    else:
-        args.append(None)
-    gs = None
-    if grad_scale is not None:
-        gs = _like("grad_scale", grad_scale, grad_scale.shape if grad_scale.numel() == 1 else (1,), torch.float32, dev)
-    _check(fn(len(numels), *args, step, *hyper, gs, *extra, LR_F32 if gd == torch.float32 else LR_BF16,
-              _stream_on(stream, dev)))
+    return native().lce_bwd(x, w, target, lse, dloss, ignore, dx, dw, stream)
 
 
 def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01,
@@ -601,11 +453,8 @@ def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, 
     """One AdamW step over lists of tensors, in place: params fp32, grads fp32 or
     bf16, moments m and v fp32; copies: bf16 copies of the new weights; step
     counts from 1; grad_scale: one fp32 value on the device."""
-    if len(params) == 0:
-        return
-    f32 = torch.float32
-    _adamw_call(load().adamw_step, params, grads, (("m", m, f32), ("v", v, f32)), (), copies, grad_scale, step,
-                (lr, beta1, beta2, eps, weight_decay), (), stream)
+    native().adamw(False, params, grads, m, v, None, None, copies, grad_scale, step, lr, beta1, beta2, eps,
+                   weight_decay, 0, stream)
 
 
 ADAMW8_BLOCK = 256
@@ -625,31 +474,17 @@ def adamw8_step(params, grads, m, v, ms, vs, step, lr, seed, beta1=0.9, beta2=0.
                 weight_decay=0.01, grad_scale=None, copies=None, stream=None):
     """adamw_step with the moments in 8 bits (adamw8_state). seed: another one
     at every step (the rounding's random bits)."""
-    if len(params) == 0:
-        return
-    _adamw_call(load().adamw8_step, params, grads, (("m", m, torch.int8), ("v", v, torch.uint8)),
-                (("ms", ms), ("vs", vs)), copies, grad_scale, step, (lr, beta1, beta2, eps, weight_decay),
-                (int(seed) & 0xFFFFFFFF,), stream)
+    native().adamw(True, params, grads, m, v, ms, vs, copies, grad_scale, step, lr, beta1, beta2, eps,
+                   weight_decay, int(seed) & 0xFFFFFFFF, stream)
 
 
 def adamw8_values(mq, vq, ms, vs, m=None, v=None, stream=None):
     """The fp32 values that 8-bit moments stand for. Returns (m, v), lists of
     1-d tensors unless given."""
-    if len(mq) == 0:
-        return [], []
-    dev = mq[0].get_device()
-    if dev < 0:
-        raise ValueError("the codes must be CUDA tensors")
-    f32 = torch.float32
-    numels = list(map(_T.numel, mq))
-    nb = [(k + ADAMW8_BLOCK - 1) // ADAMW8_BLOCK for k in numels]
-    m = [torch.empty(k, dtype=f32, device=mq[0].device) for k in numels] if m is None else m
-    v = [torch.empty(k, dtype=f32, device=mq[0].device) for k in numels] if v is None else v
-    keep = [array.array("q", numels), _addresses("mq", mq, torch.int8, numels, dev),
-            _addresses("vq", vq, torch.uint8, numels, dev), _addresses("ms", ms, f32, nb, dev),
-            _addresses("vs", vs, f32, nb, dev), _addresses("m", m, f32, numels, dev),
-            _addresses("v", v, f32, numels, dev)]
-    _check(load().adamw8_values(len(numels), *[a.buffer_info()[0] for a in keep], _stream_on(stream, dev)))
+    e = lambda: [torch.empty(t.numel(), dtype=torch.float32, device=t.device) for t in mq]
+    m = e() if m is None else m
+    v = e() if v is None else v
+    native().adamw8_values(mq, vq, ms, vs, m, v, stream)
     return m, v
 
 

@@ -24,6 +24,7 @@
 // No floating-point atomics: sums over parts of the k loop are stored as parts and
 // added in order.
 #include <algorithm>
+#include <utility>
 
 #include "lce_mma.cuh"
 #include "lr_act.cuh"
@@ -152,6 +153,8 @@ __global__ void __launch_bounds__(1024)
     k_lce_join(const float2* __restrict__ part, int64_t tiles, const float* __restrict__ tl,
                const int64_t* __restrict__ target, int64_t ignore, float* __restrict__ loss, float* __restrict__ lse,
                int64_t rows, int64_t V, uint32_t* err) {
+    griddep_launch_dependents();
+    griddep_wait();
     __shared__ float2 sm[32][33];
     const int64_t n = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float M = -INFINITY, s = 0.f;
@@ -320,6 +323,8 @@ template <typename S>
 __global__ void __launch_bounds__(256)
     k_lce_sum(const float* __restrict__ part, int64_t parts, int64_t pitch, int64_t n, const uint32_t* __restrict__ top,
               S* __restrict__ out, bool vec) {
+    griddep_launch_dependents();
+    griddep_wait();
     const float a = scale_of(top);
     const int64_t step = (int64_t)gridDim.x * 256;
     if (vec) {
@@ -365,6 +370,8 @@ template <typename S, int P>
 __global__ void __launch_bounds__(256)
     k_lce_prep(const PackJob jx, const PackJob jw, const float* __restrict__ dloss, const int64_t* __restrict__ target,
                int64_t ignore, int64_t N, int64_t V, uint32_t* __restrict__ top) {
+    griddep_launch_dependents();
+    griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (blockIdx.x == 0) {
         __shared__ uint32_t sm[8];
@@ -435,6 +442,24 @@ bool operand_map(CUtensorMap* m, const Operand& o, bool mn, int box_rows) {
     return tma_encode_planes(m, o.p, o.cols, o.rows, o.planes, o.ld, o.plane, mm::kBlockK, mn ? mm::kBlockK : box_rows);
 }
 
+// Every kernel of a call is launched as a programmatic dependent of the stream's
+// previous one and waits for it (griddep_wait) before it touches memory: its
+// launch and setup, 2 to 3 us of each, run while that one finishes.
+template <class... P, class... A>
+cudaError_t launch_dep(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = grid;
+    lc.blockDim = block;
+    lc.dynamicSmemBytes = smem;
+    lc.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, std::forward<A>(args)...);
+}
+
 // Pairs of CTAs resident at once.
 template <class Epi, int TN>
 cudaError_t mm_pairs(int* pairs) {
@@ -474,8 +499,8 @@ cudaError_t mm_launch(const Operand& a, const Operand& b, const Shape& sh, const
     const uint64_t tiles = (uint64_t)sh.tm * sh.tn * sh.splits;
     if (tiles > 0x7fffffffull) return cudaErrorInvalidValue;
     const unsigned grid = 2 * (unsigned)std::min<uint64_t>(tiles, (uint64_t)pairs);
-    mm::k_mm<Epi, TN><<<grid, mm::kThreads, mm::Cfg<TN>::smem(Epi::kStaged), s>>>(ma, mb, sh, epi, err);
-    return cudaGetLastError();
+    return launch_dep(mm::k_mm<Epi, TN>, dim3(grid), dim3(mm::kThreads), mm::Cfg<TN>::smem(Epi::kStaged), s, ma, mb, sh, epi,
+                      err);
 }
 
 // How a product M x N x K is cut: tiles of 256 x tn, the k loop in `splits` parts.
@@ -500,12 +525,15 @@ Shape mm_shape(int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn, bool n_fas
 template <class Epi>
 cudaError_t mm_run(const Operand& a, const Operand& b, const Shape& sh, Epi epi, int tn, uint32_t* err, cudaStream_t s) {
     epi.tn = tn;
+    if constexpr (!Epi::kStaged) {  // the logits: B is K-major
+        if (tn == 64) return mm_launch<Epi, 64>(a, b, sh, epi, err, s);
+    }
     return tn == 256 ? mm_launch<Epi, 256>(a, b, sh, epi, err, s) : mm_launch<Epi, 128>(a, b, sh, epi, err, s);
 }
 
 // The cut of a product that takes the shortest time in a simple model: rounds of
 // tiles over the pairs, each at a pair's rate (a k-block of 64 by 256 columns takes
-// about 512 cycles, by 128 about 300: its operands come from L2 twice as often)
+// about 512 cycles, by 128 about 300, by 64 about 190: A comes from L2 more often)
 // plus about 1500 cycles of latency, plus, with more than one part, the parts' way
 // to memory and back (about 3.5 KB a cycle over the GPU).  With few tiles narrow ones
 // and parts fill the GPU; with many, parts even out its last round.
@@ -513,13 +541,14 @@ MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int planes, bool may_split) {
     const int64_t kb = (K + mm::kBlockK - 1) / mm::kBlockK, pairs = kSpanSms / 2;
     MmPlan best{256, 1};
     double best_t = 0;
-    for (int tn : {256, 128}) {
+    for (int tn : {256, 128, 64}) {
+        if (tn == 64 && may_split) break;  // MN-major B: blocks of 64 a CTA
         const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + tn - 1) / tn);
         for (int64_t s = 1; s <= (may_split ? 64 : 1) && s <= kb; ++s) {
             const int64_t per = (kb + s - 1) / s, real = (kb + per - 1) / per;
             if (real != s) continue;
             const double rounds = (double)((tiles * s + pairs - 1) / pairs);
-            double t = rounds * ((double)per * (planes == 1 ? 1 : 6) * (tn == 256 ? 512 : 300) + 1500);
+            double t = rounds * ((double)per * (planes == 1 ? 1 : 6) * (tn == 256 ? 512 : tn == 128 ? 300 : 190) + 1500);
             if (s > 1) t += (double)(s * M * N) * 8 / 3500 + 4000;
             if (best_t == 0 || t < 0.98 * best_t) {
                 best = MmPlan{tn, s};
@@ -580,8 +609,8 @@ cudaError_t prepare(const PackJob& jx, const PackJob& jw, const float* dloss, co
     const int64_t rows = jx.rows + jw.rows;
     if (rows == 0 && top == nullptr) return cudaSuccess;
     const int64_t blocks = 1 + std::min<int64_t>((rows + 7) / 8, (int64_t)sm_count() * 8);
-    k_lce_prep<S, sizeof(S) == 4 ? 3 : 1><<<(unsigned)blocks, 256, 0, s>>>(jx, jw, dloss, target, ignore, N, V, top);
-    return cudaGetLastError();
+    return launch_dep(k_lce_prep<S, sizeof(S) == 4 ? 3 : 1>, dim3((unsigned)blocks), dim3(256), 0, s, jx, jw, dloss, target,
+                      ignore, N, V, top);
 }
 
 #define LCE_TRY(x)                            \
@@ -610,9 +639,8 @@ cudaError_t lce_fwd_t(const void* x, const void* w, const int64_t* target, int64
             LCE_TRY(mm_run(a, ow, sh, StatsEpi<true, P>{part, tl, target + r, n, V, 0}, pl.tn_logits, err, s));
         else
             LCE_TRY(mm_run(a, ow, sh, StatsEpi<false, P>{part, tl, target + r, n, V, 0}, pl.tn_logits, err, s));
-        k_lce_join<<<(unsigned)((n + 31) / 32), dim3(32, 32), 0, s>>>(part, pl.tiles, tl, target + r, ignore, loss + r,
-                                                                     lse + r, n, V, err);
-        LCE_TRY(cudaGetLastError());
+        LCE_TRY(launch_dep(k_lce_join, dim3((unsigned)((n + 31) / 32)), dim3(32, 32), 0, s, part, pl.tiles, tl, target + r,
+                           ignore, loss + r, lse + r, n, V, err));
     }
     return cudaSuccess;
 }
@@ -622,8 +650,7 @@ cudaError_t sum_parts(const float* part, int64_t parts, int64_t pitch, int64_t n
                       cudaStream_t s) {
     const bool vec = ((uintptr_t)out & (4 * sizeof(S) - 1)) == 0;
     const int64_t blocks = std::min<int64_t>((n / (vec ? 4 : 1) + 255) / 256 + 1, (int64_t)sm_count() * 8);
-    k_lce_sum<S><<<(unsigned)blocks, 256, 0, s>>>(part, parts, pitch, n, top, out, vec);
-    return cudaGetLastError();
+    return launch_dep(k_lce_sum<S>, dim3((unsigned)blocks), dim3(256), 0, s, part, parts, pitch, n, top, out, vec);
 }
 
 template <typename S>

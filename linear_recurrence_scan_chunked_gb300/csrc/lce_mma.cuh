@@ -5,7 +5,7 @@
 // (cta_group::2, a cluster of two on neighbouring SMs) owns a 256 x TN tile of
 // the result: each holds 128 rows of A, half of B and the accumulators of its
 // 128 rows, so an operand byte in shared memory feeds twice the arithmetic of a
-// single CTA's tile.  TN is 256; 128 where tiles of 256 would leave pairs idle.
+// single CTA's tile.  TN is 256; 128 or (K-major B) 64 where wider tiles would leave pairs idle.
 // Per CTA: a producer thread keeps a ring of k-blocks of 64 in flight by TMA
 // (128-byte swizzle), one thread of the pair's first CTA
 // issues the MMAs, and eight warps read finished accumulators back and run the
@@ -46,7 +46,7 @@ struct Cfg {
     static constexpr int kHalfN = TN / 2;                      // rows of B that a CTA holds; columns of an epilogue warp
     static constexpr int kOperandB = kHalfN * kBlockK * 2;
     static constexpr int kStageBytes = kOperandA + kOperandB;  // of one CTA
-    static constexpr int kStages = TN == 256 ? 6 : 8;          // 192 KB
+    static constexpr int kStages = TN == 256 ? 6 : 8;          // 192 KB (TN = 64: 160 KB)
     static constexpr int kRing = kStages * kStageBytes;
     static constexpr int smem(bool scratch) { return kRing + 1024 + (scratch ? 8 * kScratch : 0); }
 };
@@ -218,11 +218,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_init_fence();
     }
     if (warp == 1) tmem_alloc(&tmem_base, 2 * TN);
+    if (threadIdx.x == 32) {
+        tma_prefetch_desc(&map_a);
+        tma_prefetch_desc(&map_b);
+    }
     fence_before();
     __syncthreads();
     pair_sync();
     fence_after();
     const uint32_t tmem = tmem_base;
+    // a programmatic launch: set up while the kernel before finishes, and let the
+    // one after do the same
+    griddep_launch_dependents();
+    griddep_wait();
 
     bool ok = true;
     if (warp == 0) {

@@ -589,16 +589,17 @@ int glr_step(const void* x, const void* zr, const void* zi, const float* lam, co
     return LR_OK;
 }
 
-// Pointers of a layer norm call: *vec when all allow 16-byte accesses.
+// Pointers of a layer norm call: *vec, the elements of a vector (all pointers
+// allow 16-byte accesses: 4, or 8 bf16 where D is a multiple).
 static int ln_ptrs(std::initializer_list<const void*> req, std::initializer_list<const void*> opt,
                    std::initializer_list<const void*> f32, std::initializer_list<const void*> f32_opt,
-                   int dtype, int64_t D, bool* vec) {
+                   int dtype, int64_t D, int* vec) {
     bool a, b;
     int st = check_ptrs(req, opt, f32, dtype, D, &a);
     if (st) return st;
     st = check_ptrs({}, f32_opt, {}, LR_F32, D, &b);
     if (st) return st;
-    *vec = a && b && D % (16 / (int64_t)esize(dtype)) == 0;
+    *vec = !(a && b) ? 1 : dtype == LR_BF16 && D % 8 == 0 ? 8 : 4;
     return LR_OK;
 }
 
@@ -609,7 +610,7 @@ int layer_norm_fwd(const void* x, const void* res, const float* w, const float* 
     if (N * D == 0) return N > 0 ? LR_ERR_INVALID_ARG : LR_OK;  // rows of no element have no mean
     if (D > kLnMaxD) return LR_ERR_TOO_LARGE;
     if ((res == nullptr) != (sum == nullptr)) return LR_ERR_INVALID_ARG;
-    bool vec;
+    int vec;
     TRY(ln_ptrs({x, y}, {res, sum}, {w}, {b}, dtype, D, &vec));
     if (!mean || !rstd) return LR_ERR_INVALID_ARG;
     if (!aligned(mean, 4) || !aligned(rstd, 4)) return LR_ERR_ALIGN;
@@ -634,7 +635,7 @@ int layer_norm_bwd(const void* x, const float* w, const float* mean, const float
         return LR_OK;
     }
     if (D > kLnMaxD) return LR_ERR_TOO_LARGE;
-    bool vec;
+    int vec;
     TRY(ln_ptrs({x, dy, dx}, {dres}, {w}, {}, dtype, D, &vec));
     for (const float* p : {mean, rstd, (const float*)dw, (const float*)db}) {
         if (!p) return LR_ERR_INVALID_ARG;

@@ -407,15 +407,15 @@ cudaError_t launch_glr_step(int dtype, bool vec, const GlrIn& in, const int32_t*
                             cudaStream_t s);
 
 // Layer norm over the last axis of [N, D] (sum: x + res, with res only).
-// D <= kLnMaxD.  vec: every pointer 16-byte aligned and D a multiple of the
-// 16-byte vector (4 fp32, 8 bf16).
+// D <= kLnMaxD.  vec: elements a vector -- 4 fp32 or 8 bf16 (16 bytes: every
+// pointer aligned to them, D a multiple), 4 bf16, else 1.
 constexpr int64_t kLnMaxD = 16384;
 constexpr int kLnMaxPartials = 2048;  // CTAs of the backward kernel, one row of partials each
-cudaError_t launch_ln_fwd(int dtype, bool vec, const void* x, const void* res, const float* w,
+cudaError_t launch_ln_fwd(int dtype, int vec, const void* x, const void* res, const float* w,
                           const float* b, void* y, void* sum, float* mean, float* rstd, int64_t N,
                           int64_t D, float eps, cudaStream_t s);
 // partials: [2][kLnMaxPartials][D] fp32 scratch (the CTAs launched use its head)
-cudaError_t launch_ln_bwd(int dtype, bool vec, const void* x, const float* w, const float* mean,
+cudaError_t launch_ln_bwd(int dtype, int vec, const void* x, const float* w, const float* mean,
                           const float* rstd, const void* dy, const void* dres, void* dx, float* dw,
                           float* db, float* partials, int64_t N, int64_t D, cudaStream_t s);
 

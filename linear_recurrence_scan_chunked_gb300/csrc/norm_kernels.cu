@@ -156,8 +156,12 @@ __global__ void __launch_bounds__(MAXT, ln_min_ctas(false, RES, VEC * NV, MAXT))
                         e[k][v] = bf_lo(px[k].w[v / 2]);
                         e[k][v + 1] = bf_hi(px[k].w[v / 2]);
                     }
-                    if (live && cl.in(k))
-                        st_u4(cl.at(sr, k), make_uint4(px[k].w[0], px[k].w[1], px[k].w[2], px[k].w[3]));
+                    if (live && cl.in(k)) {
+                        if constexpr (VEC == 8)
+                            st_u4(cl.at(sr, k), make_uint4(px[k].w[0], px[k].w[1], px[k].w[2], px[k].w[3]));
+                        else
+                            st_u2(cl.at(sr, k), make_uint2(px[k].w[0], px[k].w[1]));
+                    }
                 } else {
                     if constexpr (sizeof(S) == 2) {
 #pragma unroll
@@ -485,25 +489,27 @@ static cudaError_t ln_bwd_t(const void* x, const float* w, const float* mean, co
 #undef CALL
 }
 
-// vec: every pointer 16-byte aligned and D a multiple of the 16-byte vector
-cudaError_t launch_ln_fwd(int dtype, bool vec, const void* x, const void* res, const float* w,
+// vec: elements a vector: 8 (bf16), 4 or 1
+cudaError_t launch_ln_fwd(int dtype, int vec, const void* x, const void* res, const float* w,
                           const float* b, void* y, void* sum, float* mean, float* rstd, int64_t N,
                           int64_t D, float eps, cudaStream_t s) {
     if (dtype == 0)
-        return vec ? ln_fwd_t<float, 4>(x, res, w, b, y, sum, mean, rstd, N, D, eps, s)
-                   : ln_fwd_t<float, 1>(x, res, w, b, y, sum, mean, rstd, N, D, eps, s);
-    return vec ? ln_fwd_t<__nv_bfloat16, 8>(x, res, w, b, y, sum, mean, rstd, N, D, eps, s)
-               : ln_fwd_t<__nv_bfloat16, 1>(x, res, w, b, y, sum, mean, rstd, N, D, eps, s);
+        return vec == 4 ? ln_fwd_t<float, 4>(x, res, w, b, y, sum, mean, rstd, N, D, eps, s)
+                        : ln_fwd_t<float, 1>(x, res, w, b, y, sum, mean, rstd, N, D, eps, s);
+    return vec == 8   ? ln_fwd_t<__nv_bfloat16, 8>(x, res, w, b, y, sum, mean, rstd, N, D, eps, s)
+           : vec == 4 ? ln_fwd_t<__nv_bfloat16, 4>(x, res, w, b, y, sum, mean, rstd, N, D, eps, s)
+                      : ln_fwd_t<__nv_bfloat16, 1>(x, res, w, b, y, sum, mean, rstd, N, D, eps, s);
 }
 
-cudaError_t launch_ln_bwd(int dtype, bool vec, const void* x, const float* w, const float* mean,
+cudaError_t launch_ln_bwd(int dtype, int vec, const void* x, const float* w, const float* mean,
                           const float* rstd, const void* dy, const void* dres, void* dx, float* dw,
                           float* db, float* partials, int64_t N, int64_t D, cudaStream_t s) {
     if (dtype == 0)
-        return vec ? ln_bwd_t<float, 4>(x, w, mean, rstd, dy, dres, dx, dw, db, partials, N, D, s)
-                   : ln_bwd_t<float, 1>(x, w, mean, rstd, dy, dres, dx, dw, db, partials, N, D, s);
-    return vec ? ln_bwd_t<__nv_bfloat16, 8>(x, w, mean, rstd, dy, dres, dx, dw, db, partials, N, D, s)
-               : ln_bwd_t<__nv_bfloat16, 1>(x, w, mean, rstd, dy, dres, dx, dw, db, partials, N, D, s);
+        return vec == 4 ? ln_bwd_t<float, 4>(x, w, mean, rstd, dy, dres, dx, dw, db, partials, N, D, s)
+                        : ln_bwd_t<float, 1>(x, w, mean, rstd, dy, dres, dx, dw, db, partials, N, D, s);
+    return vec == 8   ? ln_bwd_t<__nv_bfloat16, 8>(x, w, mean, rstd, dy, dres, dx, dw, db, partials, N, D, s)
+           : vec == 4 ? ln_bwd_t<__nv_bfloat16, 4>(x, w, mean, rstd, dy, dres, dx, dw, db, partials, N, D, s)
+                      : ln_bwd_t<__nv_bfloat16, 1>(x, w, mean, rstd, dy, dres, dx, dw, db, partials, N, D, s);
 }
 
 }  // namespace lrs

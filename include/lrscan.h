@@ -423,6 +423,8 @@ int lce_fwd(const void* x, const void* w, const int64_t* target, int64_t ignore,
  * The logits are computed again, one piece of the vocabulary at a time.
  *   lse   : [N] fp32 in (lce_fwd's);  dloss : [N] fp32 in
  *   dx    : [N,D] out;  dw : [V,D] out (overwritten; N = 0: zeros)
+ * An ignored row's dx is 0 whatever the row holds; dw takes 0 times the row, so
+ * that a row that is not finite shows in it.
  * Results are bitwise reproducible (no atomics on values).
  */
 int lce_bwd(const void* x, const void* w, const int64_t* target, int64_t ignore, const float* lse,

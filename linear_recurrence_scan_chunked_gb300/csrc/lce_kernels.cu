@@ -240,6 +240,10 @@ struct GradEpi {
         if (any) gt = expm1f(pick32(v, r.at & 31) - r.z) * r.ds;
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = ex2_ftz(fmaf(v[i], kLog2e, -r.hi)) * r.f;
+        if (r.hi == INFINITY) {  // whatever its logits are, infinite or NaN
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
         if (any) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = mine && i == (r.at & 31) ? gt : v[i];
@@ -318,40 +322,66 @@ struct OutEpi {
     __device__ void end(Row&) const {}
 };
 
-// out = max|dloss| * the sum of the parts, in order.
-template <typename S>
+// out = max|dloss| * the sum of the parts.  GROUPS warps share 128 (vec) or 32
+// outputs: each adds a run of neighbouring parts in order, and the runs' sums are
+// added in order.
+template <typename S, int GROUPS>
 __global__ void __launch_bounds__(256)
     k_lce_sum(const float* __restrict__ part, int64_t parts, int64_t pitch, int64_t n, const uint32_t* __restrict__ top,
               S* __restrict__ out, bool vec) {
     griddep_launch_dependents();
     griddep_wait();
     const float a = scale_of(top);
-    const int64_t step = (int64_t)gridDim.x * 256;
-    if (vec) {
-        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n / 4; i += step) {
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int64_t k = 0; k < parts; k += 8) {  // eight loads in flight, added in order
-                Pack<float, 4> p[8];
+    constexpr int kLanes = 256 / GROUPS;  // threads of a run
+    const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+    const int64_t step = (int64_t)gridDim.x * kLanes, run = (parts + GROUPS - 1) / GROUPS;
+    const int64_t k0 = grp * run, k1 = parts < k0 + run ? parts : k0 + run;
+    __shared__ float4 sm[GROUPS > 1 ? 256 : 1];
+    auto add = [&](auto width, int64_t base, int64_t count) {
+        constexpr int W = decltype(width)::value;
+        for (int64_t i0 = (int64_t)blockIdx.x * kLanes; i0 < count; i0 += step) {
+            const int64_t i = i0 + lane;
+            float s[W];
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (k + u < parts) p[u].load(part + (k + u) * pitch + 4 * i);
-                    else p[u].ident(0.f);
+            for (int j = 0; j < W; ++j) s[j] = 0.f;
+            if (i < count) {
+                for (int64_t k = k0; k < k1; k += 8) {  // eight loads in flight, added in order
+                    Pack<float, W> p[8];
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
+                    for (int u = 0; u < 8; ++u)
+                        if (k + u < k1) p[u].load(part + (k + u) * pitch + base + W * i);
+                        else p[u].ident(0.f);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[j] += p[u].get(j);
+                    for (int u = 0; u < 8; ++u)
+#pragma unroll
+                        for (int j = 0; j < W; ++j) s[j] += p[u].get(j);
+                }
             }
+            if constexpr (GROUPS > 1) {
+                float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+                q.x = s[0];
+                if constexpr (W == 4) { q.y = s[1]; q.z = s[2]; q.w = s[3]; }
+                __syncthreads();
+                sm[threadIdx.x] = q;
+                __syncthreads();
+                if (grp > 0) continue;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] *= a;
-            store_vec<S, 4>(out + 4 * i, s);
+                for (int r = 1; r < GROUPS; ++r) {
+                    const float4 o = sm[r * kLanes + lane];
+                    s[0] += o.x;
+                    if constexpr (W == 4) { s[1] += o.y; s[2] += o.z; s[3] += o.w; }
+                }
+            }
+            if (i < count) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) s[j] *= a;
+                store_vec<S, W>(out + base + W * i, s);
+            }
         }
-    }
-    for (int64_t i = (vec ? n / 4 * 4 : 0) + (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-        float s[1] = {0.f};
-        for (int64_t k = 0; k < parts; ++k) s[0] += __ldg(part + k * pitch + i);
-        s[0] *= a;
-        store_vec<S, 1>(out + i, s);
-    }
+    };
+    if (vec) add(std::integral_constant<int, 4>{}, 0, n / 4);
+    const int64_t done = vec ? n / 4 * 4 : 0;
+    add(std::integral_constant<int, 1>{}, done, n - done);
 }
 
 // A matrix on its way into planes: [rows][D] into P bf16 planes of pitch ld (a
@@ -360,6 +390,7 @@ struct PackJob {
     const void* src;
     __nv_bfloat16* dst;
     int64_t rows, D, ld;
+    bool quads;  // rows can be read four elements at a time
 };
 
 // Before the products, one launch: block 0 takes max |dloss| over the rows that
@@ -409,12 +440,19 @@ __global__ void __launch_bounds__(256)
         const int64_t plane = j.rows * j.ld;
         for (int64_t d = lane * 4; d < j.D; d += 128) {
             float v[4];
+            if (j.quads) {
+                Pack<S, 4> p;
+                p.load(src + d);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                Pack<S, 1> p;
-                p.ident(0.f);
-                if (d + i < j.D) p.load(src + d + i);
-                v[i] = p.get(0);
+                for (int i = 0; i < 4; ++i) v[i] = p.get(i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    Pack<S, 1> p;
+                    p.ident(0.f);
+                    if (d + i < j.D) p.load(src + d + i);
+                    v[i] = p.get(0);
+                }
             }
 #pragma unroll
             for (int k = 0; k < P; ++k) {  // rows are padded to 8: 8-byte stores stay inside
@@ -596,10 +634,10 @@ Layout layout(int dtype, const void* x, const void* w, int64_t N, int64_t V, int
 template <typename S>
 Operand operand(const void* src, int64_t rows, int64_t D, void* scratch, PackJob* job) {
     constexpr int P = sizeof(S) == 4 ? 3 : 1;
-    *job = PackJob{nullptr, nullptr, 0, 0, 0};
+    *job = PackJob{nullptr, nullptr, 0, 0, 0, false};
     if (!packed(sizeof(S) == 4 ? 0 : 1, src, D)) return Operand{(const __nv_bfloat16*)src, rows, D, D, rows * D, P};
     const int64_t ld = round_up(D, 8);
-    *job = PackJob{src, (__nv_bfloat16*)scratch, rows, D, ld};
+    *job = PackJob{src, (__nv_bfloat16*)scratch, rows, D, ld, D % 4 == 0 && ((uintptr_t)src & (4 * sizeof(S) - 1)) == 0};
     return Operand{(const __nv_bfloat16*)scratch, rows, D, ld, rows * ld, P};
 }
 
@@ -649,8 +687,14 @@ template <typename S>
 cudaError_t sum_parts(const float* part, int64_t parts, int64_t pitch, int64_t n, const uint32_t* top, S* out,
                       cudaStream_t s) {
     const bool vec = ((uintptr_t)out & (4 * sizeof(S) - 1)) == 0;
-    const int64_t blocks = std::min<int64_t>((n / (vec ? 4 : 1) + 255) / 256 + 1, (int64_t)sm_count() * 8);
-    return launch_dep(k_lce_sum<S>, dim3((unsigned)blocks), dim3(256), 0, s, part, parts, pitch, n, top, out, vec);
+    // few outputs: eight warps to a warp's outputs, or the loads of one thread's
+    // parts, one round trip for eight, are the time
+    const int64_t items = n / (vec ? 4 : 1) + 1, cap = (int64_t)sm_count() * 8;
+    const bool few = parts > 8 && items < (int64_t)sm_count() * 512;
+    const int64_t lanes = few ? 32 : 256;
+    const dim3 grid((unsigned)std::min<int64_t>((items + lanes - 1) / lanes, cap));
+    return few ? launch_dep(k_lce_sum<S, 8>, grid, dim3(256), 0, s, part, parts, pitch, n, top, out, vec)
+               : launch_dep(k_lce_sum<S, 1>, grid, dim3(256), 0, s, part, parts, pitch, n, top, out, vec);
 }
 
 template <typename S>

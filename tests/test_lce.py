@@ -193,6 +193,34 @@ def test_nan_stays_in_its_rows(cuda):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 37])
+def test_ignored_rows_do_not_count_whatever_they_hold(cuda, dtype, D):
+    """Rows whose target is ignored: values whose logits overflow to infinities and
+    NaN leave dx = 0 there and nothing in dw (0 times a finite row); a NaN leaves
+    dx = 0 as well."""
+    N, V = 150, 300
+    x, w, t, dl = make(N, V, D, dtype, seed=12, pad=0.0)
+    t[[3, 60, 140]] = -100
+    x[3] = 3e38
+    x[60] = -3e38
+    x[60, ::2] = 3e38
+    x[140] = -3e38
+    xd, wd, td = x.cuda(), w.cuda(), t.cuda()
+    _, _, rdx, rdw = ref(torch.where((t == -100)[:, None], torch.zeros_like(x), x), w, t, dl)
+    loss, lse = cuda.lce_fwd(xd, wd, td, ignore=-100)
+    assert not loss[[3, 60, 140]].any()
+    dx, dw = cuda.lce_bwd(xd, wd, td, lse, dl.cuda(), ignore=-100)
+    tol = 1e-5 if dtype == "f32" else 2e-2
+    assert not dx[[3, 60, 140]].any()
+    assert dist(dx, rdx) <= tol and dist(dw, rdw) <= tol
+    x[60, 1] = float("nan")
+    loss, lse = cuda.lce_fwd(x.cuda(), wd, td, ignore=-100)
+    dx, _ = cuda.lce_bwd(x.cuda(), wd, td, lse, dl.cuda(), ignore=-100)
+    assert not loss[60] and not dx[60].any() and dist(dx, rdx) <= tol
+
+
+@pytest.mark.gpu
 def test_targets_out_of_range_are_recorded(cuda):
     x, w, t, dl = make(6, 50, 64, "f32", seed=9, pad=0.0)
     t[1], t[4] = 50, -7

@@ -118,7 +118,6 @@ __device__ __forceinline__ float byte_float(uint32_t w, int k, float bias) {
     return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u + (uint32_t)k)) - bias;
 }
 __device__ __forceinline__ float unit16(uint32_t u16) { return __uint_as_float(0x3F800000u | u16 << 7) - 1.f; }
-__device__ __forceinline__ uint32_t floor_bits(float x) { return __float_as_uint(__fadd_rz(x, 8388608.f)) & 0x3ffu; }
 
 // A sum of pairs, each of its terms rounded by itself: the compiler fuses
 // mul.rn.f32x2 into an add.f32x2 that follows (seen in the results), so the
@@ -142,52 +141,87 @@ __device__ __forceinline__ f32x2 adam_decode_v(float q0, float q1, f32x2 scale) 
     return f2_mul(f2_mul(t, t), scale);
 }
 
-// One warp per block of 256 elements, 8 consecutive ones a lane, in pairs.
-template <typename G, bool VP>
-__device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, const AdamHyper& h,
-                                            float gs, uint32_t key) {
+// A warp's next block on its way into shared memory: each lane copies what it will
+// read itself, so that a wait on its own copies is all there is to wait for.
+template <typename G>
+struct A8Stage {
+    float4 p[2][32];
+    struct alignas(4 * sizeof(G)) Quad { Pack<G, 4> v; } g[2][32];
+    uint32_t m[2][32], v[2][32];
+};
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES) : "memory");
+}
+template <typename G>
+__device__ __forceinline__ void adam8_fetch(const AdamTensor& t, int64_t blk, A8Stage<G>& st) {
     const int lane = threadIdx.x & 31;
-    const int64_t i0 = blk * 256 + lane * 8;
-    const int n = t.n - i0 >= 8 ? 8 : t.n > i0 ? (int)(t.n - i0) : 0;
-    const G* gp = (const G*)t.g;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t i = blk * 256 + h * 128 + lane * 4;
+        if (!t.vec || t.n - i < 4) continue;  // read in place
+        copy_async<16>(&st.p[h][lane], t.p + i);
+        copy_async<4 * sizeof(G)>(&st.g[h][lane], (const G*)t.g + i);
+        copy_async<4>(&st.m[h][lane], (const uint8_t*)t.m + i);
+        copy_async<4>(&st.v[h][lane], (const uint8_t*)t.v + i);
+    }
+}
+
+// With F = 2^23 + floor(x), x + (kHalfPast - F) is the fraction of x less 1/2, exactly.
+constexpr float kHalfPast = 8388607.5f;
+
+// One warp per block of 256 elements, four consecutive ones of each half a lane,
+// worked on in pairs.  About 92 instructions an element (110 with IEEE roots
+// throughout) and whole sectors in every access: eight consecutive elements a
+// lane, two accesses to each sector, took 290 us for 64M elements where this
+// takes 209 (5.1 TB/s).  64 registers, four CTAs an SM (three: 239 us); chunks of
+// 8192 took 224 us, of 16384 216, shares of one grid that fills the GPU once 310.
+template <typename G>
+__device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, const A8Stage<G>& st, float sm, float sv,
+                                            const AdamHyper& h, float gs, uint32_t key) {
+    const int lane = threadIdx.x & 31;
+    const int64_t i0 = blk * 256 + lane * 4;
     uint8_t* mq = (uint8_t*)t.m;  // int8 codes
     uint8_t* vq = (uint8_t*)t.v;
-    const float sm = t.ms[blk], sv = t.vs[blk];
     float p[8], g[8];
-    uint2 cm = make_uint2(0u, 0u), cv = make_uint2(0u, 0u);
-    if (VP && n == 8) {
-        const float4 a = *reinterpret_cast<const float4*>(t.p + i0);
-        const float4 b = *reinterpret_cast<const float4*>(t.p + i0 + 4);
-        p[0] = a.x; p[1] = a.y; p[2] = a.z; p[3] = a.w;
-        p[4] = b.x; p[5] = b.y; p[6] = b.z; p[7] = b.w;
-        cm = *reinterpret_cast<const uint2*>(mq + i0);
-        cv = *reinterpret_cast<const uint2*>(vq + i0);
-        Pack<G, 4> g0, g1;
-        g0.load(gp + i0);
-        g1.load(gp + i0 + 4);
+    uint32_t cm[2], cv[2];
+    int n[2];  // elements inside the tensor
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = k < 4 ? g0.get(k & 3) : g1.get(k & 3);
-    } else {
+    for (int h = 0; h < 2; ++h) {
+        const int64_t i = i0 + h * 128;
+        n[h] = t.n - i >= 4 ? 4 : t.n > i ? (int)(t.n - i) : 0;
+        if (t.vec && n[h] == 4) {
+            const float4 a = st.p[h][lane];
+            p[4 * h] = a.x; p[4 * h + 1] = a.y; p[4 * h + 2] = a.z; p[4 * h + 3] = a.w;
+            const Pack<G, 4> gg = st.g[h][lane].v;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            p[k] = g[k] = 0.f;
-            if (k >= n) continue;
-            p[k] = t.p[i0 + k];
-            Pack<G, 1> g1;
-            g1.load(gp + i0 + k);
-            g[k] = g1.get(0);
-            (k < 4 ? cm.x : cm.y) |= (uint32_t)mq[i0 + k] << (8 * (k & 3));
-            (k < 4 ? cv.x : cv.y) |= (uint32_t)vq[i0 + k] << (8 * (k & 3));
+            for (int k = 0; k < 4; ++k) g[4 * h + k] = gg.get(k);
+            cm[h] = st.m[h][lane];
+            cv[h] = st.v[h][lane];
+        } else {
+            cm[h] = cv[h] = 0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                p[4 * h + k] = g[4 * h + k] = 0.f;
+                if (k >= n[h]) continue;
+                p[4 * h + k] = t.p[i + k];
+                Pack<G, 1> g1;
+                g1.load((const G*)t.g + i + k);
+                g[4 * h + k] = g1.get(0);
+                cm[h] |= (uint32_t)mq[i + k] << (8 * k);
+                cv[h] |= (uint32_t)vq[i + k] << (8 * k);
+            }
         }
+        cm[h] ^= 0x80808080u;  // signed codes, biased
     }
     // the new moments
-    cm.x ^= 0x80808080u;  // signed codes, biased
-    cm.y ^= 0x80808080u;
     float m[8], v[8];
     float tm = 0.f, tv = 0.f;  // the block's new scales
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
-        const uint32_t wm = k < 4 ? cm.x : cm.y, wv = k < 4 ? cv.x : cv.y;
+        const uint32_t wm = cm[k >> 2], wv = cv[k >> 2];
         const f32x2 m0 = adam_decode_m(byte_float(wm, k & 3, 8388736.f), byte_float(wm, (k & 3) + 1, 8388736.f), f2(sm));
         const f32x2 v0 = adam_decode_v(byte_float(wv, k & 3, 8388608.f), byte_float(wv, (k & 3) + 1, 8388608.f), f2(sv));
         const f32x2 gg = f2_mul(f2(g[k], g[k + 1]), f2(gs));
@@ -207,47 +241,60 @@ __device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, co
     uint32_t qm[2] = {0u, 0u}, qv[2] = {0u, 0u};
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
-        float rm[2], r2[2], a[2], b[2], um[2], uv[2];
+        float rm[2], r2[2], root[2], a[2], b[2], um[2], uv[2], fa[2], fb[2], da[2], db[2];
         f2_get(f2_mul(f2(fabsf(m[k]), fabsf(m[k + 1])), f2(im)), rm[0], rm[1]);
         f2_get(f2_mul(f2(v[k], v[k + 1]), f2(iv)), r2[0], r2[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const uint32_t u = adam_hash((uint32_t)(i0 + k + e), key);
+            const uint32_t u = adam_hash((uint32_t)(i0 + (k >> 2) * 128 + (k & 3) + e), key);
             um[e] = unit16(u >> 16);
             uv[e] = unit16(u & 0xffffu);
-            rm[e] = __fsqrt_rn(rm[e]);
-            r2[e] = __fsqrt_rn(r2[e]);
-            b[e] = __fsqrt_rn(r2[e]);
+            a[e] = fmaf(sqrt_ftz(rm[e]), 127.f, um[e]);
+            root[e] = sqrt_ftz(r2[e]);
+            b[e] = fmaf(sqrt_ftz(root[e]), 255.f, uv[e]);
+            fa[e] = __fadd_rz(a[e], 8388608.f);
+            fb[e] = __fadd_rz(b[e], 8388608.f);
         }
-        add_apart(f2_mul(f2(rm[0], rm[1]), f2(127.f)), f2(um[0], um[1]), a[0], a[1]);
-        add_apart(f2_mul(f2(b[0], b[1]), f2(255.f)), f2(uv[0], uv[1]), b[0], b[1]);
+        f2_get(f2_add(f2(a[0], a[1]), f2_add(f2(kHalfPast), f2(-fa[0], -fa[1]))), da[0], da[1]);
+        f2_get(f2_add(f2(b[0], b[1]), f2_add(f2(kHalfPast), f2(-fb[0], -fb[1]))), db[0], db[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            p[k + e] = fmaf(-h.step, __fdividef(m[k + e], fmaf(r2[e], rv, h.eps)), h.decay * p[k + e]);
-            int q = (int)min(floor_bits(a[e]), 127u);
+            // The roots are good to a few 2^-23: a and b to 5e-5 and 1.2e-4.  Where that
+            // does not settle the code (or v / scale is subnormal: flushed; or NaN), in
+            // about one element of 1500, the IEEE roots do.
+            if (!(fabsf(da[e]) < 0.5f - 1e-4f && fabsf(db[e]) < 0.5f - 2e-4f && r2[e] >= 1.17549435e-38f)) {
+                root[e] = __fsqrt_rn(r2[e]);
+                fa[e] = __fadd_rz(__fadd_rn(__fmul_rn(__fsqrt_rn(rm[e]), 127.f), um[e]), 8388608.f);
+                fb[e] = __fadd_rz(__fadd_rn(__fmul_rn(__fsqrt_rn(root[e]), 255.f), uv[e]), 8388608.f);
+            }
+            p[k + e] = fmaf(-h.step, __fdividef(m[k + e], fmaf(root[e], rv, h.eps)), h.decay * p[k + e]);
+            int q = (int)min(__float_as_uint(fa[e]) & 0x3ffu, 127u);
             q = m[k + e] < 0.f ? -q : q;
-            uint32_t w = min(floor_bits(b[e]), 255u);
+            uint32_t w = min(__float_as_uint(fb[e]) & 0x3ffu, 255u);
             if (w == 0u && v[k + e] > 0.f) w = 1u;
             qm[k >> 2] |= ((uint32_t)q & 255u) << (8 * ((k + e) & 3));
             qv[k >> 2] |= w << (8 * ((k + e) & 3));
         }
     }
-    if (VP && n == 8) {
-        *reinterpret_cast<float4*>(t.p + i0) = make_float4(p[0], p[1], p[2], p[3]);
-        *reinterpret_cast<float4*>(t.p + i0 + 4) = make_float4(p[4], p[5], p[6], p[7]);
-        *reinterpret_cast<uint2*>(mq + i0) = make_uint2(qm[0], qm[1]);
-        *reinterpret_cast<uint2*>(vq + i0) = make_uint2(qv[0], qv[1]);
-        if (t.copy)
-            *reinterpret_cast<uint4*>((__nv_bfloat16*)t.copy + i0) =
-                make_uint4(bf_pack(p[0], p[1]), bf_pack(p[2], p[3]), bf_pack(p[4], p[5]), bf_pack(p[6], p[7]));
-    } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (k >= n) continue;
-            t.p[i0 + k] = p[k];
-            mq[i0 + k] = (uint8_t)(qm[k >> 2] >> (8 * (k & 3)));
-            vq[i0 + k] = (uint8_t)(qv[k >> 2] >> (8 * (k & 3)));
-            if (t.copy) ((__nv_bfloat16*)t.copy)[i0 + k] = __float2bfloat16_rn(p[k]);
+    for (int h = 0; h < 2; ++h) {
+        const int64_t i = i0 + h * 128;
+        const float* ph = p + 4 * h;
+        if (t.vec && n[h] == 4) {
+            *reinterpret_cast<float4*>(t.p + i) = make_float4(ph[0], ph[1], ph[2], ph[3]);
+            *reinterpret_cast<uint32_t*>(mq + i) = qm[h];
+            *reinterpret_cast<uint32_t*>(vq + i) = qv[h];
+            if (t.copy)
+                *reinterpret_cast<uint2*>((__nv_bfloat16*)t.copy + i) = make_uint2(bf_pack(ph[0], ph[1]), bf_pack(ph[2], ph[3]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k >= n[h]) continue;
+                t.p[i + k] = ph[k];
+                mq[i + k] = (uint8_t)(qm[h] >> (8 * k));
+                vq[i + k] = (uint8_t)(qv[h] >> (8 * k));
+                if (t.copy) ((__nv_bfloat16*)t.copy)[i + k] = __float2bfloat16_rn(ph[k]);
+            }
         }
     }
     if (lane == 0) {
@@ -257,19 +304,34 @@ __device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, co
 }
 
 template <typename G>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
     k_adamw8(const __grid_constant__ AdamTable tb, const AdamHyper h, const float* __restrict__ gscale,
              uint32_t seed) {
+    __shared__ A8Stage<G> st[8][2];
     const uint32_t chunk = blockIdx.x;
-    const int ti = adam_find(tb, chunk);
+    const int ti = adam_find(tb, chunk), warp = threadIdx.x >> 5;
     const AdamTensor t = tb.t[ti];
     const float gs = gscale ? __ldg(gscale) : 1.f;
     const uint32_t key = (uint32_t)(tb.base + ti) * 0x9E3779B1u + seed * 0xBB67AE85u;
     const int64_t lo = (int64_t)(chunk - tb.first[ti]) * (kAdamChunk / 256);
-    const int64_t nb = (t.n + 255) / 256;
-    for (int64_t blk = lo + (threadIdx.x >> 5); blk < nb && blk < lo + kAdamChunk / 256; blk += 8) {
-        if (t.vec) adam8_block<G, true>(t, blk, h, gs, key);
-        else adam8_block<G, false>(t, blk, h, gs, key);
+    const int64_t nb = (t.n + 255) / 256, end = nb < lo + kAdamChunk / 256 ? nb : lo + kAdamChunk / 256;
+    int64_t blk = lo + warp;
+    if (blk >= end) return;
+    adam8_fetch<G>(t, blk, st[warp][0]);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    float sm = t.ms[blk], sv = t.vs[blk];
+    for (int cur = 0; blk < end; blk += 8, cur ^= 1) {
+        float sm1 = 0.f, sv1 = 0.f;
+        if (blk + 8 < end) {  // the next block's copies fly while this one is worked on
+            adam8_fetch<G>(t, blk + 8, st[warp][cur ^ 1]);
+            sm1 = t.ms[blk + 8];
+            sv1 = t.vs[blk + 8];
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        adam8_block<G>(t, blk, st[warp][cur], sm, sv, h, gs, key);
+        sm = sm1;
+        sv = sv1;
     }
 }
 

@@ -752,9 +752,8 @@ static int adamw_tensors(std::vector<AdamTensor>& out, int64_t n_tensors, const 
         if (!aligned(t.p, 4) || !aligned(t.g, ges) || !aligned(t.copy, 2) || !aligned(t.ms, 4) || !aligned(t.vs, 4))
             return LR_ERR_ALIGN;
         if (!eight && (!aligned(t.m, 4) || !aligned(t.v, 4))) return LR_ERR_ALIGN;
-        const size_t sa = eight ? 8 : 16;
-        t.vec = aligned(t.p, 16) && aligned(t.g, eight ? 16 : 4 * ges) && aligned(t.m, sa) && aligned(t.v, sa) &&
-                aligned(t.copy, eight ? 16 : 8);
+        const size_t sa = eight ? 4 : 16;
+        t.vec = aligned(t.p, 16) && aligned(t.g, 4 * ges) && aligned(t.m, sa) && aligned(t.v, sa) && aligned(t.copy, 8);
     }
     return LR_OK;
 }

@@ -465,6 +465,9 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------- host
+//
+// Every kernel of a call is launched by launch_dep and waits for the one before it
+// (griddep_wait) before it touches memory.
 
 // An operand as the products take it: bf16 planes [planes][rows][ld].
 struct Operand {
@@ -478,24 +481,6 @@ int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // mn: the product takes it MN-major (boxes of 64 x 64), else K-major (64 x box_rows).
 bool operand_map(CUtensorMap* m, const Operand& o, bool mn, int box_rows) {
     return tma_encode_planes(m, o.p, o.cols, o.rows, o.planes, o.ld, o.plane, mm::kBlockK, mn ? mm::kBlockK : box_rows);
-}
-
-// Every kernel of a call is launched as a programmatic dependent of the stream's
-// previous one and waits for it (griddep_wait) before it touches memory: its
-// launch and setup, 2 to 3 us of each, run while that one finishes.
-template <class... P, class... A>
-cudaError_t launch_dep(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
-    cudaLaunchConfig_t lc{};
-    lc.gridDim = grid;
-    lc.blockDim = block;
-    lc.dynamicSmemBytes = smem;
-    lc.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, kernel, std::forward<A>(args)...);
 }
 
 // Pairs of CTAs resident at once.

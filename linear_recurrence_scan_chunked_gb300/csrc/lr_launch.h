@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "lr_common.cuh"
 
 // Consume lag of the walker-protocol kernel, in rounds of tickets, and the
@@ -262,6 +264,24 @@ inline CarryPlan carry_plan(Op op, int dtype, bool vec, bool tma, int64_t T, int
         }
     }
     return chain_plan(op, dtype, vec, tma, T, C);
+}
+
+// A launch as a programmatic dependent of the stream's previous one: its launch and
+// setup, 2 to 3 us, run while that one finishes; the kernel waits for it
+// (griddep_wait) before it touches memory.
+template <class... P, class... A>
+inline cudaError_t launch_dep(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = grid;
+    lc.blockDim = block;
+    lc.dynamicSmemBytes = smem;
+    lc.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, kernel, std::forward<A>(args)...);
 }
 
 // Grid of a persistent launch: every walker plus as many tile CTAs as can be

@@ -192,7 +192,7 @@ def test_refusals_on_device_tensors(cuda):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("D", [31, 32, 65, 119, 128, 250, 255, 257, 511, 520, 900, 1500, 1792, 2047, 3000, 5000, 10995, 16383])
+@pytest.mark.parametrize("D", [8, 9, 24, 31, 32, 49, 63, 64, 65, 100, 104, 119, 128, 250, 255, 257, 511, 520, 900, 1500, 1792, 2047, 3000, 5000, 10995, 16383])
 def test_every_instance(cuda, D, dtype):
     """The row shapes between the sizes above: each number of elements a thread, the wide rows."""
     c = make(67, D, dtype, seed=D)

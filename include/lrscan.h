@@ -9,7 +9,10 @@
  * along the sequence axis as a parallel prefix scan over the associative
  * operator (a1, b1) o (a2, b2) = (a1 a2, a2 b1 + b2) (earlier element on the
  * left, identity (1, 0)), and the computations built on that scan (SRU and
- * LSTM cells, forward and backward; DEER solve and its gradient).
+ * LSTM cells, forward and backward; DEER solve and its gradient), and the
+ * operators that a language model built on such a recurrence needs beside it
+ * (a gated recurrence with resets and single-token steps, layer norm, cross
+ * entropy over a vocabulary, AdamW).
  *
  * Sources (blog.hotdry.top, all dated 2025-09-21):
  *   [P1] "CUDA并行化RNN训练：从O(T)到O(log T)的工程实践与参数调优":
@@ -56,7 +59,10 @@
  *    the chunk states and aggregates, a tile ticket, an error word, DEER's
  *    second iterate buffer, residual slots, per-sequence stop state, clamp
  *    counters and the last iteration count of each DEER form and shape,
- *    bias-gradient partials), grown on demand with cudaMalloc.  Calls on
+ *    bias-gradient partials; the gated recurrence's aggregates of spans of
+ *    time and its parameter partials, the layer norm's column sums, and the
+ *    cross entropy's scratch, up to 2 GB of gradients of logits plus packed
+ *    copies of fp32 or unaligned operands), grown on demand with cudaMalloc.  Calls on
  *    different streams are serialised through it with CUDA events; every
  *    call records its event on every return once it has begun enqueueing,
  *    errors included, so a later call on another stream still waits for
@@ -65,11 +71,9 @@
  *    take on the device from the workspace's ticket word (every launch takes
  *    a fresh one), so a call of lr_scan_fwd, lr_scan_bwd, sru_fwd, sru_bwd,
  *    lstm_cell_fwd, lstm_cell_bwd, glr_fwd, glr_bwd, glr_step,
- *    layer_norm_fwd, layer_norm_bwd, lce_fwd, lce_bwd, adamw_step, adamw8_step
- *    or deer_diag_bwd
- *    captured into a graph
- *    gives the right result on every replay, with whatever the captured
- *    buffers hold then.  Make one uncaptured call of the same shape first
+ *    layer_norm_fwd, layer_norm_bwd, lce_fwd, lce_bwd, adamw_step,
+ *    adamw8_step or deer_diag_bwd captured into a graph gives the right
+ *    result on every replay, with whatever the captured buffers hold then.  Make one uncaptured call of the same shape first
  *    (it sizes the workspace and sets up the kernels; capture fails if the
  *    workspace would have to grow).  A graph keeps using the workspace
  *    buffers it captured: the carry packets and the bias partials that a

@@ -21,7 +21,10 @@
 // Bytes bound it: each element of p, g, m, v crosses HBM once each way.  A
 // launch takes up to kAdamTensors tensors, whose pointers travel in the kernel's
 // arguments (no copy to the device, nothing to keep for a graph); a CTA finds
-// its tensor by binary search over the chunk counts.
+// its tensor by binary search over the chunk counts.  Measured: 128M elements in
+// 160 tensors, bf16 gradients and copies, 546 us = 6.9 TB/s (copy 6.78); 8-bit
+// moments, 64M elements in 90 tensors, fp32 gradients, 209 us = 5.1 TB/s, and their
+// values written out 100 us = 6.7 TB/s.
 #include "lr_act.cuh"
 #include "lr_launch.h"
 

@@ -16,23 +16,32 @@
 // h_{t-1} as the forward pass stored it (bf16 storage: rounded once, 2^-9), the
 // way the other cells do: keeping fp32 states would double what it reads of h.
 //
-// The split.  An element costs about 45 instructions forward and 75 backward (two
-// gates, a decay, a square root), so at 8 to 32 bytes an element the issue slots
-// are as scarce as the bytes, and the carry must not make an element's gates be
-// computed twice.  The time axis is cut into S spans; a CTA owns one span of one
-// channel strip and walks it through time, tile by tile, its state in shared
-// memory, so CTAs wait for nothing but their own loads.  Wide problems have strips
-// enough: S = 1 and one launch.  Narrow ones first run k_glr_agg, which computes only
-// the spans' aggregates (A, B) -- backward that takes the decay and dh, two of the
-// five inputs -- with every warp folding a run of its own and no barrier but the
-// last; each CTA of k_glr_span then folds the aggregates of the spans before its
-// own.  Every association depends on the shape alone: the same bits every run.
+// The split.  An element costs about 54 instructions forward (49 without resets)
+// and 75 backward (two gates, a decay, a square root), so at 8 to 32 bytes an
+// element the issue slots are as scarce as the bytes, and the carry must not make
+// an element's gates be computed twice.  The time axis is cut into S spans; a CTA
+// owns one span of one channel strip and walks it through time, tile by tile, its
+// state in shared memory, so CTAs wait for nothing but their own loads.  Wide
+// problems have strips enough: S = 1 and one launch.  Narrow ones first run
+// k_glr_agg, which computes only the spans' aggregates (A, B) -- backward that takes
+// the decay and dh, two of the five inputs -- with every warp folding a run of its
+// own and no barrier but the last; each CTA of k_glr_span then folds the aggregates
+// of the spans before its own.  Every association depends on the shape alone: the
+// same bits every run.
+//
+// Measured (HBM copy 6.78 TB/s).  Forward bf16 8192 x 16 x 4096 with resets: 1016 us,
+// 4.2 TB/s, issue slots 74% busy over the launch (the strips do not divide evenly
+// over the SMs).  Backward bf16 65536 x 1 x 1024 with resets: 283 us = k_glr_agg 88 +
+// k_glr_span 186 (5.5 TB/s of what it moves) + the parameter sums 6; fp32
+// 2048 x 32 x 1024: 381 us, 5.6 TB/s.  On the scan's engine, tiles carried from CTA
+// to CTA, the same three took 1523, 667 and 391.
 #include "lr_act.cuh"
 #include "lr_launch.h"
 #include "lr_tma.cuh"
 
 #include <string.h>
 
+#include <algorithm>
 #include <type_traits>
 
 namespace lrs {
@@ -918,11 +927,21 @@ Geom span_geom(const GlrSpans& pl, int64_t T, int64_t C, int64_t D) {
 
 }  // namespace
 
-// The spans of a problem.  vec: the 16-byte path's pointers and D a multiple of
-// 4.  One span while the strips alone keep the GPU busy -- a quarter of the CTAs
-// that fit, forward, where the aggregates would read every input again; half of
-// them backward, where they read two of five -- else as many as fill it, of at
-// least two chunks each.
+// The spans of a problem.  vec: the 16-byte path's pointers and D a multiple of 4.
+//
+// One span while the strips alone keep the SMs busy, else the aggregates' pass,
+// which reads some inputs again, costs less than idle slots do.  Measured with
+// 2^27 elements, one span against the spans chosen here, us:
+//   strips        128        192        256        320        384
+//   bf16 fwd   635 / 420  500 / 415  378 / 412                296 / 399
+//   fp32 fwd   715 / 553  549 / 547  426 / 543                355 / 538
+//   bf16 bwd   881 / 484  698 / 488  534 / 473  522 / 479  445 / 474
+//   fp32 bwd   871 / 815  750 / 824  656 / 789  691 / 799  704 / 796
+// Cut: at first as many spans as make one CTA for every slot (7 an SM forward, 5
+// backward); where spans stay 32 tiles long, up to three times as many, which even
+// out the SMs (4096 channels of 32768 steps, bf16 451 -> 429 us forward, 532 -> 486
+// backward, fp32 902 -> 814; of 2048 steps, where a span would be three tiles, 35 ->
+// 39 forward, so not there).  At least two tiles a span.
 GlrSpans glr_spans(bool bwd, int dtype, bool vec, int64_t T, int64_t C) {
     GlrSpans p{};
     const int es = dtype == 1 ? 2 : 4;
@@ -933,11 +952,12 @@ GlrSpans glr_spans(bool bwd, int dtype, bool vec, int64_t T, int64_t C) {
     p.n_chunks = (T + p.rows - 1) / p.rows;
     p.n_ct = (C + cw - 1) / cw;
     const int64_t slots = (bwd ? 5 : 7) * (int64_t)kSpanSms;
+    // strips an SM, in quarters, from which one span is faster
+    const int64_t enough = dtype == 1 ? (bwd ? 9 : 6) : (bwd ? 4 : 5);
     p.S = 1;
-    if (p.n_ct < slots / (bwd ? 2 : 4)) {
-        p.S = slots / p.n_ct;
-        if (p.S > p.n_chunks / 2) p.S = p.n_chunks / 2;
-        if (p.S < 1) p.S = 1;
+    if (4 * p.n_ct < enough * kSpanSms) {
+        p.S = std::max(slots / p.n_ct, std::min(3 * slots / p.n_ct, p.n_chunks / 32));
+        p.S = std::max<int64_t>(std::min(p.S, p.n_chunks / 2), 1);
     }
     p.cps = (p.n_chunks + p.S - 1) / p.S;
     p.S = (p.n_chunks + p.cps - 1) / p.cps;

@@ -23,6 +23,13 @@
 //
 // No floating-point atomics: sums over parts of the k loop are stored as parts and
 // added in order.
+//
+// Measured (cuBLAS bf16 1.92 PFLOP/s in a burst, 1.71 sustained).  bf16 8192 x 1024,
+// V 65536, loss and gradients: 2.71 to 2.97 ms over boxes (power capped), 1.62 to
+// 1.48 PFLOP/s over the 8 N V D; in one such call logits 666 us, their gradient 690,
+// dx 623, dW 671, the rest 49.  Loss alone, 4096 x 4096, V 131072: 2.57 to 2.78 ms,
+// 1.71 to 1.58 PFLOP/s.  fp32 509 x 250, V 10007: 110 us in nine launches, the
+// largest 33, none of which fills the GPU for long.
 #include <algorithm>
 #include <utility>
 
@@ -559,7 +566,9 @@ cudaError_t mm_run(const Operand& a, const Operand& b, const Shape& sh, Epi epi,
 // about 512 cycles, by 128 about 300, by 64 about 190: A comes from L2 more often)
 // plus about 1500 cycles of latency, plus, with more than one part, the parts' way
 // to memory and back (about 3.5 KB a cycle over the GPU).  With few tiles narrow ones
-// and parts fill the GPU; with many, parts even out its last round.
+// and parts fill the GPU; with many, parts even out its last round.  (fp32 509 x 250,
+// V 10007, loss and gradients: 195 us with 256-column tiles only, 160 with the
+// choice between 256 and 128, before the other steps.)
 MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int planes, bool may_split) {
     const int64_t kb = (K + mm::kBlockK - 1) / mm::kBlockK, pairs = kSpanSms / 2;
     MmPlan best{256, 1};

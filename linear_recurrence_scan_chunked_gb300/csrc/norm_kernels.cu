@@ -16,6 +16,10 @@
 // are persistent over the rows, which keeps w and b, and backward the columns'
 // partial sums, in registers; backward each CTA leaves one row of partial sums
 // and a second kernel adds them in a fixed order (bitwise reproducible).
+//
+// Bytes bound it where rows are aligned: bf16 131072 x 4096 with the residual 670 us,
+// 6.4 TB/s (copy 6.78).  Odd rows are read an element at a time and issue bounds
+// them: fp32 30011 x 1111 backward 82 us, 4.9 TB/s.
 #include "lr_launch.h"
 
 #include <type_traits>

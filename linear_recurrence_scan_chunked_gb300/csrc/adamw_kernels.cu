@@ -23,7 +23,7 @@
 // arguments (no copy to the device, nothing to keep for a graph); a CTA finds
 // its tensor by binary search over the chunk counts.  Measured: 128M elements in
 // 160 tensors, bf16 gradients and copies, 546 us = 6.9 TB/s (copy 6.78); 8-bit
-// moments, 64M elements in 90 tensors, fp32 gradients, 209 us = 5.1 TB/s, and their
+// moments, 64M elements in 90 tensors, fp32 gradients, 197 us = 5.5 TB/s, and their
 // values written out 100 us = 6.7 TB/s.
 #include "lr_act.cuh"
 #include "lr_launch.h"
@@ -115,12 +115,12 @@ __device__ __forceinline__ uint32_t adam_hash(uint32_t i, uint32_t key) {
 // Small integers as floats and back without the conversion instructions, which
 // issue at a quarter of the rate of the others and were what bound this kernel: a
 // byte b under the exponent of 2^23 is the float 2^23 + b; 16 bits under that of
-// 1 are 1 + u / 2^16; and adding 2^23 rounding towards zero leaves floor(x) in the
+// 1 are 1 + u / 2^16 (unit16); and adding 2^23 rounding towards zero leaves floor(x) in the
 // low bits of the sum (0 <= x < 2^23).
 __device__ __forceinline__ float byte_float(uint32_t w, int k, float bias) {
     return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u + (uint32_t)k)) - bias;
 }
-__device__ __forceinline__ float unit16(uint32_t u16) { return __uint_as_float(0x3F800000u | u16 << 7) - 1.f; }
+__device__ __forceinline__ float unit16(uint32_t u16) { return __uint_as_float(0x3F800000u | u16 << 7); }
 
 // A sum of pairs, each of its terms rounded by itself: the compiler fuses
 // mul.rn.f32x2 into an add.f32x2 that follows (seen in the results), so the
@@ -172,15 +172,29 @@ __device__ __forceinline__ void adam8_fetch(const AdamTensor& t, int64_t blk, A8
     }
 }
 
-// With F = 2^23 + floor(x), x + (kHalfPast - F) is the fraction of x less 1/2, exactly.
-constexpr float kHalfPast = 8388607.5f;
+// With F = 2^23 + floor(x - 1), x + (kHalfPast - F) is the fraction of x less 1/2,
+// exactly.
+constexpr float kHalfPast = 8388606.5f;
+
+// The low byte of each of four floats, and 0xFF for each that is negative.
+__device__ __forceinline__ uint32_t low_bytes(const float* f) {
+    const uint32_t lo = __byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040);
+    return __byte_perm(lo, __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040), 0x5410);
+}
+__device__ __forceinline__ uint32_t sign_bytes(const float* f) {
+    uint32_t lo, hi;  // selector nibbles B and F: the sign of byte 3 of either word, eight times
+    asm("prmt.b32 %0, %1, %2, 0x00FB;" : "=r"(lo) : "r"(__float_as_uint(f[0])), "r"(__float_as_uint(f[1])));
+    asm("prmt.b32 %0, %1, %2, 0x00FB;" : "=r"(hi) : "r"(__float_as_uint(f[2])), "r"(__float_as_uint(f[3])));
+    return __byte_perm(lo, hi, 0x5410);
+}
 
 // One warp per block of 256 elements, four consecutive ones of each half a lane,
-// worked on in pairs.  About 92 instructions an element (110 with IEEE roots
-// throughout) and whole sectors in every access: eight consecutive elements a
-// lane, two accesses to each sector, took 290 us for 64M elements where this
-// takes 209 (5.1 TB/s).  64 registers, four CTAs an SM (three: 239 us); chunks of
-// 8192 took 224 us, of 16384 216, shares of one grid that fills the GPU once 310.
+// worked on in pairs.  About 97 instructions an element (131 with IEEE roots and
+// codes put together one by one), issue slots 83% busy.  What it took for 64M
+// elements, fp32 gradients: eight consecutive elements a lane, two accesses to every
+// sector, 290 us; this layout 239 with three CTAs an SM, 224 with four (64 registers;
+// five spill: 269); chunks of 4096 209 (of 16384 216, of 32768 227, shares of one grid
+// that fills the GPU once slower still); the codes packed by bytes 197, 5.5 TB/s.
 template <typename G>
 __device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, const A8Stage<G>& st, float sm, float sv,
                                             const AdamHyper& h, float gs, uint32_t key) {
@@ -241,43 +255,50 @@ __device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, co
     const float im = tm > 0.f ? __fdiv_rn(1.f, tm) : 0.f, iv = tv > 0.f ? __fdiv_rn(1.f, tv) : 0.f;
     // sqrt(v) = sqrt(v / scale) sqrt(scale): the first root is the code's too
     const float rv = sqrtf(tv) * h.rk2;
-    uint32_t qm[2] = {0u, 0u}, qv[2] = {0u, 0u};
+    uint32_t qm[2], qv[2];
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-        float rm[2], r2[2], root[2], a[2], b[2], um[2], uv[2], fa[2], fb[2], da[2], db[2];
-        f2_get(f2_mul(f2(fabsf(m[k]), fabsf(m[k + 1])), f2(im)), rm[0], rm[1]);
-        f2_get(f2_mul(f2(v[k], v[k + 1]), f2(iv)), r2[0], r2[1]);
+    for (int h4 = 0; h4 < 2; ++h4) {
+        float fa[4], fb[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t u = adam_hash((uint32_t)(i0 + (k >> 2) * 128 + (k & 3) + e), key);
-            um[e] = unit16(u >> 16);
-            uv[e] = unit16(u & 0xffffu);
-            a[e] = fmaf(sqrt_ftz(rm[e]), 127.f, um[e]);
-            root[e] = sqrt_ftz(r2[e]);
-            b[e] = fmaf(sqrt_ftz(root[e]), 255.f, uv[e]);
-            fa[e] = __fadd_rz(a[e], 8388608.f);
-            fb[e] = __fadd_rz(b[e], 8388608.f);
-        }
-        f2_get(f2_add(f2(a[0], a[1]), f2_add(f2(kHalfPast), f2(-fa[0], -fa[1]))), da[0], da[1]);
-        f2_get(f2_add(f2(b[0], b[1]), f2_add(f2(kHalfPast), f2(-fb[0], -fb[1]))), db[0], db[1]);
+        for (int j = 0; j < 4; j += 2) {
+            const int k = 4 * h4 + j;
+            float rm[2], r2[2], root[2], a[2], b[2], um[2], uv[2], da[2], db[2];
+            f2_get(f2_mul(f2(v[k], v[k + 1]), f2(iv)), r2[0], r2[1]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            // The roots are good to a few 2^-23: a and b to 5e-5 and 1.2e-4.  Where that
-            // does not settle the code (or v / scale is subnormal: flushed; or NaN), in
-            // about one element of 1500, the IEEE roots do.
-            if (!(fabsf(da[e]) < 0.5f - 1e-4f && fabsf(db[e]) < 0.5f - 2e-4f && r2[e] >= 1.17549435e-38f)) {
-                root[e] = __fsqrt_rn(r2[e]);
-                fa[e] = __fadd_rz(__fadd_rn(__fmul_rn(__fsqrt_rn(rm[e]), 127.f), um[e]), 8388608.f);
-                fb[e] = __fadd_rz(__fadd_rn(__fmul_rn(__fsqrt_rn(root[e]), 255.f), uv[e]), 8388608.f);
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t u = adam_hash((uint32_t)(i0 + h4 * 128 + j + e), key);
+                um[e] = unit16(u >> 16);
+                uv[e] = unit16(u & 0xffffu);
+                rm[e] = __fmul_rn(fabsf(m[k + e]), im);
+                root[e] = sqrt_ftz(r2[e]);
+                a[e] = fmaf(sqrt_ftz(rm[e]), 127.f, um[e]);  // one more than the code's sum
+                b[e] = fmaf(sqrt_ftz(root[e]), 255.f, uv[e]);
+                fa[j + e] = __fadd_rz(a[e], 8388607.f);
+                fb[j + e] = __fadd_rz(b[e], 8388607.f);
             }
-            p[k + e] = fmaf(-h.step, __fdividef(m[k + e], fmaf(root[e], rv, h.eps)), h.decay * p[k + e]);
-            int q = (int)min(__float_as_uint(fa[e]) & 0x3ffu, 127u);
-            q = m[k + e] < 0.f ? -q : q;
-            uint32_t w = min(__float_as_uint(fb[e]) & 0x3ffu, 255u);
-            if (w == 0u && v[k + e] > 0.f) w = 1u;
-            qm[k >> 2] |= ((uint32_t)q & 255u) << (8 * ((k + e) & 3));
-            qv[k >> 2] |= w << (8 * ((k + e) & 3));
+            f2_get(f2_add(f2(a[0], a[1]), f2_add(f2(kHalfPast), f2(-fa[j], -fa[j + 1]))), da[0], da[1]);
+            f2_get(f2_add(f2(b[0], b[1]), f2_add(f2(kHalfPast), f2(-fb[j], -fb[j + 1]))), db[0], db[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // The roots are good to a few 2^-23: a and b to 6e-5 and 1.4e-4.  Where
+                // that does not settle the code (or v / scale is subnormal: flushed; or
+                // NaN), in about one element of 1500, the IEEE roots do.
+                if (!(fabsf(da[e]) < 0.5f - 1e-4f && fabsf(db[e]) < 0.5f - 2e-4f && r2[e] >= 1.17549435e-38f)) {
+                    root[e] = __fsqrt_rn(r2[e]);
+                    const float x = __fadd_rn(__fmul_rn(__fsqrt_rn(rm[e]), 127.f), um[e] - 1.f);
+                    const float y = __fadd_rn(__fmul_rn(__fsqrt_rn(root[e]), 255.f), uv[e] - 1.f);
+                    fa[j + e] = fminf(__fadd_rz(x, 8388608.f), 8388608.f + 127.f);
+                    fb[j + e] = fminf(__fadd_rz(y, 8388608.f), 8388608.f + 255.f);
+                }
+                if (v[k + e] > 0.f) fb[j + e] = fmaxf(fb[j + e], 8388609.f);
+                p[k + e] = fmaf(-h.step, __fdividef(m[k + e], fmaf(root[e], rv, h.eps)), h.decay * p[k + e]);
+            }
         }
+        // the four codes of each: the floats' low bytes, m's with its sign (bytes that
+        // are biased by 128 stay positive, so the sums below carry nothing over)
+        const uint32_t mag = low_bytes(fa), neg = sign_bytes(m + 4 * h4);
+        qm[h4] = (0x80808080u + (mag & ~neg) - (mag & neg)) ^ 0x80808080u;
+        qv[h4] = low_bytes(fb);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {

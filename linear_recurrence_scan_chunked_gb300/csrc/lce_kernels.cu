@@ -352,16 +352,22 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int j = 0; j < W; ++j) s[j] = 0.f;
             if (i < count) {
-                for (int64_t k = k0; k < k1; k += 8) {  // eight loads in flight, added in order
+                int64_t k = k0;
+                for (; k + 8 <= k1; k += 8) {  // eight loads in flight, added in order
                     Pack<float, W> p[8];
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        if (k + u < k1) p[u].load(part + (k + u) * pitch + base + W * i);
-                        else p[u].ident(0.f);
+                    for (int u = 0; u < 8; ++u) p[u].load(part + (k + u) * pitch + base + W * i);
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
 #pragma unroll
                         for (int j = 0; j < W; ++j) s[j] += p[u].get(j);
+                }
+#pragma unroll 4
+                for (; k < k1; ++k) {
+                    Pack<float, W> p;
+                    p.load(part + k * pitch + base + W * i);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) s[j] += p.get(j);
                 }
             }
             if constexpr (GROUPS > 1) {

@@ -19,7 +19,7 @@
 //
 // Bytes bound it where rows are aligned: bf16 131072 x 4096 with the residual 670 us,
 // 6.4 TB/s (copy 6.78).  Odd rows are read an element at a time and issue bounds
-// them: fp32 30011 x 1111 backward 82 us, 4.9 TB/s.
+// them: fp32 30011 x 1111 backward 79 us, 5.1 TB/s.
 #include "lr_launch.h"
 
 #include <type_traits>
@@ -353,14 +353,18 @@ __global__ void __launch_bounds__(1024)
     const float* p = partials + (int64_t)blockIdx.y * G * D + d;
     float acc = 0.f;
     griddep_wait();
-    if (d < D)
-        for (int k0 = threadIdx.y; k0 < G; k0 += 256) {  // eight loads in flight, added in order
+    if (d < D) {
+        int k = threadIdx.y;
+        for (; k + 224 < G; k += 256) {  // eight loads in flight, added in order
             float v[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = k0 + 32 * u < G ? __ldg(p + (int64_t)(k0 + 32 * u) * D) : 0.f;
+            for (int u = 0; u < 8; ++u) v[u] = __ldg(p + (int64_t)(k + 32 * u) * D);
 #pragma unroll
             for (int u = 0; u < 8; ++u) acc += v[u];
         }
+#pragma unroll 4
+        for (; k < G; k += 32) acc += __ldg(p + (int64_t)k * D);
+    }
     part[threadIdx.y][threadIdx.x] = acc;
     __syncthreads();
     // transposed: warp j sums column j's 32 lanes

@@ -31,8 +31,8 @@
 //
 // Measured (HBM copy 6.78 TB/s).  Forward bf16 8192 x 16 x 4096 with resets: 1016 us,
 // 4.2 TB/s, issue slots 74% busy over the launch (the strips do not divide evenly
-// over the SMs).  Backward bf16 65536 x 1 x 1024 with resets: 283 us = k_glr_agg 88 +
-// k_glr_span 186 (5.5 TB/s of what it moves) + the parameter sums 6; fp32
+// over the SMs).  Backward bf16 65536 x 1 x 1024 with resets: 284 us = k_glr_agg 86 +
+// k_glr_span 187 (5.5 TB/s of what it moves) + the parameter sums; fp32
 // 2048 x 32 x 1024: 381 us, 5.6 TB/s.  On the scan's engine, tiles carried from CTA
 // to CTA, the same three took 1523, 667 and 391.
 #include "lr_act.cuh"

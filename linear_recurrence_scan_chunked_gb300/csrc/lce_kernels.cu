@@ -28,7 +28,7 @@
 // V 65536, loss and gradients: 2.71 to 2.97 ms over boxes (power capped), 1.62 to
 // 1.48 PFLOP/s over the 8 N V D; in one such call logits 666 us, their gradient 690,
 // dx 623, dW 671, the rest 49.  Loss alone, 4096 x 4096, V 131072: 2.57 to 2.78 ms,
-// 1.71 to 1.58 PFLOP/s.  fp32 509 x 250, V 10007: 110 us in nine launches, the
+// 1.71 to 1.58 PFLOP/s.  fp32 509 x 250, V 10007: 110 us in eight launches, the
 // largest 33, none of which fills the GPU for long.
 #include <algorithm>
 #include <utility>
@@ -171,8 +171,18 @@ __global__ void __launch_bounds__(1024)
         s = s * (M == m ? 1.f : ex2_ftz(M - m)) + p.y * (p.x == m ? 1.f : ex2_ftz(p.x - m));
         M = m;
     };
-    if (n < rows)
-        for (int64_t k = threadIdx.y; k < tiles; k += 32) fold(__ldg(part + k * rows + n));
+    if (n < rows) {
+        int64_t k = threadIdx.y;
+        for (; k + 224 < tiles; k += 256) {  // eight loads in flight
+            float2 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = __ldg(part + (k + 32 * u) * rows + n);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) fold(v[u]);
+        }
+#pragma unroll 4
+        for (; k < tiles; k += 32) fold(__ldg(part + k * rows + n));
+    }
     sm[threadIdx.y][threadIdx.x] = make_float2(M, s);
     __syncthreads();
     if (threadIdx.y != 0 || n >= rows) return;
@@ -403,14 +413,17 @@ struct PackJob {
     const void* src;
     __nv_bfloat16* dst;
     int64_t rows, D, ld;
-    bool quads;  // rows can be read four elements at a time
+    int vec;  // elements that can be read at once: 4, 2 or 1
 };
 
 // Before the products, one launch: block 0 takes max |dloss| over the rows that
 // count (finite ones) into `top`, as float bits; the other blocks pack x and W --
 // fp32 data split into three planes, bf16 data whose rows TMA cannot read (odd
-// widths, unaligned views) copied.  A warp takes a row, four elements a lane.
-template <typename S, int P>
+// widths, unaligned views) copied.  A warp takes a row, four elements a lane; LONG
+// rows (from 512 elements) four times four, whose loads are in flight together
+// (bf16 9928 x 2074: 25 -> 16 us; shorter rows pay for the registers: fp32
+// 62522 x 261 28 -> 33 us).
+template <typename S, int P, bool LONG>
 __global__ void __launch_bounds__(256)
     k_lce_prep(const PackJob jx, const PackJob jw, const float* __restrict__ dloss, const int64_t* __restrict__ target,
                int64_t ignore, int64_t N, int64_t V, uint32_t* __restrict__ top) {
@@ -451,13 +464,44 @@ __global__ void __launch_bounds__(256)
         const S* src = (const S*)j.src + r * j.D;
         __nv_bfloat16* dst = j.dst + r * j.ld;
         const int64_t plane = j.rows * j.ld;
-        for (int64_t d = lane * 4; d < j.D; d += 128) {
-            float v[4];
-            if (j.quads) {
-                Pack<S, 4> p;
-                p.load(src + d);
+        // rows are padded to 8: 8-byte stores stay inside
+        auto put = [&](int64_t d, float (&v)[4]) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = p.get(i);
+            for (int k = 0; k < P; ++k) {
+                const uint32_t a = bf_pack(v[0], v[1]), b = bf_pack(v[2], v[3]);
+                *reinterpret_cast<uint2*>(dst + k * plane + d) = make_uint2(a, b);
+                v[0] -= bf_lo(a); v[1] -= bf_hi(a); v[2] -= bf_lo(b); v[3] -= bf_hi(b);
+            }
+        };
+        auto get = [&](auto width, int64_t d, float (&v)[4]) {
+            constexpr int W = decltype(width)::value;
+#pragma unroll
+            for (int i = 0; i < 4; i += W) {
+                Pack<S, W> p;
+                p.load(src + d + i);
+#pragma unroll
+                for (int k = 0; k < W; ++k) v[i + k] = p.get(k);
+            }
+        };
+        int64_t d = lane * 4;
+        if constexpr (LONG) {
+            auto bulk = [&](auto width) {  // four quads in flight
+                for (; d + 384 + 4 <= j.D; d += 512) {
+                    float v[4][4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) get(width, d + 128 * q, v[q]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) put(d + 128 * q, v[q]);
+                }
+            };
+            if (j.vec == 4) bulk(std::integral_constant<int, 4>{});
+            else if (j.vec == 2) bulk(std::integral_constant<int, 2>{});
+            else bulk(std::integral_constant<int, 1>{});
+        }
+        for (; d < j.D; d += 128) {
+            float v[4];
+            if (j.vec == 4) {
+                get(std::integral_constant<int, 4>{}, d, v);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -467,12 +511,7 @@ __global__ void __launch_bounds__(256)
                     v[i] = p.get(0);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < P; ++k) {  // rows are padded to 8: 8-byte stores stay inside
-                const uint32_t a = bf_pack(v[0], v[1]), b = bf_pack(v[2], v[3]);
-                *reinterpret_cast<uint2*>(dst + k * plane + d) = make_uint2(a, b);
-                v[0] -= bf_lo(a); v[1] -= bf_hi(a); v[2] -= bf_lo(b); v[3] -= bf_hi(b);
-            }
+            put(d, v);
         }
     }
 }
@@ -634,10 +673,12 @@ Layout layout(int dtype, const void* x, const void* w, int64_t N, int64_t V, int
 template <typename S>
 Operand operand(const void* src, int64_t rows, int64_t D, void* scratch, PackJob* job) {
     constexpr int P = sizeof(S) == 4 ? 3 : 1;
-    *job = PackJob{nullptr, nullptr, 0, 0, 0, false};
+    *job = PackJob{nullptr, nullptr, 0, 0, 0, 1};
     if (!packed(sizeof(S) == 4 ? 0 : 1, src, D)) return Operand{(const __nv_bfloat16*)src, rows, D, D, rows * D, P};
     const int64_t ld = round_up(D, 8);
-    *job = PackJob{src, (__nv_bfloat16*)scratch, rows, D, ld, D % 4 == 0 && ((uintptr_t)src & (4 * sizeof(S) - 1)) == 0};
+    int vec = 4;
+    while (vec > 1 && (D % vec != 0 || ((uintptr_t)src & (vec * sizeof(S) - 1)) != 0)) vec /= 2;
+    *job = PackJob{src, (__nv_bfloat16*)scratch, rows, D, ld, vec};
     return Operand{(const __nv_bfloat16*)scratch, rows, D, ld, rows * ld, P};
 }
 
@@ -647,8 +688,10 @@ cudaError_t prepare(const PackJob& jx, const PackJob& jw, const float* dloss, co
     const int64_t rows = jx.rows + jw.rows;
     if (rows == 0 && top == nullptr) return cudaSuccess;
     const int64_t blocks = 1 + std::min<int64_t>((rows + 7) / 8, (int64_t)sm_count() * 8);
-    return launch_dep(k_lce_prep<S, sizeof(S) == 4 ? 3 : 1>, dim3((unsigned)blocks), dim3(256), 0, s, jx, jw, dloss, target,
-                      ignore, N, V, top);
+    constexpr int P = sizeof(S) == 4 ? 3 : 1;
+    const bool wide = std::max(jx.D, jw.D) >= 512;
+    return launch_dep(wide ? k_lce_prep<S, P, true> : k_lce_prep<S, P, false>, dim3((unsigned)blocks), dim3(256), 0, s, jx, jw,
+                      dloss, target, ignore, N, V, top);
 }
 
 #define LCE_TRY(x)                            \

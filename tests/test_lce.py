@@ -74,7 +74,8 @@ def mx(got, want):
 # one of everything, exact tiles, one past and one short of them, odd widths (no 16-byte rows)
 SHAPES = [(1, 1, 1), (1, 2, 8), (2, 3, 5), (1, 1000, 64), (5, 257, 64), (128, 256, 64), (129, 255, 72), (64, 128, 128),
           (200, 1000, 250), (300, 513, 33), (256, 512, 256), (257, 777, 264), (130, 5000, 1000), (1, 20000, 136),
-          (1000, 130, 64), (513, 129, 1024), (40, 300, 4096), (31, 9000, 1023)]
+          (1000, 130, 64), (513, 129, 1024), (40, 300, 4096), (31, 9000, 1023), (9, 140, 514),
+          (33, 300, 1030), (20, 90, 516), (7, 65, 511), (6, 40, 2562)]
 
 
 @pytest.mark.gpu

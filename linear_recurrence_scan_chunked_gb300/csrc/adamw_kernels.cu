@@ -189,12 +189,12 @@ __device__ __forceinline__ uint32_t sign_bytes(const float* f) {
 }
 
 // One warp per block of 256 elements, four consecutive ones of each half a lane,
-// worked on in pairs.  About 97 instructions an element (131 with IEEE roots and
-// codes put together one by one), issue slots 83% busy.  What it took for 64M
-// elements, fp32 gradients: eight consecutive elements a lane, two accesses to every
-// sector, 290 us; this layout 239 with three CTAs an SM, 224 with four (64 registers;
-// five spill: 269); chunks of 4096 209 (of 16384 216, of 32768 227, shares of one grid
-// that fills the GPU once slower still); the codes packed by bytes 197, 5.5 TB/s.
+// worked on in pairs.  About 97 instructions an element (104 with the codes put
+// together one by one; IEEE roots throughout cost another 17), issue slots 83% busy.
+// What it took for 64M elements, fp32 gradients: eight consecutive elements a lane,
+// two accesses to every sector, 290 us; this layout 239 with three CTAs an SM, 224
+// with four (64 registers; five spill: 269); chunks of 4096 209 (of 16384 216, of
+// 32768 227); the codes packed by bytes 197, 5.5 TB/s.
 template <typename G>
 __device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, const A8Stage<G>& st, float sm, float sv,
                                             const AdamHyper& h, float gs, uint32_t key) {

@@ -202,10 +202,13 @@ __device__ __forceinline__ float scale_of(const uint32_t* top) {
     return s > 0.f ? s : 1.f;
 }
 
-// Backward: g / max|dloss| of a tile, in P bf16 planes.
-template <int P>
+// Backward: g / max|dloss| of a tile, in P bf16 planes.  Its logits are the forward
+// pass's to the last bit (the k loop in the same chunks): p - 1 of a confident row is
+// the difference of a logit and lse, which then are off by the same.  (One accumulator
+// over k = 4096 here, chunks there: a gradient at p = 0.999 came out 19% off.)
+template <bool CHUNKED, int P>
 struct GradEpi {
-    static constexpr bool kChunked = P > 1, kStaged = false;
+    static constexpr bool kChunked = CHUNKED, kStaged = false;
     static constexpr int kPlanes = P;
     __nv_bfloat16* g;  // [P][rows][pitch]
     int64_t pitch;     // a multiple of 16
@@ -762,8 +765,13 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
         wp.p += v0 * ow.ld;
         wp.rows = vc;
         const Operand og{g, N, vc, pitch, N * pitch, P};
-        LCE_TRY(mm_run(ox, wp, mm_shape(N, vc, D, false, false, false, MmPlan{pl.tn_logits, 1}),
-                       GradEpi<P>{g, pitch, N * pitch, lse, dloss, target, top, ignore, N, v0, vc, V, 0}, pl.tn_logits, err, s));
+        const Shape sl = mm_shape(N, vc, D, false, false, false, MmPlan{pl.tn_logits, 1});
+        auto logits = [&](auto chunked) {
+            return mm_run(ox, wp, sl,
+                          GradEpi<decltype(chunked)::value, P>{g, pitch, N * pitch, lse, dloss, target, top, ignore, N, v0, vc, V, 0},
+                          pl.tn_logits, err, s);
+        };
+        LCE_TRY(sl.kb > mm::chunk_of(P) ? logits(std::true_type{}) : logits(std::false_type{}));
         // dx: rows of x by features, over the words of the piece
         const Shape sx = mm_shape(N, D, vc, false, true, true, MmPlan{pl.tn_dx, pl.dx_splits});
         const bool dx_direct = pl.dx_parts == 1;

@@ -327,3 +327,25 @@ def test_refusals_on_device_tensors(cuda):
                  lambda: cuda.lce_bwd(x, w, t, dl, dl, dx=x.bfloat16())):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [1024, 4096, 16384])
+def test_confident_rows_at_long_widths(cuda, D):
+    """bf16, the target's p about 0.999 and its logit a sum of thousands of terms of one
+    sign, which the tensor cores shrink: loss and gradients of the two passes together
+    against fp64.  p - 1 takes the difference of the backward pass's logit and the
+    forward pass's lse, so both have to be off by the same."""
+    N, V = 32, 300
+    g = torch.Generator().manual_seed(17)
+    w = torch.randn(V, D, generator=g).to(torch.bfloat16)  # words nearly orthogonal
+    t = torch.arange(N) % V
+    x = (12.6 * w[t].float() / w[t].float().square().sum(1, keepdim=True)).to(torch.bfloat16)
+    dl = torch.ones(N) / N
+    xd, wd, td = x.cuda(), w.cuda(), t.cuda()
+    loss, lse = cuda.lce_fwd(xd, wd, td)
+    rl, rz, rdx, rdw = ref(x, w, t, dl)
+    assert mx(loss, rl) <= 1e-5 and mx(lse, rz) <= 1e-5
+    dx, dw = cuda.lce_bwd(xd, wd, td, lse, dl.cuda())
+    sx, sw = slack(x, w, t, dl, rdx, rdw)
+    assert dist(dx, rdx) <= GTOL["bf16"] + sx and dist(dw, rdw) <= GTOL["bf16"] + sw

@@ -46,6 +46,11 @@ using mm::Shape;
 using mm::Tile;
 
 constexpr int64_t kPieceBytes = (int64_t)2 << 30;  // g of one piece, all planes
+// k-blocks of a chunk of dx and dW, bf16 data.  8192 x 1024, V 65536, and the mean error
+// of dx over 131072 words whose terms have one sign: 16 2963 us, 32 2928 us and 8e-6,
+// 64 2916 us and 1.5e-5, one accumulator 2892 us and 7e-4 (the results' rounding: 1e-3
+// of each, but with either sign).
+constexpr uint32_t kSumChunk = 32;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // 32 bytes of a row (sm_100+: one sector in one store).
@@ -102,6 +107,7 @@ template <bool CHUNKED, int P>
 struct StatsEpi {
     static constexpr bool kChunked = CHUNKED, kStaged = false;
     static constexpr int kPlanes = P;
+    static constexpr uint32_t kChunk = mm::chunk_of(P);
     float2* part;           // [half tiles][rows]
     float* tl;              // the targets' logits
     const int64_t* target;
@@ -210,6 +216,7 @@ template <bool CHUNKED, int P>
 struct GradEpi {
     static constexpr bool kChunked = CHUNKED, kStaged = false;
     static constexpr int kPlanes = P;
+    static constexpr uint32_t kChunk = mm::chunk_of(P);
     __nv_bfloat16* g;  // [P][rows][pitch]
     int64_t pitch;     // a multiple of 16
     int64_t plane;     // elements of a plane
@@ -283,10 +290,11 @@ struct GradEpi {
 
 // A product's tile: rounded to the result (scaled by max|dloss|), or one part of
 // the k loop, fp32.
-template <typename S>
+template <bool CHUNKED, typename S>
 struct OutEpi {
-    static constexpr bool kChunked = sizeof(S) == 4, kStaged = true;
+    static constexpr bool kChunked = CHUNKED, kStaged = true;
     static constexpr int kPlanes = sizeof(S) == 4 ? 3 : 1;
+    static constexpr uint32_t kChunk = kPlanes == 1 ? kSumChunk : mm::chunk_of(kPlanes);
     S* out;         // nullptr: parts
     float* part;    // [splits][rows x cols]
     int64_t pitch;  // elements of a part
@@ -758,6 +766,7 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
     float* pw = (float*)(sc + l.pw);
     const int64_t xpitch = round_up(N * D, 8), wpitch = round_up(pl.piece * D, 8);
     const bool wide_s = D * (int64_t)sizeof(S) % 32 == 0, wide_f = D % 8 == 0;
+    const uint32_t sum_chunk = OutEpi<true, S>::kChunk;
     int64_t part = 0;
     for (int64_t v0 = 0; v0 < V; v0 += pl.piece) {
         const int64_t vc = std::min(pl.piece, V - v0), pitch = round_up(vc, 16);
@@ -775,19 +784,25 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
         // dx: rows of x by features, over the words of the piece
         const Shape sx = mm_shape(N, D, vc, false, true, true, MmPlan{pl.tn_dx, pl.dx_splits});
         const bool dx_direct = pl.dx_parts == 1;
-        LCE_TRY(mm_run(og, wp, sx,
-                       OutEpi<S>{dx_direct ? (S*)dx : nullptr, px + part * xpitch, xpitch, top, N, D, 0,
-                                 dx_direct ? wide_s && ((uintptr_t)dx & 31) == 0 : wide_f},
-                       pl.tn_dx, err, s));
+        auto dx_of = [&](auto chunked) {
+            return mm_run(og, wp, sx,
+                          OutEpi<decltype(chunked)::value, S>{dx_direct ? (S*)dx : nullptr, px + part * xpitch, xpitch, top, N,
+                                                              D, 0, dx_direct ? wide_s && ((uintptr_t)dx & 31) == 0 : wide_f},
+                          pl.tn_dx, err, s);
+        };
+        LCE_TRY(sx.kb_split > sum_chunk ? dx_of(std::true_type{}) : dx_of(std::false_type{}));
         part += sx.splits;
         // dw: words of the piece by features, over the rows of x
         const Shape sw = mm_shape(vc, D, N, true, true, true, MmPlan{pl.tn_dw, pl.dw_splits});
         const bool dw_direct = pl.dw_splits == 1;
         S* dwp = (S*)dw + v0 * D;
-        LCE_TRY(mm_run(og, ox, sw,
-                       OutEpi<S>{dw_direct ? dwp : nullptr, pw, wpitch, top, vc, D, 0,
-                                 dw_direct ? wide_s && ((uintptr_t)dwp & 31) == 0 : wide_f},
-                       pl.tn_dw, err, s));
+        auto dw_of = [&](auto chunked) {
+            return mm_run(og, ox, sw,
+                          OutEpi<decltype(chunked)::value, S>{dw_direct ? dwp : nullptr, pw, wpitch, top, vc, D, 0,
+                                                              dw_direct ? wide_s && ((uintptr_t)dwp & 31) == 0 : wide_f},
+                          pl.tn_dw, err, s);
+        };
+        LCE_TRY(sw.kb_split > sum_chunk ? dw_of(std::true_type{}) : dw_of(std::false_type{}));
         if (!dw_direct) LCE_TRY(sum_parts<S>(pw, sw.splits, wpitch, vc * D, top, dwp, s));
     }
     if (pl.dx_parts > 1) LCE_TRY(sum_parts<S>(px, part, xpitch, N * D, top, (S*)dx, s));

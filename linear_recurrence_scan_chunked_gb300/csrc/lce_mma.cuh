@@ -14,10 +14,10 @@
 // The tensor cores add into their fp32 accumulators by truncation: a step of 16 shrinks
 // a sum by about 5e-9 of itself where its terms have random signs (measured on the loss:
 // 1.3e-6 over k = 4096) and by 6e-8 to 9e-8 where they have one sign (a confident row's
-// logit: 1.5e-5 over k = 4096; a gradient over 131072 words: 7e-4).  Where the result is
-// fp32 or goes into an exponential, the loop is cut into chunks of kChunk
-// k-blocks whose accumulators the epilogue warps add up in registers, rounding to
-// nearest; where it is rounded to bf16 (2^-9) one accumulator does.
+// logit: 1.5e-5 over k = 4096; a gradient over 131072 words: 7e-4).  So the loop is cut
+// into chunks of k-blocks (kChunk for the logits of bf16 data, more for its gradients,
+// fewer for fp32) whose accumulators the epilogue warps add up in registers, rounding
+// to nearest.
 //
 // Operands are [rows][cols] matrices of bf16 planes: one plane for bf16 data,
 // three for fp32 data split as a = a1 + a2 + a3 (8 bits of mantissa each), whose
@@ -40,7 +40,7 @@ constexpr int kHalf = 128;       // rows of A that a CTA holds
 constexpr int kBlockK = 64;      // k-block: 128 bytes of bf16, the swizzle's width
 constexpr int kOperandA = kHalf * kBlockK * 2;  // 16 KB: A of a stage
 constexpr int kThreads = 320;    // producer warp, MMA warp, 8 epilogue warps
-constexpr uint32_t kChunk = 16;  // k-blocks of a chunk: k = 1024, a shrinkage of 3e-7 (fp32 planes: 2)
+constexpr uint32_t kChunk = 16;  // k-blocks of a chunk: k = 1024, 3e-7 of a logit of random signs (fp32 planes: 2)
 constexpr int kScratch = 32 * 33 * 4;  // bytes an epilogue warp may use
 
 template <int TN>
@@ -187,7 +187,7 @@ __device__ __forceinline__ uint32_t tile_steps(const Shape& s, const Tile& t) {
 }
 
 // Epilogue: a struct with
-//   kChunked                       sum the k loop in chunks
+//   kChunked, kChunk               sum the k loop in chunks, of so many k-blocks
 //   kStaged                        cols() uses the warp's scratch
 //   kPlanes                        planes of the operands: 1, or 3 (six products a k-block)
 //   Row                            what a thread keeps of its row of a tile
@@ -286,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t it = 0, seq = 0;
             for (uint32_t t = pair; t < n_tiles && ok; t += n_pairs) {
                 const uint32_t steps = tile_steps(sh, tile_of(sh, t));
-                const uint32_t chunk = Epi::kChunked ? chunk_of(kPlanes) : steps;
+                const uint32_t chunk = Epi::kChunked ? Epi::kChunk : steps;
                 for (uint32_t c0 = 0; c0 < steps && ok; c0 += chunk, ++seq) {
                     const uint32_t buf = seq & 1;
                     if (seq >= 2 && !wait_cluster(&tempty[buf], (seq / 2 - 1) & 1, err)) {
@@ -346,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Tile tl = tile_of(sh, t);
             const int width = epi.width(tl, half);
             if constexpr (Epi::kChunked) {
-                const uint32_t chunks = (tile_steps(sh, tl) + chunk_of(kPlanes) - 1) / chunk_of(kPlanes);
+                const uint32_t chunks = (tile_steps(sh, tl) + Epi::kChunk - 1) / Epi::kChunk;
                 float acc[C::kHalfN];
 #pragma unroll
                 for (int i = 0; i < C::kHalfN; ++i) acc[i] = 0.f;

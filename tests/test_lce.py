@@ -349,3 +349,28 @@ def test_confident_rows_at_long_widths(cuda, D):
     dx, dw = cuda.lce_bwd(xd, wd, td, lse, dl.cuda())
     sx, sw = slack(x, w, t, dl, rdx, rdw)
     assert dist(dx, rdx) <= GTOL["bf16"] + sx and dist(dw, rdw) <= GTOL["bf16"] + sw
+
+
+@pytest.mark.gpu
+def test_long_sums_do_not_shrink(cuda):
+    """bf16 gradients over a k loop of 131072 terms of one sign: the mean relative
+    error over the 5 million results, whose roundings average out (2^-9 / sqrt(3) /
+    sqrt(5e6) = 5e-7; g's roundings are independent as well), stays below 1e-5."""
+    N, V, D = 4864, 131072, 1024
+    g = torch.Generator(device="cuda").manual_seed(18)
+    x = (0.02 * torch.randn(N, D, device="cuda", generator=g)).bfloat16()
+    w = torch.rand(V, D, device="cuda", generator=g).bfloat16()
+    t = torch.zeros(N, dtype=torch.int64, device="cuda")
+    w[0] = 0
+    dl = torch.full((N,), 1.0 / N, device="cuda")
+    _, lse = cuda.lce_fwd(x, w, t)
+    dx, _ = cuda.lce_bwd(x, w, t, lse, dl)
+    off = n = 0.0
+    wd = w.double()
+    for r in range(0, N, 608):
+        p = torch.exp(x[r:r + 608].double() @ wd.T - lse[r:r + 608].double()[:, None])
+        want = (p @ wd) / N  # the target's word is 0
+        off += float((dx[r:r + 608].double() - want).sum())
+        n += float(want.sum())
+    print("bias", off / n)
+    assert abs(off / n) <= 1e-5

@@ -598,6 +598,15 @@ int lr_test_fail_after_enqueue(float* x, int64_t n, float value, uint64_t sleep_
                                void* stream);
 
 /*
+ * Test hook for the choice between the vector and the element path of the AdamW
+ * calls: 1 when a tensor at these addresses takes vector accesses.  kind: 0
+ * adamw_step, 1 adamw8_step, 2 adamw8_values (p and g: where m's values go, m and
+ * v: the codes, copy: where v's values go); copy may be NULL.  No device needed.
+ */
+int lr_test_adamw_vec(int kind, int gdtype, const void* p, const void* g, const void* m, const void* v,
+                      const void* copy);
+
+/*
  * Test hook for the activations of the fused kernels: tanh_out[i] = tanh(x[i]),
  * sigmoid_out[i] = 1 / (1 + exp(-x[i])) and expm1_out[i] = exp(x[i]) - 1 as the
  * SRU, LSTM and DEER kernels evaluate them (tanh and sigmoid in exponential

@@ -86,6 +86,7 @@ def load():
     lib.lr_test_activations.argtypes = [P, P, P, P, I64, P]
     lib.lr_test_fail_after_enqueue.argtypes = [P, I64, ctypes.c_float, ctypes.c_uint64, P]
     lib.lr_test_fail_after_enqueue.restype = I
+    lib.lr_test_adamw_vec.argtypes = [I, I] + [P] * 5
     lib.lr_plan_info.argtypes = [I, I, I, I64, I64, P, P, P, P]
     lib.lr_plan_info.restype = I
     for f in ("lr_scan_fwd", "lr_scan_bwd", "sru_fwd", "sru_bwd", "deer_diag_solve", "deer_diag_bwd",

@@ -725,10 +725,20 @@ static int adamw_hyper(int64_t step, double lr, double beta1, double beta2, doub
     return LR_OK;
 }
 
+// The tensor's accesses are vectors of four elements: weights 16 bytes, gradients four
+// of their type, fp32 moments 16 bytes and codes four, copies 8 bytes; for the values
+// of the codes, p and copy are where the fp32 moments go, 16 bytes each.
+static bool adamw_vec(AdamKind kind, int gdtype, const void* p, const void* g, const void* m, const void* v,
+                      const void* copy) {
+    const size_t sa = kind == ADAM_32BIT ? 16 : 4, ca = kind == ADAM_VALUES ? 16 : 8;
+    return aligned(p, 16) && aligned(g, 4 * esize(gdtype)) && aligned(m, sa) && aligned(v, sa) && aligned(copy, ca);
+}
+
 // Collects the tensors of a call and checks their pointers.
 static int adamw_tensors(std::vector<AdamTensor>& out, int64_t n_tensors, const int64_t* n, float* const* p,
                          const void* const* g, void* const* m, void* const* v, float* const* ms,
-                         float* const* vs, void* const* copies, int gdtype, bool eight) {
+                         float* const* vs, void* const* copies, int gdtype, AdamKind kind) {
+    const bool eight = kind != ADAM_32BIT;
     if (gdtype != LR_F32 && gdtype != LR_BF16) return LR_ERR_INVALID_ARG;
     if (n_tensors < 0) return LR_ERR_INVALID_ARG;
     if (n_tensors == 0) return LR_OK;
@@ -752,8 +762,7 @@ static int adamw_tensors(std::vector<AdamTensor>& out, int64_t n_tensors, const 
         if (!aligned(t.p, 4) || !aligned(t.g, ges) || !aligned(t.copy, 2) || !aligned(t.ms, 4) || !aligned(t.vs, 4))
             return LR_ERR_ALIGN;
         if (!eight && (!aligned(t.m, 4) || !aligned(t.v, 4))) return LR_ERR_ALIGN;
-        const size_t sa = eight ? 4 : 16;
-        t.vec = aligned(t.p, 16) && aligned(t.g, 4 * ges) && aligned(t.m, sa) && aligned(t.v, sa) && aligned(t.copy, 8);
+        t.vec = adamw_vec(kind, gdtype, t.p, t.g, t.m, t.v, t.copy);
     }
     return LR_OK;
 }
@@ -767,7 +776,7 @@ int adamw_step(int64_t n_tensors, const int64_t* n, float* const* p, const void*
     if (!aligned(grad_scale, 4)) return LR_ERR_ALIGN;
     std::vector<AdamTensor> t;
     TRY(adamw_tensors(t, n_tensors, n, p, g, (void* const*)m, (void* const*)v, nullptr, nullptr, copies,
-                      gdtype, false));
+                      gdtype, ADAM_32BIT));
     CK(launch_adamw(ADAM_32BIT, gdtype, t.data(), n_tensors, h, grad_scale, 0, (cudaStream_t)stream));
     return LR_OK;
 }
@@ -780,7 +789,7 @@ int adamw8_step(int64_t n_tensors, const int64_t* n, float* const* p, const void
     TRY(adamw_hyper(step, lr, beta1, beta2, eps, weight_decay, &h));
     if (!aligned(grad_scale, 4)) return LR_ERR_ALIGN;
     std::vector<AdamTensor> t;
-    TRY(adamw_tensors(t, n_tensors, n, p, g, (void* const*)m, (void* const*)v, ms, vs, copies, gdtype, true));
+    TRY(adamw_tensors(t, n_tensors, n, p, g, (void* const*)m, (void* const*)v, ms, vs, copies, gdtype, ADAM_8BIT));
     CK(launch_adamw(ADAM_8BIT, gdtype, t.data(), n_tensors, h, grad_scale, seed, (cudaStream_t)stream));
     return LR_OK;
 }
@@ -791,7 +800,7 @@ int adamw8_values(int64_t n_tensors, const int64_t* n, const int8_t* const* mq, 
     std::vector<AdamTensor> t;
     // p: where m goes (also in g's place, which is not read), copy: where v goes
     TRY(adamw_tensors(t, n_tensors, n, m, (const void* const*)m, (void* const*)mq, (void* const*)vq,
-                      (float* const*)ms, (float* const*)vs, (void* const*)v, LR_F32, true));
+                      (float* const*)ms, (float* const*)vs, (void* const*)v, LR_F32, ADAM_VALUES));
     for (AdamTensor& x : t)
         if (x.n > 0 && !aligned(x.copy, 4)) return LR_ERR_ALIGN;
     CK(launch_adamw(ADAM_VALUES, LR_F32, t.data(), n_tensors, AdamHyper{}, nullptr, 0, (cudaStream_t)stream));
@@ -1261,6 +1270,11 @@ int lr_plan_info(int op, int dtype, int vec, int64_t T, int64_t C, int* protocol
     if (tile_rows) *tile_rows = cp.ts.L;
     if (n_chunks) *n_chunks = cp.n_chunks;
     return LR_OK;
+}
+
+int lr_test_adamw_vec(int kind, int gdtype, const void* p, const void* g, const void* m, const void* v,
+                      const void* copy) {
+    return adamw_vec((AdamKind)kind, gdtype, p, g, m, v, copy) ? 1 : 0;
 }
 
 int lr_test_fail_after_enqueue(float* x, int64_t n, float value, uint64_t sleep_ns, void* stream) {

@@ -253,3 +253,38 @@ def test_refusals_on_device_tensors(cuda):
             call()
     with pytest.raises(TypeError):
         cuda.adamw_step(t, h, t, t, step=1, lr=1e-3)
+
+
+def test_vector_path_needs_what_its_accesses_need():
+    """The element path wherever an address does not allow the widths that the kernels
+    access with: 16 bytes of fp32 weights, moments and of the values of both codes, 8
+    of bf16 gradients and copies, 4 of codes (CPU: fake addresses, no access)."""
+    lib, base = lrs.load(), 1 << 20
+    # kind, gradient type, bytes of (p, g, m, v, copy)
+    for kind, gd, need in ((0, 0, (16, 16, 16, 16, 8)), (0, 1, (16, 8, 16, 16, 8)), (1, 0, (16, 16, 4, 4, 8)),
+                           (1, 1, (16, 8, 4, 4, 8)), (2, 0, (16, 16, 4, 4, 16))):
+        assert lib.lr_test_adamw_vec(kind, gd, *[base] * 5) == 1
+        for at, bytes_ in enumerate(need):
+            for off in range(1, 16):
+                ptr = [base] * 5
+                ptr[at] += off
+                assert lib.lr_test_adamw_vec(kind, gd, *ptr) == (off % bytes_ == 0), (kind, gd, at, off)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("off", [0, 1, 2, 3])
+def test_values_into_views_at_any_offset(cuda, off, which):
+    """fp32 outputs of the codes' values at 4, 8 and 12 bytes past a vector's start."""
+    n = 1030
+    g = torch.Generator().manual_seed(6)
+    m = [torch.randint(-127, 128, (n,), dtype=torch.int8, generator=g).cuda()]
+    v = [torch.randint(0, 256, (n,), dtype=torch.uint8, generator=g).cuda()]
+    ms, vs = [torch.rand(5, generator=g).cuda()], [torch.rand(5, generator=g).cuda()]
+    want = cuda.adamw8_values(m, v, ms, vs)
+    buf = torch.zeros(n + 4, device="cuda")
+    out = [[torch.zeros(n, device="cuda")], [torch.zeros(n, device="cuda")]]
+    out[which] = [buf[off:off + n]]
+    got = cuda.adamw8_values(m, v, ms, vs, *out)
+    assert torch.equal(got[0][0], want[0][0]) and torch.equal(got[1][0], want[1][0])
+    assert not buf[:off].any() and not buf[off + n:].any()

@@ -463,7 +463,11 @@ int adamw_step(int64_t n_tensors, const int64_t* n, float* const* p, const void*
  *   m = scale sign(q) (q / 127)^2  (int8),   v = scale (q / 255)^4  (uint8).
  * Zero codes and scales are zero moments.  The new codes are rounded up or down
  * at random, right in the mean, by a hash of (element, tensor index, seed): give
- * another seed at every step.  A positive v keeps a positive code.
+ * another seed at every step.  A positive v keeps a positive code.  A scale below
+ * 2^-120 and its block are both scaled by 2^64 before the codes are taken (fp32 holds no
+ * reciprocal of one below 2^-128).  The weights are moved with the moments before they are
+ * rounded to codes.  An infinite or NaN gradient makes its own weight and the moments of
+ * its block of 256 non-finite, from the next step on that block's weights.
  */
 int adamw8_step(int64_t n_tensors, const int64_t* n, float* const* p, const void* const* g,
                 int8_t* const* m, uint8_t* const* v, float* const* ms, float* const* vs,

@@ -16,7 +16,9 @@
 // (element, tensor, seed): reproducible, and nothing is kept between calls.  A
 // positive v never becomes 0 (the step divides by its root).  The codes are
 // chosen with separately rounded IEEE operations (no contraction), so that they
-// are the same wherever they are computed.
+// are the same wherever they are computed.  Where a block's scale is below 2^-120 (fp32
+// holds no reciprocal below 2^-128), the block is taken times 2^64 first, which is
+// exact: a moment that fades, or a first gradient of 1e-20, keeps its zeros at zero.
 //
 // Bytes bound it: each element of p, g, m, v crosses HBM once each way.  A
 // launch takes up to kAdamTensors tensors, whose pointers travel in the kernel's
@@ -175,6 +177,7 @@ __device__ __forceinline__ void adam8_fetch(const AdamTensor& t, int64_t blk, A8
 // With F = 2^23 + floor(x - 1), x + (kHalfPast - F) is the fraction of x less 1/2,
 // exactly.
 constexpr float kHalfPast = 8388606.5f;
+constexpr float kTinyScale = 0x1p-120f;
 
 // The low byte of each of four floats, and 0xFF for each that is negative.
 __device__ __forceinline__ uint32_t low_bytes(const float* f) {
@@ -252,9 +255,27 @@ __device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, co
         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, off));
         tv = fmaxf(tv, __shfl_xor_sync(0xffffffffu, tv, off));
     }
+    if (lane == 0) {
+        t.ms[blk] = tm;
+        t.vs[blk] = tv;
+    }
+    tv = fminf(tv, 0x1.fffffep127f);  // beside an infinite v the others keep their roots
+    float step = h.step, rk2 = h.rk2;
+    if (__builtin_expect(!(fminf(tm, tv) >= kTinyScale), 0)) {
+        const bool um = tm < kTinyScale, uv = tv < kTinyScale;
+        tm *= um ? 0x1p64f : 1.f;
+        tv *= uv ? 0x1p64f : 1.f;
+        step *= um ? 0x1p-64f : 1.f;  // it takes the block's m
+        rk2 *= uv ? 0x1p-32f : 1.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            m[k] *= um ? 0x1p64f : 1.f;
+            v[k] *= uv ? 0x1p64f : 1.f;
+        }
+    }
     const float im = tm > 0.f ? __fdiv_rn(1.f, tm) : 0.f, iv = tv > 0.f ? __fdiv_rn(1.f, tv) : 0.f;
     // sqrt(v) = sqrt(v / scale) sqrt(scale): the first root is the code's too
-    const float rv = sqrtf(tv) * h.rk2;
+    const float rv = sqrtf(tv) * rk2;
     uint32_t qm[2], qv[2];
 #pragma unroll
     for (int h4 = 0; h4 < 2; ++h4) {
@@ -289,9 +310,11 @@ __device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, co
                     const float y = __fadd_rn(__fmul_rn(__fsqrt_rn(root[e]), 255.f), uv[e] - 1.f);
                     fa[j + e] = fminf(__fadd_rz(x, 8388608.f), 8388608.f + 127.f);
                     fb[j + e] = fminf(__fadd_rz(y, 8388608.f), 8388608.f + 255.f);
+                    // a ratio that fp32 holds in part or not at all: its root is in range
+                    if (r2[e] < 1.17549435e-38f && v[k + e] > 0.f) root[e] = __fdiv_rn(__fsqrt_rn(v[k + e]), sqrtf(tv));
                 }
                 if (v[k + e] > 0.f) fb[j + e] = fmaxf(fb[j + e], 8388609.f);
-                p[k + e] = fmaf(-h.step, __fdividef(m[k + e], fmaf(root[e], rv, h.eps)), h.decay * p[k + e]);
+                p[k + e] = fmaf(-step, __fdividef(m[k + e], fmaf(root[e], rv, h.eps)), h.decay * p[k + e]);
             }
         }
         // the four codes of each: the floats' low bytes, m's with its sign (bytes that
@@ -320,10 +343,6 @@ __device__ __forceinline__ void adam8_block(const AdamTensor& t, int64_t blk, co
                 if (t.copy) ((__nv_bfloat16*)t.copy)[i + k] = __float2bfloat16_rn(ph[k]);
             }
         }
-    }
-    if (lane == 0) {
-        t.ms[blk] = tm;
-        t.vs[blk] = tv;
     }
 }
 

@@ -288,3 +288,106 @@ def test_values_into_views_at_any_offset(cuda, off, which):
     got = cuda.adamw8_values(m, v, ms, vs, *out)
     assert torch.equal(got[0][0], want[0][0]) and torch.equal(got[1][0], want[1][0])
     assert not buf[:off].any() and not buf[off + n:].any()
+
+
+def ratio(x, s):
+    """x / s in blocks of 256 as the codes take it, also where 1 / s is past fp32's
+    largest number: both times 2^64 then, which is exact."""
+    up = F(2.0 ** 64)
+    tiny = (s > 0) & (s < F(2.0 ** -120))
+    inv = np.where(s > 0, F(1) / np.where(tiny, s * up, np.where(s > 0, s, F(1))), F(0)).astype(F)
+    k = np.repeat(tiny, 256)[:len(x)]
+    return np.where(k, np.abs(x) * up, np.abs(x)).astype(F) * np.repeat(inv, 256)[:len(x)]
+
+
+def block_max(x):
+    return np.array([np.abs(x[i:i + 256]).max() for i in range(0, len(x), 256)], F)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("vec", [True, False])
+def test_8_bits_moments_too_small_to_invert(cuda, vec):
+    """Blocks whose largest v, or m, is a positive number whose reciprocal fp32 does
+    not hold, beside elements without any gradient: weights to fp64, codes and scales
+    bit for bit."""
+    sizes = [4 * 256 + 40, 300, 256, 256]
+    g = [torch.zeros(n) for n in sizes]
+    rng = np.random.default_rng(3)
+    for b, mag in enumerate((1e-18, 1e-19, 1e-20, 1e-21, 3e-19)):  # v about 5e-38 .. 5e-44
+        at = rng.integers(0, 40, 5) + 256 * b
+        g[0][at] = torch.from_numpy(rng.standard_normal(5).astype(F)) * mag
+    g[1][::7] = 1e-20
+    g[2][::3] = 2e-38  # m subnormal, v = 0
+    g[3][5], g[3][6] = 1e-21, 1.0
+    buf = [torch.ones(n + 1, device="cuda") for n in sizes]
+    p = [b[:-1] if vec else b[1:] for b in buf]
+    for t in p:
+        t.copy_(torch.from_numpy(rng.standard_normal(t.numel()).astype(F)))
+    m, v, ms, vs = cuda.adamw8_state(p)
+    have = [(np.zeros(n, F), np.zeros(n, F)) for n in sizes]
+    for step in (1, 2, 3):
+        before = [t.cpu().clone() for t in p]
+        cuda.adamw8_step(p, [t.cuda() for t in g], m, v, ms, vs, step=step, seed=step, **H)
+        for i, n in enumerate(sizes):
+            rp, _, _ = ref_step(before[i], g[i], torch.from_numpy(have[i][0]), torch.from_numpy(have[i][1]), step)
+            assert torch.isfinite(p[i]).all()
+            check_p(p[i], rp, before[i])
+            nm, nv, _, _ = np_moments(g[i].numpy(), *have[i])
+            um, uv = np_noise(n, step, i)
+            sm, sv = block_max(nm), block_max(nv)
+            qm = np.minimum(np.floor(np.sqrt(ratio(nm, sm)) * F(127) + um), 127)
+            qv = np.minimum(np.floor(np.sqrt(np.sqrt(ratio(nv, sv))) * F(255) + uv), 255)
+            qm, qv = np.where(nm < 0, -qm, qm).astype(np.int8), np.where((nv > 0) & (qv < 1), 1, qv).astype(np.uint8)
+            assert np.array_equal(ms[i].cpu().numpy(), sm) and np.array_equal(vs[i].cpu().numpy(), sv)
+            assert np.array_equal(m[i].cpu().numpy(), qm) and np.array_equal(v[i].cpu().numpy(), qv)
+            have[i] = np_decode(qm, sm, qv, sv)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("width", [64, 256])
+def test_8_bits_an_embedding_whose_tokens_stay_away(cuda, width):
+    """One row of an embedding gets a gradient once; 1500 steps of zero gradients
+    take the block's v through the subnormal numbers.  Weights against fp64 from the
+    moments that the codes stood for, every step."""
+    p = [torch.randn(16, width, generator=torch.Generator().manual_seed(1)).cuda()]
+    g = torch.zeros(16, width)
+    g[::4] = 1e-4 * torch.randn(4, width, generator=torch.Generator().manual_seed(2))
+    m, v, ms, vs = cuda.adamw8_state(p)
+    zero, g = torch.zeros_like(p[0]), g.cuda()
+    worst = torch.zeros((), device="cuda", dtype=torch.float64)
+    for step in range(1, 1501):
+        have = cuda.adamw8_values(m, v, ms, vs)
+        before = p[0].clone()
+        now = g if step == 1 else zero
+        cuda.adamw8_step(p, [now], m, v, ms, vs, step=step, seed=step, **H)
+        rp, _, _ = ref_step(before, now, have[0][0].view_as(now), have[1][0].view_as(now), step)
+        bound = 2.0 ** -23 * rp.abs() + 1e-6 * (rp - before.double()).abs().clamp(min=10 * H["lr"])
+        over = ((p[0].double() - rp).abs() / bound).max()
+        worst = torch.maximum(worst, torch.nan_to_num(over, nan=1e9))
+    assert float(worst) <= 1.0
+    assert 0 < float(vs[0].max()) < 2.9e-39  # the range was reached
+
+
+@pytest.mark.gpu
+def test_8_bits_an_infinite_gradient_moves_no_other_weight(cuda):
+    g = 1e-2 * torch.randn(256, generator=torch.Generator().manual_seed(4))
+    g[5] = float("inf")
+    p = [torch.ones(256, device="cuda")]
+    cuda.adamw8_step(p, [g.cuda()], *cuda.adamw8_state(p), step=1, seed=1, **H)
+    z = torch.zeros(256)
+    rp, _, _ = ref_step(torch.ones(256), g, z, z, 1)
+    keep = torch.arange(256) != 5
+    assert not torch.isfinite(p[0][5])
+    check_p(p[0].cpu()[keep], rp[keep], torch.ones(255))
+
+
+@pytest.mark.gpu
+def test_8_bits_a_v_far_below_its_block(cuda):
+    """v / scale below fp32's numbers and no eps to hide it: the step is lr all the same
+    (v itself is a subnormal of 3500 units, its root good to 7e-5)."""
+    g = torch.full((256,), 1e-20)
+    g[9] = 1e3
+    p = [torch.ones(256, device="cuda")]
+    cuda.adamw8_step(p, [g.cuda()], *cuda.adamw8_state(p), step=1, seed=1, lr=1e-2, beta1=0.9, beta2=0.95, eps=0.0,
+                     weight_decay=0.0)
+    assert torch.allclose(p[0], torch.full_like(p[0], 0.99), rtol=0, atol=1e-6 + 1e-2 * 1e-4)

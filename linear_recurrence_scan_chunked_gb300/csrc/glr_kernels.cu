@@ -231,6 +231,7 @@ struct GlrFwdOp {
     static constexpr int VEC = VEC_, NW = 4, R = 4, MINB = 7;
     static constexpr bool REV = false;
     static constexpr int NSUM = 0;
+    static constexpr float kMaxShared = 8.5e37f;  // just below 2^126
     using Params = GlrFwdParams<S>;
     struct Regs {
         Pack<S, VEC> x[R], zr[R], zi[R];
@@ -261,7 +262,8 @@ struct GlrFwdOp {
     }
     // Two elements at a time (neighbouring channels, on the scalar path
     // neighbouring rows), one reciprocal for both gates: 1/(PQ) times Q and P.
-    // Where PQ overflows or a rate is past the pairs' range, the general forms.
+    // Where PQ overflows, its reciprocal is flushed to 0 (from 2^126), or a rate is past
+    // the pairs' range, the general forms.
     template <class L>
     __device__ static __forceinline__ void gates(const Params& p, const SpanGeom& sg, const L& ln, const Block& bk,
                                                  const Feat<VEC>& ft, const Regs& rg, Work& w,
@@ -288,7 +290,7 @@ struct GlrFwdOp {
             f2_get(a, w.fa[r0][v0], w.fa[r1][v1]);
             f2_get(f2_mul(u, f2_mul(q, f2(rsqrt_ftz(q0), rsqrt_ftz(q1)))), w.fb[r0][v0], w.fb[r1][v1]);
         }
-        const bool gen = ft.gen || pmax > 1e38f;
+        const bool gen = ft.gen || pmax > kMaxShared;
         if (gen || rg.rs != 0 || !ln.cok || !bk.full) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {

@@ -382,3 +382,21 @@ def test_shapes_cover_every_plan():
                 seen.add((p["protocol"], p["tma"], D % 4 == 0))
         assert seen == {(pr, *kind) for pr in ("chain", "spans")
                         for kind in ((True, True), (False, True), (False, False))}, seen
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("br", [0.0, 3.0, 20.0])
+@pytest.mark.parametrize("T,D", [(20, 128), (64, 128), (20, 33)])
+def test_input_gates_shut_to_the_last_bit(cuda, T, D, br, dtype):
+    """1 + e^-z of the input gate through the range where its reciprocal leaves
+    fp32's normal numbers (z about -87.4): the decay beside it stays what it is.
+    (The gates are the same at every step, so are the decays' errors: T 1e-7.)"""
+    d = make(T, 2, D, dtype, seed=21, resets="none")
+    d["zr"][:], d["zi"][:] = 0.0, 0.0
+    d["bi"] = torch.linspace(-87.7, -86.5, D)
+    d["br"] = torch.full((D,), br)
+    c = dev(d)
+    h, last = cuda.glr_fwd(*[c[k] for k in NAMES], h0=c["h0"])
+    rh, rlast = ref_fwd(d)
+    assert err(h, rh) <= TOL[dtype] and err(last, rlast) <= 1e-5

@@ -65,7 +65,8 @@ struct Lane {
     int64_t c;           // first channel
     int64_t cd;          // c mod D
     uint32_t seq;        // c / D
-    uint32_t row0;       // time row of the thread's first row within the block
+    uint32_t first;      // the thread's first row within the block, in scan order
+    uint32_t row0;       // its time row
     bool cok;
     uint32_t vo[Op::R];  // byte offset of each row within the block
     __device__ __forceinline__ Lane(const SpanGeom& sg, uint32_t j, int first_row) {
@@ -74,6 +75,7 @@ struct Lane {
         seq = (uint32_t)chan_seq(sg.g, c);
         cd = c - (int64_t)seq * sg.g.D;
         cok = c < sg.g.C;
+        first = (uint32_t)first_row;
         row0 = (uint32_t)(Op::REV ? BLOCK_ROWS - 1 - first_row : first_row);
 #pragma unroll
         for (int r = 0; r < Op::R; ++r) vo[r] = (uint32_t)((row(r) * sg.g.C + c) * (int64_t)sizeof(S));
@@ -97,26 +99,32 @@ template <class L>
 __device__ __forceinline__ bool inside(const L& ln, const Block& bk, const SpanGeom& sg, int r) {
     return ln.cok && (bk.full || bk.t + ln.row(r) < sg.g.T);
 }
-// The reset flags of the thread's rows, bit r.  Where the warp's channels are one
-// sequence's (one: the usual case), lane r reads row r's and a vote tells all.
-template <class Op, class L>
+// The reset flags of a block's rows in scan order, bit k.  Where the warp's channels are
+// one sequence's (one: the usual case), lane k reads row k's and a vote tells all; else
+// a thread reads those of its own rows and the others' bits are set (they may be resets).
+template <class Op, int BLOCK_ROWS, class L>
 __device__ __forceinline__ uint32_t resets(const GlrIn& in, const L& ln, const Block& bk, const SpanGeom& sg, bool one) {
     if (in.reset == nullptr) return 0u;
     const uint8_t* b = in.reset + bk.t * sg.nb;
     if (one) {
-        const int r = (int)(threadIdx.x & 31);
-        const uint32_t row = Op::REV ? ln.row0 - r : ln.row0 + r;
+        const int k = (int)(threadIdx.x & 31);
+        const uint32_t row = Op::REV ? BLOCK_ROWS - 1 - k : k;
         bool hit = false;
-        if (r < Op::R && (bk.full || bk.t + row < sg.g.T)) hit = __ldg(b + row * (uint32_t)sg.nb + ln.seq) != 0;
+        if (k < BLOCK_ROWS && (bk.full || bk.t + row < sg.g.T)) hit = __ldg(b + row * (uint32_t)sg.nb + ln.seq) != 0;
         return __ballot_sync(0xffffffffu, hit);
     }
+    constexpr uint32_t own = (1u << Op::R) - 1, all = (1u << BLOCK_ROWS) - 1;
     uint32_t m = 0;
 #pragma unroll
     for (int r = 0; r < Op::R; ++r) {
         const uint32_t o = (uint32_t)ln.row(r) * (uint32_t)sg.nb + ln.seq;
         if (inside(ln, bk, sg, r) && __ldg(b + o) != 0) m |= 1u << r;
     }
-    return m;
+    return (all & ~(own << ln.first)) | m << ln.first;
+}
+template <int R, class L>
+__device__ __forceinline__ uint32_t own_resets(uint32_t m, const L& ln) {
+    return m >> ln.first & ((1u << R) - 1);
 }
 // Whether the warp's channels all belong to its first lane's sequence.
 template <class L>
@@ -215,6 +223,24 @@ __device__ __forceinline__ void store_row(S* p, const float (&x)[VEC]) {
     }
 }
 
+// A reset step drops what is before it in scan order, finite or not (0 times an infinite
+// or NaN state would be NaN).  Its decay is held as -0, which no other decay and no
+// product of them is: where a decay underflows to +0, a NaN goes on through its document.
+constexpr float kReset = -0.f;
+__device__ __forceinline__ bool is_reset(float a) { return __float_as_uint(a) == 0x80000000u; }
+__device__ __forceinline__ float scan_enter(float a, float s, float b) { return is_reset(a) ? b : __fmaf_rn(a, s, b); }
+__device__ __forceinline__ void scan_join(float& A, float& B, float a, float b) {
+    B = scan_enter(a, B, b);
+    A = is_reset(a) ? kReset : A * a;  // -0 times a decay is -0
+}
+// An aggregate taken onto a state: of a block without resets, and with them.
+struct ScanPlain {
+    __device__ __forceinline__ float operator()(float a, float s, float b) const { return __fmaf_rn(a, s, b); }
+};
+struct ScanReset {
+    __device__ __forceinline__ float operator()(float a, float s, float b) const { return scan_enter(a, s, b); }
+};
+
 // ------------------------------------------------------------------ forward
 
 template <typename S>
@@ -235,10 +261,10 @@ struct GlrFwdOp {
     using Params = GlrFwdParams<S>;
     struct Regs {
         Pack<S, VEC> x[R], zr[R], zi[R];
-        uint32_t rs;  // reset rows
+        uint32_t rs;  // reset rows of the block
     };
     struct Work {
-        float fa[R][VEC], fb[R][VEC];  // scan element (a, f i x)
+        float fa[R][VEC], fb[R][VEC];  // scan element (a, f i x); a reset step: (kReset, i x)
     };
     __device__ static const float* init_ptr(const Params& p) { return p.h0; }
 
@@ -291,21 +317,6 @@ struct GlrFwdOp {
             f2_get(f2_mul(u, f2_mul(q, f2(rsqrt_ftz(q0), rsqrt_ftz(q1)))), w.fb[r0][v0], w.fb[r1][v1]);
         }
         const bool gen = ft.gen || pmax > kMaxShared;
-        if (gen || rg.rs != 0 || !ln.cok || !bk.full) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const bool ok = inside(ln, bk, sg, r), reset = (rg.rs >> r & 1u) != 0;
-                if (ok && !reset && !gen) continue;
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    float a, q;
-                    act_decay(ft.log_a(v, ft.gate(rg.zr[r].get(v), ft.b2r[v])), a, q);
-                    const float u = ft.gate(rg.zi[r].get(v), ft.b2i[v]) * rg.x[r].get(v);
-                    w.fa[r][v] = ok ? (reset ? 0.f : a) : 1.f;
-                    w.fb[r][v] = ok ? (reset ? u : sqrt_ftz(q) * u) : 0.f;
-                }
-            }
-        }
 #pragma unroll
         for (int v = 0; v < VEC; ++v) { A[v] = w.fa[0][v]; B[v] = w.fb[0][v]; }
 #pragma unroll
@@ -315,17 +326,50 @@ struct GlrFwdOp {
                 B[v] = __fmaf_rn(w.fa[r][v], B[v], w.fb[r][v]);
                 A[v] *= w.fa[r][v];
             }
+        const uint32_t rs = own_resets<R>(rg.rs, ln);
+        if (gen || rs != 0 || !ln.cok || !bk.full) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const bool ok = inside(ln, bk, sg, r), reset = (rs >> r & 1u) != 0;
+                if (ok && !reset && !gen) continue;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    float a, q;
+                    act_decay(ft.log_a(v, ft.gate(rg.zr[r].get(v), ft.b2r[v])), a, q);
+                    const float u = ft.gate(rg.zi[r].get(v), ft.b2i[v]) * rg.x[r].get(v);
+                    w.fa[r][v] = ok ? (reset ? kReset : a) : 1.f;
+                    w.fb[r][v] = ok ? (reset ? u : sqrt_ftz(q) * u) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                A[v] = 1.f;
+                B[v] = 0.f;
+#pragma unroll
+                for (int r = 0; r < R; ++r) scan_join(A[v], B[v], w.fa[r][v], w.fb[r][v]);
+            }
+        }
     }
-    template <class L>
+    // enter(s, e): s becomes the state entering the rows, each aggregate taken by e
+    template <class L, class Enter>
     __device__ static __forceinline__ void finish(const Params& p, const SpanGeom& sg, const L& ln, const Block& bk,
-                                                  const Feat<VEC>&, const Regs&, const Work& w,
-                                                  float (&s)[VEC], float (&)[1][VEC]) {
+                                                  const Feat<VEC>&, const Regs& rg, const Work& w,
+                                                  float (&s)[VEC], float (&)[1][VEC], const Enter& enter) {
         S* h = p.h + bk.at;
         float o[R][VEC];
+        if (rg.rs == 0) {
+            enter(s, ScanPlain());
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) o[r][v] = s[v] = __fmaf_rn(w.fa[r][v], s[v], w.fb[r][v]);
+                for (int v = 0; v < VEC; ++v) o[r][v] = s[v] = __fmaf_rn(w.fa[r][v], s[v], w.fb[r][v]);
+        } else {
+            enter(s, ScanReset());
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) o[r][v] = s[v] = scan_enter(w.fa[r][v], s[v], w.fb[r][v]);
+        }
         if (bk.full) {
             if (ln.cok) {
 #pragma unroll
@@ -369,10 +413,10 @@ struct GlrBwdOp {
     using Params = GlrBwdParams<S>;
     struct Regs {
         Pack<S, VEC> x[R], zr[R], zi[R], dh[R], hp[R];
-        uint32_t rs;  // reset rows
+        uint32_t rs;  // reset rows of the block
     };
     struct Work {
-        float F[R][VEC];   // a (0 on a reset step, 1 outside)
+        float F[R][VEC];   // a (kReset on a reset step, 1 outside)
         float rr[R][VEC];  // r
         float q[R][VEC];   // 1 - a^2
         bool gen;          // some row needs the general forms
@@ -424,19 +468,8 @@ struct GlrBwdOp {
             f2_get(a, w.F[r0][v0], w.F[r1][v1]);
             f2_get(q, w.q[r0][v0], w.q[r1][v1]);
         }
-        w.gen = ft.gen || rg.rs != 0 || (p.h0 != nullptr && bk.t + ln.row(R - 1) == 0);
-        if (ft.gen || rg.rs != 0 || !ln.cok || !bk.full) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const bool ok = inside(ln, bk, sg, r), reset = (rg.rs >> r & 1u) != 0;
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    float a = w.F[r][v], q;
-                    if (ft.gen) act_decay(ft.log_a(v, w.rr[r][v]), a, q);
-                    w.F[r][v] = ok ? (reset ? 0.f : a) : 1.f;
-                }
-            }
-        }
+        const uint32_t rs = own_resets<R>(rg.rs, ln);
+        w.gen = ft.gen || rs != 0 || (p.h0 != nullptr && bk.t + ln.row(R - 1) == 0);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) { A[v] = w.F[0][v]; B[v] = w.F[0][v] * rg.dh[0].get(v); }
 #pragma unroll
@@ -446,19 +479,54 @@ struct GlrBwdOp {
                 B[v] = w.F[r][v] * (rg.dh[r].get(v) + B[v]);
                 A[v] *= w.F[r][v];
             }
-    }
-    template <class L>
-    __device__ static __forceinline__ void finish(const Params& p, const SpanGeom& sg, const L& ln, const Block& bk,
-                                                  const Feat<VEC>& ft, const Regs& rg, const Work& w,
-                                                  float (&s)[VEC], float (&sum)[3][VEC]) {
-        float d[R][VEC];  // d_t
+        if (ft.gen || rs != 0 || !ln.cok || !bk.full) {
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r) {
+                const bool ok = inside(ln, bk, sg, r), reset = (rs >> r & 1u) != 0;
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    float a = w.F[r][v], q;
+                    if (ft.gen) act_decay(ft.log_a(v, w.rr[r][v]), a, q);
+                    w.F[r][v] = ok ? (reset ? kReset : a) : 1.f;
+                }
+            }
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                d[r][v] = rg.dh[r].get(v) + s[v];
-                s[v] = w.F[r][v] * d[r][v];
+                A[v] = 1.f;
+                B[v] = 0.f;
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float F = w.F[r][v];
+                    B[v] = is_reset(F) ? 0.f : F * (rg.dh[r].get(v) + B[v]);
+                    A[v] = is_reset(F) ? kReset : A[v] * F;
+                }
             }
+        }
+    }
+    template <class L, class Enter>
+    __device__ static __forceinline__ void finish(const Params& p, const SpanGeom& sg, const L& ln, const Block& bk,
+                                                  const Feat<VEC>& ft, const Regs& rg, const Work& w,
+                                                  float (&s)[VEC], float (&sum)[3][VEC], const Enter& enter) {
+        float d[R][VEC];  // d_t
+        if (rg.rs == 0) {
+            enter(s, ScanPlain());
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    d[r][v] = rg.dh[r].get(v) + s[v];
+                    s[v] = w.F[r][v] * d[r][v];
+                }
+        } else {
+            enter(s, ScanReset());
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    d[r][v] = rg.dh[r].get(v) + s[v];
+                    s[v] = is_reset(w.F[r][v]) ? 0.f : w.F[r][v] * d[r][v];
+                }
+        }
         float dx[R][VEC], dzr[R][VEC], dzi[R][VEC], dl_[R][VEC];
         if (!w.gen) {
             const f32x2 one = f2(1.f), none = f2(-1.f), nl = f2(-kLog2e);
@@ -490,7 +558,7 @@ struct GlrBwdOp {
         } else {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                const bool reset = (rg.rs >> r & 1u) != 0;
+                const bool reset = (own_resets<R>(rg.rs, ln) >> r & 1u) != 0;
                 float hp[VEC];
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) hp[v] = rg.hp[r].get(v);
@@ -507,10 +575,10 @@ struct GlrBwdOp {
                     const float f = reset ? 1.f : q * rf;
                     const float u = ii * rg.x[r].get(v);
                     const float K = reset || q == 0.f ? 0.f : a * (hp[v] - u * a * rf);
-                    const float dl = -d[r][v] * K * rr;
+                    const float dl = reset ? 0.f : -d[r][v] * K * rr;
                     dx[r][v] = d[r][v] * f * ii;
                     dzi[r][v] = d[r][v] * f * u * (1.f - ii);
-                    dzr[r][v] = dl * (-16.f * ft.l16[v]) * (1.f - rr);
+                    dzr[r][v] = reset ? 0.f : dl * (-16.f * ft.l16[v]) * (1.f - rr);
                     dl_[r][v] = dl;
                 }
             }
@@ -555,6 +623,23 @@ struct SpanSmem {
     float carry[2][32][VEC];
 };
 
+// The state entering a warp's rows: the carried one, with the aggregates of the warps
+// before taken onto it by `take`.
+template <int VEC, int NW, int PAR>
+struct Entering {
+    const SpanSmem<VEC, NW>& sm;
+    int warp, lane;
+    template <class Take>
+    __device__ __forceinline__ void operator()(float (&s)[VEC], const Take& take) const {
+#pragma unroll
+        for (int w = 0; w < NW - 1; ++w)
+            if (w < warp) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) s[v] = take(sm.a[PAR][w][lane][v], s[v], sm.b[PAR][w][lane][v]);
+            }
+    }
+};
+
 // The aggregate of span sp, strip j: (A, B) of its rows in scan order.  Warp w
 // folds the span's row groups [w cps, (w+1) cps), loading one group ahead.
 template <class Op>
@@ -580,7 +665,7 @@ __global__ void __launch_bounds__(Op::NW * 32)
     typename Op::Regs rg[2];
     auto fetch = [&](const Block& bk, typename Op::Regs& r) {
         load_global<true, Op>(p, ln, bk, sg, r);
-        r.rs = resets<Op>(p.in, ln, bk, sg, one);
+        r.rs = resets<Op, Op::R>(p.in, ln, bk, sg, one);
     };
     Block bk = place(Op::REV ? rows - Op::R - g0 * Op::R : g0 * Op::R);
     fetch(bk, rg[0]);
@@ -595,9 +680,9 @@ __global__ void __launch_bounds__(Op::NW * 32)
             float a[VEC], b[VEC];
             Op::gates(p, sg, ln, bk, ft, rg[h], w, a, b);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                B[v] = __fmaf_rn(a[v], B[v], b[v]);
-                A[v] *= a[v];
+            for (int v = 0; v < VEC; ++v) {  // scan_join, told by the rows' flags
+                B[v] = rg[h].rs != 0 ? b[v] : __fmaf_rn(a[v], B[v], b[v]);
+                A[v] = rg[h].rs != 0 ? kReset : A[v] * a[v];
             }
             bk = nx;
         }
@@ -609,10 +694,7 @@ __global__ void __launch_bounds__(Op::NW * 32)
 #pragma unroll
     for (int w = 1; w < NW; ++w)
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            B[v] = __fmaf_rn(sa[w][lane][v], B[v], sb[w][lane][v]);
-            A[v] *= sa[w][lane][v];
-        }
+        for (int v = 0; v < VEC; ++v) scan_join(A[v], B[v], sa[w][lane][v], sb[w][lane][v]);
 #pragma unroll
     for (int v = 0; v < VEC; ++v) agg[(int64_t)sp * sg.g.C + ln.c + v] = make_float2(A[v], B[v]);
 }
@@ -666,7 +748,7 @@ __global__ void __launch_bounds__(Op::NW * 32, ST > 0 ? Op::MINB : Op::MINB - 2)
     bk.full = bk.t + L <= sg.g.T;
     typename Op::Regs rg, ahead;
     if constexpr (ST == 0) load_global<false, Op>(p, ln, bk, sg, rg);
-    rg.rs = resets<Op>(p.in, ln, bk, sg, one);
+    rg.rs = resets<Op, L>(p.in, ln, bk, sg, one);
     Feat<VEC> ft;
     ft.load(p.in, ln.cd, ln.cok);
     const uint32_t mine = ln.row0 * (32 * VEC * (uint32_t)sizeof(typename Op::S)) + lane * (VEC * (uint32_t)sizeof(typename Op::S));
@@ -682,8 +764,7 @@ __global__ void __launch_bounds__(Op::NW * 32, ST > 0 ? Op::MINB : Op::MINB - 2)
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) {
                     const float2 e = agg[(int64_t)k * sg.g.C + ln.c + v];
-                    B[v] = __fmaf_rn(e.x, B[v], e.y);
-                    A[v] *= e.x;
+                    scan_join(A[v], B[v], e.x, e.y);
                 }
         }
 #pragma unroll
@@ -698,7 +779,7 @@ __global__ void __launch_bounds__(Op::NW * 32, ST > 0 ? Op::MINB : Op::MINB - 2)
 #pragma unroll
             for (int w = 0; w < NW; ++w)
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) s[v] = __fmaf_rn(sm.a[1][w][lane][v], s[v], sm.b[1][w][lane][v]);
+                for (int v = 0; v < VEC; ++v) s[v] = scan_enter(sm.a[1][w][lane][v], s[v], sm.b[1][w][lane][v]);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) sm.carry[0][lane][v] = s[v];
         }
@@ -725,7 +806,7 @@ __global__ void __launch_bounds__(Op::NW * 32, ST > 0 ? Op::MINB : Op::MINB - 2)
         } else if (more) {
             load_global<false, Op>(p, ln, nx, sg, ahead);
         }
-        if (more) ahead.rs = resets<Op>(p.in, ln, nx, sg, one);
+        if (more) ahead.rs = resets<Op, L>(p.in, ln, nx, sg, one);
         float A[VEC], B[VEC];
         typename Op::Work w;
         Op::gates(p, sg, ln, bk, ft, rg, w, A, B);
@@ -741,13 +822,7 @@ __global__ void __launch_bounds__(Op::NW * 32, ST > 0 ? Op::MINB : Op::MINB - 2)
         float s[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) s[v] = sm.carry[PAR][lane][v];
-#pragma unroll
-        for (int w2 = 0; w2 < NW - 1; ++w2)
-            if (w2 < warp) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) s[v] = __fmaf_rn(sm.a[PAR][w2][lane][v], s[v], sm.b[PAR][w2][lane][v]);
-            }
-        Op::finish(p, sg, ln, bk, ft, rg, w, s, sum);
+        Op::finish(p, sg, ln, bk, ft, rg, w, s, sum, Entering<VEC, NW, PAR>{sm, warp, lane});
         if (warp == NW - 1) {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) sm.carry[PAR ^ 1][lane][v] = s[v];

@@ -400,3 +400,105 @@ def test_input_gates_shut_to_the_last_bit(cuda, T, D, br, dtype):
     h, last = cuda.glr_fwd(*[c[k] for k in NAMES], h0=c["h0"])
     rh, rlast = ref_fwd(d)
     assert err(h, rh) <= TOL[dtype] and err(last, rlast) <= 1e-5
+
+
+def piece(d, lo, hi):
+    """Steps lo .. hi - 1 of a problem, as one that starts and ends without states."""
+    cut = {k: v[lo:hi] if k in ("x", "zr", "zi", "dh", "reset") else v for k, v in d.items()}
+    return dict(cut, h0=None, dh_last=None)
+
+
+# one span and several, in vectors by TMA and element by element
+RESET_SHAPES = [(20, 128), (300, 128), (20, 33), (300, 33)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("T,D", RESET_SHAPES)
+def test_a_reset_drops_a_state_that_is_not_finite(cuda, T, D, bad, dtype):
+    """A document whose state overflowed, or an initial state that did, and what a
+    reset step's own decay gate holds, reach nothing after the reset."""
+    d = make(T, 3, D, dtype, seed=22, resets="none")
+    k = T // 2 + 1
+    d["reset"] = torch.zeros(T, 3, dtype=torch.uint8)
+    d["reset"][k] = 1
+    d["h0"][0] = bad
+    d["x"][2, 1] = bad
+    d["x"][k - 1, 2] = bad
+    d["zr"][3, 2, ::3] = bad
+    d["zr"][k, :, ::2] = bad
+    c = dev(d)
+    h, last = cuda.glr_fwd(*[c[n] for n in NAMES], h0=c["h0"], reset=c["reset"])
+    clean = dict(d, zr=d["zr"].clone())
+    clean["zr"][k] = 0.0
+    late = piece(clean, k, T)
+    rh, rlast = ref_fwd(late)
+    assert not torch.isfinite(h[k - 1]).any()
+    assert err(h[k:], rh) <= TOL[dtype] and err(last, rlast) <= 1e-5
+    got = cuda.glr_bwd(*[c[n] for n in NAMES], h, c["dh"], h0=c["h0"], reset=c["reset"])
+    ref, _ = ref_bwd(late, h[k:].cpu())
+    for n in ("dx", "dzr", "dzi"):
+        assert err(got[n][k:], ref[n]) <= TOL[dtype], n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("T,D", RESET_SHAPES)
+def test_a_reset_stops_a_gradient_that_is_not_finite(cuda, T, D, bad, dtype):
+    """Nothing of a later document's gradient, or of the last state's, reaches the
+    steps before its reset."""
+    d = make(T, 3, D, dtype, seed=23, resets="none")
+    k = T // 2 - 1
+    d["reset"] = torch.zeros(T, 3, dtype=torch.uint8)
+    d["reset"][k] = 1
+    d["dh_last"][0] = bad
+    d["dh"][T - 2, 1] = bad
+    d["dh"][k, 2] = bad
+    c = dev(d)
+    args = [c[n] for n in NAMES]
+    h, _ = cuda.glr_fwd(*args, h0=c["h0"], reset=c["reset"])
+    got = cuda.glr_bwd(*args, h, c["dh"], h0=c["h0"], reset=c["reset"], dh_last=c["dh_last"])
+    ref, _ = ref_bwd(dict(piece(d, 0, k), h0=d["h0"]), h[:k].cpu())
+    for n in ("dx", "dzr", "dzi"):
+        assert err(got[n][:k], ref[n]) <= TOL[dtype], n
+    assert err(got["dh0"], ref["dh0"]) <= 1e-5
+    assert not torch.isfinite(got["dx"][k, 2]).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("with_resets", [False, True])
+@pytest.mark.parametrize("T,D", RESET_SHAPES)
+def test_a_nan_stays_in_its_document_and_fills_it(cuda, T, D, with_resets):
+    """Decays whose products underflow to 0 are no resets: a NaN reaches the end of its
+    document (and its gradient the start), over spans and all."""
+    d = make(T, 3, D, "f32", seed=24, resets="none")
+    d["lam"] = torch.full((D,), 60.0)
+    lo, hi, t0 = T // 4, 3 * T // 4, T // 2
+    if with_resets:
+        d["reset"] = torch.zeros(T, 3, dtype=torch.uint8)
+        d["reset"][lo] = d["reset"][hi] = 1
+    else:
+        lo, hi = 0, T
+    d["x"][t0, 1] = float("nan")
+    c = dev(d)
+    args = [c[n] for n in NAMES]
+    h, _ = cuda.glr_fwd(*args, h0=c["h0"], reset=c["reset"])
+    bad = torch.zeros(T, 3, dtype=torch.bool)
+    bad[t0:hi, 1] = True
+    assert torch.equal(torch.isnan(h).cpu(), bad[:, :, None].expand(T, 3, D))
+    d["dh"][t0, 2] = float("nan")
+    got = cuda.glr_bwd(*args, c["x"].nan_to_num(), d["dh"].cuda(), h0=c["h0"], reset=c["reset"])
+    bad = torch.zeros(T, 3, dtype=torch.bool)
+    bad[lo:t0 + 1, 2] = True
+    # a sequence's own NaN in x shows in its own step only
+    assert torch.equal(torch.isnan(got["dx"]).cpu(), bad[:, :, None].expand(T, 3, D))
+
+
+def test_reset_shapes_are_one_span_and_several():
+    for op in ("glr_fwd", "glr_bwd"):
+        for dt in ("f32", "bf16"):
+            kinds = [lrs.plan_info(op, dt, D % 4 == 0, T, 3 * D) for T, D in RESET_SHAPES]
+            assert [p["protocol"] for p in kinds] == ["chain", "spans", "chain", "spans"]
+            assert [p["tma"] for p in kinds] == [True, True, False, False]

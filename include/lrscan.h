@@ -416,6 +416,9 @@ int layer_norm_bwd(const void* x, const float* w, const float* mean, const float
  *               ignored and is recorded as LR_ERR_INDEX in the device error word
  *   loss, lse : [N] fp32 out (lse is kept for lce_bwd)
  * V >= 1, 1 <= D <= 65536; N = 0 is a no-op.  Sums and statistics are fp32.
+ * Logits of any finite size are right to their rounding; words that a row's logits
+ * hold out with the type's lowest value (or -inf, bf16 data) count as 0.  fp32 data is
+ * multiplied as three bf16 planes: an infinity in it makes its rows' results NaN.
  */
 int lce_fwd(const void* x, const void* w, const int64_t* target, int64_t ignore, float* loss,
             float* lse, int64_t N, int64_t V, int64_t D, int dtype, void* stream);

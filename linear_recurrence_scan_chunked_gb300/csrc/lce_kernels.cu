@@ -7,8 +7,8 @@
 //   dx = g W,   dW = g^T x.
 //
 // Forward: the epilogue of the product x W^T reduces each 128 columns of
-// logits to a pair per row, a power-of-two bound 2^M of its exponentials and
-// their sum relative to it, and a second kernel joins the tiles' pairs.  Backward:
+// logits to a pair per row, their largest M and the sum of exp(l - M), and a second
+// kernel joins the tiles' pairs.  Backward:
 // for a piece of the vocabulary the product runs again, its epilogue writes g
 // (scratch, bounded by kPieceBytes), and two more products give the piece's dW and
 // its share of dx.  That is 8 N V D operations where a form that kept the logits
@@ -51,7 +51,6 @@ constexpr int64_t kPieceBytes = (int64_t)2 << 30;  // g of one piece, all planes
 // 64 2916 us and 1.5e-5, one accumulator 2892 us and 7e-4 (the results' rounding: 1e-3
 // of each, but with either sign).
 constexpr uint32_t kSumChunk = 32;
-constexpr float kLn2 = 0.6931471805599453f;
 
 // 32 bytes of a row (sm_100+: one sector in one store).
 __device__ __forceinline__ void st_32b(void* p, const uint32_t (&w)[8]) {
@@ -100,9 +99,15 @@ __device__ __forceinline__ float pick32(const float (&v)[32], int j) {
     return r;
 }
 
-// Forward: the pair of a tile and a row.  With M = ceil(max l log2 e), the sum
-// of 2^(l log2 e - M): M is an integer, so its subtraction inside the
-// multiply-add rounds nothing but the result, and no common error enters the sum.
+// 2^(x log2 e), and what a sum of exponentials relative to `from` is worth relative to
+// `to` (infinite ones included: a tile that holds nothing has from = -inf).
+__device__ __forceinline__ float exp_fast(float x) { return ex2_ftz(x * kLog2e); }
+__device__ __forceinline__ float rescale(float from, float to) { return from == to ? 1.f : exp_fast(from - to); }
+
+// Forward: the pair of a tile and a row, M = max l and the sum of e^(l - M).  The
+// difference is taken before it is scaled, so that logits of any finite size keep
+// their places, words masked by the type's lowest value count as 0 and only a NaN or
+// +inf logit makes the sum NaN or infinite.
 template <bool CHUNKED, int P>
 struct StatsEpi {
     static constexpr bool kChunked = CHUNKED, kStaged = false;
@@ -145,14 +150,16 @@ struct StatsEpi {
         float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
         for (int i = 4; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
-        const float m = ceilf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kLog2e);
+        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (m > r.M) {
-            r.s *= ex2_ftz(r.M - m);  // the first time 2^-inf = 0
+            r.s *= exp_fast(r.M - m);  // the first time e^-inf = 0
             r.M = m;
         }
+        // nothing but -inf so far, or a +inf: their own exponentials
+        const float base = fabsf(r.M) < INFINITY ? r.M : 0.f;
         float e[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) e[i & 3] += ex2_ftz(fmaf(v[i], kLog2e, -r.M));
+        for (int i = 0; i < 32; ++i) e[i & 3] += exp_fast(v[i] - base);
         r.s += (e[0] + e[1]) + (e[2] + e[3]);
     }
     __device__ void end(Row& r) const {
@@ -172,9 +179,8 @@ __global__ void __launch_bounds__(1024)
     const int64_t n = (int64_t)blockIdx.x * 32 + threadIdx.x;
     float M = -INFINITY, s = 0.f;
     auto fold = [&](const float2 p) {
-        // a tile's M is -inf or NaN only where its logits are: its sum is NaN then
         const float m = fmaxf(M, p.x);
-        s = s * (M == m ? 1.f : ex2_ftz(M - m)) + p.y * (p.x == m ? 1.f : ex2_ftz(p.x - m));
+        s = s * rescale(M, m) + p.y * rescale(p.x, m);
         M = m;
     };
     if (n < rows) {
@@ -195,7 +201,7 @@ __global__ void __launch_bounds__(1024)
     M = -INFINITY;
     s = 0.f;
     for (int k = 0; k < 32 && k < tiles; ++k) fold(sm[k][threadIdx.x]);
-    const float z = fmaf(M, kLn2, logf(s));
+    const float z = M + logf(s);
     lse[n] = z;
     const int64_t t = target[n];
     const bool in = t >= 0 && t < V;
@@ -230,7 +236,8 @@ struct GradEpi {
         int64_t n;
         __nv_bfloat16* out;
         int width, at;
-        float f, ds, hi, z;
+        bool live;      // the row counts
+        float ds, z;
     };
     __device__ int width(const Tile& t, int half) const {
         const int64_t w = vc - ((int64_t)t.n * 2 + half) * (tn / 2);
@@ -242,18 +249,15 @@ struct GradEpi {
         const int64_t c0 = ((int64_t)t.n * 2 + half) * (tn / 2);
         r.width = width(t, half);
         r.out = g + r.n * pitch + c0;
-        r.f = r.ds = r.z = 0.f;
-        r.hi = INFINITY;  // a row that does not count: 2^-inf = 0
+        r.ds = r.z = 0.f;
+        r.live = false;
         r.at = -1;
         if (r.n < rows) {
             const int64_t tg = __ldg(target + r.n);
             if (tg != ignore && tg >= 0 && tg < V) {
                 r.ds = __fdiv_rn(__ldg(dloss + r.n), scale_of(top));
                 r.z = __ldg(lse + r.n);
-                // lse log2 e = hi + lo: 2^-lo goes into the row's factor, so that
-                // hi's rounding is no common error of the row
-                r.hi = r.z * kLog2e;
-                r.f = r.ds * ex2_ftz(fmaf(-r.z, kLog2e, r.hi));
+                r.live = true;
                 const int64_t q = tg - v0 - c0;
                 if (q >= 0 && q < r.width) r.at = (int)q;
             }
@@ -266,8 +270,8 @@ struct GradEpi {
         // the target's p - 1 without cancellation where p is near 1
         if (any) gt = expm1f(pick32(v, r.at & 31) - r.z) * r.ds;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = ex2_ftz(fmaf(v[i], kLog2e, -r.hi)) * r.f;
-        if (r.hi == INFINITY) {  // whatever its logits are, infinite or NaN
+        for (int i = 0; i < 32; ++i) v[i] = exp_fast(v[i] - r.z) * r.ds;
+        if (!r.live) {  // whatever its logits are, infinite or NaN
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
@@ -418,6 +422,12 @@ __global__ void __launch_bounds__(256)
     add(std::integral_constant<int, 1>{}, done, n - done);
 }
 
+// bf16's largest number in place of finite ones beyond it.
+constexpr float kBfMax = 0x1.fep127f;
+__device__ __forceinline__ float bf_bound(float x) {
+    return fabsf(x) > kBfMax && fabsf(x) < INFINITY ? copysignf(kBfMax, x) : x;
+}
+
 // A matrix on its way into planes: [rows][D] into P bf16 planes of pitch ld (a
 // multiple of 8; the columns past D are never read).
 struct PackJob {
@@ -479,7 +489,15 @@ __global__ void __launch_bounds__(256)
         auto put = [&](int64_t d, float (&v)[4]) {
 #pragma unroll
             for (int k = 0; k < P; ++k) {
-                const uint32_t a = bf_pack(v[0], v[1]), b = bf_pack(v[2], v[3]);
+                uint32_t a = bf_pack(v[0], v[1]), b = bf_pack(v[2], v[3]);
+                if constexpr (P > 1) {
+                    // past bf16's largest number the first plane is that number, not infinite
+                    const float t = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+                    if (k == 0 && t > kBfMax) {
+                        a = bf_pack(bf_bound(v[0]), bf_bound(v[1]));
+                        b = bf_pack(bf_bound(v[2]), bf_bound(v[3]));
+                    }
+                }
                 *reinterpret_cast<uint2*>(dst + k * plane + d) = make_uint2(a, b);
                 v[0] -= bf_lo(a); v[1] -= bf_hi(a); v[2] -= bf_lo(b); v[3] -= bf_hi(b);
             }

@@ -374,3 +374,89 @@ def test_long_sums_do_not_shrink(cuda):
         n += float(want.sum())
     print("bias", off / n)
     assert abs(off / n) <= 1e-5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 37])
+def test_words_masked_by_the_lowest_value(cuda, dtype, D):
+    """Words that a bias column holds out with the type's lowest value, whole tiles of
+    columns and ragged ones: their exponentials are 0, whichever comes first."""
+    N, V = 70, 700
+    x, w, t, dl = make(N, V, D, dtype, seed=13, pad=0.0)
+    off = torch.zeros(V, dtype=torch.bool)
+    off[:150] = off[300:333] = off[650:] = True
+    x[:, 0] = 1.0
+    w[off] = 0.0
+    w[off, 0] = torch.finfo(DT[dtype]).min
+    t = torch.arange(N) % 130 + 160
+    rl, rz, rdx, rdw = ref(x, w, t, dl)
+    xd, wd, td = x.cuda(), w.cuda(), t.cuda()
+    loss, lse = cuda.lce_fwd(xd, wd, td)
+    assert mx(loss, rl) <= 1e-5 and mx(lse, rz) <= 1e-5
+    dx, dw = cuda.lce_bwd(xd, wd, td, lse, dl.cuda())
+    _, _, rdx, rdw = ref(x, w, t, dl, lse_in=lse)
+    sx, sw = slack(x, w[~off], t, dl, rdx, rdw[~off])
+    assert dist(dx, rdx) <= GTOL[dtype] + sx and dist(dw, rdw) <= GTOL[dtype] + sw
+    assert not dw.cpu()[off].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_logits_of_any_finite_size(cuda, dtype):
+    """Rows whose logits are of the order of 1e6 to 1e37: loss and lse to 1e-5 of the
+    row's largest, where exp(l) has left every range long ago; and a row that is
+    masked throughout by one very low value: V equal words."""
+    N, V, D = 33, 300, 64
+    x, w, t, dl = make(N, V, D, dtype, seed=14, pad=0.0)
+    x = x.float() * torch.logspace(0, 37, N)[:, None]
+    x[32] = 0.0
+    x[32, 0] = 1.0
+    w[:, 0] = 0.0
+    x, w = x.to(DT[dtype]), w.clone()
+    rl, rz, _, _ = ref(x, w, t, dl)
+    big = (x.double() @ w.double().T).abs().amax(1).clamp(min=1.0)
+    loss, lse = cuda.lce_fwd(x.cuda(), w.cuda(), t.cuda())
+    assert float(((loss.double().cpu() - rl).abs() / big).max()) <= 1e-5
+    assert float(((lse.double().cpu() - rz).abs() / big).max()) <= 1e-5
+    dx, dw = cuda.lce_bwd(x.cuda(), w.cuda(), t.cuda(), lse, dl.cuda())
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+    low = torch.zeros(V, D, dtype=DT[dtype])
+    low[:, 0] = -3e38
+    loss, lse = cuda.lce_fwd(x[32:].cuda(), low.cuda(), t[32:].cuda())
+    assert float(lse) == float(low[0, 0]) and float(loss) == 0.0  # log V is below lse's last bit
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_an_infinite_logit_shows_in_the_gradient(cuda, dtype):
+    """exp(l - lse) of an infinite lse is not 0 for every word: the row's gradient is
+    NaN, like the formula's, whether the target's logit is infinite or not."""
+    N, V, D = 40, 300, 64
+    x, w, t, dl = make(N, V, D, dtype, seed=15, pad=0.0)
+    t[7], t[8] = 200, 201
+    w[200, 0], w[201, 0] = 1.0, -1.0
+    x[7:9, 0] = float("inf")
+    xd, wd, td = x.cuda(), w.cuda(), t.cuda()
+    loss, lse = cuda.lce_fwd(xd, wd, td)
+    assert not torch.isfinite(lse[7:9]).any() and not torch.isfinite(loss[7:9]).any()
+    keep = (torch.arange(N) != 7) & (torch.arange(N) != 8)
+    assert mx(lse.cpu()[keep], ref(x, w, t, dl)[1][keep]) <= 1e-5
+    dx, _ = cuda.lce_bwd(xd, wd, td, lse, dl.cuda())
+    assert torch.isnan(dx[7:9]).all() and torch.isfinite(dx.cpu()[keep]).all()
+
+
+@pytest.mark.gpu
+def test_infinitely_masked_words_bf16(cuda):
+    """Words at -inf: loss and lse are those of the others."""
+    N, V, D = 40, 300, 64
+    x, w, t, dl = make(N, V, D, "bf16", seed=16, pad=0.0)
+    x[:, 0] = 1.0
+    off = torch.zeros(V, dtype=torch.bool)
+    off[:64] = off[280:] = True
+    w[off] = 0.0
+    w[off, 0] = -float("inf")
+    t = torch.arange(N) % 200 + 70
+    rl, rz, _, _ = ref(x, w, t, dl)
+    loss, lse = cuda.lce_fwd(x.cuda(), w.cuda(), t.cuda())
+    assert mx(loss, rl) <= 1e-5 and mx(lse, rz) <= 1e-5

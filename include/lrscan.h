@@ -61,8 +61,9 @@
  *    counters and the last iteration count of each DEER form and shape,
  *    bias-gradient partials; the gated recurrence's aggregates of spans of
  *    time and its parameter partials, the layer norm's column sums, and the
- *    cross entropy's scratch, up to 2 GB of gradients of logits plus packed
- *    copies of fp32 or unaligned operands), grown on demand with cudaMalloc.  Calls on
+ *    cross entropy's scratch, which lce_plan_info states: up to 2 GB of gradients of
+ *    logits, packed copies of fp32 or unaligned operands, and fp32 copies of dx
+ *    where it is summed in parts), grown on demand with cudaMalloc.  Calls on
  *    different streams are serialised through it with CUDA events; every
  *    call records its event on every return once it has begun enqueueing,
  *    errors included, so a later call on another stream still waits for
@@ -603,6 +604,24 @@ int lr_test_lookback_timeout(uint32_t spin_limit, void* stream);
  */
 int lr_test_fail_after_enqueue(float* x, int64_t n, float value, uint64_t sleep_ns,
                                void* stream);
+
+/*
+ * How lce_fwd (bwd 0) or lce_bwd (bwd 1) cuts a problem, from the shape alone: no
+ * device is needed.  vec is 1 when x and w are 16-byte aligned.  Outputs (each may be
+ * NULL): rows of a round, words of a piece, parts of dx in a piece, and the bytes of
+ * scratch, of which g = dL/dlogits of a piece (or a round's statistics) takes 2 GB or
+ * 256 words (rows) worth, whichever is more; packed copies of x and w 2 bytes (bf16) or
+ * 6 (fp32) an element where they are needed; and dx, where a call has several pieces or
+ * parts, 4 bytes an element for each part and, bf16 with several pieces, once more.
+ */
+int lce_plan_info(int bwd, int dtype, int vec, int64_t N, int64_t V, int64_t D, int64_t* rows, int64_t* piece,
+                  int64_t* dx_splits, int64_t* bytes);
+
+/*
+ * Test hook: the budget of lce_fwd's and lce_bwd's scratch that lce_plan_info names, in
+ * bytes (0: 2 GB again), so that small problems take several pieces and rounds.
+ */
+int lr_test_lce_budget(int64_t bytes);
 
 /*
  * Test hook for the choice between the vector and the element path of the AdamW

@@ -86,6 +86,8 @@ def load():
     lib.lr_test_activations.argtypes = [P, P, P, P, I64, P]
     lib.lr_test_fail_after_enqueue.argtypes = [P, I64, ctypes.c_float, ctypes.c_uint64, P]
     lib.lr_test_fail_after_enqueue.restype = I
+    lib.lce_plan_info.argtypes = [I, I, I, I64, I64, I64, P, P, P, P]
+    lib.lr_test_lce_budget.argtypes = [I64]
     lib.lr_test_adamw_vec.argtypes = [I, I] + [P] * 5
     lib.lr_plan_info.argtypes = [I, I, I, I64, I64, P, P, P, P]
     lib.lr_plan_info.restype = I
@@ -522,6 +524,25 @@ def plan_info(op: str, dtype: str, vec: bool, T: int, C: int) -> dict:
         raise ValueError(f"lr_plan_info: {status_str(st)}")
     return {"protocol": PROTOCOLS[proto.value], "tma": bool(tma.value), "tile_rows": rows.value,
             "n_chunks": nch.value}
+
+
+def lce_plan_info(bwd: bool, dtype: str, vec: bool, N: int, V: int, D: int) -> dict:
+    """How lce_fwd or lce_bwd cuts a problem (host only, no device): {"rows" of a
+    round, words of a "piece", "dx_splits", "bytes" of scratch}.  Raises ValueError on
+    an argument error."""
+    if dtype not in ("f32", "bf16"):
+        raise ValueError(f"dtype must be 'f32' or 'bf16', got {dtype!r}")
+    v = [ctypes.c_int64(-1) for _ in range(4)]
+    st = load().lce_plan_info(1 if bwd else 0, LR_F32 if dtype == "f32" else LR_BF16, 1 if vec else 0, int(N), int(V),
+                              int(D), *(ctypes.byref(x) for x in v))
+    if st != LR_OK:
+        raise ValueError(f"lce_plan_info: {status_str(st)}")
+    return dict(zip(("rows", "piece", "dx_splits", "bytes"), (x.value for x in v)))
+
+
+def test_lce_budget(bytes_: int = 0) -> int:
+    """Sets the scratch budget of the cross entropy (0: its own) for tests of several pieces."""
+    return int(load().lr_test_lce_budget(int(bytes_)))
 
 
 def test_activations(x, stream=None, with_expm1=False):

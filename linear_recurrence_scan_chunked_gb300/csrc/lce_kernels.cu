@@ -354,22 +354,23 @@ struct OutEpi {
     __device__ void end(Row&) const {}
 };
 
-// out = max|dloss| * the sum of the parts.  GROUPS warps share 128 (vec) or 32
+// out = scale * (add + the sum of the parts), scale = max|dloss| or, without `top`, 1;
+// add (nullptr: none): fp32, may be `out` itself.  GROUPS warps share 128 (vec) or 32
 // outputs: each adds a run of neighbouring parts in order, and the runs' sums are
 // added in order.
 template <typename S, int GROUPS>
 __global__ void __launch_bounds__(256)
-    k_lce_sum(const float* __restrict__ part, int64_t parts, int64_t pitch, int64_t n, const uint32_t* __restrict__ top,
-              S* __restrict__ out, bool vec) {
+    k_lce_sum(const float* __restrict__ part, int64_t parts, int64_t pitch, int64_t n, const float* add,
+              const uint32_t* __restrict__ top, S* out, bool vec) {
     griddep_launch_dependents();
     griddep_wait();
-    const float a = scale_of(top);
+    const float a = top != nullptr ? scale_of(top) : 1.f;
     constexpr int kLanes = 256 / GROUPS;  // threads of a run
     const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
     const int64_t step = (int64_t)gridDim.x * kLanes, run = (parts + GROUPS - 1) / GROUPS;
     const int64_t k0 = grp * run, k1 = parts < k0 + run ? parts : k0 + run;
     __shared__ float4 sm[GROUPS > 1 ? 256 : 1];
-    auto add = [&](auto width, int64_t base, int64_t count) {
+    auto sum = [&](auto width, int64_t base, int64_t count) {
         constexpr int W = decltype(width)::value;
         for (int64_t i0 = (int64_t)blockIdx.x * kLanes; i0 < count; i0 += step) {
             const int64_t i = i0 + lane;
@@ -377,6 +378,10 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int j = 0; j < W; ++j) s[j] = 0.f;
             if (i < count) {
+                if (add != nullptr && grp == 0) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) s[j] = add[base + W * i + j];
+                }
                 int64_t k = k0;
                 for (; k + 8 <= k1; k += 8) {  // eight loads in flight, added in order
                     Pack<float, W> p[8];
@@ -417,9 +422,9 @@ __global__ void __launch_bounds__(256)
             }
         }
     };
-    if (vec) add(std::integral_constant<int, 4>{}, 0, n / 4);
+    if (vec) sum(std::integral_constant<int, 4>{}, 0, n / 4);
     const int64_t done = vec ? n / 4 * 4 : 0;
-    add(std::integral_constant<int, 1>{}, done, n - done);
+    sum(std::integral_constant<int, 1>{}, done, n - done);
 }
 
 // bf16's largest number in place of finite ones beyond it.
@@ -666,7 +671,7 @@ MmPlan mm_plan(int64_t M, int64_t N, int64_t K, int planes, bool may_split) {
 }
 
 struct Layout {  // offsets into the scratch
-    size_t x, w, top, part, tl, g, px, pw, bytes;
+    size_t x, w, top, part, tl, g, px, acc, pw, bytes;
 };
 
 bool packed(int dtype, const void* p, int64_t D) { return dtype == 0 || D % 8 != 0 || ((uintptr_t)p & 15) != 0; }
@@ -687,7 +692,8 @@ Layout layout(int dtype, const void* x, const void* w, int64_t N, int64_t V, int
     if (packed(dtype, w, D)) l.w = take(at, planes * V * ld * 2);
     if (bwd) {
         l.g = take(at, planes * N * round_up(p.piece, 16) * 2);
-        if (p.dx_parts > 1) l.px = take(at, (size_t)p.dx_parts * round_up(N * D, 8) * 4);
+        if (p.dx_splits > 1 || p.piece < V) l.px = take(at, (size_t)p.dx_splits * round_up(N * D, 8) * 4);
+        if (dtype == 1 && p.piece < V) l.acc = take(at, (size_t)(N * D) * 4);
         if (p.dw_splits > 1) l.pw = take(at, (size_t)p.dw_splits * round_up(p.piece * D, 8) * 4);
     } else {
         l.part = take(at, (size_t)(p.tiles * p.rows) * 8);
@@ -756,8 +762,8 @@ cudaError_t lce_fwd_t(const void* x, const void* w, const int64_t* target, int64
 }
 
 template <typename S>
-cudaError_t sum_parts(const float* part, int64_t parts, int64_t pitch, int64_t n, const uint32_t* top, S* out,
-                      cudaStream_t s) {
+cudaError_t sum_parts(const float* part, int64_t parts, int64_t pitch, int64_t n, const float* add, const uint32_t* top,
+                      S* out, cudaStream_t s) {
     const bool vec = ((uintptr_t)out & (4 * sizeof(S) - 1)) == 0;
     // few outputs: eight warps to a warp's outputs, or the loads of one thread's
     // parts, one round trip for eight, are the time
@@ -765,8 +771,8 @@ cudaError_t sum_parts(const float* part, int64_t parts, int64_t pitch, int64_t n
     const bool few = parts > 8 && items < (int64_t)sm_count() * 512;
     const int64_t lanes = few ? 32 : 256;
     const dim3 grid((unsigned)std::min<int64_t>((items + lanes - 1) / lanes, cap));
-    return few ? launch_dep(k_lce_sum<S, 8>, grid, dim3(256), 0, s, part, parts, pitch, n, top, out, vec)
-               : launch_dep(k_lce_sum<S, 1>, grid, dim3(256), 0, s, part, parts, pitch, n, top, out, vec);
+    return few ? launch_dep(k_lce_sum<S, 8>, grid, dim3(256), 0, s, part, parts, pitch, n, add, top, out, vec)
+               : launch_dep(k_lce_sum<S, 1>, grid, dim3(256), 0, s, part, parts, pitch, n, add, top, out, vec);
 }
 
 template <typename S>
@@ -785,7 +791,9 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
     const int64_t xpitch = round_up(N * D, 8), wpitch = round_up(pl.piece * D, 8);
     const bool wide_s = D * (int64_t)sizeof(S) % 32 == 0, wide_f = D % 8 == 0;
     const uint32_t sum_chunk = OutEpi<true, S>::kChunk;
-    int64_t part = 0;
+    // several pieces: dx grows piece by piece, in fp32, in the order of the vocabulary
+    const bool pieces = pl.piece < V;
+    float* acc = sizeof(S) == 4 ? (float*)dx : (float*)(sc + l.acc);
     for (int64_t v0 = 0; v0 < V; v0 += pl.piece) {
         const int64_t vc = std::min(pl.piece, V - v0), pitch = round_up(vc, 16);
         Operand wp = ow;
@@ -801,15 +809,19 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
         LCE_TRY(sl.kb > mm::chunk_of(P) ? logits(std::true_type{}) : logits(std::false_type{}));
         // dx: rows of x by features, over the words of the piece
         const Shape sx = mm_shape(N, D, vc, false, true, true, MmPlan{pl.tn_dx, pl.dx_splits});
-        const bool dx_direct = pl.dx_parts == 1;
+        const bool dx_direct = pl.dx_splits == 1 && !pieces;
         auto dx_of = [&](auto chunked) {
             return mm_run(og, wp, sx,
-                          OutEpi<decltype(chunked)::value, S>{dx_direct ? (S*)dx : nullptr, px + part * xpitch, xpitch, top, N,
-                                                              D, 0, dx_direct ? wide_s && ((uintptr_t)dx & 31) == 0 : wide_f},
+                          OutEpi<decltype(chunked)::value, S>{dx_direct ? (S*)dx : nullptr, px, xpitch, top, N, D, 0,
+                                                              dx_direct ? wide_s && ((uintptr_t)dx & 31) == 0 : wide_f},
                           pl.tn_dx, err, s);
         };
         LCE_TRY(sx.kb_split > sum_chunk ? dx_of(std::true_type{}) : dx_of(std::false_type{}));
-        part += sx.splits;
+        if (!dx_direct) {
+            const float* before = v0 > 0 ? acc : nullptr;
+            if (v0 + vc < V) LCE_TRY(sum_parts<float>(px, sx.splits, xpitch, N * D, before, nullptr, acc, s));
+            else LCE_TRY(sum_parts<S>(px, sx.splits, xpitch, N * D, before, top, (S*)dx, s));
+        }
         // dw: words of the piece by features, over the rows of x
         const Shape sw = mm_shape(vc, D, N, true, true, true, MmPlan{pl.tn_dw, pl.dw_splits});
         const bool dw_direct = pl.dw_splits == 1;
@@ -821,23 +833,24 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
                           pl.tn_dw, err, s);
         };
         LCE_TRY(sw.kb_split > sum_chunk ? dw_of(std::true_type{}) : dw_of(std::false_type{}));
-        if (!dw_direct) LCE_TRY(sum_parts<S>(pw, sw.splits, wpitch, vc * D, top, dwp, s));
+        if (!dw_direct) LCE_TRY(sum_parts<S>(pw, sw.splits, wpitch, vc * D, nullptr, top, dwp, s));
     }
-    if (pl.dx_parts > 1) LCE_TRY(sum_parts<S>(px, part, xpitch, N * D, top, (S*)dx, s));
     return cudaSuccess;
 }
 
 }  // namespace
 
-LcePlan lce_plan(int dtype, const void* x, const void* w, int64_t N, int64_t V, int64_t D, bool bwd) {
+LcePlan lce_plan(int dtype, const void* x, const void* w, int64_t N, int64_t V, int64_t D, bool bwd, int64_t budget) {
     LcePlan p{};
     const int planes = dtype == 0 ? 3 : 1;
+    if (budget <= 0) budget = kPieceBytes;
     if (!bwd) {
-        p.rows = std::min<int64_t>(N, 16384);
+        // rounds of rows whose pairs (of 128 words at least, but for small problems) fit
+        p.rows = std::min<int64_t>(std::min<int64_t>(N, 16384), std::max<int64_t>(budget / (V / 128 * 8 + 8) / kTile, 1) * kTile);
         p.tn_logits = mm_plan(p.rows, V, D, planes, false).tn;
         p.tiles = (V + p.tn_logits / 2 - 1) / (p.tn_logits / 2);
     } else {
-        p.piece = std::max<int64_t>(kPieceBytes / (N * 2 * planes) / kTile, 1) * kTile;
+        p.piece = std::max<int64_t>(budget / (N * 2 * planes) / kTile, 1) * kTile;
         if (p.piece >= V) p.piece = V;
         p.tn_logits = mm_plan(N, p.piece, D, planes, false).tn;
         const MmPlan dx = mm_plan(N, D, p.piece, planes, true), dw = mm_plan(p.piece, D, N, planes, true);
@@ -845,9 +858,6 @@ LcePlan lce_plan(int dtype, const void* x, const void* w, int64_t N, int64_t V, 
         p.dx_splits = dx.splits;
         p.tn_dw = dw.tn;
         p.dw_splits = dw.splits;
-        p.dx_parts = 0;
-        for (int64_t v0 = 0; v0 < V; v0 += p.piece)
-            p.dx_parts += mm_shape(N, D, std::min(p.piece, V - v0), false, true, true, dx).splits;
     }
     p.bytes = layout(dtype, x, w, N, V, D, p, bwd).bytes;
     return p;

@@ -159,6 +159,7 @@ struct DevWS {
 };
 
 std::mutex g_mu;
+int64_t g_lce_budget = 0;  // lr_test_lce_budget
 std::vector<DevWS*> g_ws;
 
 int get_ws(DevWS** out) {
@@ -673,7 +674,7 @@ int lce_fwd(const void* x, const void* w, const int64_t* target, int64_t ignore,
     TRY(get_ws(&ws));
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
-    const LcePlan pl = lce_plan(dtype, x, w, N, V, D, false);
+    const LcePlan pl = lce_plan(dtype, x, w, N, V, D, false, g_lce_budget);
     TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.bytes, false, true));
     CK(launch_lce_fwd(dtype, x, w, target, ignore, loss, lse, N, V, D, pl, ws->lce, ws->words + kWordErr, s));
     return lv.done();
@@ -699,7 +700,7 @@ int lce_bwd(const void* x, const void* w, const int64_t* target, int64_t ignore,
     TRY(get_ws(&ws));
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
-    const LcePlan pl = lce_plan(dtype, x, w, N, V, D, true);
+    const LcePlan pl = lce_plan(dtype, x, w, N, V, D, true, g_lce_budget);
     TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.bytes, false, true));
     CK(launch_lce_bwd(dtype, x, w, target, ignore, lse, dloss, dx, dw, N, V, D, pl, ws->lce, ws->words + kWordErr, s));
     return lv.done();
@@ -1269,6 +1270,28 @@ int lr_plan_info(int op, int dtype, int vec, int64_t T, int64_t C, int* protocol
     if (tma) *tma = cp.tma ? 1 : 0;
     if (tile_rows) *tile_rows = cp.ts.L;
     if (n_chunks) *n_chunks = cp.n_chunks;
+    return LR_OK;
+}
+
+int lr_test_lce_budget(int64_t bytes) {
+    if (bytes < 0) return LR_ERR_INVALID_ARG;
+    GUARD;
+    g_lce_budget = bytes;
+    return LR_OK;
+}
+
+int lce_plan_info(int bwd, int dtype, int vec, int64_t N, int64_t V, int64_t D, int64_t* rows, int64_t* piece,
+                  int64_t* dx_splits, int64_t* bytes) {
+    TRY(check_sizes(N, V, D, dtype));
+    if (N < 1 || V < 1 || D < 1) return LR_ERR_INVALID_ARG;
+    if (N >= (int64_t)1 << 31 || V >= (int64_t)1 << 31 || D > 65536) return LR_ERR_TOO_LARGE;
+    GUARD;
+    const void* at = (const void*)(uintptr_t)(vec ? 16 : 4);  // an aligned address, or not
+    const LcePlan p = lce_plan(dtype, at, at, N, V, D, bwd != 0, g_lce_budget);
+    if (rows) *rows = bwd ? N : p.rows;
+    if (piece) *piece = bwd ? p.piece : V;
+    if (dx_splits) *dx_splits = bwd ? p.dx_splits : 0;
+    if (bytes) *bytes = (int64_t)p.bytes;
     return LR_OK;
 }
 

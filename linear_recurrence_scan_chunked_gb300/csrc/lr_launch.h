@@ -470,15 +470,15 @@ cudaError_t launch_adamw(AdamKind kind, int gdtype, const AdamTensor* t, int64_t
 struct LcePlan {
     int64_t tiles;      // forward: half tiles of the vocabulary (a pair of statistics each, per row)
     int64_t rows;       // forward: rows per round
-    int tn_logits;      // columns of the products' tiles, 256 or 128
+    int tn_logits;      // columns of the products' tiles: 256 or 128, the logits' also 64
     int tn_dx, tn_dw;
     int64_t piece;      // backward: vocabulary rows per piece
     int64_t dx_splits;  // backward: parts of the k loops
     int64_t dw_splits;
-    int64_t dx_parts;   // parts of dx over all pieces
     size_t bytes;       // scratch
 };
-LcePlan lce_plan(int dtype, const void* x, const void* w, int64_t N, int64_t V, int64_t D, bool bwd);
+// budget: bytes of a piece's gradients of logits, or of a round's statistics (0: 2 GB)
+LcePlan lce_plan(int dtype, const void* x, const void* w, int64_t N, int64_t V, int64_t D, bool bwd, int64_t budget);
 cudaError_t launch_lce_fwd(int dtype, const void* x, const void* w, const int64_t* target, int64_t ignore, float* loss,
                            float* lse, int64_t N, int64_t V, int64_t D, const LcePlan& pl, void* scratch, uint32_t* err,
                            cudaStream_t s);

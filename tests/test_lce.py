@@ -460,3 +460,100 @@ def test_infinitely_masked_words_bf16(cuda):
     rl, rz, _, _ = ref(x, w, t, dl)
     loss, lse = cuda.lce_fwd(x.cuda(), w.cuda(), t.cuda())
     assert mx(loss, rl) <= 1e-5 and mx(lse, rz) <= 1e-5
+
+
+# budget of the scratch, N, D, words past two whole pieces
+PIECES = [(1 << 20, 70, 96, 1), (1 << 20, 70, 33, 700), (1 << 20, 1, 64, 5), (8 << 20, 2560, 2048, 300),
+          (1 << 18, 129, 250, 255)]
+
+
+def pieced(budget, N, D, more, dtype):
+    """(V, plan) of a problem of two whole pieces and a last one of `more` words."""
+    lrs.test_lce_budget(budget)
+    V = 2 * lrs.lce_plan_info(True, dtype, True, N, 1 << 30, D)["piece"] + more
+    return V, lrs.lce_plan_info(True, dtype, True, N, V, D)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("budget,N,D,more", PIECES)
+def test_pieces_of_the_vocabulary(cuda, budget, N, D, more, dtype):
+    """The gradients in three pieces, the last one ragged or a single word, with dx
+    summed over them, and targets in each."""
+    try:
+        V, _ = pieced(budget, N, D, more, dtype)
+        if V * D > 1 << 26:  # a few rows make long pieces
+            V = (1 << 26) // D
+        x, w, t, dl = make(N, V, D, dtype, seed=19)
+        t[0], t[N // 2], t[N - 1] = V - 1, 0, V - 1
+        xd, wd, td, dd = (v.cuda() for v in (x, w, t, dl))
+        loss, lse = cuda.lce_fwd(xd, wd, td)
+        dx, dw = cuda.lce_bwd(xd, wd, td, lse, dd)
+        again = cuda.lce_bwd(xd, wd, td, lse, dd, dx=torch.full_like(dx, 9.0), dw=torch.full_like(dw, 9.0))
+        assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+    finally:
+        lrs.test_lce_budget(0)
+    xg, wg, tg, dg = xd.double(), wd.double(), td, dd.double()  # the fp64 form on the GPU: the largest is 5e10 products
+    l = xg @ wg.T
+    live = tg != -100
+    at = torch.where(live, tg, 0)[:, None]
+    rl = torch.where(live, torch.logsumexp(l, 1) - l.gather(1, at)[:, 0], 0.0)
+    g = torch.exp(l - lse.double()[:, None]).scatter_add(1, at, -torch.ones_like(l[:, :1]))
+    g *= torch.where(live, dg, 0.0)[:, None]
+    rdx, rdw = (g @ wg).cpu(), (g.T @ xg).cpu()
+    assert mx(loss, rl.cpu()) <= 1e-5
+    e = 2.0 ** -21 * float(l.abs().max())
+    p = torch.softmax(l, 1) * torch.where(live, dg, 0.0)[:, None]
+    sx = e * float((p.abs() @ wg.abs()).norm()) / float(rdx.norm())
+    sw = e * float((p.abs().T @ xg.abs()).norm()) / float(rdw.norm())
+    assert dist(dx, rdx) <= GTOL[dtype] + sx and dist(dw, rdw) <= GTOL[dtype] + sw
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rounds_of_rows(cuda, dtype):
+    N, V, D = 1300, 2000, 72
+    x, w, t, dl = make(N, V, D, dtype, seed=20)
+    rl, rz, _, _ = ref(x, w, t, dl)
+    want = cuda.lce_fwd(x.cuda(), w.cuda(), t.cuda())
+    try:
+        lrs.test_lce_budget(1 << 16)
+        assert lrs.lce_plan_info(False, dtype, True, N, V, D)["rows"] == 512
+        loss, lse = cuda.lce_fwd(x.cuda(), w.cuda(), t.cuda())
+    finally:
+        lrs.test_lce_budget(0)
+    assert mx(loss, rl) <= 1e-5 and mx(lse, rz) <= 1e-5
+    assert mx(loss, want[0].cpu()) <= 1e-6
+
+
+def test_plans_and_scratch():
+    """The shapes above take several pieces, with and without parts of dx; the scratch
+    of large problems is what the header states, whatever the number of pieces."""
+    try:
+        seen = set()
+        for budget, N, D, more in PIECES:
+            for dtype in ("f32", "bf16"):
+                V, plan = pieced(budget, N, D, more, dtype)
+                assert V == 2 * plan["piece"] + more
+                seen.add(plan["dx_splits"] > 1)
+        assert seen == {False, True}
+    finally:
+        lrs.test_lce_budget(0)
+    for dtype, es, planes in (("bf16", 2, 1), ("f32", 4, 3)):
+        for N, V, D in ((8192, 65536, 1024), (32768, 131072, 4096), (131072, 131072, 4096), (65536, 131072, 4096),
+                        (1 << 20, 50000, 1024), (1, 1 << 24, 64), (4096, 1 << 20, 4096)):
+            p = lrs.lce_plan_info(True, dtype, True, N, V, D)
+            g = max(2 << 30, 256 * N * 2 * planes)
+            packed = 6 * (N + V) * D if dtype == "f32" else 0
+            several = p["piece"] < V
+            parts = 4 * N * D * (p["dx_splits"] if several or p["dx_splits"] > 1 else 0)
+            acc = 4 * N * D if several and dtype == "bf16" else 0
+            assert p["bytes"] <= g + packed + parts + acc + (256 << 20), (dtype, N, V, D, p)
+            assert p["dx_splits"] <= 2 or N * D <= 1 << 24
+            f = lrs.lce_plan_info(False, dtype, True, N, V, D)
+            assert f["bytes"] <= packed + (2 << 30) + (64 << 20)
+    with pytest.raises(ValueError):
+        lrs.lce_plan_info(True, "f16", True, 1, 1, 1)
+    with pytest.raises(ValueError):
+        lrs.lce_plan_info(True, "f32", True, 0, 1, 1)
+    assert lrs.test_lce_budget(-1) == lrs.LR_ERR_INVALID_ARG

@@ -77,9 +77,9 @@
  *    result on every replay, with whatever the captured buffers hold then.  Make one uncaptured call of the same shape first
  *    (it sizes the workspace and sets up the kernels; capture fails if the
  *    workspace would have to grow).  A graph keeps using the workspace
- *    buffers it captured: the carry packets and the bias partials that a
- *    later, larger call outgrows are kept, not freed, until the process
- *    exits (lr_workspace_bytes counts the current ones only).  A captured
+ *    buffers it captured: one that a later, larger call outgrows is kept until the
+ *    process exits where a graph captured a call that uses it, and freed otherwise
+ *    (lr_workspace_bytes counts the current ones only).  A captured
  *    call is ordered, when the graph runs, by the stream the graph is
  *    launched on only: do not run it concurrently with other calls on the
  *    same device.  The DEER solves read residuals back on the host and

@@ -137,6 +137,7 @@ int cuda_fail(cudaError_t e) {
 // error word, DEER residual slots and second iterate, SRU bias partials.
 struct DevWS {
     u64* pk = nullptr;           size_t pk_cap = 0;        // carry packets (state, aggregate)
+    bool pk_held = false, partials_held = false, lce_held = false;  // a graph captured the buffer
     uint32_t* words = nullptr;   // ticket word, error bits, DEER residual slots (kWord*)
     float* partials = nullptr;   size_t partials_cap = 0; // floats
     void* ybuf = nullptr;        size_t ybuf_cap = 0;     // bytes
@@ -180,20 +181,30 @@ int get_ws(DevWS** out) {
     return LR_OK;
 }
 
-// Grow a workspace buffer to hold `need` elements.  keep: the outgrown buffer
-// is kept until the process exits instead of freed -- a CUDA graph that
-// captured a launch holds its address (the carry packets, the bias partials).
+bool capturing(cudaStream_t s) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    return cudaStreamIsCapturing(s, &cs) == cudaSuccess && cs != cudaStreamCaptureStatusNone;
+}
+
+// Grow a workspace buffer to hold `need` elements.  held: given for the buffers that a
+// call on stream `s` may use under capture, and set once it does -- the CUDA graph holds
+// the buffer's address, so that it is kept until the process exits when it is outgrown.
+// Any other outgrown buffer is freed.
 template <typename T>
-int grow(DevWS& ws, T** p, size_t* cap, size_t need, bool zero, bool keep = false) {
-    if (need <= *cap) return LR_OK;
+int grow(DevWS& ws, T** p, size_t* cap, size_t need, bool zero, bool* held = nullptr, cudaStream_t s = nullptr) {
+    if (need <= *cap) {
+        if (held && !*held) *held = capturing(s);
+        return LR_OK;
+    }
     size_t n = need + need / 4;
     CK(cudaDeviceSynchronize());  // nothing in flight may still use the old buffer
     if (*p) {
-        if (keep) {
+        ws.bytes -= (int64_t)(*cap * sizeof(T));
+        if (held && *held) {
             ws.kept.push_back(*p);
+            *held = false;
         } else {
             CK(cudaFree(*p));
-            ws.bytes -= (int64_t)(*cap * sizeof(T));
         }
     }
     *p = nullptr;
@@ -208,10 +219,6 @@ int grow(DevWS& ws, T** p, size_t* cap, size_t need, bool zero, bool keep = fals
 // Order this call after the previous call on any other stream.  A call
 // being captured into a CUDA graph is not ordered here: when the graph runs,
 // the stream it is launched on orders it.
-bool capturing(cudaStream_t s) {
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    return cudaStreamIsCapturing(s, &cs) == cudaSuccess && cs != cudaStreamCaptureStatusNone;
-}
 int enter(DevWS& ws, cudaStream_t s) {
     if (capturing(s)) return LR_OK;
     if (ws.has_last && ws.last_stream != s) CK(cudaStreamWaitEvent(s, ws.done, 0));
@@ -275,7 +282,7 @@ int plan(DevWS& ws, Op op, int dtype, bool vec, int64_t T, int64_t C, int64_t D,
     g->n_draws = 0;  // set by the launcher from the grid it picks
     g->ticket_base = 0;
     g->max_grid = 0;
-    int st = grow(ws, &ws.pk, &ws.pk_cap, cp.inc_elems + cp.agg_elems, true, true);
+    int st = grow(ws, &ws.pk, &ws.pk_cap, cp.inc_elems + cp.agg_elems, true, &ws.pk_held, s);
     if (st) return st;
     st = count_launch(ws, s);
     if (st) return st;
@@ -434,8 +441,7 @@ int sru_bwd(const void* xt, const void* uf, const void* ur, const void* x, const
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
     TRY(plan(*ws, OP_SRU_BWD, dtype, vec, T, B * D, D, &g, &cr, s));
-    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(2 * g.n_chunks * g.C + 2 * g.C), false,
-             true));
+    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(2 * g.n_chunks * g.C + 2 * g.C), false, &ws->partials_held, s));
     CK(launch_sru_bwd(dtype, vec, xt, uf, ur, x, bf, br, c0, c, dh, dxt, duf, dur, dx, dc0,
                       ws->partials, g, cr, s));
     CK(launch_bias_reduce(ws->partials, g.n_chunks, 2, B, D, BiasOut{{dbf, dbr}}, s));
@@ -492,8 +498,7 @@ int lstm_cell_bwd(const void* zf, const void* zi, const void* zc, const void* zo
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
     TRY(plan(*ws, OP_LSTM_BWD, dtype, vec, T, B * D, D, &g, &cr, s));
-    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(4 * g.n_chunks * g.C + 4 * g.C), false,
-             true));
+    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(4 * g.n_chunks * g.C + 4 * g.C), false, &ws->partials_held, s));
     CK(launch_lstm_bwd(dtype, vec, LstmGates{zf, zi, zc, zo}, LstmBias{bf, bi, bc, bo}, c0, c, dh,
                        LstmGates{dzf, dzi, dzc, dzo}, dc0, ws->partials, g, cr, s));
     CK(launch_bias_reduce(ws->partials, g.n_chunks, 4, B, D, BiasOut{{dbf, dbi, dbc, dbo}}, s));
@@ -524,7 +529,7 @@ int glr_fwd(const void* x, const void* zr, const void* zi, const float* lam, con
     Leave lv(*ws, s);
     const GlrSpans pl = glr_spans(false, dtype, vec, T, B * D);
     if (pl.S * pl.n_ct > INT32_MAX || pl.n_chunks > INT32_MAX || B * D > kSpanMaxChannels) return LR_ERR_TOO_LARGE;
-    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(2 * pl.S * B * D), false, true));
+    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(2 * pl.S * B * D), false, &ws->partials_held, s));
     CK(launch_glr_fwd(dtype, pl, GlrIn{x, zr, zi, lam, br, bi, reset}, h0, h, h_last, ws->partials, T, B * D, D,
                       ws->words + kWordErr, s));
     return lv.done();
@@ -562,7 +567,7 @@ int glr_bwd(const void* x, const void* zr, const void* zi, const float* lam, con
     Leave lv(*ws, s);
     const GlrSpans pl = glr_spans(true, dtype, vec, T, B * D);
     if (pl.S * pl.n_ct > INT32_MAX || pl.n_chunks > INT32_MAX || B * D > kSpanMaxChannels) return LR_ERR_TOO_LARGE;
-    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(5 * pl.S * B * D + 3 * B * D), false, true));
+    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(5 * pl.S * B * D + 3 * B * D), false, &ws->partials_held, s));
     CK(launch_glr_bwd(dtype, pl, GlrIn{x, zr, zi, lam, br, bi, reset}, h0, h, dh, dh_last, dx, dzr, dzi, dh0,
                       ws->partials, T, B * D, D, ws->words + kWordErr, s));
     CK(launch_bias_reduce(ws->partials + 2 * pl.S * B * D, pl.S, 3, B, D, BiasOut{{dlam, dbr, dbi, nullptr}}, s));
@@ -647,7 +652,7 @@ int layer_norm_bwd(const void* x, const float* w, const float* mean, const float
     TRY(get_ws(&ws));
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
-    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)2 * kLnMaxPartials * D, false, true));
+    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)2 * kLnMaxPartials * D, false, &ws->partials_held, s));
     CK(launch_ln_bwd(dtype, vec, x, w, mean, rstd, dy, dres, dx, dw, db, ws->partials, N, D, s));
     return lv.done();
 }
@@ -675,7 +680,7 @@ int lce_fwd(const void* x, const void* w, const int64_t* target, int64_t ignore,
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
     const LcePlan pl = lce_plan(dtype, x, w, N, V, D, false, g_lce_budget);
-    TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.bytes, false, true));
+    TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.bytes, false, &ws->lce_held, s));
     CK(launch_lce_fwd(dtype, x, w, target, ignore, loss, lse, N, V, D, pl, ws->lce, ws->words + kWordErr, s));
     return lv.done();
 }
@@ -701,7 +706,7 @@ int lce_bwd(const void* x, const void* w, const int64_t* target, int64_t ignore,
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
     const LcePlan pl = lce_plan(dtype, x, w, N, V, D, true, g_lce_budget);
-    TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.bytes, false, true));
+    TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.bytes, false, &ws->lce_held, s));
     CK(launch_lce_bwd(dtype, x, w, target, ignore, lse, dloss, dx, dw, N, V, D, pl, ws->lce, ws->words + kWordErr, s));
     return lv.done();
 }
@@ -846,7 +851,7 @@ static int onepass_begin(DevWS& ws, Op op, int dtype, bool vec, int64_t T, int64
     *cp = carry_plan(op, dtype, vec, use_tma(dtype, vec, T, C), T, C);
     *on = cp->mode == CARRY_WALK && cp->tma;
     if (!*on) return LR_OK;
-    TRY(grow(ws, &ws.pk, &ws.pk_cap, cp->inc_elems + 2 * cp->agg_elems, true, true));
+    TRY(grow(ws, &ws.pk, &ws.pk_cap, cp->inc_elems + 2 * cp->agg_elems, true, &ws.pk_held, s));
     if (ws.launches + (uint64_t)kmax + 8 >= kEpochClear) TRY(count_launch(ws, s, kEpochClear));
     return LR_OK;
 }
@@ -1187,7 +1192,7 @@ int deer_diag_bwd(const float* w, const void* y, const void* h0, const void* dy,
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
     TRY(plan(*ws, OP_DEER_BWD, dtype, vec, T, B * D, D, &g, &cr, s));
-    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(g.n_chunks * g.C + g.C), false, true));
+    TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(g.n_chunks * g.C + g.C), false, &ws->partials_held, s));
     CK(launch_deer_bwd(dtype, vec, w, y, h0, dy, du, dh0, ws->partials, g, cr, s));
     CK(launch_bias_reduce(ws->partials, g.n_chunks, 1, B, D, BiasOut{{dw}}, s));
     return lv.done();

@@ -557,3 +557,55 @@ def test_plans_and_scratch():
     with pytest.raises(ValueError):
         lrs.lce_plan_info(True, "f32", True, 0, 1, 1)
     assert lrs.test_lce_budget(-1) == lrs.LR_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+def test_outgrown_scratch_is_given_back(cuda):
+    """Batches that grow slowly, in a process of their own: what the library holds on
+    the device is its current scratch, not the sum of all that it outgrew; what a graph
+    has captured stays, and the graph's replay is right after the scratch has moved."""
+    import os
+    import subprocess
+    import sys
+    code = r"""
+import torch, linear_recurrence_scan_chunked_gb300 as lrs
+V, D, N = 20000, 64, 6000
+w, x = torch.randn(V, D, device="cuda"), torch.randn(N, D, device="cuda")
+t, dl = torch.zeros(N, dtype=torch.int64, device="cuda"), torch.ones(N, device="cuda")
+dx, dw, loss, lse = torch.empty_like(x), torch.empty_like(w), torch.empty_like(dl), torch.empty_like(dl)
+def call(n, x=x, dx=dx):
+    lrs.lce_fwd(x[:n], w, t[:n], loss=loss[:n], lse=lse[:n])
+    lrs.lce_bwd(x[:n], w, t[:n], lse[:n], dl[:n], dx=dx[:n], dw=dw)
+call(8)  # the kernels are loaded
+torch.cuda.synchronize()
+free, held = torch.cuda.mem_get_info()[0], lrs.workspace_bytes()
+for n in (1000, 1500, 2000, 2600, 3400, 4500):
+    call(n)
+torch.cuda.synchronize()
+used, grown = free - torch.cuda.mem_get_info()[0], lrs.workspace_bytes() - held
+need = 1.25 * lrs.lce_plan_info(True, "f32", True, 4500, V, D)["bytes"]
+assert 200 << 20 < need, need
+assert grown <= need, (grown, need)
+assert used <= need + (64 << 20), (used, need)
+g = torch.cuda.CUDAGraph()
+gx, gdx = x[:100].clone(), torch.empty_like(x[:100])
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    call(100, gx, gdx)
+torch.cuda.synchronize()
+before = torch.cuda.mem_get_info()[0]
+call(6000)  # outgrows what the graph uses
+torch.cuda.synchronize()
+assert before - torch.cuda.mem_get_info()[0] >= lrs.lce_plan_info(True, "f32", True, 6000, V, D)["bytes"]
+call(100, gx, gdx)
+torch.cuda.synchronize()
+want, want_w = gdx.clone(), dw.clone()
+gdx.zero_(), dw.zero_()
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(gdx, want) and torch.equal(dw, want_w)
+assert lrs.last_error() == lrs.LR_OK
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(lrs.__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr

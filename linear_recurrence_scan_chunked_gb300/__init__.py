@@ -12,6 +12,7 @@ Tensors are CUDA, contiguous, [T, B, D] for sequences, [B, D] for states and
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.util
 import os
@@ -171,12 +172,28 @@ def _param(name, t, D, ref):
     return t
 
 
+def _like(t, stream):
+    """An output like t, of the memory of the stream that writes it: what the
+    allocator has taken back on the current stream may still be in use there."""
+    with _on(stream):
+        return torch.empty_like(t)
+
+
+def _new(shape, dtype, ref, stream):
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=ref.device)
+
+
+def _on(stream):
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def lr_scan_fwd(a, b, h0=None, h=None, stream=None):
     """h_t = a_t * h_{t-1} + b_t (h_{-1} = h0). Returns h."""
     _seq("a", a)
     _seq("b", b, a)
     _state("h0", h0, a)
-    h = torch.empty_like(a) if h is None else _seq("h", h, a)
+    h = _like(a, stream) if h is None else _seq("h", h, a)
     T, B, D = a.shape
     _check(load().lr_scan_fwd(_p(a), _p(b), _p(h0), _p(h), B, T, D, _code(a), _stream(stream, a)))
     return h
@@ -189,10 +206,10 @@ def lr_scan_bwd(a, h, dh, h0=None, da=None, db=None, dh0=None, want_dh0=True, st
     _seq("dh", dh, a)
     _state("h0", h0, a)
     T, B, D = a.shape
-    da = torch.empty_like(a) if da is None else _seq("da", da, a)
-    db = torch.empty_like(a) if db is None else _seq("db", db, a)
+    da = _like(a, stream) if da is None else _seq("da", da, a)
+    db = _like(a, stream) if db is None else _seq("db", db, a)
     if dh0 is None and want_dh0:
-        dh0 = torch.empty((B, D), dtype=a.dtype, device=a.device)
+        dh0 = _new((B, D), a.dtype, a, stream)
     _state("dh0", dh0, a)
     _check(load().lr_scan_bwd(_p(a), _p(h), _p(h0), _p(dh), _p(da), _p(db), _p(dh0), B, T, D,
                               _code(a), _stream(stream, a)))
@@ -208,8 +225,8 @@ def sru_fwd(xt, uf, ur, x, bf, br, c0=None, h=None, c=None, stream=None):
     _param("bf", bf, D, xt)
     _param("br", br, D, xt)
     _state("c0", c0, xt)
-    h = torch.empty_like(xt) if h is None else _seq("h", h, xt)
-    c = torch.empty_like(xt) if c is None else _seq("c", c, xt)
+    h = _like(xt, stream) if h is None else _seq("h", h, xt)
+    c = _like(xt, stream) if c is None else _seq("c", c, xt)
     _check(load().sru_fwd(_p(xt), _p(uf), _p(ur), _p(x), _p(bf), _p(br), _p(c0), _p(h), _p(c),
                           B, T, D, _code(xt), _stream(stream, xt)))
     return h, c
@@ -226,11 +243,11 @@ def sru_bwd(xt, uf, ur, x, bf, br, c, dh, c0=None, out=None, want_dc0=True, stre
     _state("c0", c0, xt)
     o = dict(out or {})
     for k in ("dxt", "duf", "dur", "dx"):
-        o[k] = torch.empty_like(xt) if o.get(k) is None else _seq(k, o[k], xt)
+        o[k] = _like(xt, stream) if o.get(k) is None else _seq(k, o[k], xt)
     for k in ("dbf", "dbr"):
-        o[k] = torch.empty(D, dtype=torch.float32, device=xt.device) if o.get(k) is None else _param(k, o[k], D, xt)
+        o[k] = _new(D, torch.float32, xt, stream) if o.get(k) is None else _param(k, o[k], D, xt)
     if o.get("dc0") is None and want_dc0:
-        o["dc0"] = torch.empty((B, D), dtype=xt.dtype, device=xt.device)
+        o["dc0"] = _new((B, D), xt.dtype, xt, stream)
     _state("dc0", o.get("dc0"), xt)
     _check(load().sru_bwd(_p(xt), _p(uf), _p(ur), _p(x), _p(bf), _p(br), _p(c0), _p(c), _p(dh),
                           _p(o["dxt"]), _p(o["duf"]), _p(o["dur"]), _p(o["dx"]), _p(o["dbf"]),
@@ -248,8 +265,8 @@ def lstm_cell_fwd(zf, zi, zc, zo, bf, bi, bc, bo, c0=None, h=None, c=None, strea
     for n, t in (("bf", bf), ("bi", bi), ("bc", bc), ("bo", bo)):
         _param(n, t, D, zf)
     _state("c0", c0, zf)
-    h = torch.empty_like(zf) if h is None else _seq("h", h, zf)
-    c = torch.empty_like(zf) if c is None else _seq("c", c, zf)
+    h = _like(zf, stream) if h is None else _seq("h", h, zf)
+    c = _like(zf, stream) if c is None else _seq("c", c, zf)
     _check(load().lstm_cell_fwd(_p(zf), _p(zi), _p(zc), _p(zo), _p(bf), _p(bi), _p(bc), _p(bo),
                                 _p(c0), _p(h), _p(c), B, T, D, _code(zf), _stream(stream, zf)))
     return h, c
@@ -267,11 +284,11 @@ def lstm_cell_bwd(zf, zi, zc, zo, bf, bi, bc, bo, c, dh, c0=None, out=None, want
     _state("c0", c0, zf)
     o = dict(out or {})
     for k in ("dzf", "dzi", "dzc", "dzo"):
-        o[k] = torch.empty_like(zf) if o.get(k) is None else _seq(k, o[k], zf)
+        o[k] = _like(zf, stream) if o.get(k) is None else _seq(k, o[k], zf)
     for k in ("dbf", "dbi", "dbc", "dbo"):
-        o[k] = torch.empty(D, dtype=torch.float32, device=zf.device) if o.get(k) is None else _param(k, o[k], D, zf)
+        o[k] = _new(D, torch.float32, zf, stream) if o.get(k) is None else _param(k, o[k], D, zf)
     if o.get("dc0") is None and want_dc0:
-        o["dc0"] = torch.empty((B, D), dtype=zf.dtype, device=zf.device)
+        o["dc0"] = _new((B, D), zf.dtype, zf, stream)
     _state("dc0", o.get("dc0"), zf)
     _check(load().lstm_cell_bwd(_p(zf), _p(zi), _p(zc), _p(zo), _p(bf), _p(bi), _p(bc), _p(bo),
                                 _p(c0), _p(c), _p(dh), _p(o["dzf"]), _p(o["dzi"]), _p(o["dzc"]),
@@ -290,7 +307,7 @@ def deer_diag_solve(w, u, h0=None, y=None, eps=1e-5, kmax=20, stream=None):
     T, B, D = u.shape
     _param("w", w, D, u)
     _state("h0", h0, u)
-    y = torch.empty_like(u) if y is None else _seq("y", y, u)
+    y = _like(u, stream) if y is None else _seq("y", y, u)
     iters = ctypes.c_int(0)
     resid = ctypes.c_float(0.0)
     hist = (ctypes.c_float * max(1, int(kmax)))()
@@ -315,7 +332,7 @@ def deer_diag_solve_ex(w, u, h0=None, y=None, y_init=None, eps=1e-5, kmax=20,
     _state("h0", h0, u)
     if y_init is not None:
         _seq("y_init", y_init, u)
-    y = torch.empty_like(u) if y is None else _seq("y", y, u)
+    y = _like(u, stream) if y is None else _seq("y", y, u)
     it = ctypes.c_int(0)
     rho = ctypes.c_float(0.0)
     hist = (ctypes.c_float * int(kmax))()
@@ -342,7 +359,7 @@ def deer_ode_solve(w, u, dt, h0=None, y=None, eps=1e-5, kmax=20, stream=None):
     _param("w", w, D, u)
     _param("dt", dt, T, u)
     _state("h0", h0, u)
-    y = torch.empty_like(u) if y is None else _seq("y", y, u)
+    y = _like(u, stream) if y is None else _seq("y", y, u)
     iters = ctypes.c_int(0)
     resid = ctypes.c_float(0.0)
     clamps = ctypes.c_int64(0)
@@ -364,10 +381,10 @@ def deer_diag_bwd(w, y, dy, h0=None, du=None, dw=None, dh0=None, want_dh0=True, 
     T, B, D = y.shape
     _param("w", w, D, y)
     _state("h0", h0, y)
-    du = torch.empty_like(y) if du is None else _seq("du", du, y)
-    dw = torch.empty(D, dtype=torch.float32, device=y.device) if dw is None else _param("dw", dw, D, y)
+    du = _like(y, stream) if du is None else _seq("du", du, y)
+    dw = _new(D, torch.float32, y, stream) if dw is None else _param("dw", dw, D, y)
     if dh0 is None and want_dh0:
-        dh0 = torch.empty((B, D), dtype=y.dtype, device=y.device)
+        dh0 = _new((B, D), y.dtype, y, stream)
     _state("dh0", dh0, y)
     _check(load().deer_diag_bwd(_p(w), _p(y), _p(h0), _p(dy), _p(du), _p(dw), _p(dh0), B, T, D,
                                 _code(y), _stream(stream, y)))
@@ -484,7 +501,7 @@ def adamw8_step(params, grads, m, v, ms, vs, step, lr, seed, beta1=0.9, beta2=0.
 def adamw8_values(mq, vq, ms, vs, m=None, v=None, stream=None):
     """The fp32 values that 8-bit moments stand for. Returns (m, v), lists of
     1-d tensors unless given."""
-    e = lambda: [torch.empty(t.numel(), dtype=torch.float32, device=t.device) for t in mq]
+    e = lambda: [_new(t.numel(), torch.float32, t, stream) for t in mq]
     m = e() if m is None else m
     v = e() if v is None else v
     native().adamw8_values(mq, vq, ms, vs, m, v, stream)
@@ -551,8 +568,8 @@ def test_activations(x, stream=None, with_expm1=False):
     expm1)."""
     if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous fp32 CUDA tensor")
-    th, sg = torch.empty_like(x), torch.empty_like(x)
-    em = torch.empty_like(x) if with_expm1 else None
+    th, sg = _like(x, stream), _like(x, stream)
+    em = _like(x, stream) if with_expm1 else None
     _check(load().lr_test_activations(_p(x), _p(th), _p(sg), _p(em), x.numel(), _stream(stream, x)))
     return (th, sg, em) if with_expm1 else (th, sg)
 

@@ -7,6 +7,7 @@
 // neither float32 nor bfloat16), library statuses go to the package's _check.
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <pybind11/pybind11.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -89,6 +90,16 @@ void* stream_on(const py::object& s, int dev) {
         throw py::value_error("the stream belongs to cuda:" + std::to_string(sd) + ", the tensors to cuda:" + std::to_string(dev));
     return (void*)s.attr("cuda_stream").cast<uintptr_t>();
 }
+// The call's stream, current while its outputs are allocated: memory that another
+// stream may still be reading (the allocator's, taken back there) is none to write on it.
+struct OnStream {
+    void* s;
+    c10::cuda::OptionalCUDAStreamGuard guard;
+    OnStream(const py::object& stream, int dev) : s(stream_on(stream, dev)) {
+        if (!stream.is_none())
+            guard.reset_stream(c10::cuda::getStreamFromExternal((cudaStream_t)s, (c10::DeviceIndex)dev));
+    }
+};
 void check(int st) {
     if (st == LR_OK) return;
     py::module_::import("linear_recurrence_scan_chunked_gb300").attr("_check")(st);
@@ -131,13 +142,13 @@ py::tuple p_glr_fwd(py::object x_, py::object zr, py::object zi, py::object lam,
     const float* p0 = (const float*)opt("h0", h0, st, at::kFloat, dev);
     const uint8_t* rs = flags(reset, x.sizes().slice(0, 2), dev);
     const int dt = code(x);
+    const OnStream on(stream, dev);
     const Tensor h = make(arg("h", h_), x.sizes(), x.scalar_type(), x);
     Tensor last = arg("h_last", last_);
     if (!last.defined() && want_last) last = make(last, st, at::kFloat, x);
     void* ph = like("h", h, x.sizes(), x.scalar_type(), dev);
     float* pl = (float*)opt("h_last", last, st, at::kFloat, dev);
-    void* s = stream_on(stream, dev);
-    call([&] { return glr_fwd(a.x, a.zr, a.zi, a.lam, a.br, a.bi, p0, rs, ph, pl, B, T, D, dt, s); });
+    call([&] { return glr_fwd(a.x, a.zr, a.zi, a.lam, a.br, a.bi, p0, rs, ph, pl, B, T, D, dt, on.s); });
     return py::make_tuple(wrap(h), wrap(last));
 }
 
@@ -157,6 +168,7 @@ py::tuple p_glr_bwd(py::object x_, py::object zr, py::object zi, py::object lam_
     const void* pdh = like("dh", need("dh", dh_), sq, t, dev);
     const float* pdl = (const float*)opt("dh_last", dlast, st, at::kFloat, dev);
     const int dt = code(x);
+    const OnStream on(stream, dev);
     static const char* names[7] = {"dx", "dzr", "dzi", "dlam", "dbr", "dbi", "dh0"};
     Tensor o[7];
     void* p[7];
@@ -167,10 +179,9 @@ py::tuple p_glr_bwd(py::object x_, py::object zr, py::object zi, py::object lam_
         if (k < 6 || want_dh0) o[k] = make(o[k], shape, type, x);
         p[k] = opt(names[k], o[k], shape, type, dev);
     }
-    void* s = stream_on(stream, dev);
     call([&] {
         return glr_bwd(a.x, a.zr, a.zi, a.lam, a.br, a.bi, p0, rs, ph, pdh, pdl, p[0], p[1], p[2], (float*)p[3], (float*)p[4],
-                       (float*)p[5], (float*)p[6], B, T, D, dt, s);
+                       (float*)p[5], (float*)p[6], B, T, D, dt, on.s);
     });
     return py::make_tuple(wrap(o[0]), wrap(o[1]), wrap(o[2]), wrap(o[3]), wrap(o[4]), wrap(o[5]), wrap(o[6]));
 }
@@ -188,10 +199,10 @@ py::object p_glr_step(py::object x_, py::object zr, py::object zi, py::object la
     const uint8_t* rs = flags(reset, x.sizes().slice(0, 1), dev);
     const int32_t* psl = (const int32_t*)opt("slots", slots, x.sizes().slice(0, 1), at::kInt, dev);
     const int dt = code(x);
+    const OnStream on(stream, dev);
     const Tensor h = make(arg("h", h_), x.sizes(), x.scalar_type(), x);
     void* ph = like("h", h, x.sizes(), x.scalar_type(), dev);
-    void* s = stream_on(stream, dev);
-    call([&] { return glr_step(a.x, a.zr, a.zi, a.lam, a.br, a.bi, rs, psl, ps, ph, B, n_slots, D, dt, s); });
+    call([&] { return glr_step(a.x, a.zr, a.zi, a.lam, a.br, a.bi, rs, psl, ps, ph, B, n_slots, D, dt, on.s); });
     return wrap(h);
 }
 
@@ -209,16 +220,16 @@ py::tuple p_layer_norm_fwd(py::object x_, py::object w_, py::object b_, py::obje
     Tensor sum = arg("s", s_);
     if (sum.defined() && !res.defined()) throw py::value_error("s is an output of the residual add: give res with it");
     const int dt = code(x);
+    const OnStream on(stream, dev);
     if (res.defined()) sum = make(sum, shape, t, x);
     const Tensor y = make(arg("y", y_), shape, t, x), mean = make(Tensor(), row, at::kFloat, x),
                  rstd = make(Tensor(), row, at::kFloat, x);
     void* py_ = like("y", y, shape, t, dev);
     void* psum = opt("s", sum, shape, t, dev);
-    void* s = stream_on(stream, dev);
     const int64_t N = mean.numel(), D = d[0];
     call([&] {
         return layer_norm_fwd(x.data_ptr(), pr, pw, pb, py_, psum, mean.data_ptr<float>(), rstd.data_ptr<float>(), N, D,
-                              (float)eps, dt, s);
+                              (float)eps, dt, on.s);
     });
     if (!res.defined()) return py::make_tuple(wrap(y), wrap(mean), wrap(rstd));
     return py::make_tuple(wrap(y), wrap(mean), wrap(rstd), wrap(sum));
@@ -237,14 +248,14 @@ py::tuple p_layer_norm_bwd(py::object x_, py::object w_, py::object mean_, py::o
     const void* pdy = like("dy", need("dy", dy_), shape, t, dev);
     const void* pr = opt("dres", dres, shape, t, dev);
     const int dt = code(x);
+    const OnStream on(stream, dev);
     const Tensor dx = make(arg("dx", dx_), shape, t, x), dw = make(arg("dw", dw_), d, at::kFloat, x),
                  db = make(arg("db", db_), d, at::kFloat, x);
     void* pdx = like("dx", dx, shape, t, dev);
     float* pdw = (float*)like("dw", dw, d, at::kFloat, dev);
     float* pdb = (float*)like("db", db, d, at::kFloat, dev);
-    void* s = stream_on(stream, dev);
     const int64_t N = mean.numel(), D = d[0];
-    call([&] { return layer_norm_bwd(x.data_ptr(), pw, pm, pq, pdy, pr, pdx, pdw, pdb, N, D, dt, s); });
+    call([&] { return layer_norm_bwd(x.data_ptr(), pw, pm, pq, pdy, pr, pdx, pdw, pdb, N, D, dt, on.s); });
     return py::make_tuple(wrap(dx), wrap(dw), wrap(db));
 }
 
@@ -271,12 +282,12 @@ py::tuple p_lce_fwd(py::object x_, py::object w_, py::object t_, int64_t ignore,
     const LceArgs a = lce_args(x_, w_, t_);
     const IntArrayRef row = a.target.sizes();
     const int dt = code(a.x);
+    const OnStream on(stream, a.dev);
     const Tensor loss = make(arg("loss", loss_), row, at::kFloat, a.x), lse = make(arg("lse", lse_), row, at::kFloat, a.x);
     float* pl = (float*)like("loss", loss, row, at::kFloat, a.dev);
     float* pz = (float*)like("lse", lse, row, at::kFloat, a.dev);
-    void* s = stream_on(stream, a.dev);
     call([&] {
-        return lce_fwd(a.x.data_ptr(), a.w.data_ptr(), a.target.data_ptr<int64_t>(), ignore, pl, pz, a.N, a.V, a.D, dt, s);
+        return lce_fwd(a.x.data_ptr(), a.w.data_ptr(), a.target.data_ptr<int64_t>(), ignore, pl, pz, a.N, a.V, a.D, dt, on.s);
     });
     return py::make_tuple(wrap(loss), wrap(lse));
 }
@@ -289,13 +300,13 @@ py::tuple p_lce_bwd(py::object x_, py::object w_, py::object t_, py::object lse_
     const float* pg = (const float*)like("dloss", need("dloss", dloss_), row, at::kFloat, a.dev);
     const ScalarType t = a.x.scalar_type();
     const int dt = code(a.x);
+    const OnStream on(stream, a.dev);
     const Tensor dx = make(arg("dx", dx_), a.x.sizes(), t, a.x), dw = make(arg("dw", dw_), a.w.sizes(), t, a.x);
     void* pdx = like("dx", dx, a.x.sizes(), t, a.dev);
     void* pdw = like("dw", dw, a.w.sizes(), t, a.dev);
-    void* s = stream_on(stream, a.dev);
     call([&] {
         return lce_bwd(a.x.data_ptr(), a.w.data_ptr(), a.target.data_ptr<int64_t>(), ignore, pz, pg, pdx, pdw, a.N, a.V, a.D,
-                       dt, s);
+                       dt, on.s);
     });
     return py::make_tuple(wrap(dx), wrap(dw));
 }

@@ -205,3 +205,36 @@ def test_every_instance(cuda, D, dtype):
     assert err(got["dx"], dx) <= 2 * TOL[dtype]
     for k, t in (("dw", tw), ("db", tb)):
         assert float(((got[k].double().cpu() - t.sum(0)).abs() / t.abs().sum(0).clamp(min=1.0)).max()) <= 2e-6, k
+
+
+@pytest.mark.gpu
+def test_outputs_belong_to_the_stream_that_writes_them(cuda):
+    """Memory that the caching allocator has just taken back on the current stream may
+    still be read there: an output written on another stream is not made of it."""
+    x = torch.randn(8192, 1, 128, device="cuda")
+    w = torch.ones(128, device="cuda")
+    t = torch.zeros(8192, 1, dtype=torch.int64, device="cuda")
+    rows = torch.randn(8192, 128, device="cuda")
+    pool = torch.zeros(8192, 128, device="cuda")
+    lse = torch.ones(8192, 1, device="cuda")
+    s = torch.cuda.Stream()
+
+    def step(**k):
+        pool.zero_()
+        torch.cuda.synchronize()
+        return cuda.glr_step(rows, rows, rows, w, w, w, pool, **k)
+
+    for call in (lambda **k: cuda.layer_norm_fwd(x, w, **k)[0], lambda **k: cuda.layer_norm_bwd(x, w, lse, lse, x, **k)["dx"],
+                 lambda **k: cuda.glr_fwd(x, x, x, w, w, w, **k)[0], lambda **k: cuda.glr_bwd(x, x, x, w, w, w, x, x, **k)["dx"],
+                 step,
+                 lambda **k: cuda.lce_bwd(x, rows, t, lse, lse, **k)[0], lambda **k: cuda.lr_scan_fwd(x, x, **k),
+                 lambda **k: cuda.sru_fwd(x, x, x, x, w, w, **k)[0]):
+        want = call()
+        torch.cuda.synchronize()
+        old = torch.empty_like(x)
+        taken = old.data_ptr()
+        del old
+        y = call(stream=s)
+        assert y.data_ptr() != taken
+        s.synchronize()
+        assert torch.equal(y, want)

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "lr_common.cuh"
@@ -287,15 +288,16 @@ inline cudaError_t launch_dep(void (*kernel)(P...), dim3 grid, dim3 block, size_
 // Grid of a persistent launch: every walker plus as many tile CTAs as can be
 // resident at once (never more than there are tiles).
 inline int sm_count() {
-    static int sms[64] = {0};
+    static std::atomic<int> sms[64];  // zeros; some calls take no lock
     int dev = 0;
     cudaGetDevice(&dev);
-    int& n_sm = sms[dev & 63];
-    if (n_sm <= 0) {
-        cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
-        if (n_sm <= 0) n_sm = 1;
+    std::atomic<int>& slot = sms[dev & 63];
+    int n = slot.load(std::memory_order_relaxed);
+    if (n <= 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 1;
+        slot.store(n, std::memory_order_relaxed);
     }
-    return n_sm;
+    return n;
 }
 inline uint32_t persist_grid(const Geom& g, const Carry& cr, int occ_per_sm) {
     const int n_sm = sm_count();

@@ -22,6 +22,7 @@
 // them: fp32 30011 x 1111 backward 79 us, 5.1 TB/s.
 #include "lr_launch.h"
 
+#include <atomic>
 #include <type_traits>
 #include <utility>
 
@@ -407,15 +408,17 @@ static LnShape ln_shape(int64_t D, int vec) {
 
 // CTAs of a launch: the groups of rows, at most as many as are resident at once
 // (asked once per kernel, device and block size: `known`, one entry per warp count).
+// Atomic: the forward call takes no lock, and calls of several threads meet here.
+using LnKnown = std::atomic<int>[64][33];
 template <class K>
-static int ln_grid(K kernel, int threads, size_t smem, int64_t groups, int (&known)[64][33]) {
+static int ln_grid(K kernel, int threads, size_t smem, int64_t groups, LnKnown& known) {
     int dev = 0;
     cudaGetDevice(&dev);
-    int& n = known[dev & 63][threads / 32];
+    std::atomic<int>& slot = known[dev & 63][threads / 32];
+    int n = slot.load(std::memory_order_relaxed);
     if (n <= 0) {
-        int b = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, threads, smem) != cudaSuccess || b <= 0) b = 1;
-        n = b;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n <= 0) n = 1;
+        slot.store(n, std::memory_order_relaxed);
     }
     const int64_t cap = (int64_t)n * sm_count();
     return (int)(groups < cap ? groups : cap);
@@ -425,7 +428,7 @@ template <typename S, int VEC, int NV, int MAXT, bool RES>
 static cudaError_t ln_fwd_r(const LnShape& sh, const void* x, const void* res, const float* w,
                             const float* b, void* y, void* sum, float* mean, float* rstd, int64_t N,
                             int64_t D, float eps, cudaStream_t s) {
-    static int known[64][33] = {};
+    static LnKnown known;  // zeros
     const int grid = ln_grid(k_ln_fwd<S, VEC, NV, MAXT, RES>, sh.t * sh.rows, 0, (N + sh.rows - 1) / sh.rows, known);
     k_ln_fwd<S, VEC, NV, MAXT, RES><<<grid, dim3(sh.t, sh.rows), 0, s>>>(
         (const S*)x, (const S*)res, w, b, (S*)y, (S*)sum, mean, rstd, N, (int)D, eps);
@@ -442,7 +445,7 @@ static cudaError_t ln_bwd_r(const LnShape& sh, const void* x, const float* w, co
                                                    2 * 1024 * 16 * (int)sizeof(float));
         if (e != cudaSuccess) return e;
     }
-    static int known[64][33] = {};
+    static LnKnown known;  // zeros
     int grid = ln_grid(k_ln_bwd<S, VEC, NV, MAXT, RES>, sh.t * sh.rows, smem, (N + sh.rows - 1) / sh.rows, known);
     if (grid > kLnMaxPartials) grid = kLnMaxPartials;
     k_ln_bwd<S, VEC, NV, MAXT, RES><<<grid, dim3(sh.t, sh.rows), smem, s>>>(

@@ -238,3 +238,30 @@ def test_outputs_belong_to_the_stream_that_writes_them(cuda):
         assert y.data_ptr() != taken
         s.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.gpu
+def test_calls_from_several_threads(cuda):
+    """The forward call takes no lock and the binding gives up the GIL: threads on
+    streams of their own, each through shapes that the others ask for first as well."""
+    import threading
+    shapes = [(4000, 128), (900, 1111), (300, 4096), (100, 8200), (5000, 49)]
+    data = [make(N, D, "f32", seed=N) for N, D in shapes]
+    xs, ws = [d["x"].cuda() for d in data], [d["w"].cuda() for d in data]
+    torch.cuda.synchronize()
+    got = {}
+
+    def work(k):
+        s = torch.cuda.Stream()
+        for i in range(20):
+            j = (i * 3 + k) % len(shapes)
+            got[k, i] = (j, cuda.layer_norm_fwd(xs[j], ws[j], stream=s)[0])
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    want = [cuda.layer_norm_fwd(x, w)[0] for x, w in zip(xs, ws)]
+    assert len(got) == 160 and all(torch.equal(y, want[j]) for j, y in got.values())

@@ -108,7 +108,7 @@ typedef enum {
     LR_ERR_INVALID_ARG = 1,   /* NULL required pointer, negative size, bad dtype */
     LR_ERR_ALIGN = 2,         /* pointer not aligned to its element size */
     LR_ERR_CUDA = 3,          /* a CUDA runtime call failed (message: lr_cuda_error_string) */
-    LR_ERR_TIMEOUT = 4,       /* device: a carry wait ran out; outputs are NaN */
+    LR_ERR_TIMEOUT = 4,       /* device: a wait ran out; what it was waited for is NaN */
     LR_ERR_NONFINITE = 5,     /* DEER: a residual was NaN or Inf */
     LR_ERR_NOT_CONVERGED = 6, /* DEER: kmax iterations without residual < eps */
     LR_ERR_TOO_LARGE = 7,     /* sizes beyond the supported range */
@@ -616,6 +616,15 @@ int lr_test_fail_after_enqueue(float* x, int64_t n, float value, uint64_t sleep_
  */
 int lce_plan_info(int bwd, int dtype, int vec, int64_t N, int64_t V, int64_t D, int64_t* rows, int64_t* piece,
                   int64_t* dx_splits, int64_t* bytes);
+
+/*
+ * Test hook for the bounded waits of the newer kernels: until it is called with 0,
+ * glr_fwd, glr_bwd, lce_fwd and lce_bwd issue none of their tile copies and give up
+ * each wait after limit_ns nanoseconds (1 s at most).  Such a call leaves
+ * LR_ERR_TIMEOUT in the device error word and NaN in what it computed.  Nothing faults
+ * or hangs.
+ */
+int lr_test_stall(uint64_t limit_ns);
 
 /*
  * Test hook: the budget of lce_fwd's and lce_bwd's scratch that lce_plan_info names, in

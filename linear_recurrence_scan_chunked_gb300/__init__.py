@@ -89,6 +89,7 @@ def load():
     lib.lr_test_fail_after_enqueue.restype = I
     lib.lce_plan_info.argtypes = [I, I, I, I64, I64, I64, P, P, P, P]
     lib.lr_test_lce_budget.argtypes = [I64]
+    lib.lr_test_stall.argtypes = [ctypes.c_uint64]
     lib.lr_test_adamw_vec.argtypes = [I, I] + [P] * 5
     lib.lr_plan_info.argtypes = [I, I, I, I64, I64, P, P, P, P]
     lib.lr_plan_info.restype = I
@@ -560,6 +561,12 @@ def lce_plan_info(bwd: bool, dtype: str, vec: bool, N: int, V: int, D: int) -> d
 def test_lce_budget(bytes_: int = 0) -> int:
     """Sets the scratch budget of the cross entropy (0: its own) for tests of several pieces."""
     return int(load().lr_test_lce_budget(int(bytes_)))
+
+
+def test_stall(limit_ns: int = 0) -> int:
+    """Until called with 0: the tiled calls load nothing and their waits run out after
+    limit_ns (the test of bounded waits)."""
+    return int(load().lr_test_stall(int(limit_ns)))
 
 
 def test_activations(x, stream=None, with_expm1=False):

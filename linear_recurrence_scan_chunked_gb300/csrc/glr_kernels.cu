@@ -54,6 +54,8 @@ struct SpanGeom {
     uint32_t cps;   // chunks per span
     uint32_t S;
     int64_t nb;     // sequences (row pitch of reset)
+    uint64_t wait_ns;   // limit of a wait
+    uint32_t stalled;   // test: no tile is loaded, so that every wait runs out
 };
 
 // A thread's place in a block of rows: VEC channels of R rows, consecutive in scan
@@ -195,6 +197,11 @@ struct Feat {
             b2r[v] = -kLog2e * br[v];
             b2i[v] = -kLog2e * bi[v];
         }
+    }
+    // both gates NaN: whatever the rows hold, the results are
+    __device__ __forceinline__ void spoil() {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) b2r[v] = b2i[v] = __int_as_float(0x7fc00000);
     }
     // the general forms' arguments, exact up to the last bits of the products
     __device__ __forceinline__ float log_a(int v, float r) const { return 16.f * l16[v] * r; }
@@ -735,7 +742,7 @@ __global__ void __launch_bounds__(Op::NW * 32, ST > 0 ? Op::MINB : Op::MINB - 2)
     if (ST > 0 && threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) mbar_init(&full[i], 1);
         mbar_init_fence();
-        for (uint32_t i = 0; i < (uint32_t)ST && i < n; ++i)
+        for (uint32_t i = 0; i < (uint32_t)ST && i < n && !sg.stalled; ++i)
             span_issue<Op, ST>(sg, td, ring, full, i, q0 + i, j);
     }
     using Ln = Lane<Op, L>;
@@ -753,7 +760,6 @@ __global__ void __launch_bounds__(Op::NW * 32, ST > 0 ? Op::MINB : Op::MINB - 2)
     ft.load(p.in, ln.cd, ln.cok);
     const uint32_t mine = ln.row0 * (32 * VEC * (uint32_t)sizeof(typename Op::S)) + lane * (VEC * (uint32_t)sizeof(typename Op::S));
     {  // the state entering the span: each warp folds its share of the spans before
-        griddep_wait();  // (launched while k_glr_agg runs)
         float A[VEC], B[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) { A[v] = 1.f; B[v] = 0.f; }
@@ -798,9 +804,10 @@ __global__ void __launch_bounds__(Op::NW * 32, ST > 0 ? Op::MINB : Op::MINB - 2)
         const int64_t t = bk.t + tstep;
         const Block nx{t, bk.at + estep, t + L <= sg.g.T};
         if constexpr (ST > 0) {
-            if (!mbar_wait(&full[PAR], (it >> 1) & 1u, err)) {
-                dead = true;  // the states become NaN
+            if (!mbar_wait(&full[PAR], (it >> 1) & 1u, err, sg.wait_ns)) {
+                dead = true;  // this tile's results and the next ones' become NaN
                 atomicOr(err, ERRBIT_TIMEOUT);
+                ft.spoil();
             }
             Op::template load<false>(FromStage<Op>{ring + PAR * tma_stage_bytes<Op>() + mine}, p, rg);
         } else if (more) {
@@ -810,10 +817,6 @@ __global__ void __launch_bounds__(Op::NW * 32, ST > 0 ? Op::MINB : Op::MINB - 2)
         float A[VEC], B[VEC];
         typename Op::Work w;
         Op::gates(p, sg, ln, bk, ft, rg, w, A, B);
-        if (ST > 0 && dead) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) B[v] = __int_as_float(0x7fc00000);
-        }
 #pragma unroll
         for (int v = 0; v < VEC; ++v) { sm.a[PAR][warp][lane][v] = A[v]; sm.b[PAR][warp][lane][v] = B[v]; }
         csync<NW>();  // the tile's one barrier: its stage has been read too
@@ -951,7 +954,7 @@ cudaError_t span_run(const typename Op::Params& p, const GlrSpans& pl, const Geo
     int slots = 0;
     const cudaError_t e = span_slots<Op, ST>(&slots);
     if (e != cudaSuccess) return e;
-    const SpanGeom sg{g, (uint32_t)pl.cps, (uint32_t)pl.S, g.C / g.D};
+    const SpanGeom sg{g, (uint32_t)pl.cps, (uint32_t)pl.S, g.C / g.D, pl.stall_ns ? pl.stall_ns : kMbarLimitNs, pl.stall_ns != 0};
     TmaDesc td;
     memset(&td, 0, sizeof td);
     if (ST > 0) {

@@ -618,7 +618,7 @@ struct MmPlan {
     int64_t splits;
 };
 
-Shape mm_shape(int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn, bool n_fast, const MmPlan& pl) {
+Shape mm_shape(int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn, bool n_fast, const MmPlan& pl, uint64_t stall_ns) {
     Shape s{};
     s.tm = (uint32_t)((M + kTile - 1) / kTile);
     s.tn = (uint32_t)((N + pl.tn - 1) / pl.tn);
@@ -628,6 +628,8 @@ Shape mm_shape(int64_t M, int64_t N, int64_t K, bool a_mn, bool b_mn, bool n_fas
     s.n_fast = n_fast;
     s.a_mn = a_mn;
     s.b_mn = b_mn;
+    s.wait_ns = stall_ns ? stall_ns : kMbarLimitNs;
+    s.stalled = stall_ns != 0;
     return s;
 }
 
@@ -749,7 +751,7 @@ cudaError_t lce_fwd_t(const void* x, const void* w, const int64_t* target, int64
         Operand a = ox;
         a.p += r * a.ld;
         a.rows = n;
-        const Shape sh = mm_shape(n, V, D, false, false, false, MmPlan{pl.tn_logits, 1});
+        const Shape sh = mm_shape(n, V, D, false, false, false, MmPlan{pl.tn_logits, 1}, pl.stall_ns);
         constexpr int P = sizeof(S) == 4 ? 3 : 1;
         if (sh.kb > mm::chunk_of(P))
             LCE_TRY(mm_run(a, ow, sh, StatsEpi<true, P>{part, tl, target + r, n, V, 0}, pl.tn_logits, err, s));
@@ -800,7 +802,7 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
         wp.p += v0 * ow.ld;
         wp.rows = vc;
         const Operand og{g, N, vc, pitch, N * pitch, P};
-        const Shape sl = mm_shape(N, vc, D, false, false, false, MmPlan{pl.tn_logits, 1});
+        const Shape sl = mm_shape(N, vc, D, false, false, false, MmPlan{pl.tn_logits, 1}, pl.stall_ns);
         auto logits = [&](auto chunked) {
             return mm_run(ox, wp, sl,
                           GradEpi<decltype(chunked)::value, P>{g, pitch, N * pitch, lse, dloss, target, top, ignore, N, v0, vc, V, 0},
@@ -808,7 +810,7 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
         };
         LCE_TRY(sl.kb > mm::chunk_of(P) ? logits(std::true_type{}) : logits(std::false_type{}));
         // dx: rows of x by features, over the words of the piece
-        const Shape sx = mm_shape(N, D, vc, false, true, true, MmPlan{pl.tn_dx, pl.dx_splits});
+        const Shape sx = mm_shape(N, D, vc, false, true, true, MmPlan{pl.tn_dx, pl.dx_splits}, pl.stall_ns);
         const bool dx_direct = pl.dx_splits == 1 && !pieces;
         auto dx_of = [&](auto chunked) {
             return mm_run(og, wp, sx,
@@ -823,7 +825,7 @@ cudaError_t lce_bwd_t(const void* x, const void* w, const int64_t* target, int64
             else LCE_TRY(sum_parts<S>(px, sx.splits, xpitch, N * D, before, top, (S*)dx, s));
         }
         // dw: words of the piece by features, over the rows of x
-        const Shape sw = mm_shape(vc, D, N, true, true, true, MmPlan{pl.tn_dw, pl.dw_splits});
+        const Shape sw = mm_shape(vc, D, N, true, true, true, MmPlan{pl.tn_dw, pl.dw_splits}, pl.stall_ns);
         const bool dw_direct = pl.dw_splits == 1;
         S* dwp = (S*)dw + v0 * D;
         auto dw_of = [&](auto chunked) {

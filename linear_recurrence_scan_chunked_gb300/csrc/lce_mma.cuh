@@ -26,8 +26,9 @@
 // it runs across them; both come out of TMA in the layouts that the matrix
 // descriptors name, so no product needs a transposed copy.
 //
-// Every wait is bounded: one that runs out records LR_ERR_TIMEOUT, and every role
-// then leaves its loop, the pair meets, lets its copies land and frees its TMEM.
+// Every wait is bounded: one that runs out records LR_ERR_TIMEOUT, the epilogue makes
+// NaN of the results that it waited for, the other roles leave their loops, the pair
+// meets, lets its copies land and frees its TMEM.
 #pragma once
 
 #include "lr_tma.cuh"
@@ -61,6 +62,8 @@ struct Shape {
     uint32_t kb_split;      // k-blocks of a part
     uint32_t n_fast;        // neighbouring tiles along the columns (else along the rows)
     uint32_t a_mn, b_mn;    // MN-major operands
+    uint64_t wait_ns;       // limit of a wait
+    uint32_t stalled;       // test: no operand is loaded, so that every wait runs out
 };
 
 // Both CTAs of the pair, all threads.
@@ -83,13 +86,13 @@ __device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* m, i
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool wait_cluster(uint64_t* b, uint32_t parity, const uint32_t* err) {
+__device__ __forceinline__ bool wait_cluster(uint64_t* b, uint32_t parity, const uint32_t* err, uint64_t limit_ns) {
     if (mbar_try_wait_cluster(b, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t n = 1;; ++n) {
         if (mbar_try_wait_cluster(b, parity)) return true;
         if ((n & 255u) == 0) {
-            if (globaltimer_ns() - t0 > kMbarLimitNs) return false;
+            if (globaltimer_ns() - t0 > limit_ns) return false;
             if (ld_relaxed_u32(err) & ERRBIT_TIMEOUT) return false;
         }
     }
@@ -239,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     bool ok = true;
     if (warp == 0) {
-        if (lane == 0) {  // producer
+        if (lane == 0 && !sh.stalled) {  // producer
             uint32_t it = 0;
             for (uint32_t t = pair; t < n_tiles && ok; t += n_pairs) {
                 const Tile tl = tile_of(sh, t);
@@ -250,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int32_t kk = (int32_t)(k * kBlockK);
                     for (int32_t p = 0; p < kPlanes; ++p, ++it) {
                         const uint32_t st = it % kStages;
-                        if (it >= kStages && !wait_cluster(&empty[st], (it / kStages - 1) & 1, err)) {
+                        if (it >= kStages && !wait_cluster(&empty[st], (it / kStages - 1) & 1, err, sh.wait_ns)) {
                             ok = false;
                             break;
                         }
@@ -277,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // barriers has landed) before the CTA ends
             const uint32_t tail = it < kStages ? it : kStages;
             for (uint32_t i = it - tail; i < it && ok; ++i)
-                ok = wait_cluster(&empty[i % kStages], (i / kStages) & 1, err);
+                ok = wait_cluster(&empty[i % kStages], (i / kStages) & 1, err, sh.wait_ns);
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {  // MMA issue
@@ -289,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t chunk = Epi::kChunked ? Epi::kChunk : steps;
                 for (uint32_t c0 = 0; c0 < steps && ok; c0 += chunk, ++seq) {
                     const uint32_t buf = seq & 1;
-                    if (seq >= 2 && !wait_cluster(&tempty[buf], (seq / 2 - 1) & 1, err)) {
+                    if (seq >= 2 && !wait_cluster(&tempty[buf], (seq / 2 - 1) & 1, err, sh.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -301,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (uint32_t p = 0; p < (uint32_t)kPlanes; ++p) {
                             const uint32_t st = (it + p) % kStages;
-                            ok = ok && wait_cluster(&full[st], ((it + p) / kStages) & 1, err);
+                            ok = ok && wait_cluster(&full[st], ((it + p) / kStages) & 1, err, sh.wait_ns);
                             const uint32_t a = smem_u32(ring + st * kStageBytes);
                             da[p] = smem_desc(a, sh.a_mn);
                             db[p] = smem_desc(a + kOperandA, sh.b_mn);
@@ -333,7 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float* scratch = reinterpret_cast<float*>(ring + C::kRing + (warp - 2) * kScratch);  // with Epi::kStaged
         uint32_t seq = 0;
         auto wait = [&](uint32_t buf) {
-            const bool good = __all_sync(0xffffffffu, wait_cluster(&tfull[buf], (seq / 2) & 1, err));
+            const bool good = __all_sync(0xffffffffu, wait_cluster(&tfull[buf], (seq / 2) & 1, err, sh.wait_ns));
             fence_after();
             return good;
         };
@@ -342,7 +345,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) arrive_cluster(cluster_addr(&tempty[buf], 0));
         };
-        for (uint32_t t = pair; t < n_tiles && ok; t += n_pairs) {
+        // a wait that ran out: this tile's results and the next ones' are NaN
+        for (uint32_t t = pair; t < n_tiles; t += n_pairs) {
             const Tile tl = tile_of(sh, t);
             const int width = epi.width(tl, half);
             if constexpr (Epi::kChunked) {
@@ -364,7 +368,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     }
                     done(buf);
                 }
-                if (!ok) break;
+                if (!ok) {
+#pragma unroll
+                    for (int i = 0; i < C::kHalfN; ++i) acc[i] = __int_as_float(0x7fc00000);
+                }
                 typename Epi::Row r = epi.begin(tl, row, half);
 #pragma unroll
                 for (int g = 0; g < C::kHalfN / 32; ++g) {
@@ -379,17 +386,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             } else {
                 const uint32_t buf = seq & 1;
                 typename Epi::Row r = epi.begin(tl, row, half);
-                ok = wait(buf);
-                if (!ok) break;
+                ok = ok && wait(buf);
                 for (int g = 0; g < C::kHalfN / 32 && g * 32 < width; ++g) {
                     float v[32];
                     __syncwarp();  // the load is one instruction of the whole warp
-                    tmem_load32(lanes + buf * TN + g * 32, v);
+                    if (ok) {
+                        tmem_load32(lanes + buf * TN + g * 32, v);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __int_as_float(0x7fc00000);
+                    }
                     epi.cols(r, g, v, scratch);
                 }
                 epi.end(r);
                 __syncwarp();
-                done(buf);
+                if (ok) done(buf);
                 ++seq;
             }
         }

@@ -161,6 +161,7 @@ struct DevWS {
 
 std::mutex g_mu;
 int64_t g_lce_budget = 0;  // lr_test_lce_budget
+uint64_t g_stall_ns = 0;   // lr_test_stall
 std::vector<DevWS*> g_ws;
 
 int get_ws(DevWS** out) {
@@ -527,7 +528,8 @@ int glr_fwd(const void* x, const void* zr, const void* zi, const float* lam, con
     TRY(get_ws(&ws));
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
-    const GlrSpans pl = glr_spans(false, dtype, vec, T, B * D);
+    GlrSpans pl = glr_spans(false, dtype, vec, T, B * D);
+    pl.stall_ns = g_stall_ns;
     if (pl.S * pl.n_ct > INT32_MAX || pl.n_chunks > INT32_MAX || B * D > kSpanMaxChannels) return LR_ERR_TOO_LARGE;
     TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(2 * pl.S * B * D), false, &ws->partials_held, s));
     CK(launch_glr_fwd(dtype, pl, GlrIn{x, zr, zi, lam, br, bi, reset}, h0, h, h_last, ws->partials, T, B * D, D,
@@ -565,7 +567,8 @@ int glr_bwd(const void* x, const void* zr, const void* zi, const float* lam, con
     TRY(get_ws(&ws));
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
-    const GlrSpans pl = glr_spans(true, dtype, vec, T, B * D);
+    GlrSpans pl = glr_spans(true, dtype, vec, T, B * D);
+    pl.stall_ns = g_stall_ns;
     if (pl.S * pl.n_ct > INT32_MAX || pl.n_chunks > INT32_MAX || B * D > kSpanMaxChannels) return LR_ERR_TOO_LARGE;
     TRY(grow(*ws, &ws->partials, &ws->partials_cap, (size_t)(5 * pl.S * B * D + 3 * B * D), false, &ws->partials_held, s));
     CK(launch_glr_bwd(dtype, pl, GlrIn{x, zr, zi, lam, br, bi, reset}, h0, h, dh, dh_last, dx, dzr, dzi, dh0,
@@ -679,7 +682,8 @@ int lce_fwd(const void* x, const void* w, const int64_t* target, int64_t ignore,
     TRY(get_ws(&ws));
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
-    const LcePlan pl = lce_plan(dtype, x, w, N, V, D, false, g_lce_budget);
+    LcePlan pl = lce_plan(dtype, x, w, N, V, D, false, g_lce_budget);
+    pl.stall_ns = g_stall_ns;
     TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.bytes, false, &ws->lce_held, s));
     CK(launch_lce_fwd(dtype, x, w, target, ignore, loss, lse, N, V, D, pl, ws->lce, ws->words + kWordErr, s));
     return lv.done();
@@ -705,7 +709,8 @@ int lce_bwd(const void* x, const void* w, const int64_t* target, int64_t ignore,
     TRY(get_ws(&ws));
     TRY(enter(*ws, s));
     Leave lv(*ws, s);
-    const LcePlan pl = lce_plan(dtype, x, w, N, V, D, true, g_lce_budget);
+    LcePlan pl = lce_plan(dtype, x, w, N, V, D, true, g_lce_budget);
+    pl.stall_ns = g_stall_ns;
     TRY(grow(*ws, &ws->lce, &ws->lce_cap, pl.bytes, false, &ws->lce_held, s));
     CK(launch_lce_bwd(dtype, x, w, target, ignore, lse, dloss, dx, dw, N, V, D, pl, ws->lce, ws->words + kWordErr, s));
     return lv.done();
@@ -1275,6 +1280,13 @@ int lr_plan_info(int op, int dtype, int vec, int64_t T, int64_t C, int* protocol
     if (tma) *tma = cp.tma ? 1 : 0;
     if (tile_rows) *tile_rows = cp.ts.L;
     if (n_chunks) *n_chunks = cp.n_chunks;
+    return LR_OK;
+}
+
+int lr_test_stall(uint64_t limit_ns) {
+    if (limit_ns > 1000000000ull) return LR_ERR_INVALID_ARG;
+    GUARD;
+    g_stall_ns = limit_ns;
     return LR_OK;
 }
 

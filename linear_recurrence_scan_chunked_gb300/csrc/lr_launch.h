@@ -412,6 +412,7 @@ constexpr int kSpanSms = 152;  // GB300: the plan depends on the shape alone
 struct GlrSpans {
     int64_t rows, n_chunks, n_ct, cps, S;
     bool vec, tma;
+    uint64_t stall_ns;  // test: no tile is loaded, waits give up after this (0: neither)
 };
 constexpr int64_t kSpanMaxChannels = (int64_t)1 << 25;  // 32-bit offsets within a tile of 16 rows
 GlrSpans glr_spans(bool bwd, int dtype, bool vec, int64_t T, int64_t C);
@@ -478,6 +479,7 @@ struct LcePlan {
     int64_t dx_splits;  // backward: parts of the k loops
     int64_t dw_splits;
     size_t bytes;       // scratch
+    uint64_t stall_ns;  // test: no tile is loaded, waits give up after this (0: neither)
 };
 // budget: bytes of a piece's gradients of logits, or of a round's statistics (0: 2 GB)
 LcePlan lce_plan(int dtype, const void* x, const void* w, int64_t N, int64_t V, int64_t D, bool bwd, int64_t budget);

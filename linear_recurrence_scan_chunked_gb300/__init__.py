@@ -12,7 +12,6 @@ Tensors are CUDA, contiguous, [T, B, D] for sequences, [B, D] for states and
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import importlib.util
 import os
@@ -176,17 +175,17 @@ def _param(name, t, D, ref):
 def _like(t, stream):
     """An output like t, of the memory of the stream that writes it: what the
     allocator has taken back on the current stream may still be in use there."""
-    with _on(stream):
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
         return torch.empty_like(t)
 
 
 def _new(shape, dtype, ref, stream):
-    with _on(stream):
+    if stream is None:
         return torch.empty(shape, dtype=dtype, device=ref.device)
-
-
-def _on(stream):
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=ref.device)
 
 
 def lr_scan_fwd(a, b, h0=None, h=None, stream=None):

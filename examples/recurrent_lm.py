@@ -146,14 +146,13 @@ def synthetic(vocab, T, B, gen, device="cuda"):
     """Packed documents in which every token follows from the one before (plus 1
     or times 2, by the document): a batch of (tokens, targets, resets)."""
     tok = torch.empty(T + 1, B, dtype=torch.int64)
-    reset = torch.zeros(T, B, dtype=torch.uint8)
+    start = torch.zeros(T + 1, B, dtype=torch.uint8)
     for b in range(B):
         t = 0
         while t <= T:
             n = int(torch.randint(8, 40, (1,), generator=gen))
             x, add = int(torch.randint(0, vocab, (1,), generator=gen)), int(torch.randint(0, 2, (1,), generator=gen))
-            if t < T:
-                reset[t, b] = 1
+            start[t, b] = 1
             for _ in range(n):
                 if t > T:
                     break
@@ -161,7 +160,8 @@ def synthetic(vocab, T, B, gen, device="cuda"):
                 x = (x + 1) % vocab if add else (2 * x + 1) % vocab
                 t += 1
     target = tok[1:].clone()
-    target[:-1][reset[1:].bool()] = IGNORE  # a document's first token follows from nothing
+    target[start[1:].bool()] = IGNORE  # a document's first token follows from nothing
+    reset = start[:T].contiguous()
     return tok[:T].contiguous().to(device), target.to(device), reset.to(device)
 
 

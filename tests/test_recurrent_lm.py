@@ -103,3 +103,16 @@ def test_training_learns(cuda, lm, bits):
         first = last if first is None else first
     assert first > 3.5 and last < 2.0, (first, last)
     assert cuda.last_error() == cuda.LR_OK
+
+
+def test_synthetic_targets_follow_from_their_tokens(lm):
+    """Every target that counts is what one of the two rules makes of its token, the
+    last step's as well, after which a document may start (CPU)."""
+    gen = torch.Generator().manual_seed(6)
+    for T in (1, 7, 64, 129):
+        tok, target, reset = lm.synthetic(509, T, 32, gen, device="cpu")
+        live = target != lm.IGNORE
+        follows = (target == (tok + 1) % 509) | (target == (2 * tok + 1) % 509)
+        assert bool(follows[live].all())
+        assert reset.shape == (T, 32) and bool(reset[0].all())
+        assert not bool(live[:-1][reset[1:].bool()].any())

@@ -25,8 +25,8 @@
 // arguments (no copy to the device, nothing to keep for a graph); a CTA finds
 // its tensor by binary search over the chunk counts.  Measured: 128M elements in
 // 160 tensors, bf16 gradients and copies, 546 us = 6.9 TB/s (copy 6.78); 8-bit
-// moments, 64M elements in 90 tensors, fp32 gradients, 197 us = 5.5 TB/s, and their
-// values written out 100 us = 6.7 TB/s.
+// moments, 64M elements in 90 tensors, fp32 gradients, 198 us = 5.4 TB/s, and their
+// values written out 99 us = 6.8 TB/s.
 #include "lr_act.cuh"
 #include "lr_launch.h"
 
@@ -192,8 +192,8 @@ __device__ __forceinline__ uint32_t sign_bytes(const float* f) {
 }
 
 // One warp per block of 256 elements, four consecutive ones of each half a lane,
-// worked on in pairs.  About 97 instructions an element (104 with the codes put
-// together one by one; IEEE roots throughout cost another 17), issue slots 83% busy.
+// worked on in pairs.  About 100 instructions an element (7 more with the codes put
+// together one by one; IEEE roots throughout cost another 17), issue slots 84% busy.
 // What it took for 64M elements, fp32 gradients: eight consecutive elements a lane,
 // two accesses to every sector, 290 us; this layout 239 with three CTAs an SM, 224
 // with four (64 registers; five spill: 269); chunks of 4096 209 (of 16384 216, of

@@ -29,11 +29,11 @@
 // of the spans before its own.  Every association depends on the shape alone: the
 // same bits every run.
 //
-// Measured (HBM copy 6.78 TB/s).  Forward bf16 8192 x 16 x 4096 with resets: 1016 us,
-// 4.2 TB/s, issue slots 74% busy over the launch (the strips do not divide evenly
-// over the SMs).  Backward bf16 65536 x 1 x 1024 with resets: 284 us = k_glr_agg 86 +
-// k_glr_span 187 (5.5 TB/s of what it moves) + the parameter sums; fp32
-// 2048 x 32 x 1024: 381 us, 5.6 TB/s.  On the scan's engine, tiles carried from CTA
+// Measured (HBM copy 6.78 TB/s).  Forward bf16 8192 x 16 x 4096 with resets: 1019 us,
+// 4.2 TB/s, issue slots 75% busy (what warps wait for besides a slot: fixed latencies,
+// loads, the pipes of the exponentials and roots).  Backward bf16 65536 x 1 x 1024 with
+// resets, 128 spans: 289 us = k_glr_agg 84 + k_glr_span 196 (5.3 TB/s of what it moves)
+// + the parameter sums 7; fp32 2048 x 32 x 1024: 381 us, 5.6 TB/s.  On the scan's engine, tiles carried from CTA
 // to CTA, the same three took 1523, 667 and 391.
 #include "lr_act.cuh"
 #include "lr_launch.h"
@@ -1013,15 +1013,15 @@ Geom span_geom(const GlrSpans& pl, int64_t T, int64_t C, int64_t D) {
 // which reads some inputs again, costs less than idle slots do.  Measured with
 // 2^27 elements, one span against the spans chosen here, us:
 //   strips        128        192        256        320        384
-//   bf16 fwd   635 / 420  500 / 415  378 / 412                296 / 399
-//   fp32 fwd   715 / 553  549 / 547  426 / 543                355 / 538
-//   bf16 bwd   881 / 484  698 / 488  534 / 473  522 / 479  445 / 474
-//   fp32 bwd   871 / 815  750 / 824  656 / 789  691 / 799  704 / 796
+//   bf16 fwd   666 / 432  526 / 427  396 / 424  358 / 417  302 / 418
+//   fp32 fwd   690 / 547  529 / 541  418 / 538  392 / 531  351 / 536
+//   bf16 bwd   884 / 482  687 / 482  524 / 474  527 / 478  450 / 474
+//   fp32 bwd   930 / 808  769 / 805  656 / 805  681 / 796  705 / 814
 // Cut: at first as many spans as make one CTA for every slot (7 an SM forward, 5
 // backward); where spans stay 32 tiles long, up to three times as many, which even
-// out the SMs (4096 channels of 32768 steps, bf16 451 -> 429 us forward, 532 -> 486
-// backward, fp32 902 -> 814; of 2048 steps, where a span would be three tiles, 35 ->
-// 39 forward, so not there).  At least two tiles a span.
+// out the SMs (4096 channels of 32768 steps, when it was chosen: bf16 451 -> 429 us
+// forward, 532 -> 486 backward, fp32 902 -> 814; of 2048 steps, where a span would be
+// three tiles, 35 -> 39 forward, so not there).  At least two tiles a span.
 GlrSpans glr_spans(bool bwd, int dtype, bool vec, int64_t T, int64_t C) {
     GlrSpans p{};
     const int es = dtype == 1 ? 2 : 4;

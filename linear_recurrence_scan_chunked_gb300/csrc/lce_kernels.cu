@@ -11,8 +11,9 @@
 // kernel joins the tiles' pairs.  Backward:
 // for a piece of the vocabulary the product runs again, its epilogue writes g
 // (scratch, bounded by kPieceBytes), and two more products give the piece's dW and
-// its share of dx.  That is 8 N V D operations where a form that kept the logits
-// needs 6, but no N x V array of them.
+// its share of dx, which is added onto one fp32 sum where there are several pieces.
+// That is 8 N V D operations where a form that kept the logits needs 6, but no N x V
+// array past the budget.
 //
 // Types.  g is held in bf16 for bf16 data: relative error 2^-9 an element,
 // independent from element to element, as much as the rounding of the results.
@@ -25,10 +26,10 @@
 // added in order.
 //
 // Measured (cuBLAS bf16 1.92 PFLOP/s in a burst, 1.71 sustained).  bf16 8192 x 1024,
-// V 65536, loss and gradients: 2.71 to 2.97 ms over boxes (power capped), 1.62 to
-// 1.48 PFLOP/s over the 8 N V D; in one such call logits 666 us, their gradient 690,
-// dx 623, dW 671, the rest 49.  Loss alone, 4096 x 4096, V 131072: 2.57 to 2.78 ms,
-// 1.71 to 1.58 PFLOP/s.  fp32 509 x 250, V 10007: 110 us in eight launches, the
+// V 65536, loss and gradients: 2.93 to 3.00 ms over boxes (power capped), 1.50 to
+// 1.47 PFLOP/s over the 8 N V D; each product from cold: logits 696 us, their gradient
+// 716, dx 665, dW 703, the rest 42.  Loss alone, 4096 x 4096, V 131072: 2.76 to 2.78 ms,
+// 1.59 to 1.58 PFLOP/s.  fp32 509 x 250, V 10007: 110 us in eight launches, the
 // largest 33, none of which fills the GPU for long.
 #include <algorithm>
 #include <utility>

@@ -99,9 +99,18 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* b, uint32_t parity, const
 }
 
 // ---- tcgen05
+//
+// TMEM is managed by a warp of each CTA of the pair together, and an instruction of one
+// reaches the other's TMEM: the peer has to be running when either is issued, both have to
+// hold their columns before one gives up its permit, and neither may end before both
+// have given their columns back.  The pair meets at each of these points.  (With only the
+// meeting before the columns are given back, one CTA in some 10^6 waited for its columns
+// for ever while its peer had its own.  Taking them has no limit of its own.)
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
                  : "memory");
+}
+__device__ __forceinline__ void tmem_permit_back() {
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
 }
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
@@ -225,15 +234,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         mbar_init_fence();
     }
-    if (warp == 1) tmem_alloc(&tmem_base, 2 * TN);
-    if (threadIdx.x == 32) {
+    if (threadIdx.x == 64) {
         tma_prefetch_desc(&map_a);
         tma_prefetch_desc(&map_b);
     }
+    __syncthreads();
+    pair_sync();  // both CTAs run
+    if (warp == 1) tmem_alloc(&tmem_base, 2 * TN);
     fence_before();
     __syncthreads();
-    pair_sync();
+    pair_sync();  // both hold their columns
     fence_after();
+    if (warp == 1) tmem_permit_back();
     const uint32_t tmem = tmem_base;
     // a programmatic launch: set up while the kernel before finishes, and let the
     // one after do the same
@@ -417,6 +429,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     pair_sync();  // the peer's arrivals on this CTA's barriers have landed
     fence_after();
     if (warp == 1) tmem_free(tmem, 2 * TN);
+    __syncthreads();
+    pair_sync();  // both have given their columns back
 }
 
 }  // namespace mm

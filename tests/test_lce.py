@@ -609,3 +609,28 @@ assert lrs.last_error() == lrs.LR_OK
     root = os.path.dirname(os.path.dirname(os.path.abspath(lrs.__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,V,D,dtype", [(82, 23040, 79, "f32"), (82, 5000, 64, "bf16"), (300, 300, 300, "f32")])
+def test_calls_one_behind_the_other(cuda, N, V, D, dtype):
+    """Thousands of small calls without a wait between them, each kernel set up while
+    the one before ends: the pairs of CTAs take and give back their tensor memory in
+    step.  The last call's bits are the first one's."""
+    import time
+    x, w, t, dl = (v.cuda() for v in make(N, V, D, dtype, seed=21))
+    loss, lse = cuda.lce_fwd(x, w, t)
+    dx, dw = cuda.lce_bwd(x, w, t, lse, dl)
+    want = [v.clone() for v in (loss, lse, dx, dw)]
+    for _ in range(4):
+        for _ in range(2500):
+            cuda.lce_fwd(x, w, t, loss=loss, lse=lse)
+            cuda.lce_bwd(x, w, t, lse, dl, dx=dx, dw=dw)
+        done = torch.cuda.Event()
+        done.record()
+        limit = time.monotonic() + 60
+        while not done.query():
+            assert time.monotonic() < limit, "the calls do not end"
+            time.sleep(1e-3)
+    assert all(torch.equal(a, b) for a, b in zip((loss, lse, dx, dw), want))
+    assert cuda.last_error() == cuda.LR_OK

@@ -28,8 +28,8 @@
 // Measured (cuBLAS bf16 1.92 PFLOP/s in a burst, 1.71 sustained).  bf16 8192 x 1024,
 // V 65536, loss and gradients: 2.93 to 3.02 ms over boxes (power capped), 1.50 to
 // 1.46 PFLOP/s over the 8 N V D; each product from cold: logits 696 us, their gradient
-// 716, dx 665, dW 703, the rest 42.  Loss alone, 4096 x 4096, V 131072: 2.76 to 2.78 ms,
-// 1.59 to 1.58 PFLOP/s.  fp32 509 x 250, V 10007: 113 us in eight launches, the
+// 716, dx 665, dW 703, the rest 42.  Loss alone, 4096 x 4096, V 131072: 2.76 to 2.80 ms,
+// 1.59 to 1.57 PFLOP/s.  fp32 509 x 250, V 10007: 113 us in eight launches, the
 // largest 33, none of which fills the GPU for long.
 #include <algorithm>
 #include <utility>
